@@ -144,7 +144,8 @@ int pkv_seqs_leave(pkv_alloc *a, const int32_t *seq_ids, int32_t n);
 /*
  * Host part of one decode step for the B listed (distinct, live) sequences.
  * Outputs (host arrays, row b = seq_ids[b]):
- *   positions[B]      int32  position of the new token (= cached length before)
+ *   positions[B]      int32  position of the new token (= cached length before, plus the
+ *                            sequence's offset, pkv_seq_set_offset)
  *   slot_mapping[B]   int64  cache slot of the new token
  *   seq_lens[B]       int32  length after the append (what attention reads)
  *   block_tables[B*bt_stride] int32, row-major, padded with -1
@@ -176,6 +177,18 @@ int pkv_seq_blocks(const pkv_alloc *a, int32_t seq_id, int32_t *out, int32_t cap
  * is negative or beyond the length; nothing is changed. */
 int pkv_seq_slots(const pkv_alloc *a, int32_t seq_id, int32_t start, int32_t count,
                   int32_t *positions, int64_t *slot_mapping);
+/* Positions that run ahead of the cached length.  A sequence's next token sits at
+ * position length + offset (0 at join): pkv_seq_set_offset sets the offset (a
+ * sequence behind a shared prefix: the prefix's length; offset >= 0), and
+ * pkv_prepare_step's positions include it.  Slots, lengths and tables do not. */
+int pkv_seq_set_offset(pkv_alloc *a, int32_t seq_id, int32_t offset);
+int pkv_seq_offset(const pkv_alloc *a, int32_t seq_id, int32_t *offset);
+/* After pkv_evict: sequence seq_ids[i] now holds keep_lens[i] tokens (if it held
+ * more; else nothing changes for it).  The blocks behind them return to the free
+ * list in table order, and the offset grows by the tokens dropped, so that
+ * positions go on where they were.  All or nothing: every id must be live and
+ * listed once, every keep_lens[i] >= 0. */
+int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_t *keep_lens, int32_t n);
 int pkv_num_free(const pkv_alloc *a, int32_t *n);
 /* Pool auto-sizing ("neurogrid releases" v0.7.0: the pool is sized from the
  * VRAM budget): the number of 16-token blocks whose K and V, for every KV head
@@ -391,6 +404,199 @@ int pkv_lse_merge(const void *workspace, size_t workspace_bytes, const int32_t *
                   int32_t bt_stride, int32_t bias_stride, int32_t B, int32_t Hq,
                   int32_t Hkv, int32_t d, int32_t num_parts, void *out, int32_t dtype,
                   void *stream);
+
+/* ======================================================================== */
+/* rotary positions in other layouts and scalings, with the append           */
+/* ======================================================================== */
+/*
+ * What pkv_rope_append does for whole heads in the rotate-half layout, for the
+ * other ways in which heads carry positions.  Pair i < rot_dim/2 of a head at
+ * position p turns by theta = p * f_i:
+ *   PKV_ROTARY_HALF         (x1, x2) = (x[i], x[i + rot_dim/2])
+ *   PKV_ROTARY_INTERLEAVED  (x1, x2) = (x[2i], x[2i+1])
+ *   x1' = amplitude * (x1 cos - x2 sin),  x2' = amplitude * (x2 cos + x1 sin)
+ * Elements from rot_dim on are copied.  With g_i = base^(-2i/rot_dim):
+ *   PKV_ROTARY_PLAIN   f_i = g_i
+ *   PKV_ROTARY_LINEAR  f_i = g_i / factor
+ *   PKV_ROTARY_NTK     f_i = g_i with base * factor^(rot_dim/(rot_dim-2)) for base
+ *   PKV_ROTARY_RAMP    f_i = g_i (1-w) + g_i/factor w, w = clamp((i-lo)/(hi-lo), 0, 1),
+ *                      lo = max(0, floor(D(high))), hi = min(rot_dim-1, ceil(D(low))),
+ *                      D(t) = rot_dim ln(original_len/(2 pi t)) / (2 ln base): the pair
+ *                      that makes t turns over original_len (hi - lo is at least 0.001)
+ *   PKV_ROTARY_BANDS   f_i = s g_i + (1-s) g_i/factor, s = clamp((t_i-low)/(high-low), 0, 1),
+ *                      t_i = original_len g_i/(2 pi), the turns of pair i
+ * Angles are formed modulo 2*pi exactly, as pkv_rope forms them (positions may
+ * be negative here), rotated in float32 and rounded once to dtype; PLAIN over
+ * the whole head in the HALF layout gives pkv_rope's values bit for bit.
+ */
+#define PKV_ROTARY_HALF 0
+#define PKV_ROTARY_INTERLEAVED 1
+#define PKV_ROTARY_PLAIN 0
+#define PKV_ROTARY_LINEAR 1
+#define PKV_ROTARY_NTK 2
+#define PKV_ROTARY_RAMP 3
+#define PKV_ROTARY_BANDS 4
+
+typedef struct pkv_rotary_spec {
+  int32_t rot_dim;                   /* rotated elements at the front of a head: even, 2..d */
+  int32_t layout;                    /* PKV_ROTARY_HALF, PKV_ROTARY_INTERLEAVED */
+  int32_t scaling;                   /* PKV_ROTARY_PLAIN .. PKV_ROTARY_BANDS */
+  int32_t original_len;              /* RAMP, BANDS: the trained length, > 0 */
+  double base;                       /* >= 1 (> 1 for RAMP) */
+  double factor;                     /* >= 1 (unused by PLAIN) */
+  double low, high;                  /* RAMP, BANDS: turns, 0 < low < high */
+  double amplitude;                  /* > 0; 1 for none */
+} pkv_rotary_spec;
+
+/* What the kernels need of a spec, filled by pkv_rotary_init (host only) and
+ * kept by the caller; it owns nothing. */
+typedef struct pkv_rotary {
+  int32_t d, rot_dim, layout;
+  float amplitude;
+  uint64_t turns[128];               /* 2^64 * f_i / (2 pi) */
+  uint32_t check;                    /* set by pkv_rotary_init */
+} pkv_rotary;
+int pkv_rotary_init(const pkv_rotary_spec *spec, int32_t d, pkv_rotary *out);
+
+typedef struct pkv_rotary_args {
+  const pkv_rotary *rotary;          /* host */
+  const void *q, *k, *v;             /* T tokens of [Hq,d], [Hkv,d], [Hkv,d]; a token's heads
+                                        are dense, tokens lie q_stride, k_stride, v_stride
+                                        elements apart (slices of one projection's output) */
+  int64_t q_stride, k_stride, v_stride;
+  void *q_out, *k_out;               /* rotated q and k (k_out nullable when appending) */
+  int64_t q_out_stride, k_out_stride;
+  const int32_t *positions;          /* [T] */
+  const int64_t *slot_mapping;       /* [T], or NULL: nothing is appended */
+  void *k_cache, *v_cache;           /* [num_blocks,Hkv,16,d]; used with slot_mapping */
+  int32_t num_blocks, T, Hq, Hkv, d, dtype;
+  int32_t *dev_err_flag;             /* nullable */
+} pkv_rotary_args;
+/*
+ * Rotates the queries and keys of T tokens (a decode step's rows or a prompt's
+ * tokens) and, with slot_mapping, writes the rotated keys and the values into
+ * the cache as pkv_append does (negative slot: nothing; a slot beyond the pool
+ * sets PKV_DEVERR_BAD_SLOT; of tokens naming one slot, any one's row may stay).
+ * Hq or Hkv may be 0.  In place (q_out == q with the same stride, k_out == k) is
+ * allowed; no other overlap is.  d even, 2..256; appending needs
+ * d * sizeof(dtype) and the caches' addresses to be multiples of 16 bytes.
+ */
+int pkv_rotary_append(const pkv_rotary_args *args, void *stream);
+
+/* ======================================================================== */
+/* decode attention over shared prefixes, with per-token weights             */
+/* ======================================================================== */
+/*
+ * Rows that begin with the same tokens (a system prompt, a document) keep those
+ * tokens in blocks of their own, once: row b attends over the tokens of prefix
+ * row_prefix[b] followed by its own seq_lens[b] tokens, which are all that its
+ * block table names.  Each prefix's keys and values are read once for all of its
+ * rows, as matrix products over the rows' queries; the rows' own tokens go
+ * through the split-KV kernel, whose epilogue merges the two by log-sum-exp:
+ *   out[b,h] = sum_t softmax_t(q_rot[b,h] . k_t * scale + bias_t) v_t
+ * over t in prefix ++ own (the bias, if any, covers own tokens only; -inf, or a
+ * value below -2.35e38 such as float32's lowest, excludes a token).  A row with no
+ * token at all, or none that is not excluded, outputs zeros and lse = -inf.
+ *
+ * Positions are the caller's: a row's own token i sits at position
+ * prefix length + i (pkv_seq_set_offset lets the allocator count that way).
+ *
+ * pkv_shared_plan (host only) groups the rows by prefix and splits the work
+ * over num_ctas CTAs; it depends on which row has which prefix and on the
+ * prefixes' lengths, so a plan stays valid until one of those changes.  Row b
+ * has prefix row_prefix[b] in [0, n_prefixes), or none if that is negative;
+ * prefix p has prefix_lens[p] >= 0 tokens.  plan receives at most plan_cap
+ * int32, *plan_ints of them used; pkv_shared_plan_cap gives a sufficient
+ * capacity.  The plan's own description of its size is what
+ * pkv_shared_workspace_bytes needs: *slots, the partial results it keeps.
+ * num_ctas <= 0 stands for the number of SMs of the current device.
+ */
+int pkv_shared_plan_cap(int32_t B, int32_t n_prefixes, int32_t Hq, int32_t Hkv,
+                        int32_t num_ctas, int32_t *plan_cap, int32_t *max_slots);
+int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32_t *prefix_lens,
+                    int32_t n_prefixes, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                    int32_t num_ctas, int32_t *plan, int32_t plan_cap, int32_t *plan_ints,
+                    int32_t *slots);
+/* Workspace of pkv_decode_attn_shared: the bytes of pkv_attn_workspace_bytes plus
+ * the row sums and the partials of `slots` (0 without prefixes; max_slots above
+ * serves every plan of those sizes).  Same rules: 256-byte aligned, zero-filled
+ * once, calls that share it must not overlap. */
+int pkv_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                               int32_t num_parts, int32_t slots, size_t *bytes);
+
+typedef struct pkv_shared_args {
+  const void *q_rot;                 /* [B,Hq,d] */
+  const void *k_cache, *v_cache;     /* [num_blocks,Hkv,16,d] */
+  const int32_t *block_tables;       /* [B*bt_stride] own tokens */
+  const int32_t *seq_lens;           /* [B] own tokens */
+  const float *attn_bias;            /* nullable [B*bias_stride], own tokens */
+  const int32_t *plan;               /* nullable: pkv_plan_parts of the own tokens */
+  const int32_t *prefix_tables;      /* [n_prefixes*pt_stride], or NULL: no prefixes */
+  const int32_t *prefix_plan;        /* device copy of pkv_shared_plan's output (int32[plan_ints],
+                                        16-byte aligned), required with prefix_tables */
+  float *mass;                       /* nullable [num_blocks,Hkv,16]: accumulated weights */
+  float *scores;                     /* with mass: scratch [num_blocks,Hkv,16,Hq/Hkv], 16-byte
+                                        aligned */
+  const int32_t *mass_lens;          /* with mass: nullable [B] */
+  void *workspace;
+  size_t workspace_bytes;
+  void *out;                         /* [B,Hq,d] */
+  float *lse_out;                    /* nullable [B,Hq]: natural log-sum-exp */
+  int32_t *dev_err_flag;             /* nullable */
+  int32_t num_blocks, bt_stride, bias_stride, n_prefixes, pt_stride, plan_ints, slots;
+  int32_t B, Hq, Hkv, d, dtype, flags, num_parts, num_ctas;
+  float scale, mass_decay;
+} pkv_shared_args;
+/*
+ * With mass, every own token's weight is added to its accumulator: for token t
+ * of row b in block k, row r, KV head g,
+ *   mass[k,g,r] = (t < mass_lens[b] ? mass_decay * mass[k,g,r] : 0)
+ *                 + sum over the group's heads of softmax weight of t
+ * (mass_lens NULL stands for seq_lens[b] - 1: the step's new token starts from
+ * zero, whatever its block held before).  The weights are relative to prefix and
+ * own tokens together.  A block may then belong to one row only.
+ *
+ * Sizes as pkv_decode_attn_split; flags: PKV_ATTN_SIMT (own tokens),
+ * PKV_ATTN_CHECK_PLAN, PKV_ATTN_SHORT_WAITS.  A block id outside the pool sets
+ * PKV_DEVERR_BAD_BLOCK and its tokens are left out; plan records that do not
+ * fit the call set PKV_DEVERR_BAD_PLAN and are skipped.  plan_ints, slots and
+ * num_ctas are pkv_shared_plan's.
+ */
+int pkv_decode_attn_shared(const pkv_shared_args *args, void *stream);
+
+/* ======================================================================== */
+/* eviction by accumulated weight                                            */
+/* ======================================================================== */
+/*
+ * Row b of L = seq_lens[b] tokens keeps K = keep_lens[b] of them, for each KV
+ * head its own choice: its last r = min(recent, K) tokens, its first
+ * s = min(sink, K - r), and of those between the K - r - s with the largest
+ * mass (equal ones: the lowest index; NaN counts as the largest).  The kept
+ * tokens' keys, values and mass move, in their order, to the front of the row's
+ * blocks (in place: slots 0..K-1 of its block table); what lies behind is left
+ * as it was.  Keys stay rotated at their own positions.  A row with L <= K is
+ * left alone.  kept[b,g,j] receives the index of the j-th kept token (-1 from
+ * min(L,K) on), for all kept_stride entries of every row.
+ *
+ * A row with a bad length (L < 0, L > 16*bt_stride, K < 0, or min(L,K) >
+ * kept_stride) sets PKV_DEVERR_BAD_LEN, one with a block id outside the pool
+ * PKV_DEVERR_BAD_BLOCK; such a row is left alone, its kept entries are -1.  A
+ * block may appear once among the rows' tables.  The host then shortens the
+ * sequences with pkv_seqs_evict.
+ * d * sizeof(dtype) a multiple of 16; caches 16-byte aligned; B <= 65536.
+ */
+typedef struct pkv_evict_args {
+  void *k_cache, *v_cache;           /* [num_blocks,Hkv,16,d] */
+  float *mass;                       /* [num_blocks,Hkv,16] */
+  const int32_t *block_tables;       /* [B*bt_stride] */
+  const int32_t *seq_lens;           /* [B] */
+  const int32_t *keep_lens;          /* [B] */
+  int32_t *kept;                     /* [B,Hkv,kept_stride] */
+  int32_t *dev_err_flag;             /* nullable */
+  int32_t num_blocks, bt_stride, kept_stride, sink, recent;
+  int32_t B, Hkv, d, dtype;
+} pkv_evict_args;
+int pkv_evict(const pkv_evict_args *args, void *stream);
 
 /* ======================================================================== */
 /* the whole device step: a1 -> a2 -> a3 -> a4 on one stream                */

@@ -25,6 +25,8 @@ ATTN_SHORT_WAITS = 8
 ATTN_CHECK_PLAN = 16
 LAYERS_MERGE_HELPERS = 32
 STEP_FUSED = 4
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_RAMP, ROTARY_BANDS = range(5)
 
 _c_i32 = ctypes.c_int32
 _c_i64 = ctypes.c_int64
@@ -78,6 +80,60 @@ class ServerDesc(ctypes.Structure):
     _fields_ = [
         ("step", StepArgs), ("alloc", _vp), ("rows", _vp),
         ("meta_host", _vp * 2), ("prefix_host", _vp * 2), ("max_prefix_tokens", _c_i32),
+    ]
+
+
+class RotarySpec(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", _c_i32), ("layout", _c_i32), ("scaling", _c_i32), ("original_len", _c_i32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+        ("high", ctypes.c_double), ("amplitude", ctypes.c_double),
+    ]
+
+
+class RotaryTable(ctypes.Structure):
+    _fields_ = [
+        ("d", _c_i32), ("rot_dim", _c_i32), ("layout", _c_i32), ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_uint64 * 128), ("check", ctypes.c_uint32),
+    ]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [
+        ("rotary", ctypes.POINTER(RotaryTable)),
+        ("q", _vp), ("k", _vp), ("v", _vp),
+        ("q_stride", _c_i64), ("k_stride", _c_i64), ("v_stride", _c_i64),
+        ("q_out", _vp), ("k_out", _vp), ("q_out_stride", _c_i64), ("k_out_stride", _c_i64),
+        ("positions", _vp), ("slot_mapping", _vp), ("k_cache", _vp), ("v_cache", _vp),
+        ("num_blocks", _c_i32), ("T", _c_i32), ("Hq", _c_i32), ("Hkv", _c_i32), ("d", _c_i32),
+        ("dtype", _c_i32), ("dev_err_flag", _vp),
+    ]
+
+
+class SharedArgs(ctypes.Structure):
+    _fields_ = [
+        ("q_rot", _vp), ("k_cache", _vp), ("v_cache", _vp),
+        ("block_tables", _vp), ("seq_lens", _vp), ("attn_bias", _vp), ("plan", _vp),
+        ("prefix_tables", _vp), ("prefix_plan", _vp),
+        ("mass", _vp), ("scores", _vp), ("mass_lens", _vp),
+        ("workspace", _vp), ("workspace_bytes", _size_t),
+        ("out", _vp), ("lse_out", _vp), ("dev_err_flag", _vp),
+        ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("bias_stride", _c_i32),
+        ("n_prefixes", _c_i32), ("pt_stride", _c_i32), ("plan_ints", _c_i32), ("slots", _c_i32),
+        ("B", _c_i32), ("Hq", _c_i32), ("Hkv", _c_i32), ("d", _c_i32), ("dtype", _c_i32),
+        ("flags", _c_i32), ("num_parts", _c_i32), ("num_ctas", _c_i32),
+        ("scale", ctypes.c_float), ("mass_decay", ctypes.c_float),
+    ]
+
+
+class EvictArgs(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", _vp), ("v_cache", _vp), ("mass", _vp),
+        ("block_tables", _vp), ("seq_lens", _vp), ("keep_lens", _vp), ("kept", _vp),
+        ("dev_err_flag", _vp),
+        ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("kept_stride", _c_i32),
+        ("sink", _c_i32), ("recent", _c_i32),
+        ("B", _c_i32), ("Hkv", _c_i32), ("d", _c_i32), ("dtype", _c_i32),
     ]
 
 
@@ -154,6 +210,20 @@ SIGNATURES = {
                                        _vp]),
     "pkv_server_rows": (ctypes.c_int, [_vp, _p_i32]),
     "pkv_server_destroy": (None, [_vp]),
+    "pkv_seq_set_offset": (ctypes.c_int, [_vp, _c_i32, _c_i32]),
+    "pkv_seq_offset": (ctypes.c_int, [_vp, _c_i32, _p_i32]),
+    "pkv_seqs_evict": (ctypes.c_int, [_vp, _p_i32, _p_i32, _c_i32]),
+    "pkv_rotary_init": (ctypes.c_int, [ctypes.POINTER(RotarySpec), _c_i32,
+                                       ctypes.POINTER(RotaryTable)]),
+    "pkv_rotary_append": (ctypes.c_int, [ctypes.POINTER(RotaryArgs), _vp]),
+    "pkv_shared_plan_cap": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _p_i32,
+                                           _p_i32]),
+    "pkv_shared_plan": (ctypes.c_int, [_p_i32, _c_i32, _p_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                       _c_i32, _c_i32, _p_i32, _c_i32, _p_i32, _p_i32]),
+    "pkv_shared_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                                  ctypes.POINTER(_size_t)]),
+    "pkv_decode_attn_shared": (ctypes.c_int, [ctypes.POINTER(SharedArgs), _vp]),
+    "pkv_evict": (ctypes.c_int, [ctypes.POINTER(EvictArgs), _vp]),
 }
 
 _LIB = None
@@ -349,6 +419,25 @@ class BlockAllocator:
                                        _np_ptr(pos, ctypes.c_int32, int(count)),
                                        _np_ptr(slots, ctypes.c_int64, int(count))))
         return pos, slots
+
+    def set_offset(self, seq_id, offset):
+        """The sequence's next position is its cached length plus ``offset`` from
+        now on (``pkv_seq_set_offset``)."""
+        _check(self._lib.pkv_seq_set_offset(self._h, int(seq_id), int(offset)))
+
+    def offset(self, seq_id):
+        n = ctypes.c_int32()
+        _check(self._lib.pkv_seq_offset(self._h, int(seq_id), ctypes.byref(n)))
+        return n.value
+
+    def evict_many(self, seq_ids, keep_lens):
+        """Shortens the sequences to ``keep_lens`` after ``evict`` (``pkv_seqs_evict``)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32)
+        keep = np.ascontiguousarray(keep_lens, dtype=np.int32)
+        if len(ids) != len(keep):
+            raise PkvError(ERR_INVALID_ARG, "one keep length per sequence")
+        _check(self._lib.pkv_seqs_evict(self._h, _np_ptr(ids, ctypes.c_int32),
+                                        _np_ptr(keep, ctypes.c_int32), len(ids)))
 
     def num_free(self):
         n = ctypes.c_int32()
@@ -676,6 +765,318 @@ def dense_extract(k_dense, v_dense, cap, rows, prefix_lens, padded_len, steps, k
                                     int(padded_len), int(steps), _ptr_array(k_snaps),
                                     _ptr_array(v_snaps), Hkv, d, dtype_code(k_dense),
                                     _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# rotary layouts and scalings, shared-prefix attention, eviction
+# --------------------------------------------------------------------------
+# These calls take argument structs made once (``make_*_args``: every pointer,
+# size and type is checked there) and launched as often as wanted; the struct
+# keeps its tensors alive.
+def _want(t, name, shape=None, dtype=None, device=None, host=False):
+    """The checked address of a dense tensor: shape (None: any size there), type
+    and device as stated; ``host`` allows pinned host memory read in place."""
+    if shape is not None and (t.dim() != len(shape) or any(
+            w is not None and w != n for w, n in zip(shape, t.shape))):
+        raise PkvError(ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise PkvError(ERR_INVALID_ARG, f"{name}: {t.dtype}, expected {dtype}")
+    if host and not t.is_cuda:
+        return mapped_pointer(t)
+    if device is not None and t.device != device:
+        raise PkvError(ERR_INVALID_ARG, f"{name} is on {t.device}, expected {device}")
+    return _ptr(t)
+
+
+def _heads(t, name, T, d, dtype, device):
+    """Address and token stride of ``t [T,H,d]`` whose heads are dense (a slice of
+    a wider projection's output has a larger token stride)."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise PkvError(ERR_INVALID_ARG, f"{name}: shape {tuple(t.shape)}, expected [{T}, H, {d}]")
+    if t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise PkvError(ERR_INVALID_ARG, f"{name}: {t.dtype} on {t.device}, expected {dtype} on "
+                                        f"one CUDA device")
+    if t.numel() and ((t.stride(2) != 1 and d > 1) or (t.stride(1) != d and t.shape[1] > 1)):
+        raise PkvError(ERR_INVALID_ARG, f"{name}: the heads of a token must be dense")
+    return _vp(t.data_ptr()), t.stride(0) if T > 1 else t.shape[1] * d
+
+
+def _overlap(a, b):
+    """Whether the memory of two non-empty tensors overlaps (by first and last byte)."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _launch_on(args, stream):
+    """The stream of a launch: ``stream`` or the current one, on the tensors' device."""
+    torch = _torch()
+    if torch.cuda.current_device() != args.device.index:
+        raise PkvError(ERR_INVALID_ARG, f"tensors are on {args.device}, the current device is "
+                                        f"cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+class Rotary:
+    """Rotary frequencies of a head of ``d`` elements (``pkv_rotary_init``): the
+    first ``rot_dim`` rotate, in the ``"half"`` or ``"interleaved"`` layout, scaled
+    ``"plain"``, ``"linear"``, ``"ntk"``, ``"ramp"`` or ``"bands"`` (include/pkv.h
+    states the formulas)."""
+    LAYOUTS = {"half": ROTARY_HALF, "interleaved": ROTARY_INTERLEAVED}
+    SCALINGS = {"plain": ROTARY_PLAIN, "linear": ROTARY_LINEAR, "ntk": ROTARY_NTK,
+                "ramp": ROTARY_RAMP, "bands": ROTARY_BANDS}
+
+    def __init__(self, d, rot_dim=None, layout="half", scaling="plain", base=10000.0, factor=1.0,
+                 low=1.0, high=32.0, original_len=0, amplitude=1.0):
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise PkvError(ERR_UNSUPPORTED, f"layout {layout!r}, scaling {scaling!r}")
+        self.d, self.rot_dim = int(d), int(d if rot_dim is None else rot_dim)
+        spec = RotarySpec(self.rot_dim, self.LAYOUTS[layout], self.SCALINGS[scaling],
+                          int(original_len), float(base), float(factor), float(low), float(high),
+                          float(amplitude))
+        self.table = RotaryTable()
+        _check(load().pkv_rotary_init(ctypes.byref(spec), self.d, ctypes.byref(self.table)))
+
+
+def make_rotary_args(rotary, q, k, v, positions, q_out=None, k_out=None, slot_mapping=None,
+                     k_cache=None, v_cache=None, err=None):
+    """``pkv_rotary_args``: ``q [T,Hq,d]`` and ``k, v [T,Hkv,d]`` may be slices of
+    one projection's output (any token stride); without ``slot_mapping`` nothing is
+    appended and ``v`` may be None; ``q`` (with ``q_out``) or ``k`` may be None.
+    ``q_out``/``k_out`` may be ``q``/``k`` themselves; ``k_out`` None reports no
+    rotated keys (they still go to the cache)."""
+    torch = _torch()
+    first = q if q is not None else k
+    if first is None or not first.is_cuda:
+        raise PkvError(ERR_INVALID_ARG, "q or k must be a CUDA tensor")
+    T, d, dt, dev = first.shape[0], first.shape[-1], first.dtype, first.device
+    a = RotaryArgs()
+    a.rotary = ctypes.pointer(rotary.table)
+    a.T, a.d, a.dtype = T, d, dtype_code(first)
+    if q is not None:
+        if q_out is None:
+            raise PkvError(ERR_INVALID_ARG, "q needs q_out")
+        a.Hq = q.shape[1]
+        a.q, a.q_stride = _heads(q, "q", T, d, dt, dev)
+        a.q_out, a.q_out_stride = _heads(q_out, "q_out", T, d, dt, dev)
+        if q_out.shape != q.shape:
+            raise PkvError(ERR_INVALID_ARG, "q_out must have q's shape")
+    if k is not None:
+        a.Hkv = k.shape[1]
+        a.k, a.k_stride = _heads(k, "k", T, d, dt, dev)
+        if k_out is not None:
+            a.k_out, a.k_out_stride = _heads(k_out, "k_out", T, d, dt, dev)
+            if k_out.shape != k.shape:
+                raise PkvError(ERR_INVALID_ARG, "k_out must have k's shape")
+    a.positions = _want(positions, "positions", (T,), torch.int32, dev, host=True)
+    if slot_mapping is not None:
+        if k is None or v is None or k_cache is None or v_cache is None:
+            raise PkvError(ERR_INVALID_ARG, "appending needs k, v and both caches")
+        if v.shape != k.shape:
+            raise PkvError(ERR_INVALID_ARG, "v must have k's shape")
+        a.slot_mapping = _want(slot_mapping, "slot_mapping", (T,), torch.int64, dev, host=True)
+        a.v, a.v_stride = _heads(v, "v", T, d, dt, dev)
+        shape = (k_cache.shape[0], a.Hkv, BLOCK_SIZE, d)
+        a.k_cache = _want(k_cache, "k_cache", shape, dt, dev)
+        a.v_cache = _want(v_cache, "v_cache", shape, dt, dev)
+        a.num_blocks = k_cache.shape[0]
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, torch.int32, dev)
+    a.keep = (rotary, q, k, v, q_out, k_out, positions, slot_mapping, k_cache, v_cache, err)
+    a.device = dev
+    return a
+
+
+def rotary_append_args(args, stream=None):
+    """Runs ``pkv_rotary_append`` from prepared ``RotaryArgs``."""
+    _check(load().pkv_rotary_append(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def rotary_append(rotary, q, k, v, positions, slot_mapping=None, k_cache=None, v_cache=None,
+                  q_out=None, k_out=None, err=None, stream=None):
+    """Rotates ``q`` and ``k`` at ``positions`` and, with ``slot_mapping``, writes
+    the rotated keys and the values into the cache slots; returns ``(q_out, k_out)``."""
+    torch = _torch()
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    rotary_append_args(make_rotary_args(rotary, q, k, v, positions, q_out, k_out, slot_mapping,
+                                        k_cache, v_cache, err), stream)
+    return q_out, k_out
+
+
+def shared_plan_cap(B, n_prefixes, Hq, Hkv, num_ctas=0):
+    """int32 words and partial slots that serve every plan of these sizes."""
+    cap, slots = ctypes.c_int32(), ctypes.c_int32()
+    _check(load().pkv_shared_plan_cap(int(B), int(n_prefixes), int(Hq), int(Hkv), int(num_ctas),
+                                      ctypes.byref(cap), ctypes.byref(slots)))
+    return cap.value, slots.value
+
+
+def shared_plan(row_prefix, prefix_lens, Hq, Hkv, d, dtype, num_ctas=0, out=None):
+    """Host plan of the shared-prefix attention (``pkv_shared_plan``): row b has
+    prefix ``row_prefix[b]`` (negative: none) of ``prefix_lens[p]`` tokens.  Returns
+    the plan (numpy int32, the used part of ``out`` if given)."""
+    rows = np.ascontiguousarray(row_prefix, dtype=np.int32)
+    lens = np.ascontiguousarray(prefix_lens, dtype=np.int32)
+    if out is None:
+        out = np.empty(shared_plan_cap(len(rows), len(lens), Hq, Hkv, num_ctas)[0], np.int32)
+    n, slots = ctypes.c_int32(), ctypes.c_int32()
+    _check(load().pkv_shared_plan(_np_ptr(rows, ctypes.c_int32), len(rows),
+                                  _np_ptr(lens, ctypes.c_int32), len(lens), int(Hq), int(Hkv),
+                                  int(d), int(dtype), int(num_ctas), _np_ptr(out, ctypes.c_int32),
+                                  out.size, ctypes.byref(n), ctypes.byref(slots)))
+    return out[:n.value]
+
+
+def shared_workspace_bytes(B, Hq, Hkv, d, num_parts, slots):
+    n = _size_t()
+    _check(load().pkv_shared_workspace_bytes(int(B), int(Hq), int(Hkv), int(d), int(num_parts),
+                                             int(slots), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_scores(num_blocks, Hq, device=None):
+    """Scratch of the weights' accumulation: the scores of every cache slot."""
+    torch = _torch()
+    return torch.empty((num_blocks, Hq * BLOCK_SIZE), dtype=torch.float32, device=device or "cuda")
+
+
+def make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out,
+                     prefix_tables=None, prefix_plan=None, slots=None, num_ctas=None, mass=None,
+                     scores=None, mass_lens=None, decay=1.0, lse=None, attn_bias=None, plan=None,
+                     num_parts=None, workspace=None, flags=0, err=None):
+    """``pkv_shared_args``.  ``prefix_plan`` is ``shared_plan``'s output on the
+    device (or pinned); ``slots`` and ``num_ctas`` are read from it once unless
+    given (give them, with a workspace for ``slots``, when the buffer will later
+    hold other plans)."""
+    torch = _torch()
+    if q_rot.dim() != 3 or k_cache.dim() != 4 or not q_rot.is_cuda:
+        raise PkvError(ERR_INVALID_ARG, "q_rot must be [B,Hq,d] and the caches [blocks,Hkv,16,d], "
+                                        "on a CUDA device")
+    B, Hq, d = q_rot.shape
+    nb, Hkv = k_cache.shape[0], k_cache.shape[1]
+    dt, dev = q_rot.dtype, q_rot.device
+    i32, f32 = torch.int32, torch.float32
+    a = SharedArgs()
+    a.dtype = dtype_code(q_rot)
+    a.q_rot = _want(q_rot, "q_rot", (B, Hq, d), dt, dev)
+    a.k_cache = _want(k_cache, "k_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.v_cache = _want(v_cache, "v_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.block_tables = _want(block_tables, "block_tables", (B, None), i32, dev, host=True)
+    a.seq_lens = _want(seq_lens, "seq_lens", (B,), i32, dev, host=True)
+    a.out = _want(out, "out", (B, Hq, d), dt, dev)
+    if _overlap(out, q_rot):
+        raise PkvError(ERR_INVALID_ARG, "out must not overlap q_rot")
+    a.num_blocks, a.bt_stride = nb, block_tables.shape[1]
+    a.B, a.Hq, a.Hkv, a.d = B, Hq, Hkv, d
+    a.scale, a.mass_decay, a.flags = float(scale), float(decay), int(flags)
+    if attn_bias is not None:
+        a.attn_bias = _want(attn_bias, "attn_bias", (B, None), f32, dev)
+        a.bias_stride = attn_bias.shape[1]
+    if plan is not None:
+        if num_parts is None:
+            num_parts = plan.shape[0]
+        a.plan = _want(plan, "plan", (num_parts, PLAN_INTS), i32, dev, host=True)
+    if prefix_tables is not None and prefix_tables.shape[0] > 0:
+        if prefix_plan is None:
+            raise PkvError(ERR_INVALID_ARG, "prefix_tables need a prefix_plan")
+        a.prefix_tables = _want(prefix_tables, "prefix_tables", (None, None), i32, dev, host=True)
+        a.n_prefixes, a.pt_stride = prefix_tables.shape
+        a.prefix_plan = _want(prefix_plan, "prefix_plan", (None,), i32, dev, host=True)
+        a.plan_ints = prefix_plan.numel()
+        if slots is None or num_ctas is None:
+            head = prefix_plan[:8].cpu().tolist()
+            slots = head[3] if slots is None else slots
+            num_ctas = head[4] if num_ctas is None else num_ctas
+        a.slots, a.num_ctas = int(slots), int(num_ctas)
+    if mass is not None:
+        if scores is None:
+            raise PkvError(ERR_INVALID_ARG, "mass needs scores (alloc_scores)")
+        a.mass = _want(mass, "mass", (nb, Hkv, BLOCK_SIZE), f32, dev)
+        a.scores = _want(scores, "scores", (nb, Hq * BLOCK_SIZE), f32, dev)
+        if mass_lens is not None:
+            a.mass_lens = _want(mass_lens, "mass_lens", (B,), i32, dev, host=True)
+    if lse is not None:
+        a.lse_out = _want(lse, "lse", (B, Hq), f32, dev)
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, i32, dev)
+    a.num_parts = int(num_parts) if num_parts is not None else default_parts(d, a.dtype, 0, Hq, Hkv)
+    if workspace is None and B > 0:
+        nbytes = shared_workspace_bytes(B, Hq, Hkv, d, a.num_parts, a.slots)
+        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)
+        a.workspace_bytes = workspace.numel()
+    a.keep = (q_rot, k_cache, v_cache, block_tables, seq_lens, out, prefix_tables, prefix_plan, mass,
+              scores, mass_lens, lse, attn_bias, plan, workspace, err)
+    a.device = dev
+    return a
+
+
+def decode_attn_shared_args(args, stream=None):
+    """Runs ``pkv_decode_attn_shared`` from prepared ``SharedArgs``."""
+    _check(load().pkv_decode_attn_shared(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def decode_attention_shared(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out=None,
+                            stream=None, **kw):
+    """Attention over shared prefixes and own tokens: returns ``out [B,Hq,d]`` (see
+    ``make_shared_args`` for the rest)."""
+    out = _torch().empty_like(q_rot) if out is None else out
+    args = make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out, **kw)
+    decode_attn_shared_args(args, stream)
+    return out
+
+
+def make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, sink=0,
+                    recent=0, err=None):
+    """``pkv_evict_args``: ``kept [B,Hkv,>=kept tokens]`` int32 receives the kept
+    tokens' indices."""
+    torch = _torch()
+    if k_cache.dim() != 4 or not k_cache.is_cuda:
+        raise PkvError(ERR_INVALID_ARG, "caches must be [blocks,Hkv,16,d] on a CUDA device")
+    nb, Hkv, _, d = k_cache.shape
+    B, dt, dev, i32 = block_tables.shape[0], k_cache.dtype, k_cache.device, torch.int32
+    a = EvictArgs()
+    a.dtype = dtype_code(k_cache)
+    a.k_cache = _want(k_cache, "k_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.v_cache = _want(v_cache, "v_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.mass = _want(mass, "mass", (nb, Hkv, BLOCK_SIZE), torch.float32, dev)
+    a.block_tables = _want(block_tables, "block_tables", (B, None), i32, dev, host=True)
+    a.seq_lens = _want(seq_lens, "seq_lens", (B,), i32, dev, host=True)
+    a.keep_lens = _want(keep_lens, "keep_lens", (B,), i32, dev, host=True)
+    a.kept = _want(kept, "kept", (B, Hkv, None), i32, dev)
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, i32, dev)
+    a.num_blocks, a.bt_stride, a.kept_stride = nb, block_tables.shape[1], kept.shape[2]
+    a.sink, a.recent = int(sink), int(recent)
+    a.B, a.Hkv, a.d = B, Hkv, d
+    a.keep = (k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, err)
+    a.device = dev
+    return a
+
+
+def evict_args(args, stream=None):
+    """Runs ``pkv_evict`` from prepared ``EvictArgs``."""
+    _check(load().pkv_evict(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def evict(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, max_keep, sink=0, recent=0,
+          kept=None, err=None, stream=None):
+    """Evicts rows down to ``keep_lens`` tokens by ``mass``; returns ``kept
+    [B,Hkv,max_keep]``, the indices of the tokens kept."""
+    if kept is None:
+        kept = _torch().empty((block_tables.shape[0], k_cache.shape[1], max(int(max_keep), 1)),
+                              dtype=_torch().int32, device=k_cache.device)
+    evict_args(make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, sink,
+                               recent, err), stream)
+    return kept
 
 
 def pool_blocks(budget_bytes, n_layers, Hkv, d, dtype):

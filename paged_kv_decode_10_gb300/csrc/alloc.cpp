@@ -24,9 +24,10 @@ struct pkv_alloc {
   std::vector<int32_t> tables;           // [max_seqs * max_blocks_per_seq]
   std::vector<int32_t> n_blocks;         // per sequence id
   std::vector<int32_t> lengths;          // per sequence id
+  std::vector<int32_t> offsets;          // per sequence id: position of the next token - length
   std::vector<uint8_t> live;             // per sequence id
   std::vector<uint32_t> stamp;           // per sequence id, duplicate detection
-  std::vector<int32_t> generation;       // per sequence id, joins so far (ids are reused)
+  std::vector<int32_t> generation;       // per sequence id, joins and evictions so far (ids are reused)
   uint32_t epoch = 0;
   std::priority_queue<int32_t, std::vector<int32_t>, std::greater<int32_t>> free_ids;
 
@@ -81,6 +82,7 @@ extern "C" int pkv_alloc_create(int32_t num_blocks, int32_t block_size, int32_t 
     a->tables.assign(static_cast<size_t>(max_seqs) * max_blocks_per_seq, -1);
     a->n_blocks.assign(max_seqs, 0);
     a->lengths.assign(max_seqs, 0);
+    a->offsets.assign(max_seqs, 0);
     a->live.assign(max_seqs, 0);
     a->stamp.assign(max_seqs, 0);
     a->generation.assign(max_seqs, 0);
@@ -116,6 +118,7 @@ extern "C" int pkv_seq_join(pkv_alloc *a, int32_t prefix_len, int32_t *seq_id) {
   }
   a->n_blocks[sid] = static_cast<int32_t>(need);
   a->lengths[sid] = prefix_len;
+  a->offsets[sid] = 0;
   a->live[sid] = 1;
   ++a->generation[sid];
   *seq_id = sid;
@@ -166,6 +169,8 @@ int prepare_step_impl(pkv_alloc *a, const int32_t *seq_ids, int32_t B, int32_t *
     PKV_REQUIRE(blocks_for(len + 1) <= width, PKV_ERR_INVALID_ARG,
                 "sequence %d would need %lld blocks > %d", s, (long long)blocks_for(len + 1),
                 width);
+    PKV_REQUIRE(len + a->offsets[s] <= INT32_MAX, PKV_ERR_INVALID_ARG,
+                "sequence %d: position beyond 32 bits", s);
     if (len % kBlock == 0) ++need;
   }
   PKV_REQUIRE(need <= static_cast<int64_t>(a->free_stack.size()), PKV_ERR_OUT_OF_BLOCKS,
@@ -178,7 +183,7 @@ int prepare_step_impl(pkv_alloc *a, const int32_t *seq_ids, int32_t B, int32_t *
       t[a->n_blocks[s]++] = a->free_stack.back();
       a->free_stack.pop_back();
     }
-    positions[b] = pos;
+    positions[b] = pos + a->offsets[s];
     slot_mapping[b] = static_cast<int64_t>(t[pos / kBlock]) * kBlock + pos % kBlock;
     a->lengths[s] = pos + 1;
     seq_lens[b] = pos + 1;
@@ -189,7 +194,7 @@ int prepare_step_impl(pkv_alloc *a, const int32_t *seq_ids, int32_t B, int32_t *
       for (int32_t j = n; j < bt_stride; ++j) row[j] = -1;
       continue;
     }
-    // row_state[3b..3b+2]: sequence id, its join generation, entries held
+    // row_state[3b..3b+2]: sequence id, its generation, entries held
     int32_t *rs = row_state + 3 * static_cast<size_t>(b);
     const bool same = rs[0] == s && rs[1] == a->generation[s] && rs[2] >= 0 && rs[2] <= n;
     if (same) {
@@ -282,6 +287,61 @@ extern "C" int pkv_seqs_leave(pkv_alloc *a, const int32_t *seq_ids, int32_t n) {
   for (int32_t i = 0; i < n; ++i) {
     const int rc = pkv_seq_leave(a, seq_ids[i]);
     if (rc != PKV_OK) return rc;
+  }
+  return PKV_OK;
+}
+
+extern "C" int pkv_seq_set_offset(pkv_alloc *a, int32_t seq_id, int32_t offset) {
+  pkv::clear_error();
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL allocator");
+  PKV_REQUIRE(a->is_live(seq_id), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", seq_id);
+  PKV_REQUIRE(offset >= 0, PKV_ERR_INVALID_ARG, "offset %d < 0", offset);
+  a->offsets[seq_id] = offset;
+  return PKV_OK;
+}
+
+extern "C" int pkv_seq_offset(const pkv_alloc *a, int32_t seq_id, int32_t *offset) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && offset, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(a->is_live(seq_id), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", seq_id);
+  *offset = a->offsets[seq_id];
+  return PKV_OK;
+}
+
+extern "C" int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_t *keep_lens,
+                              int32_t n) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && n >= 0, PKV_ERR_INVALID_ARG, "NULL allocator or n < 0");
+  if (n == 0) return PKV_OK;
+  PKV_REQUIRE(seq_ids && keep_lens, PKV_ERR_INVALID_ARG, "NULL argument");
+  if (++a->epoch == 0) {
+    std::fill(a->stamp.begin(), a->stamp.end(), 0u);
+    a->epoch = 1;
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t s = seq_ids[i];
+    PKV_REQUIRE(a->is_live(s), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", s);
+    PKV_REQUIRE(a->stamp[s] != a->epoch, PKV_ERR_INVALID_ARG, "sequence %d listed twice", s);
+    a->stamp[s] = a->epoch;
+    PKV_REQUIRE(keep_lens[i] >= 0, PKV_ERR_INVALID_ARG, "sequence %d: keep_len %d < 0", s,
+                keep_lens[i]);
+    const int64_t drop = static_cast<int64_t>(a->lengths[s]) - keep_lens[i];
+    PKV_REQUIRE(drop <= 0 || drop + a->offsets[s] <= INT32_MAX, PKV_ERR_INVALID_ARG,
+                "sequence %d: position beyond 32 bits", s);
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t s = seq_ids[i];
+    const int32_t drop = a->lengths[s] - keep_lens[i];
+    if (drop <= 0) continue;
+    const int32_t left = static_cast<int32_t>(blocks_for(keep_lens[i]));
+    const int32_t *t = a->table(s);
+    for (int32_t j = left; j < a->n_blocks[s]; ++j) a->free_stack.push_back(t[j]);
+    a->n_blocks[s] = left;
+    a->lengths[s] = keep_lens[i];
+    a->offsets[s] += drop;
+    // a cached table row of this sequence may hold entries that are free now:
+    // it is rewritten like a new sequence's
+    ++a->generation[s];
   }
   return PKV_OK;
 }

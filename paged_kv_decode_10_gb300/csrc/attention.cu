@@ -94,6 +94,8 @@ struct TmapCache {
   int used = 0, next = 0;
 };
 
+}  // namespace
+
 int get_tmap(const void *base, long long rows, int D, int dtype, CUtensorMap *out) {
   static TmapCache cache;
   std::lock_guard<std::mutex> lock(cache.mu);
@@ -129,7 +131,17 @@ int get_tmap(const void *base, long long rows, int D, int dtype, CUtensorMap *ou
   return PKV_OK;
 }
 
-bool pick_variant(int dtype, int D, int G, int flags, AttnVariant *v) {
+int current_sms(int *sms) {
+  int dev = 0;
+  PKV_CUDA_CHECK(cudaGetDevice(&dev));
+  PKV_CUDA_CHECK(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return PKV_OK;
+}
+
+namespace {
+
+bool pick_variant(int dtype, int D, int G, int flags, AttnVariant *v, bool ext = false) {
+  if (ext) return dtype == PKV_BF16 ? attn_variant_ext_bf16(D, v) : attn_variant_ext_f32(D, G, v);
   if (dtype == PKV_BF16 && !(flags & PKV_ATTN_SIMT)) return attn_variant_mma(D, v);
   if (dtype == PKV_BF16) return attn_variant_simt_bf16(D, G, v);
   return attn_variant_simt_f32(D, G, v);
@@ -273,7 +285,7 @@ int attn_launch(const void *q_rot, const void *k_cache, const void *v_cache, int
                 int32_t d, float scale, int32_t num_parts, void *workspace,
                 size_t workspace_bytes, void *out, int32_t dtype, int32_t flags,
                 int32_t *dev_err_flag, void *stream, const pkv_step_args *step,
-                const int32_t *plan, bool allow_helpers = true) {
+                const int32_t *plan, bool allow_helpers = true, const AttnExt *ext = nullptr) {
   int rc = check_shapes(B, Hq, Hkv, d, dtype);
   if (rc != PKV_OK) return rc;
   if (B == 0) return PKV_OK;
@@ -311,7 +323,8 @@ int attn_launch(const void *q_rot, const void *k_cache, const void *v_cache, int
   PKV_REQUIRE(workspace_bytes >= ws.bytes, PKV_ERR_INVALID_ARG,
               "workspace of %zu bytes < %zu needed", workspace_bytes, ws.bytes);
   AttnVariant v;
-  PKV_REQUIRE(pick_variant(dtype, d, G, flags, &v), PKV_ERR_UNSUPPORTED, "no kernel variant");
+  PKV_REQUIRE(pick_variant(dtype, d, G, flags, &v, ext != nullptr), PKV_ERR_UNSUPPORTED,
+              "no kernel variant");
   const long long rows = static_cast<long long>(num_blocks) * Hkv * kBlockTokens;
   CUtensorMap tk, tv;
   rc = get_tmap(k_cache, rows, d, dtype, &tk);
@@ -353,6 +366,7 @@ int attn_launch(const void *q_rot, const void *k_cache, const void *v_cache, int
   p.num_blocks = num_blocks;
   p.num_parts = num_parts;
   p.scale_log2 = scale * kLog2e;
+  p.ext = ext ? *ext : AttnExt{};
   cudaError_t e;
   if (step) {
     PKV_REQUIRE(step->q && step->k && step->v && step->k_rot && step->positions &&
@@ -382,6 +396,14 @@ int attn_launch(const void *q_rot, const void *k_cache, const void *v_cache, int
 }
 
 }  // namespace
+
+int pkv::attn_launch_ext(const pkv_shared_args &a, int num_parts, const AttnExt &ext,
+                         void *stream) {
+  return attn_launch(a.q_rot, a.k_cache, a.v_cache, a.num_blocks, a.block_tables, a.bt_stride,
+                     a.seq_lens, a.attn_bias, a.bias_stride, a.B, a.Hq, a.Hkv, a.d, a.scale,
+                     num_parts, a.workspace, a.workspace_bytes, a.out, a.dtype, a.flags,
+                     a.dev_err_flag, stream, nullptr, a.plan, /*allow_helpers=*/true, &ext);
+}
 
 extern "C" int pkv_decode_attn_split(const void *q_rot, const void *k_cache, const void *v_cache,
                                      int32_t num_blocks, const int32_t *block_tables,

@@ -2,6 +2,8 @@
 #pragma once
 #include <stddef.h>
 
+#include "pkv.h"
+
 namespace pkv {
 
 // Pages of streaming a unit boundary costs a CTA (segment combine, pipeline
@@ -20,5 +22,12 @@ size_t workspace_counter_bytes(int B, int Hq, int Hkv, int D, int C);
 // Shape rules every attention call checks (dtype, head size, B, the group
 // size Hq / Hkv); PKV_OK or the error, with the message set.
 int check_shapes(int B, int Hq, int Hkv, int D, int dtype);
+
+// Streaming multiprocessors of the current device.
+int current_sms(int *sms);
+
+// The EXT attention kernel over the rows' own tokens (pkv_decode_attn_shared).
+struct AttnExt;
+int attn_launch_ext(const pkv_shared_args &a, int num_parts, const AttnExt &ext, void *stream);
 
 }  // namespace pkv

@@ -49,6 +49,20 @@
 
 namespace pkv {
 
+// What the EXT build of the kernel adds (pkv_decode_attn_shared): partial results
+// of a shared prefix joined into every row's output, the row sums, and the raw
+// scores of the rows' own tokens.
+struct AttnExt {
+  const int32_t *row_part;  // nullable [B, 2]: first partial slot and partials of each row
+  const float *pre_o;       // [slots, Hq, D] normalised, and
+  const float *pre_lse;     // [slots, Hq] base-2 log-sum-exp of the prefix partials
+  float *scores;            // nullable [num_blocks, Hkv, 16, G] base-2 scores
+  float *lse2;              // nullable [B, Hq] base-2 log-sum-exp of the whole row
+  float *lse_out;           // nullable [B, Hq] natural log-sum-exp
+  int slots;
+  int dependent;            // launched behind the prefix kernel as its programmatic dependent
+};
+
 struct AttnParams {
   const void *q;            // [B, Hq, D] rotated queries
   const int32_t *block_tables;
@@ -80,6 +94,7 @@ struct AttnParams {
   void *q_rot_out, *k_rot_out;         // [B,Hq,D], [B,Hkv,D]
   long long num_slots;                 // num_blocks * 16
   unsigned long long turns[128];       // RoPE fixed-point turns (fill_rope_turns)
+  AttnExt ext;                         // EXT kernels only
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -284,18 +299,77 @@ __device__ __forceinline__ void merge_store(T *out_rows, int col, int D, const M
   store4<T>(out_rows + h * D + 4 * d4, o);
 }
 
+// EXT: adds the prefix partials of row b, head hq (of the whole row), float4
+// column d4 to a.
+__device__ __forceinline__ void ext_add_prefix(MergeAcc &a, const AttnParams &p, int b, int hq,
+                                               int d4, int D) {
+  if (!p.ext.row_part) return;
+  const int s0 = p.ext.row_part[2 * b], n = p.ext.row_part[2 * b + 1];
+  if (n <= 0) return;
+  if (s0 < 0 || n > p.ext.slots - s0) {   // never read outside the workspace
+    if (d4 == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+    return;
+  }
+  constexpr int K = 4;
+  for (int i0 = 0; i0 < n; i0 += K) {
+    float l[K];
+    float4 v[K];
+#pragma unroll
+    for (int t = 0; t < K; ++t) {
+      const bool on = i0 + t < n;
+      const size_t at = static_cast<size_t>(s0 + (on ? i0 + t : 0)) * p.Hq + hq;
+      l[t] = on ? __ldcg(p.ext.pre_lse + at) : -INFINITY;
+      v[t] = on ? __ldcg(reinterpret_cast<const float4 *>(p.ext.pre_o + at * D) + d4)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    merge_acc_add<K>(a, l, v);
+  }
+}
+
+// EXT: joins the prefix partials into a and stores the column and the row sums.
+template <typename T>
+__device__ __forceinline__ void ext_store(MergeAcc a, const AttnParams &p, int b, int hq, int d4,
+                                          int D) {
+  ext_add_prefix(a, p, b, hq, d4, D);
+  merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D,
+                 a);
+  if (d4 == 0) {
+    const float l2 = a.den > 0.f ? a.M + log2f(a.den) : -INFINITY;
+    const size_t at = static_cast<size_t>(b) * p.Hq + hq;
+    if (p.ext.lse2) p.ext.lse2[at] = l2;
+    if (p.ext.lse_out) p.ext.lse_out[at] = l2 * 0.6931471805599453f;
+  }
+}
+
+// EXT: a row without own tokens: the prefix alone, or zeros.
+template <typename T>
+__device__ __forceinline__ void ext_empty_row(const AttnParams &p, int b, int D, int tid, int nthr) {
+  for (int c = tid; c < p.Hq * (D / 4); c += nthr)
+    ext_store<T>(MergeAcc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}, p, b, c / (D / 4),
+                 c % (D / 4), D);
+}
+
 // Helper r of H: columns [r*NC/H, (r+1)*NC/H) of unit u_idx (parts cf ..
 // cf+nseg-1) merged into out_rows [G, D] by the NTHR consumer threads.  When
 // the slice has fewer columns than threads, R = NTHR / cols threads share a
 // column (each takes every R-th partial) and combine through `scratch`
 // (NTHR * 6 floats of shared memory; all NTHR threads must call this).
-template <typename T, int NTHR>
+template <typename T, int NTHR, bool EXT>
 __device__ __forceinline__ void merge_slice(const AttnParams &p, int u_idx, int cf, int nseg,
                                             long long P, int C, int r, int H, int D, T *out_rows,
                                             float *scratch, int tid) {
   const int NC = p.G * (D / 4);
   const int col0 = r * NC / H, cols = (r + 1) * NC / H - col0;
   const int R = max(1, NTHR / cols);
+  const int ub = u_idx / p.Hkv, ug = u_idx - ub * p.Hkv;   // EXT: the unit's row and KV head
+  if (EXT && R == 1) {
+    for (int c = tid; c < cols; c += NTHR) {
+      const int col = col0 + c;
+      ext_store<T>(merge_partials(p.o_part, p.lse_part, u_idx, cf, nseg, 0, 1, col, p.G, D, P, C), p,
+                   ub, ug * p.G + col / (D / 4), col % (D / 4), D);
+    }
+    return;
+  }
   if (R == 1) {
     for (int c = tid; c < cols; c += NTHR)
       merge_store<T>(out_rows, col0 + c, D,
@@ -331,7 +405,10 @@ __device__ __forceinline__ void merge_slice(const AttnParams &p, int u_idx, int 
         t.acc.w = fmaf(w, f[5], t.acc.w);
       }
     }
-    merge_store<T>(out_rows, col0 + tid, D, t);
+    if constexpr (EXT)
+      ext_store<T>(t, p, ub, ug * p.G + (col0 + tid) / (D / 4), (col0 + tid) % (D / 4), D);
+    else
+      merge_store<T>(out_rows, col0 + tid, D, t);
   }
 }
 
@@ -478,10 +555,13 @@ __device__ __forceinline__ void mma_begin(MmaState<D> &s, const AttnParams &p, i
 }
 
 // One 16-token page: tokens t0 .. t0+15 of which the first `valid` count.
-template <int D>
+// EXT: spage is the page's scores [16][G] (nullable), and the normaliser sums
+// the weights before they are rounded to bf16 for the P.V product, so that the
+// row sums are float32 sums.
+template <int D, bool EXT>
 __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, uint32_t ktile,
                                          uint32_t vtile, int valid, int b, int t0, int lane,
-                                         bool may_bias) {
+                                         bool may_bias, float *spage) {
   const int r = lane >> 2, c = lane & 3;
   const int mq = lane >> 3;
   const int krow = (lane & 7) + (mq & 1) * 8, kj = mq >> 1;
@@ -516,6 +596,21 @@ __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, ui
   }
   if (r >= valid) sc[0] = sc[1] = -INFINITY;
   if (r + 8 >= valid) sc[2] = sc[3] = -INFINITY;
+  if constexpr (EXT) {
+    if (spage) {
+      if (p.G == 1) {
+        if (c == 0) {
+          if (r < valid) spage[r] = sc[0];
+          if (r + 8 < valid) spage[r + 8] = sc[2];
+        }
+      } else if (2 * c < p.G) {
+        if (r < valid)
+          *reinterpret_cast<float2 *>(spage + r * p.G + 2 * c) = make_float2(sc[0], sc[1]);
+        if (r + 8 < valid)
+          *reinterpret_cast<float2 *>(spage + (r + 8) * p.G + 2 * c) = make_float2(sc[2], sc[3]);
+      }
+    }
+  }
   float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) {
@@ -528,11 +623,18 @@ __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, ui
   const float al0 = ex2(s.m[0] - mu0), al1 = ex2(s.m[1] - mu1);
   s.m[0] = mn0;
   s.m[1] = mn1;
-  const uint32_t p01 = pack_bf16(ex2(sc[0] - mu0), ex2(sc[1] - mu1));
-  const uint32_t p23 = pack_bf16(ex2(sc[2] - mu0), ex2(sc[3] - mu1));
-  // the normaliser sums the same bf16-rounded weights the P.V product uses
-  s.l[0] = s.l[0] * al0 + bf16_lo(p01) + bf16_lo(p23);
-  s.l[1] = s.l[1] * al1 + bf16_hi(p01) + bf16_hi(p23);
+  const float w0 = ex2(sc[0] - mu0), w1 = ex2(sc[1] - mu1);
+  const float w2 = ex2(sc[2] - mu0), w3 = ex2(sc[3] - mu1);
+  const uint32_t p01 = pack_bf16(w0, w1);
+  const uint32_t p23 = pack_bf16(w2, w3);
+  if constexpr (EXT) {
+    s.l[0] = s.l[0] * al0 + (w0 + w2);
+    s.l[1] = s.l[1] * al1 + (w1 + w3);
+  } else {
+    // the normaliser sums the same bf16-rounded weights the P.V product uses
+    s.l[0] = s.l[0] * al0 + bf16_lo(p01) + bf16_lo(p23);
+    s.l[1] = s.l[1] * al1 + bf16_hi(p01) + bf16_hi(p23);
+  }
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
     s.acc[mt][0] *= al0;
@@ -804,11 +906,11 @@ __device__ __forceinline__ void simt_begin(SimtState<T, D, G> &s, const AttnPara
   s.l = 0.f;
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool EXT>
 __device__ __forceinline__ void simt_page(SimtState<T, D, G> &s, const AttnParams &p,
                                           const char *ktile, const char *vtile, int valid, int b,
                                           int t0, int lane, float *pbuf, float *abuf,
-                                          bool may_bias) {
+                                          bool may_bias, float *spage) {
   constexpr int DPL = D / 32;
   constexpr int LPH = 32 / G;
   float sc[kBlockTokens];
@@ -837,6 +939,13 @@ __device__ __forceinline__ void simt_page(SimtState<T, D, G> &s, const AttnParam
       sc[i] = -INFINITY;
     }
     mx = fmaxf(mx, sc[i]);
+  }
+  if constexpr (EXT) {
+    if (spage && lane % LPH == 0 && lane / LPH < p.G) {
+#pragma unroll
+      for (int i = 0; i < kBlockTokens; ++i)
+        if (i < valid) spage[i * p.G + lane / LPH] = sc[i];
+    }
   }
   const float mn = fmaxf(s.m, mx);
   const float mu = mn == -INFINITY ? 0.f : mn;
@@ -899,7 +1008,8 @@ __device__ __forceinline__ void simt_stash(SimtState<T, D, G> &s, float *red_acc
 // (p.plan != nullptr, !p.check_plan, p.bias == nullptr): the row-length scan,
 // the plan check and the bias are compiled out, and the smaller kernel runs
 // faster (its instructions come cold at both ends of every CTA).
-template <typename T, int D, int NW, int NS, int KIND, int G, bool FUSE, bool PLAN>
+// EXT: joins prefix partials into the output and writes scores and row sums (AttnExt).
+template <typename T, int D, int NW, int NS, int KIND, int G, bool FUSE, bool PLAN, bool EXT>
 __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     attn_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v,
@@ -1025,8 +1135,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       }
     }
     // rows with no token (or an invalid length) output zeros; part c clears
-    // rows c, c + C, ...
-    for (int b = blockIdx.x; b < p.B; b += C) {   // (after the barrier above: lens_s is complete)
+    // rows c, c + C, ... (EXT: below, where only the consumers wait)
+    for (int b = EXT ? p.B : blockIdx.x; b < p.B; b += C) {   // (after the barrier above: lens_s is complete)
       bool bad;
       const int len = b < Q::kLensCache ? lens_s[b] : p.seq_lens[b];
       if (pages_of_len(len, p.bt_stride, has_bias, p.bias_stride, &bad) == 0) {
@@ -1062,13 +1172,18 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     p.meta[2 * p.B * p.Hkv + 1] = static_cast<int32_t>(P >> 32);
   }
   // rows with no token: without the scan, the consumer warps clear them (off
-  // the producer's path)
-  if (!scanned && warp < NW) {
+  // the producer's path); EXT: they get the prefix alone, once it is there
+  if ((EXT || !scanned) && warp < NW) {
     for (int b = blockIdx.x; b < p.B; b += C) {
       bool bad;
       if (pages_of_len(p.seq_lens[b], p.bt_stride, has_bias, p.bias_stride, &bad) == 0) {
-        T *o = static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D;
-        for (int e = tid; e < p.Hq * D; e += NW * 32) o[e] = from_f32<T>(0.f);
+        if constexpr (EXT) {
+          pdl_wait();
+          ext_empty_row<T>(p, b, D, tid, NW * 32);
+        } else {
+          T *o = static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D;
+          for (int e = tid; e < p.Hq * D; e += NW * 32) o[e] = from_f32<T>(0.f);
+        }
       }
       if (bad && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
     }
@@ -1145,7 +1260,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       qpos = static_cast<uint32_t>(p.positions[b]);
     };
     int x = 0, k = 0;
-    bool aborted = false, waited = FUSE;
+    // (EXT: the queries were written before the prefix kernel was launched)
+    bool aborted = false, waited = FUSE || EXT;
     // pages [j0, j1) of unit u lie in this part's positions [start, end); the
     // unit's pages sit at positions off + A .. off + A + n - 1.  Only a part
     // that lies inside one unit's first A positions has no page at all.
@@ -1288,13 +1404,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
             }
             const bool ok = !dead && blk >= 0 && blk < p.num_blocks;
             if (!dead) {
-              stage_bad[st] = ok ? 0 : 1;
+              // EXT: the consumers also need the page's block id (~id <= 0)
+              stage_bad[st] = ok ? (EXT ? ~blk : 0) : 1;
               stage_pg[st] = xx;
             }
             if (ok) {
               // the last page of a unit holds the token appended by the kernel
               // before this one: wait for that grid before reading it
-              if (!FUSE && jb + i + lane == u.n - 1) pdl_wait();
+              if (!FUSE && !EXT && jb + i + lane == u.n - 1) pdl_wait();
               mbar_arrive_expect_tx(&full[st], Q::kStageBytes);
               const uint32_t kdst = smem_u32(smem + st * Q::kStageBytes);
               const uint32_t vdst = kdst + Q::kTileBytes;
@@ -1378,6 +1495,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     }
     misc[6] = ok ? 0 : 1;
   };
+  auto score_page = [&](int blk, int g) -> float * {   // EXT: where a page's scores go
+    if (!EXT || !p.ext.scores) return nullptr;
+    return p.ext.scores + (static_cast<size_t>(blk) * p.Hkv + g) * kBlockTokens * p.G;
+  };
   if (tid == 0) wait_segment(0);
   asm volatile("bar.sync 1, %0;" ::"r"(kConsumers) : "memory");
   while (misc[6] == 0) {
@@ -1419,10 +1540,11 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
           set_dev_err(p.err, PKV_DEVERR_TIMEOUT);
           ready = false;
         }
-        if (ready && !stage_bad[st]) {
+        const int mark = ready ? stage_bad[st] : 1;
+        if (mark <= 0) {
           const uint32_t kt = smem_u32(smem + st * Q::kStageBytes);
-          mma_page<D>(s, p, kt, kt + Q::kTileBytes, min(kBlockTokens, L - j * kBlockTokens), u.b,
-                      j * kBlockTokens, lane, !PLAN);
+          mma_page<D, EXT>(s, p, kt, kt + Q::kTileBytes, min(kBlockTokens, L - j * kBlockTokens),
+                           u.b, j * kBlockTokens, lane, !PLAN, score_page(~mark, u.g));
         }
         __syncwarp();
         // a stage is handed back only after its page was seen to land
@@ -1452,10 +1574,12 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
           set_dev_err(p.err, PKV_DEVERR_TIMEOUT);
           ready = false;
         }
-        if (ready && !stage_bad[st]) {
+        const int mark = ready ? stage_bad[st] : 1;
+        if (mark <= 0) {
           const char *kt = reinterpret_cast<const char *>(smem + st * Q::kStageBytes);
-          simt_page<T, D, G>(s, p, kt, kt + Q::kTileBytes, min(kBlockTokens, L - j * kBlockTokens),
-                             u.b, j * kBlockTokens, lane, pbuf, abuf, !PLAN);
+          simt_page<T, D, G, EXT>(s, p, kt, kt + Q::kTileBytes,
+                                  min(kBlockTokens, L - j * kBlockTokens), u.b, j * kBlockTokens,
+                                  lane, pbuf, abuf, !PLAN, score_page(~mark, u.g));
         }
         __syncwarp();
         if (lane == 0 && ready) mbar_arrive(&empty[st]);
@@ -1470,6 +1594,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     // rescale factors are recomputed by every thread that needs them (a few
     // shared loads and NW ex2), which costs less than a separate pass and a
     // barrier
+    if (EXT && nseg == 1) pdl_wait();   // the prefix partials come from the kernel before this one
     for (int e4 = tid; e4 < gq * (D / 4); e4 += kConsumers) {
       const int h = e4 / (D / 4), d4 = e4 - h * (D / 4);
       float M = -INFINITY;
@@ -1497,14 +1622,18 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       o.y *= inv;
       o.z *= inv;
       o.w *= inv;
-      if (nseg == 1) {
+      if (EXT && nseg == 1) {
+        ext_store<T>(MergeAcc{den > 0.f ? M + log2f(den) : -INFINITY, den > 0.f ? 1.f : 0.f, o}, p,
+                     u.b, u.g * gq + h, d4, D);
+      } else if (nseg == 1) {
         store4<T>(static_cast<T *>(p.out) + (static_cast<size_t>(u.b) * p.Hq + u.g * gq + h) * D +
                       4 * d4,
                   o);
       } else {
         const size_t idx = static_cast<size_t>(u_idx) + blockIdx.x;
         *reinterpret_cast<float4 *>(p.o_part + (idx * gq + h) * D + 4 * d4) = o;
-        if (d4 == 0) p.lse_part[idx * gq + h] = den > 0.f ? M + lg2(den) : -INFINITY;
+        if (d4 == 0)
+          p.lse_part[idx * gq + h] = den > 0.f ? M + (EXT ? log2f(den) : lg2(den)) : -INFINITY;
       }
     }
     if (tid == 0 && j0 == 0) {
@@ -1575,6 +1704,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
   asm volatile("bar.sync 1, %0;" ::"r"(kConsumers) : "memory");
   const int ra = roles[0], Ha = roles[1], rb = roles[2], Hb = roles[3];
   if (ra < 0 && rb < 0) return;   // (the same for every consumer thread)
+  if constexpr (EXT) pdl_wait();
   float *scratch = red_acc;       // free: the segment combines are done
   auto rows_of = [&](int q) {
     return static_cast<T *>(p.out) +
@@ -1589,18 +1719,22 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     for (int item = tid; item < n0 + n1; item += kConsumers) {
       const int q = item >= n0 ? 1 : 0;
       const int col = item - q * n0;
-      merge_store<T>(rows_of(q), col, D,
-                     merge_partials(p.o_part, p.lse_part, q ? pend_u[1] : pend_u[0],
-                                    q ? pend_c[1] : pend_c[0], q ? pend_n[1] : pend_n[0], 0, 1,
-                                    col, p.G, D, P, C));
+      const MergeAcc acc = merge_partials(p.o_part, p.lse_part, q ? pend_u[1] : pend_u[0],
+                                          q ? pend_c[1] : pend_c[0], q ? pend_n[1] : pend_n[0], 0,
+                                          1, col, p.G, D, P, C);
+      if constexpr (EXT)
+        ext_store<T>(acc, p, q ? pend_b[1] : pend_b[0],
+                     (q ? pend_g[1] : pend_g[0]) * p.G + col / (D / 4), col % (D / 4), D);
+      else
+        merge_store<T>(rows_of(q), col, D, acc);
     }
   } else {
     for (int q = 0; q < npend; ++q) {
       const int r = q ? rb : ra, H = q ? Hb : Ha;
       if (r < 0) continue;
-      merge_slice<T, kConsumers>(p, q ? pend_u[1] : pend_u[0], q ? pend_c[1] : pend_c[0],
-                                 q ? pend_n[1] : pend_n[0], P, C, r, H, D, rows_of(q), scratch,
-                                 tid);
+      merge_slice<T, kConsumers, EXT>(p, q ? pend_u[1] : pend_u[0], q ? pend_c[1] : pend_c[0],
+                                      q ? pend_n[1] : pend_n[0], P, C, r, H, D, rows_of(q), scratch,
+                                      tid);
       asm volatile("bar.sync 1, %0;" ::"r"(kConsumers) : "memory");   // scratch reuse
     }
   }
@@ -1636,10 +1770,10 @@ struct AttnVariant {
 template <typename T, int D, int NW, int NS, int KIND, int G>
 struct AttnLauncher {
   using Q = Geo<T, D, NW, NS>;
-  template <bool FUSE, bool PLAN>
+  template <bool FUSE, bool PLAN, bool EXT = false>
   static cudaError_t launch_impl(const CUtensorMap &tk, const CUtensorMap &tv,
                                  const AttnParams &p, cudaStream_t s) {
-    auto kern = attn_split_kernel<T, D, NW, NS, KIND, G, FUSE, PLAN>;
+    auto kern = attn_split_kernel<T, D, NW, NS, KIND, G, FUSE, PLAN, EXT>;
     static std::atomic<unsigned long long> attrs_set{0};
     cudaError_t e = set_attributes_once(attrs_set, [&] {
       cudaError_t r =
@@ -1666,7 +1800,7 @@ struct AttnLauncher {
       attr[na].id = cudaLaunchAttributeCooperative;
       attr[na++].val.cooperative = 1;
     }
-    if (!FUSE) {
+    if (EXT ? p.ext.dependent != 0 : !FUSE) {
       attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }
@@ -1689,11 +1823,26 @@ struct AttnLauncher {
                    : launch_impl<true, false>(tk, tv, p, s);
   }
   static cudaError_t occupancy(int *n) {
-    auto kern = attn_split_kernel<T, D, NW, NS, KIND, G, false, false>;
+    auto kern = attn_split_kernel<T, D, NW, NS, KIND, G, false, false, false>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, Q::kThreads, Q::kSmemBytes);
+  }
+  // EXT build (its own variant entry: no whole-step form)
+  static cudaError_t launch_ext(const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
+                                cudaStream_t s) {
+    return launch_impl<false, false, true>(tk, tv, p, s);
+  }
+  static cudaError_t occupancy_ext(int *n) {
+    auto kern = attn_split_kernel<T, D, NW, NS, KIND, G, false, false, true>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, Q::kThreads, Q::kSmemBytes);
+  }
+  static AttnVariant variant_ext() {
+    return AttnVariant{&launch_ext, nullptr, &occupancy_ext, Q::kSmemBytes, Q::kThreads};
   }
   static AttnVariant variant() {
     return AttnVariant{&launch, &launch_step, &occupancy, Q::kSmemBytes, Q::kThreads};
@@ -1704,5 +1853,10 @@ struct AttnLauncher {
 bool attn_variant_mma(int D, AttnVariant *v);
 bool attn_variant_simt_bf16(int D, int G, AttnVariant *v);
 bool attn_variant_simt_f32(int D, int G, AttnVariant *v);
+bool attn_variant_ext_bf16(int D, AttnVariant *v);
+bool attn_variant_ext_f32(int D, int G, AttnVariant *v);
+
+// The cached TMA descriptor of a cache [rows, D] (attention.cu).
+int get_tmap(const void *base, long long rows, int D, int dtype, CUtensorMap *out);
 
 }  // namespace pkv
