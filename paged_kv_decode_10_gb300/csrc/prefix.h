@@ -37,7 +37,7 @@ __device__ __forceinline__ bool prefix_item(const PrefixParams &p, int i, int ma
   *it = PrefixItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
   return it->prefix >= 0 && it->prefix < p.n_prefixes && it->g >= 0 && it->g < p.Hkv &&
          it->r0 >= 0 && it->rows > 0 && it->rows * p.G <= max_rows && it->r0 <= p.B - it->rows &&
-         it->t0 >= 0 && it->t0 < it->t1 && it->t1 <= 16ll * p.pt_stride && it->split >= 0;
+         it->t0 >= 0 && it->t0 % kBlockTokens == 0 && it->t0 < it->t1 && it->t1 <= 16ll * p.pt_stride && it->split >= 0;
 }
 // Batch row i of an item and the slot its partial goes to (-1: does not fit).
 __device__ __forceinline__ int prefix_row(const PrefixParams &p, const PrefixItem &it, int i,

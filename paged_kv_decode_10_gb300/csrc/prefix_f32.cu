@@ -174,11 +174,4 @@ cudaError_t launch_prefix_f32(const PrefixParams &p, int D, cudaStream_t s) {
   return D == 64 ? launch<float, 64>(p, kTileRowsF32, s) : launch<float, 128>(p, kTileRowsF32, s);
 }
 
-// (bf16 on the same path)
-cudaError_t launch_prefix_bf16(const CUtensorMap &, const CUtensorMap &, const PrefixParams &p,
-                               int D, cudaStream_t s) {
-  return D == 64 ? launch<__nv_bfloat16, 64>(p, kTileRowsBf16, s)
-                 : launch<__nv_bfloat16, 128>(p, kTileRowsBf16, s);
-}
-
 }  // namespace pkv
