@@ -402,7 +402,7 @@ int pkv::attn_launch_ext(const pkv_shared_args &a, int num_parts, const AttnExt 
   return attn_launch(a.q_rot, a.k_cache, a.v_cache, a.num_blocks, a.block_tables, a.bt_stride,
                      a.seq_lens, a.attn_bias, a.bias_stride, a.B, a.Hq, a.Hkv, a.d, a.scale,
                      num_parts, a.workspace, a.workspace_bytes, a.out, a.dtype, a.flags,
-                     a.dev_err_flag, stream, nullptr, a.plan, /*allow_helpers=*/true, &ext);
+                     a.dev_err_flag, stream, nullptr, a.plan, /*allow_helpers=*/ext.dependent == 0, &ext);
 }
 
 extern "C" int pkv_decode_attn_split(const void *q_rot, const void *k_cache, const void *v_cache,

@@ -49,17 +49,15 @@
 
 namespace pkv {
 
-// What the EXT build of the kernel adds (pkv_decode_attn_shared): partial results
-// of a shared prefix joined into every row's output, the row sums, and the raw
-// scores of the rows' own tokens.
+// What the EXT build of the kernel adds (pkv_decode_attn_shared): the row sums and
+// the raw scores of the rows' own tokens and, where rows also have prefixes, the
+// own tokens' result as a float32 partial instead of the output (the merge kernel
+// joins the two).
 struct AttnExt {
-  const int32_t *row_part;  // nullable [B, 2]: first partial slot and partials of each row
-  const float *pre_o;       // [slots, Hq, D] normalised, and
-  const float *pre_lse;     // [slots, Hq] base-2 log-sum-exp of the prefix partials
-  float *scores;            // nullable [num_blocks, Hkv, 16, G] base-2 scores
-  float *lse2;              // nullable [B, Hq] base-2 log-sum-exp of the whole row
+  float *own_o;             // nullable [B, Hq, D]: the normalised result goes here, not to out
+  float *lse2;              // nullable [B, Hq] base-2 log-sum-exp of the own tokens
   float *lse_out;           // nullable [B, Hq] natural log-sum-exp
-  int slots;
+  float *scores;            // nullable [num_blocks, Hkv, 16, G] base-2 scores
   int dependent;            // launched behind the prefix kernel as its programmatic dependent
 };
 
@@ -299,49 +297,25 @@ __device__ __forceinline__ void merge_store(T *out_rows, int col, int D, const M
   store4<T>(out_rows + h * D + 4 * d4, o);
 }
 
-// EXT: adds the prefix partials of row b, head hq (of the whole row), float4
-// column d4 to a.
-__device__ __forceinline__ void ext_add_prefix(MergeAcc &a, const AttnParams &p, int b, int hq,
-                                               int d4, int D) {
-  if (!p.ext.row_part) return;
-  const int s0 = p.ext.row_part[2 * b], n = p.ext.row_part[2 * b + 1];
-  if (n <= 0) return;
-  if (s0 < 0 || n > p.ext.slots - s0) {   // never read outside the workspace
-    if (d4 == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
-    return;
-  }
-  constexpr int K = 4;
-  for (int i0 = 0; i0 < n; i0 += K) {
-    float l[K];
-    float4 v[K];
-#pragma unroll
-    for (int t = 0; t < K; ++t) {
-      const bool on = i0 + t < n;
-      const size_t at = static_cast<size_t>(s0 + (on ? i0 + t : 0)) * p.Hq + hq;
-      l[t] = on ? __ldcg(p.ext.pre_lse + at) : -INFINITY;
-      v[t] = on ? __ldcg(reinterpret_cast<const float4 *>(p.ext.pre_o + at * D) + d4)
-                : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    merge_acc_add<K>(a, l, v);
-  }
-}
-
-// EXT: joins the prefix partials into a and stores the column and the row sums.
+// EXT: stores a column of the own tokens' result (row b, head hq of the whole row)
+// and the row sums.
 template <typename T>
-__device__ __forceinline__ void ext_store(MergeAcc a, const AttnParams &p, int b, int hq, int d4,
-                                          int D) {
-  ext_add_prefix(a, p, b, hq, d4, D);
-  merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D,
-                 a);
+__device__ __forceinline__ void ext_store(const MergeAcc &a, const AttnParams &p, int b, int hq,
+                                          int d4, int D) {
+  const size_t at = static_cast<size_t>(b) * p.Hq + hq;
+  if (p.ext.own_o)
+    merge_store<float>(p.ext.own_o + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D, a);
+  else
+    merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D,
+                   a);
   if (d4 == 0) {
     const float l2 = a.den > 0.f ? a.M + log2f(a.den) : -INFINITY;
-    const size_t at = static_cast<size_t>(b) * p.Hq + hq;
     if (p.ext.lse2) p.ext.lse2[at] = l2;
     if (p.ext.lse_out) p.ext.lse_out[at] = l2 * 0.6931471805599453f;
   }
 }
 
-// EXT: a row without own tokens: the prefix alone, or zeros.
+// EXT: a row without own tokens.
 template <typename T>
 __device__ __forceinline__ void ext_empty_row(const AttnParams &p, int b, int D, int tid, int nthr) {
   for (int c = tid; c < p.Hq * (D / 4); c += nthr)
@@ -1008,7 +982,9 @@ __device__ __forceinline__ void simt_stash(SimtState<T, D, G> &s, float *red_acc
 // (p.plan != nullptr, !p.check_plan, p.bias == nullptr): the row-length scan,
 // the plan check and the bias are compiled out, and the smaller kernel runs
 // faster (its instructions come cold at both ends of every CTA).
-// EXT: joins prefix partials into the output and writes scores and row sums (AttnExt).
+// EXT: writes scores, row sums and float32 results (AttnExt).  It reads nothing of
+// the prefix kernel's, but what follows it reads both kernels': every CTA of a
+// dependent launch waits for that kernel before it ends.
 template <typename T, int D, int NW, int NS, int KIND, int G, bool FUSE, bool PLAN, bool EXT>
 __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     attn_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -1135,7 +1111,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       }
     }
     // rows with no token (or an invalid length) output zeros; part c clears
-    // rows c, c + C, ... (EXT: below, where only the consumers wait)
+    // rows c, c + C, ... (EXT: below)
     for (int b = EXT ? p.B : blockIdx.x; b < p.B; b += C) {   // (after the barrier above: lens_s is complete)
       bool bad;
       const int len = b < Q::kLensCache ? lens_s[b] : p.seq_lens[b];
@@ -1172,13 +1148,12 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     p.meta[2 * p.B * p.Hkv + 1] = static_cast<int32_t>(P >> 32);
   }
   // rows with no token: without the scan, the consumer warps clear them (off
-  // the producer's path); EXT: they get the prefix alone, once it is there
+  // the producer's path); EXT always does it here
   if ((EXT || !scanned) && warp < NW) {
     for (int b = blockIdx.x; b < p.B; b += C) {
       bool bad;
       if (pages_of_len(p.seq_lens[b], p.bt_stride, has_bias, p.bias_stride, &bad) == 0) {
         if constexpr (EXT) {
-          pdl_wait();
           ext_empty_row<T>(p, b, D, tid, NW * 32);
         } else {
           T *o = static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D;
@@ -1188,7 +1163,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       if (bad && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
     }
   }
-  if (start >= end) return;
+  if (start >= end) {
+    if constexpr (EXT) pdl_wait();
+    return;
+  }
   if (use_plan && rec_h.x >= p.B) {   // a record naming no row: never read outside seq_lens
     if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
     return;
@@ -1467,6 +1445,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     }
     if (__shfl_sync(0xffffffffu, misc[2], 0) != 0)
       drain_copies<NS, Q::kSegSlots>(full, segfull, stage_pg, slot_seg, lane);
+    if constexpr (EXT) pdl_wait();   // (this warp alone: the consumers go on)
     return;
   }
 
@@ -1594,7 +1573,6 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     // rescale factors are recomputed by every thread that needs them (a few
     // shared loads and NW ex2), which costs less than a separate pass and a
     // barrier
-    if (EXT && nseg == 1) pdl_wait();   // the prefix partials come from the kernel before this one
     for (int e4 = tid; e4 < gq * (D / 4); e4 += kConsumers) {
       const int h = e4 / (D / 4), d4 = e4 - h * (D / 4);
       float M = -INFINITY;
@@ -1704,7 +1682,6 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
   asm volatile("bar.sync 1, %0;" ::"r"(kConsumers) : "memory");
   const int ra = roles[0], Ha = roles[1], rb = roles[2], Hb = roles[3];
   if (ra < 0 && rb < 0) return;   // (the same for every consumer thread)
-  if constexpr (EXT) pdl_wait();
   float *scratch = red_acc;       // free: the segment combines are done
   auto rows_of = [&](int q) {
     return static_cast<T *>(p.out) +

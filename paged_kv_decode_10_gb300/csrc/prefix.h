@@ -24,10 +24,13 @@ struct PrefixParams {
 struct PrefixItem {
   int prefix, g, r0, rows, t0, t1, split;
 };
-__device__ __forceinline__ bool prefix_plan_ok(const PrefixParams &p) {
-  return p.plan[0] == kSharedMagic && p.plan[2] == p.B && p.plan[4] == p.C &&
-         p.plan[5] == p.Hkv && p.plan[6] == p.G && p.plan[1] >= 0 &&
-         p.plan[1] <= (p.plan_ints - plan_items_at(p.B, p.C)) / kPlanItem;
+// (The header in two 16-byte reads, without branches between them.)
+__device__ __forceinline__ bool prefix_plan_ok(const PrefixParams &p, int *n_items) {
+  const int4 *w = reinterpret_cast<const int4 *>(p.plan);
+  const int4 a = w[0], b = w[1];
+  *n_items = a.y;
+  return (a.x == kSharedMagic) & (a.z == p.B) & (b.x == p.C) & (b.y == p.Hkv) & (b.z == p.G) &
+         (a.y >= 0) & (a.y <= (p.plan_ints - plan_items_at(p.B, p.C)) / kPlanItem);
 }
 __device__ __forceinline__ bool prefix_item(const PrefixParams &p, int i, int max_rows,
                                             PrefixItem *it) {
@@ -35,20 +38,19 @@ __device__ __forceinline__ bool prefix_item(const PrefixParams &p, int i, int ma
                                                  static_cast<size_t>(i) * kPlanItem);
   const int4 a = w[0], b = w[1];
   *it = PrefixItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
-  return it->prefix >= 0 && it->prefix < p.n_prefixes && it->g >= 0 && it->g < p.Hkv &&
-         it->r0 >= 0 && it->rows > 0 && it->rows * p.G <= max_rows && it->r0 <= p.B - it->rows &&
-         it->t0 >= 0 && it->t0 % kBlockTokens == 0 && it->t0 < it->t1 && it->t1 <= 16ll * p.pt_stride && it->split >= 0;
+  return (it->prefix >= 0) & (it->prefix < p.n_prefixes) & (it->g >= 0) & (it->g < p.Hkv) &
+         (it->r0 >= 0) & (it->rows > 0) & (it->rows <= max_rows / p.G) &
+         (it->r0 <= p.B - it->rows) & (it->t0 >= 0) & (it->t0 % kBlockTokens == 0) &
+         (it->t0 < it->t1) & (it->t1 <= 16ll * p.pt_stride) & (it->split >= 0);
 }
 // Batch row i of an item and the slot its partial goes to (-1: does not fit).
 __device__ __forceinline__ int prefix_row(const PrefixParams &p, const PrefixItem &it, int i,
                                           int *slot) {
-  const int row = p.plan[plan_order_at(p.B) + it.r0 + i];
-  *slot = -1;
-  if (row < 0 || row >= p.B) return -1;
-  const int s0 = p.plan[plan_rows_at() + 2 * row], n = p.plan[plan_rows_at() + 2 * row + 1];
-  if (s0 < 0 || it.split >= n || s0 > p.slots - n) return -1;
-  *slot = s0 + it.split;
-  return row;
+  const int at = plan_order_at(p.B) + 2 * (it.r0 + i);   // (even: the pair is one 8-byte read)
+  const int2 w = *reinterpret_cast<const int2 *>(p.plan + at);
+  const bool ok = w.x >= 0 && w.x < p.B && w.y >= 0 && it.split < p.slots - w.y;
+  *slot = ok ? w.y + it.split : -1;
+  return ok ? w.x : -1;
 }
 
 cudaError_t launch_prefix_f32(const PrefixParams &p, int D, cudaStream_t s);

@@ -14,8 +14,11 @@
 //  * warp 8: TMA producer.  16-token pages of K and V land in 128-byte-swizzled
 //    slabs, eight pages to a tile; for K a slab is the K-major operand, for V the
 //    same bytes are the MN-major operand, so neither is transposed.
-//  * warp 9: issues the products (warps 10 and 11 only complete the warpgroup).  While one slot is in its softmax the tensor
-//    cores work for the other.
+//  * warps 9 and 10: issue the products of one slot each (warp 11 only completes the
+//    warpgroup).  While one slot is in its softmax the tensor cores work for the other.
+//    An issuer's waits and bookkeeping take about as long as its products, which
+//    is why there are two: one warp for both slots left the tensor cores idle for
+//    1400 of 3700 clocks a step.
 // Above 128 query rows the slots are the two row tiles and share every K and V
 // tile; up to 128 rows they take turns in the tokens and are merged at the end.
 //
@@ -36,6 +39,7 @@ constexpr int kSoftmax = 256, kThreads = 384;
 // scores and take 216, what the third warpgroup gives up (2 * 216 + 72 = 3 * 168)
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr float kLazy = 8.0f;
+constexpr int kHalf = 2;                      // 32-token pieces of P after which P V starts
 constexpr long long kDrainCycles = 1ll << 31;
 
 template <int D>
@@ -48,7 +52,7 @@ struct Lay {
   static constexpr int kK = 2 * kMat;                     // [NS]
   static constexpr int kV = kK + NS * kMat;               // [NS]
   static constexpr int kBars = kV + NS * kMat;
-  static constexpr int kNumBars = 4 * NS + 9;
+  static constexpr int kNumBars = 4 * NS + 13;
   static constexpr int kRows = kBars + kNumBars * 8;      // row, partial index of each query row
   static constexpr int kSums = kRows + 2 * kSoftmax * 4;  // m, l of the second slot
   static constexpr int kMisc = kSums + 2 * kTile * 4;
@@ -78,6 +82,20 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// One lane of the converged warp, picked by the hardware, and a value the compiler
+// may take as the same in every lane: the operands of the products then sit in
+// uniform registers (an ordinary lane test made each issue cost ~117 clocks).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+template <typename I>
+__device__ __forceinline__ I uniform(I x) {
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 // bar gets one arrival once every product issued so far by this thread is done
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -147,6 +165,33 @@ __device__ __forceinline__ void store8(float *p, const float *v) {   // one 32-b
                : "memory");
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // An mbarrier wait that gives up when another role has, or after the limit.
 struct Waiter {
   volatile int *abort;
@@ -184,27 +229,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *k_full = bars, *k_empty = bars + NS, *v_full = bars + 2 * NS, *v_empty = bars + 3 * NS;
   uint64_t *s_full = bars + 4 * NS, *p_ready = s_full + 2, *o_full = s_full + 4;   // [2] each
   uint64_t *q_full = s_full + 6, *both = s_full + 7, *drain = s_full + 8;
+  uint64_t *turn = s_full + 9, *p_half = s_full + 11;   // [2] each
   int *rows_s = reinterpret_cast<int *>(smem + L::kRows);   // [256] batch row, [256] slot
   float *sums_s = reinterpret_cast<float *>(smem + L::kSums);
   volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);   // abort, tmem, bad pages [2]
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   pdl_launch_dependents();
+  // the plan's header and this CTA's items (under way while the CTA is set up)
+  const int *ctas = p.plan + plan_ctas_at(p.B);
+  int n_planned, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
+  const bool plan_ok = prefix_plan_ok(p, &n_planned);
+  i0 = uniform(plan_ok ? max(0, i0) : 0);
+  i1 = uniform(plan_ok ? min(n_planned, i1) : 0);
+  if (!plan_ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);   // one arrival per slot
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
-      mbar_init(&p_ready[m], kTile);
+      mbar_init(&p_ready[m], kTile / 32);   // one arrival per warp
+      mbar_init(&p_half[m], kTile / 32);
       mbar_init(&o_full[m], 1);
     }
-    mbar_init(q_full, kSoftmax);
-    mbar_init(both, kSoftmax);
-    mbar_init(drain, 1);
+    mbar_init(q_full, kSoftmax / 32);
+    mbar_init(both, kSoftmax / 32);
+    mbar_init(drain, 2);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
     misc[0] = 0;
     misc[2] = misc[3] = 0;
     fence_barrier_init();
@@ -223,22 +279,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+  const uint32_t tmem = uniform(static_cast<uint32_t>(misc[1]));
+  // (by arithmetic: arrays indexed by the slot would live in local memory)
+  auto tS = [tmem](int m) { return tmem + 128u * m; };
+  auto tO = [tmem](int m) { return tmem + 256u + 128u * m; };
   const Waiter wait{misc, p.err, p.wait_limit};
-
-  const bool plan_ok = prefix_plan_ok(p);
-  if (!plan_ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
-  const int *ctas = p.plan + plan_ctas_at(p.B);
-  const int i0 = plan_ok ? max(0, ctas[blockIdx.x]) : 0;
-  const int i1 = plan_ok ? min(p.plan[1], ctas[blockIdx.x + 1]) : 0;
 
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == 8) {
     // ======================= producer =======================
     int x = 0;                     // tiles of the items before
-    int armed[2] = {0, 0};         // K and V tiles whose copies were started
+    int armed_k = 0, armed_v = 0;  // tiles whose copies were started
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
       PrefixItem it;
@@ -274,95 +326,134 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(dst + s * L::kSlab, kv ? &tmap_v : &tmap_k, s * 64, y, full);
           }
           __syncwarp();
-          armed[kv] = x + t + 1;
+          (kv ? armed_v : armed_k) = x + t + 1;
         }
       }
       x += tiles;
     }
     // every copy has landed before the CTA ends (after a normal run they have)
-    for (int kv = 0; kv < 2; ++kv)
-      for (int n = max(0, armed[kv] - NS); n < armed[kv]; ++n)
-        mbar_wait_bounded(kv ? &v_full[n % NS] : &k_full[n % NS],
-                          static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
-  } else if (warp == 9) {
-    // ======================= products =======================
+    for (int n = max(0, armed_k - NS); n < armed_k; ++n)
+      mbar_wait_bounded(&k_full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
+    for (int n = max(0, armed_v - NS); n < armed_v; ++n)
+      mbar_wait_bounded(&v_full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
+  } else if (warp <= 10) {
+    // ======================= products of slot m =======================
+    const int m = warp - 9;
     constexpr uint32_t kIdescS = inst_desc(kTile, false), kIdescO = inst_desc(D, true);
     const uint32_t q_addr = smem_u32(smem + L::kQ), k_addr = smem_u32(smem + L::kK),
                    v_addr = smem_u32(smem + L::kV);
     int x = 0, n_items = 0;
-    uint32_t p_ph[2] = {0, 0};
+    uint32_t p_ph = 0, turn_ph = 0;
     bool ok = true;
     for (int i = i0; i < i1 && ok; ++i) {
       PrefixItem it;
-      if (!prefix_item(p, i, kTileRowsBf16, &it)) continue;
+      if (!uniform(prefix_item(p, i, kTileRowsBf16, &it) ? 1 : 0)) continue;
+      it.t0 = uniform(it.t0);
+      it.t1 = uniform(it.t1);
+      it.rows = uniform(it.rows);
       const int tiles = (it.t1 - it.t0 + kTile - 1) / kTile;
       const bool two = it.rows * p.G > kTile;   // the slots are two row tiles
-      const int n_of[2] = {two ? tiles : (tiles + 1) / 2, two ? tiles : tiles / 2};
+      const int n = two ? tiles : (tiles + 1 - m) / 2;
       ok = wait.warp(q_full, static_cast<uint32_t>(n_items) & 1u);
       if (!ok) break;
       tc_fence_after();
-      const bool bad_pages = misc[2 + (n_items & 1)] != 0;
+      const bool bad_pages = uniform(misc[2 + (n_items & 1)] + 0) != 0;
       ++n_items;
-      auto scores = [&](int m, int j) {   // S_m = Q K^T for the slot's j-th tile
-        const int t = two ? j : 2 * j + m, st = (x + t) % NS;
-        if (!wait.warp(&k_full[st], static_cast<uint32_t>((x + t) / NS) & 1u)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks / 4) * L::kSlab + (ks % 4) * 32;
-            mma_ss(tS[m], smem_desc(q_addr + (two ? m * L::kMat : 0) + off, 16, 1024),
-                   smem_desc(k_addr + st * L::kMat + off, 16, 1024), kIdescS, ks > 0);
-          }
-          mma_commit(&s_full[m]);
-          if (!two || m == 1) mma_commit(&k_empty[st]);
-        }
-        __syncwarp();
-        return true;
+      const int turns = two ? tiles : (tiles + 1) / 2;   // slot 0's tiles, at least this slot's
+      auto tile_of = [&](int j) { return two ? j : 2 * j + m; };
+      // the slots' products alternate in whole batches: interleaved one by one, both
+      // slots would finish late and then share the exponential unit as well
+      auto my_turn = [&]() {
+        const bool r = wait.warp(&turn[m], turn_ph ^ (m == 0 ? 1u : 0u));
+        turn_ph ^= 1u;
+        return r;
       };
-      for (int m = 0; m < 2 && ok; ++m)
-        if (n_of[m] > 0) ok = scores(m, 0);
-      for (int j = 0; j < n_of[0] && ok; ++j) {
-        for (int m = 0; m < 2 && ok; ++m) {
-          if (j >= n_of[m]) continue;
-          const int t = two ? j : 2 * j + m, st = (x + t) % NS;
-          const int valid = min(kTile, it.t1 - it.t0 - t * kTile);
-          ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u);
-          if (!ok) break;
-          if ((valid % kBlockTokens || bad_pages) && (!two || m == 0)) {
-            // values of tokens that do not count may be anything: their weights are
-            // zero, and so must they be
-            const int32_t *table = p.tables + static_cast<size_t>(it.prefix) * p.pt_stride;
-            unsigned char *vt = smem + L::kV + st * L::kMat;
-            for (int pg = 0; pg * kBlockTokens < valid; ++pg) {
-              const int blk = table[(it.t0 + t * kTile) / kBlockTokens + pg];
-              const int first = blk < 0 || blk >= p.num_blocks
-                                    ? 0
-                                    : min(kBlockTokens, valid - pg * kBlockTokens);
-              for (int e = lane; e < (kBlockTokens - first) * 8 * L::kSlabs; e += 32) {
-                const int s = e / ((kBlockTokens - first) * 8), c = e % ((kBlockTokens - first) * 8);
-                *reinterpret_cast<uint4 *>(vt + s * L::kSlab + (pg * kBlockTokens + first) * 128 +
-                                           c * 16) = make_uint4(0u, 0u, 0u, 0u);
-              }
+      auto next_turn = [&]() { mbar_arrive(&turn[m ^ 1]); };   // (one lane)
+      auto wait_k = [&](int t) {
+        return wait.warp(&k_full[(x + t) % NS], static_cast<uint32_t>((x + t) / NS) & 1u);
+      };
+      // a tile that one slot alone uses is handed back by it for both
+      auto release = [&](uint64_t *empty) {
+        mma_commit(empty);
+        if (!two) mma_commit(empty);
+      };
+      // S = Q K^T for tile t (issued by one lane)
+      auto issue_scores = [&](int t) {
+        const int st = (x + t) % NS;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks / 4) * L::kSlab + (ks % 4) * 32;
+          mma_ss(tS(m), smem_desc(q_addr + (two ? m * L::kMat : 0) + off, 16, 1024),
+                 smem_desc(k_addr + st * L::kMat + off, 16, 1024), kIdescS, ks > 0);
+        }
+        mma_commit(&s_full[m]);
+        release(&k_empty[st]);
+      };
+      ok = (n == 0 || wait_k(tile_of(0))) && my_turn();
+      if (ok && elect_one()) {
+        if (n > 0) issue_scores(tile_of(0));
+        next_turn();
+      }
+      __syncwarp();
+      for (int j = 0; j < turns && ok; ++j) {
+        if (j >= n) {   // slot 1 has a tile less: its turn goes by
+          ok = my_turn();
+          if (ok && elect_one()) next_turn();
+          __syncwarp();
+          continue;
+        }
+        const int t = tile_of(j), st = (x + t) % NS;
+        const int valid = min(kTile, it.t1 - it.t0 - t * kTile);
+        const bool more = j + 1 < n;
+        // the tiles first (they are there well before the weights)
+        ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u) &&
+             (!more || wait_k(tile_of(j + 1)));
+        if (!ok) break;
+        if (valid % kBlockTokens || bad_pages) {
+          // values of tokens that do not count may be anything: their weights are
+          // zero, and so must they be (both slots of a shared tile write the zeros)
+          const int32_t *table = p.tables + static_cast<size_t>(it.prefix) * p.pt_stride;
+          unsigned char *vt = smem + L::kV + st * L::kMat;
+          for (int pg = 0; pg * kBlockTokens < valid; ++pg) {
+            const int blk = table[(it.t0 + t * kTile) / kBlockTokens + pg];
+            const int first =
+                blk < 0 || blk >= p.num_blocks ? 0 : min(kBlockTokens, valid - pg * kBlockTokens);
+            for (int e = lane; e < (kBlockTokens - first) * 8 * L::kSlabs; e += 32) {
+              const int s = e / ((kBlockTokens - first) * 8), c = e % ((kBlockTokens - first) * 8);
+              *reinterpret_cast<uint4 *>(vt + s * L::kSlab + (pg * kBlockTokens + first) * 128 +
+                                         c * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
           }
-          ok = wait.warp(&p_ready[m], p_ph[m]);
-          if (!ok) break;
-          p_ph[m] ^= 1u;
-          tc_fence_after();
-          if (lane == 0) {
-            for (int ks = 0; ks * kBlockTokens < valid; ++ks)   // O_m += P_m V, a page at a time
-              mma_ts(tO[m], tS[m] + ks * 8,
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        auto weighted = [&](int from, int to) {   // O += P V, a page at a time
+#pragma unroll
+          for (int ks = from; ks < to; ++ks)
+            if (ks * kBlockTokens < valid)
+              mma_ts(tO(m), tS(m) + ks * 8,
                      smem_desc(v_addr + st * L::kMat + ks * (kBlockTokens * 128), L::kSlab, 1024),
                      kIdescO, j > 0 || ks > 0);
-            if (!two || m == 1) mma_commit(&v_empty[st]);
-            if (j + 1 == n_of[m]) mma_commit(&o_full[m]);
-          }
-          __syncwarp();
-          if (j + 1 < n_of[m]) ok = scores(m, j + 1);
+        };
+        ok = wait.warp(&p_half[m], p_ph) && my_turn();
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) weighted(0, 2 * kHalf);
+        __syncwarp();
+        ok = wait.warp(&p_ready[m], p_ph);
+        if (!ok) break;
+        p_ph ^= 1u;
+        tc_fence_after();
+        if (elect_one()) {
+          weighted(2 * kHalf, kPages);
+          release(&v_empty[st]);
+          if (more)
+            issue_scores(tile_of(j + 1));
+          else
+            mma_commit(&o_full[m]);
+          next_turn();
         }
+        __syncwarp();
       }
       x += tiles;
     }
@@ -376,15 +467,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= softmax =======================
     const int m = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes
-    const uint32_t sS = tS[m] + lanes, sO = tO[m] + lanes;
+    const uint32_t sS = tS(m) + lanes, sO = tO(m) + lanes;
     // a negative scale is taken into Q, so that the largest score stays the largest
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     int n_items = 0;
     uint32_t s_ph = 0, o_ph = 0, b_ph = 0;
     bool ok = true;
+    auto arrive = [&](uint64_t *bar) {   // for the warp, after all of its lanes
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     auto meet = [&]() {   // both warpgroups
-      mbar_arrive(both);
+      arrive(both);
       ok = ok && wait.warp(both, b_ph);
       b_ph ^= 1u;
     };
@@ -425,24 +520,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       meet();
       if (!ok) break;
-      for (int e = tid; e < (two ? 2 : 1) * kTile * (D / 8); e += kSoftmax) {
-        const int row = e / (D / 8), ch = e % (D / 8);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rows_s[row] >= 0) {
-          v = *reinterpret_cast<const uint4 *>(
+      constexpr int kStep = kSoftmax / (D / 8);   // rows between a thread's pieces
+      const int ch = tid % (D / 8);
+      for (int r0 = tid / (D / 8); r0 < (two ? 2 : 1) * kTile; r0 += 16 * kStep) {
+        uint4 v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          // (rows that do not count read row 0: a branch here would make the loads
+          // wait for one another)
+          const int row = r0 + u * kStep, b = row < kSoftmax ? rows_s[row] : 0;
+          v[u] = *reinterpret_cast<const uint4 *>(
               static_cast<const __nv_bfloat16 *>(p.q) +
-              (static_cast<size_t>(rows_s[row]) * p.Hq + it.g * p.G + row % p.G) * D + ch * 8);
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
+              (static_cast<size_t>(max(b, 0)) * p.Hq + it.g * p.G + (row & (p.G - 1))) * D + ch * 8);
         }
-        *reinterpret_cast<uint4 *>(smem + L::kQ + (row / kTile) * L::kMat + (ch / 8) * L::kSlab +
-                                   (row % kTile) * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int row = r0 + u * kStep;
+          uint4 x = make_uint4(v[u].x ^ flip, v[u].y ^ flip, v[u].z ^ flip, v[u].w ^ flip);
+          if (row >= kSoftmax || rows_s[row] < 0) x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < (two ? 2 : 1) * kTile)
+            *reinterpret_cast<uint4 *>(smem + L::kQ + (row / kTile) * L::kMat +
+                                       (ch / 8) * L::kSlab + (row % kTile) * 128 +
+                                       (((ch & 7) ^ (row & 7)) << 4)) = x;
+        }
       }
       fence_proxy_async_smem();
       tc_fence_before();   // the reads of the item before's O
-      mbar_arrive(q_full);
+      arrive(q_full);
       const bool bad_pages = *bad != 0;
       const bool active = (two ? m * kTile : 0) + (warp & 3) * 32 < total;
       float mx = -INFINITY, l = 0.f;
@@ -475,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int q = 4; q < kTile; ++q) t4[q & 3] = fmaxf(t4[q & 3], s[q]);
+          for (int q = 4; q + 1 < kTile; q += 2)
+            t4[(q >> 1) & 3] = max3(t4[(q >> 1) & 3], s[q], s[q + 1]);
           const float top = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c);
           if (__any_sync(0xffffffffu, top > mx + kLazy)) {
             const float al = top == -INFINITY ? 1.f : ex2(mx - top);   // 0 before the first score
@@ -495,24 +600,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float mu = mx == -INFINITY ? 0.f : mx;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair(c, c), mu2 = pair(-mu, -mu);
+          uint64_t l2[2] = {0, 0};   // (two zeros)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(s[32 * q + 2 * e], c, -mu));
-              const float b = ex2(fmaf(s[32 * q + 2 * e + 1], c, -mu));
-              l4[e & 3] += a + b;
+              const float2 x =
+                  unpair(fma2(pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mu2));
+              const float a = ex2(x.x), b = ex2(x.y);
+              l2[e & 1] = add2(l2[e & 1], pair(a, b));
               w[e] = pack_bf16(a, b);
             }
             tm_st16(sS + 16 * q, w);
+            if (q == kHalf - 1) {   // the product may start on these
+              tm_wait_st();
+              tc_fence_before();
+              arrive(&p_half[m]);
+            }
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          const float2 ls = unpair(add2(l2[0], l2[1]));
+          l += ls.x + ls.y;
           tm_wait_st();
+        } else {
+          arrive(&p_half[m]);
         }
         tc_fence_before();
-        mbar_arrive(&p_ready[m]);
+        arrive(&p_ready[m]);
       }
       if (ok && n > 0) {
         ok = wait.warp(&o_full[m], o_ph);

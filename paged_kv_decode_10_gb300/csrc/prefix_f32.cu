@@ -23,12 +23,13 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_simt_kernel(const PrefixPa
   int *ok_s = slots + M;   // [kTok]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  if (!prefix_plan_ok(p)) {
+  int n_items;
+  if (!prefix_plan_ok(p, &n_items)) {
     if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
     return;
   }
   const int *ctas = p.plan + plan_ctas_at(p.B);
-  const int i0 = max(0, ctas[blockIdx.x]), i1 = min(p.plan[1], ctas[blockIdx.x + 1]);
+  const int i0 = max(0, ctas[blockIdx.x]), i1 = min(n_items, ctas[blockIdx.x + 1]);
   for (int i = i0; i < i1; ++i) {
     PrefixItem it;
     if (!prefix_item(p, i, max_rows, &it)) {

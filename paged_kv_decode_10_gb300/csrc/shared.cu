@@ -3,8 +3,15 @@
 //
 // Launches: the prefix kernel (partials of every row over its prefix), the EXT
 // build of the split-KV kernel over the rows' own tokens (a programmatic
-// dependent of the prefix kernel: it streams pages while that one runs and waits
-// for it before joining the partials) and, with mass, the fold of the scores.
+// dependent of the prefix kernel that reads nothing of it, so it fills whatever
+// SMs that one leaves), the merge of the two and, with mass, the fold of the
+// scores.  Without prefixes only the second and the last.
+//
+// The merge is a kernel of its own because joining the partials in the split-KV
+// kernel's epilogue made its consumers wait, first for the prefix kernel and then
+// for chains of partial reads, while no page was streamed: that took 31 us of the
+// 122 us which the kernel needed for 64 rows of 1..4096 tokens (32/8 heads of 128)
+// behind an 8192-token prefix.
 #include <cuda.h>
 
 #include "attention_host.h"
@@ -17,16 +24,87 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct SharedSpace {
-  size_t lse2, pre_lse, pre_o, bytes;   // offsets behind the attention workspace
+  size_t lse2, own_lse, own_o, pre_lse, pre_o, bytes;   // offsets behind the attention workspace
 };
 
 SharedSpace shared_space(size_t attn_bytes, int B, int Hq, int d, int slots) {
   SharedSpace s;
   s.lse2 = align256(attn_bytes);
-  s.pre_lse = s.lse2 + align256(static_cast<size_t>(B) * Hq * sizeof(float));
+  s.own_lse = s.lse2 + align256(static_cast<size_t>(B) * Hq * sizeof(float));
+  s.own_o = s.own_lse + align256(static_cast<size_t>(B) * Hq * sizeof(float));
+  s.pre_lse = s.own_o + (slots > 0 ? align256(static_cast<size_t>(B) * Hq * d * sizeof(float)) : 0);
   s.pre_o = s.pre_lse + align256(static_cast<size_t>(slots) * Hq * sizeof(float));
   s.bytes = s.pre_o + align256(static_cast<size_t>(slots) * Hq * d * sizeof(float));
   return s;
+}
+
+// ---- prefix partials and own tokens joined -------------------------------------
+// out = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M) over the own tokens' partial
+// and the row's n prefix partials (merge_acc_add).  D / 4 lanes own one (row, head),
+// a float4 column each; the reads of four partials go out together.  Bound by L2:
+// the partials were just written.
+struct JoinParams {
+  const int32_t *row_part;
+  const float *own_o, *own_lse, *pre_o, *pre_lse;
+  void *out;
+  float *lse2, *lse_out;
+  int32_t *err;
+  int rows, Hq, slots;   // rows: B * Hq
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+  pdl_launch_dependents();
+  constexpr int LPR = D / 4, K = 4;
+  const int u = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, d4 = threadIdx.x % LPR;
+  if (u >= p.rows) {
+    pdl_wait();
+    return;
+  }
+  const int b = u / p.Hq, h = u - b * p.Hq;
+  const int2 part = *reinterpret_cast<const int2 *>(p.row_part + 2 * b);
+  int n = part.y;
+  if (n < 0 || part.x < 0 || n > p.slots - part.x) {   // never read outside the workspace
+    if (n != 0 && d4 == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+    n = 0;
+  }
+  pdl_wait();   // the partials come from the kernels before this one
+  MergeAcc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  float l1[1] = {__ldcg(p.own_lse + u)};
+  float4 v1[1] = {__ldcg(reinterpret_cast<const float4 *>(p.own_o + static_cast<size_t>(u) * D) + d4)};
+  for (int i0 = 0; i0 < n; i0 += K) {
+    float l[K];
+    float4 v[K];
+#pragma unroll
+    for (int t = 0; t < K; ++t) {
+      const bool on = i0 + t < n;
+      const size_t at = static_cast<size_t>(part.x + (on ? i0 + t : 0)) * p.Hq + h;
+      l[t] = on ? __ldcg(p.pre_lse + at) : -INFINITY;
+      v[t] = __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D) + d4);
+    }
+    merge_acc_add<K>(a, l, v);
+  }
+  merge_acc_add<1>(a, l1, v1);
+  merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(u) * D, d4, D, a);
+  if (d4 == 0) {
+    const float l2 = a.den > 0.f ? a.M + log2f(a.den) : -INFINITY;
+    if (p.lse2) p.lse2[u] = l2;
+    if (p.lse_out) p.lse_out[u] = l2 * 0.6931471805599453f;
+  }
+}
+
+template <typename K, typename P>
+cudaError_t launch_dependent(K kern, unsigned grid, const P &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // ---- the weights of the own tokens --------------------------------------------
@@ -85,20 +163,6 @@ __global__ void __launch_bounds__(256) mass_kernel(const MassParams p) {
   }
 }
 
-template <int G>
-cudaError_t launch_mass(const MassParams &p, unsigned grid, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mass_kernel<G>, p);
-}
-
 }  // namespace
 }  // namespace pkv
 
@@ -150,7 +214,8 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     rc = default_parts(a->d, a->dtype, 0, G, &num_parts);
     if (rc != PKV_OK) return rc;
   }
-  const bool prefixes = a->prefix_tables != nullptr && a->n_prefixes > 0;
+  // (a plan without partials -- no row has a prefix -- leaves the own tokens alone)
+  const bool prefixes = a->prefix_tables != nullptr && a->n_prefixes > 0 && a->slots > 0;
   int C = a->num_ctas;
   if (prefixes) {
     if (C <= 0) {
@@ -165,8 +230,8 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     PKV_REQUIRE(a->plan_ints >= plan_items_at(a->B, C), PKV_ERR_INVALID_ARG,
                 "plan of %d ints < %d: not made for B = %d, num_ctas = %d", a->plan_ints,
                 plan_items_at(a->B, C), a->B, C);
-    PKV_REQUIRE(a->slots >= 0, PKV_ERR_INVALID_ARG, "slots < 0");
   }
+  PKV_REQUIRE(a->slots >= 0, PKV_ERR_INVALID_ARG, "slots < 0");
   const int slots = prefixes ? a->slots : 0;
   size_t attn = 0;
   rc = pkv_attn_workspace_bytes(a->B, a->Hq, a->Hkv, a->d, num_parts, &attn);
@@ -219,18 +284,42 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
       e = launch_prefix_f32(p, a->d, s);
     }
     PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "prefix kernel launch: %s", cudaGetErrorString(e));
-    ext.row_part = a->prefix_plan + plan_rows_at();
-    ext.pre_o = p.o;
-    ext.pre_lse = p.lse;
-    ext.slots = slots;
+    ext.own_o = reinterpret_cast<float *>(ws + sp.own_o);
+    ext.lse2 = reinterpret_cast<float *>(ws + sp.own_lse);
+    ext.lse_out = nullptr;
     ext.dependent = 1;
   }
   rc = attn_launch_ext(*a, num_parts, ext, stream);
   if (rc != PKV_OK) return rc;
+  float *lse2 = reinterpret_cast<float *>(ws + sp.lse2);
+  if (ext.own_o) {
+    JoinParams j;
+    j.row_part = a->prefix_plan + plan_rows_at();
+    j.own_o = ext.own_o;
+    j.own_lse = ext.lse2;
+    j.pre_o = reinterpret_cast<const float *>(ws + sp.pre_o);
+    j.pre_lse = reinterpret_cast<const float *>(ws + sp.pre_lse);
+    j.out = a->out;
+    j.lse2 = a->mass ? lse2 : nullptr;
+    j.lse_out = a->lse_out;
+    j.err = a->dev_err_flag;
+    j.rows = a->B * a->Hq;
+    j.Hq = a->Hq;
+    j.slots = slots;
+    const int per_cta = 256 / (a->d / 4);
+    const unsigned grid = static_cast<unsigned>((j.rows + per_cta - 1) / per_cta);
+    const cudaError_t e =
+        a->dtype == PKV_BF16
+            ? (a->d == 64 ? launch_dependent(join_kernel<__nv_bfloat16, 64>, grid, j, s)
+                          : launch_dependent(join_kernel<__nv_bfloat16, 128>, grid, j, s))
+            : (a->d == 64 ? launch_dependent(join_kernel<float, 64>, grid, j, s)
+                          : launch_dependent(join_kernel<float, 128>, grid, j, s));
+    PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
+  }
   if (a->mass) {
     MassParams m;
     m.scores = a->scores;
-    m.lse2 = ext.lse2;
+    m.lse2 = lse2;
     m.mass = a->mass;
     m.block_tables = a->block_tables;
     m.seq_lens = a->seq_lens;
@@ -247,10 +336,10 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     const int most = a->B >= 64 ? 64 : 4096 / a->B;
     m.chunks = chunks < most ? chunks : most;
     const unsigned grid = static_cast<unsigned>(a->B) * m.chunks;
-    cudaError_t e = G == 1   ? launch_mass<1>(m, grid, s)
-                    : G == 2 ? launch_mass<2>(m, grid, s)
-                    : G == 4 ? launch_mass<4>(m, grid, s)
-                             : launch_mass<8>(m, grid, s);
+    const cudaError_t e = G == 1   ? launch_dependent(mass_kernel<1>, grid, m, s)
+                          : G == 2 ? launch_dependent(mass_kernel<2>, grid, m, s)
+                          : G == 4 ? launch_dependent(mass_kernel<4>, grid, m, s)
+                                   : launch_dependent(mass_kernel<8>, grid, m, s);
     PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "mass kernel launch: %s", cudaGetErrorString(e));
   }
   return PKV_OK;

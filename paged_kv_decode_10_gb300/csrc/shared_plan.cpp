@@ -234,8 +234,11 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
       load.push({l.first + items[i].cost, l.second});
     }
     int32_t *order_out = plan + pkv::plan_order_at(B);
-    for (int32_t i = 0; i < B; ++i)
-      order_out[i] = i < static_cast<int32_t>(order.size()) ? order[i] : -1;
+    for (int32_t i = 0; i < B; ++i) {
+      const int32_t b = i < static_cast<int32_t>(order.size()) ? order[i] : -1;
+      order_out[2 * i] = b;
+      order_out[2 * i + 1] = b < 0 ? 0 : rows_out[2 * b];
+    }
     int32_t *ctas = plan + pkv::plan_ctas_at(B);
     int32_t *out = plan + items_at;
     int32_t at = 0;

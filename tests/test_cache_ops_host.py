@@ -54,9 +54,9 @@ def test_rotary_refuses_head_sizes(bind, d):
 def read_plan(plan):
     magic, n, B, slots, C, Hkv, G, R = plan[:8]
     rows = plan[16:16 + 2 * B].reshape(B, 2)
-    order = plan[16 + 2 * B:16 + 3 * B]
-    ctas = plan[16 + 3 * B:16 + 3 * B + C + 1]
-    at = (16 + 3 * B + C + 1 + 3) // 4 * 4
+    order = plan[16 + 2 * B:16 + 4 * B].reshape(B, 2)
+    ctas = plan[16 + 4 * B:16 + 4 * B + C + 1]
+    at = (16 + 4 * B + C + 1 + 3) // 4 * 4
     items = plan[at:].reshape(-1, 8)
     assert len(items) == n and ctas[0] == 0 and ctas[-1] == n and (np.diff(ctas) >= 0).all()
     return rows, order, ctas, items, slots, R
@@ -81,8 +81,8 @@ def test_shared_plan_covers_every_token_once(bind, dtype, B, Hq, Hkv, lens, seed
     seen = {}
     for p, g, r0, n, t0, t1, split, _ in items:
         assert 0 < n <= R and 0 <= t0 < t1 <= lens[p] and 0 <= g < Hkv
-        for b in order[r0:r0 + n]:
-            assert prefix[b] == p and 0 <= split < rows[b, 1]
+        for b, first in order[r0:r0 + n]:
+            assert prefix[b] == p and 0 <= split < rows[b, 1] and first == rows[b, 0]
             slot = (rows[b, 0] + split, g)
             assert slot not in taken and slot[0] < slots
             taken.add(slot)
