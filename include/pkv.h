@@ -583,8 +583,12 @@ int pkv_decode_attn_shared(const pkv_shared_args *args, void *stream);
  * PKV_DEVERR_BAD_BLOCK; such a row is left alone, its kept entries are -1.  A
  * block may appear once among the rows' tables.  The host then shortens the
  * sequences with pkv_seqs_evict.
- * d * sizeof(dtype) a multiple of 16; caches 16-byte aligned; B <= 65536.
+ * d * sizeof(dtype) a multiple of 16, at most 1024; caches and mass 16-byte
+ * aligned; B <= 65536.  Workspace: pkv_evict_workspace_bytes(...) bytes, 256-byte
+ * aligned, any contents; calls that share it must not overlap.
  */
+int pkv_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t d, int32_t dtype,
+                              int32_t kept_stride, size_t *bytes);
 typedef struct pkv_evict_args {
   void *k_cache, *v_cache;           /* [num_blocks,Hkv,16,d] */
   float *mass;                       /* [num_blocks,Hkv,16] */
@@ -592,6 +596,8 @@ typedef struct pkv_evict_args {
   const int32_t *seq_lens;           /* [B] */
   const int32_t *keep_lens;          /* [B] */
   int32_t *kept;                     /* [B,Hkv,kept_stride] */
+  void *workspace;
+  size_t workspace_bytes;
   int32_t *dev_err_flag;             /* nullable */
   int32_t num_blocks, bt_stride, kept_stride, sink, recent;
   int32_t B, Hkv, d, dtype;

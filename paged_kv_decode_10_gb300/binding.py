@@ -130,7 +130,7 @@ class EvictArgs(ctypes.Structure):
     _fields_ = [
         ("k_cache", _vp), ("v_cache", _vp), ("mass", _vp),
         ("block_tables", _vp), ("seq_lens", _vp), ("keep_lens", _vp), ("kept", _vp),
-        ("dev_err_flag", _vp),
+        ("workspace", _vp), ("workspace_bytes", _size_t), ("dev_err_flag", _vp),
         ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("kept_stride", _c_i32),
         ("sink", _c_i32), ("recent", _c_i32),
         ("B", _c_i32), ("Hkv", _c_i32), ("d", _c_i32), ("dtype", _c_i32),
@@ -223,6 +223,8 @@ SIGNATURES = {
     "pkv_shared_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                   ctypes.POINTER(_size_t)]),
     "pkv_decode_attn_shared": (ctypes.c_int, [ctypes.POINTER(SharedArgs), _vp]),
+    "pkv_evict_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                                 ctypes.POINTER(_size_t)]),
     "pkv_evict": (ctypes.c_int, [ctypes.POINTER(EvictArgs), _vp]),
 }
 
@@ -1034,10 +1036,18 @@ def decode_attention_shared(q_rot, k_cache, v_cache, block_tables, seq_lens, sca
     return out
 
 
+def evict_workspace_bytes(B, Hkv, d, dtype, max_keep):
+    n = _size_t()
+    _check(load().pkv_evict_workspace_bytes(int(B), int(Hkv), int(d), int(dtype), int(max_keep),
+                                            ctypes.byref(n)))
+    return n.value
+
+
 def make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, sink=0,
-                    recent=0, err=None):
+                    recent=0, workspace=None, err=None):
     """``pkv_evict_args``: ``kept [B,Hkv,>=kept tokens]`` int32 receives the kept
-    tokens' indices."""
+    tokens' indices; ``workspace`` (uint8, ``evict_workspace_bytes``) is made here
+    unless given."""
     torch = _torch()
     if k_cache.dim() != 4 or not k_cache.is_cuda:
         raise PkvError(ERR_INVALID_ARG, "caches must be [blocks,Hkv,16,d] on a CUDA device")
@@ -1057,7 +1067,12 @@ def make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, k
     a.num_blocks, a.bt_stride, a.kept_stride = nb, block_tables.shape[1], kept.shape[2]
     a.sink, a.recent = int(sink), int(recent)
     a.B, a.Hkv, a.d = B, Hkv, d
-    a.keep = (k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, err)
+    if workspace is None:
+        workspace = torch.empty(evict_workspace_bytes(B, Hkv, d, a.dtype, kept.shape[2]),
+                                dtype=torch.uint8, device=dev)
+    a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)
+    a.workspace_bytes = workspace.numel()
+    a.keep = (k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, workspace, err)
     a.device = dev
     return a
 
@@ -1075,7 +1090,7 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, max_keep, s
         kept = _torch().empty((block_tables.shape[0], k_cache.shape[1], max(int(max_keep), 1)),
                               dtype=_torch().int32, device=k_cache.device)
     evict_args(make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, sink,
-                               recent, err), stream)
+                               recent, err=err), stream)
     return kept
 
 

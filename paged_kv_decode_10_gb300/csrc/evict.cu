@@ -7,13 +7,25 @@
 // the top): after each digit only the keys that share the threshold's digits so
 // far still count.  Tokens above the threshold are kept, and of those equal to
 // it the first few by index, so the choice does not depend on any order of
-// execution.  One scan in token order then writes the kept indices ascending.
+// execution.  One scan in token order then writes the kept indices ascending.  A
+// row's keys are read once and stay on chip; rows too long for one CTA, and
+// rows too few to fill the GPU, are shared by clusters whose histograms are added
+// through distributed shared memory.  Bound by latency: three passes of a handful
+// of barriers each.
 //
-// Compaction.  The i-th kept token comes from index >= i, so when a CTA walks
-// its kept tokens in order, a chunk's stores can only reach slots that this or
-// an earlier chunk has already read: load a chunk into registers, barrier,
-// store it.  CTAs share nothing: each owns one (row, KV head), one of K and V,
-// and a column slice of the rows.
+// Compaction.  The i-th kept token comes from index >= i.
+//  * Many rows: a CTA walks the kept tokens of one (row, KV head), K or V, in
+//    order.  A step's stores can only reach slots that this or an earlier step has
+//    read: read a step into registers, barrier, store it.
+//  * Few rows: chunks of T kept tokens go to CTAs of their own.  A chunk may be
+//    stored once every token that still lies in its T slots has been read; at most
+//    T kept tokens come from there, consecutive ones, so they belong to at most two
+//    chunks, earlier ones or itself: a chunk waits for two flags.  Chunks are taken
+//    by ticket in order and reading never waits, so every wait ends.
+// Both are memory bound: each kept row is read and written once.  The walk needs
+// no flags and keeps its steps back to back (64 rows of 8 heads: 89 us against
+// 150 us in chunks); with 4 (row, head) pairs it leaves the GPU empty (130 us
+// against 45 us in chunks).
 #include <cstdint>
 
 #include "common.cuh"
@@ -21,191 +33,378 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kBins = 2048;
-constexpr int kScanPer = 8;          // tokens a thread takes in a step of the final scan
+constexpr int kSelThreads = 256;
+constexpr int kBins = 2048, kBinsPer = kBins / kSelThreads;
+constexpr int kWarps = kSelThreads / 32;
+constexpr int kTileTokens = 4 * kSelThreads;       // a thread holds 4 consecutive tokens of a tile
+constexpr int kMaxCluster = 16, kMaxCached = 48;   // CTAs, steps (of 4 KB of keys)
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 8;        // 16-byte pieces a thread has in flight
+constexpr int kMoveVecs = 4;                       // 16-byte pieces of K (and of V) a thread moves
+constexpr int kChunkBytes = kMoveThreads * kMoveVecs * 16;
+constexpr int kWalkVecs = 8;                       // pieces a walking thread has in flight
+constexpr long long kWaitCycles = 1ll << 31;
 
 struct EvictParams {
   unsigned char *k_cache, *v_cache;
   float *mass;
   const int32_t *block_tables, *seq_lens, *keep_lens;
   int32_t *kept, *err;
+  int32_t *ticket, *flags;           // workspace: [1], [B * Hkv][chunks]
   int num_blocks, bt_stride, kept_stride, sink, recent;
   int B, Hkv, row_bytes;
-  int cached;                        // keys the select kernel keeps in shared memory
-  int slices, slice_bytes;           // column slices of a K (or V) row
+  int chunk, chunks;                 // tokens of a chunk, chunks of kept_stride tokens
+  int cached;                        // steps whose keys the select kernel keeps
 };
 
-// Larger key <=> larger weight; -0 and +0 are equal, every NaN is the largest.
+// Larger key <=> larger weight; -0 and +0 are equal, every NaN is the largest.  No
+// weight has key 0 (the lowest, -inf's, is 0x007fffff): that marks other tokens.
 __device__ __forceinline__ uint32_t mass_key(float x) {
   if (x != x) return 0xffffffffu;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Words of CTA `rank`'s shared memory.
+__device__ __forceinline__ uint32_t remote_addr(const void *local, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t remote_u32(const void *local, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(local, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 remote_u128(const void *local, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(remote_addr(local, rank))
+               : "memory");
+  return v;
+}
+
 // Sum over the threads before this one of v, and the total (kSelThreads threads).
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
-                                                         unsigned long long *warp_sums,
-                                                         unsigned long long *total) {
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   __syncthreads();   // warp_sums may still be read from the call before
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  unsigned long long before = 0, all = 0;
+  uint32_t w = lane < kSelThreads / 32 ? warp_sums[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const unsigned long long s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int o = 1; o < kSelThreads / 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  *total = all;
-  return before + incl - v;
+  *total = __shfl_sync(0xffffffffu, w, kSelThreads / 32 - 1);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + incl - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys_s[];   // [cached]
-  __shared__ uint32_t hist[kBins];
-  __shared__ unsigned long long warp_sums[kSelThreads / 32];
-  __shared__ int bad, digit_s, left_s;
-  const int tid = threadIdx.x;
-  const int b = blockIdx.x / p.Hkv, g = blockIdx.x - b * p.Hkv;
+// One (row, KV head) per cluster.  CTA r of the cluster has `per` tiles' worth of
+// consecutive tokens, of which each warp has a consecutive share, 128 tokens (four a
+// lane) at a time: warp, step, lane, place is token order, so the final scan needs
+// one exchange between the warps.  The keys are kept in shared memory and the loops
+// over them stay rolled: with the keys in registers the code was unrolled 16 times
+// and run once a pass, and fetching it took 40 us instead of 12 for 131072 tokens.
+// Steps beyond p.cached read the weights again in every pass.
+// kRead: steps read at once (few: more CTAs fit an SM; many: fewer rounds of reads).
+template <int kRead>
+__global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
+    evict_select_kernel(const EvictParams p) {
+  extern __shared__ uint4 keys_s[];   // [cached][kSelThreads]
+  // bin i counts digit kBins - 1 - i: ascending order of bins is descending order
+  // of keys.  Two histograms: one is cleared while the other is in use.
+  __shared__ __align__(16) uint32_t hist[2][kBins];
+  __shared__ uint32_t warp_sums[kWarps];
+  __shared__ uint32_t counts[kWarps][2], totals[2];
+  __shared__ uint32_t bad, segment;
+  __shared__ __align__(8) uint32_t found[2]; 
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank(), nc = cluster_size();
+  pdl_launch_dependents();
+  const int u = blockIdx.x / nc;
+  const int b = u / p.Hkv, g = u - b * p.Hkv;
   const int L = p.seq_lens[b], K = p.keep_lens[b];
-  int32_t *kept = p.kept + static_cast<size_t>(blockIdx.x) * p.kept_stride;
+  int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
   const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
   const bool bad_len = L < 0 || K < 0 || static_cast<long long>(L) > 16ll * p.bt_stride ||
                        min(L, K) > p.kept_stride;
+  const int step = static_cast<int>(nc) * kSelThreads, me = static_cast<int>(rank) * kSelThreads + tid;
+  // the compaction's flags and ticket
+  for (int j = me; j < p.chunks; j += step) p.flags[static_cast<size_t>(u) * p.chunks + j] = 0;
+  if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
+  for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
   if (tid == 0) bad = 0;
   __syncthreads();
-  if (bad_len) {
-    if (tid == 0 && g == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
-  } else {
-    for (int j = tid; j < (L + 15) / 16; j += kSelThreads) {
-      const int blk = table[j];
-      if (blk < 0 || blk >= p.num_blocks) bad = 1;
+  const int n_recent = min(p.recent, max(K, 0)), n_sink = min(p.sink, max(K, 0) - n_recent);
+  const int c0 = n_sink, c1 = L - n_recent;   // candidates [c0, c1)
+  const int m = K - n_recent - n_sink;        // of which m stay
+  const int len = bad_len ? 0 : L;
+  const int tiles = (len + kTileTokens - 1) / kTileTokens;
+  const int per = (tiles + static_cast<int>(nc) - 1) / static_cast<int>(nc);   // steps of a warp
+  // this lane's tokens of step i: t_of(i) .. t_of(i) + 3
+  auto t_of = [&](int i) {
+    return ((static_cast<int>(rank) * kWarps + warp) * per + i) * 128 + 4 * lane;
+  };
+  auto page_ok = [&](int blk) { return blk >= 0 && blk < p.num_blocks; };
+  auto weights = [&](int blk, int t) {
+    return __ldcg(reinterpret_cast<const float4 *>(
+        p.mass + (static_cast<size_t>(blk) * p.Hkv + g) * kBlockTokens + (t & 15)));
+  };
+  auto keys4 = [&](const float4 &x, int t) {   // 0: not a candidate
+    return make_uint4(t >= c0 && t < c1 ? mass_key(x.x) : 0u,
+                      t + 1 >= c0 && t + 1 < c1 ? mass_key(x.y) : 0u,
+                      t + 2 >= c0 && t + 2 < c1 ? mass_key(x.z) : 0u,
+                      t + 3 >= c0 && t + 3 < c1 ? mass_key(x.w) : 0u);
+  };
+  const int cached = min(per, p.cached);
+  bool wrong = false;
+  // the table, then the weights: two rounds of reads for every kRead steps
+#pragma unroll 1
+  for (int i0 = 0; i0 < per; i0 += kRead) {
+    int blk[kRead];
+#pragma unroll
+    for (int i = 0; i < kRead; ++i) {
+      const int t = t_of(i0 + i);
+      const bool mine = i0 + i < per && t < len;
+      blk[i] = mine ? table[t >> 4] : -1;
+      wrong |= mine && !page_ok(blk[i]);
     }
-    __syncthreads();
-    if (bad && tid == 0 && g == 0) set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
+    float4 x[kRead];
+#pragma unroll
+    for (int i = 0; i < kRead; ++i)
+      if (i0 + i < cached && page_ok(blk[i])) x[i] = weights(blk[i], t_of(i0 + i));
+#pragma unroll
+    for (int i = 0; i < kRead; ++i)
+      if (i0 + i < cached)
+        keys_s[(i0 + i) * kSelThreads + tid] =
+            page_ok(blk[i]) ? keys4(x[i], t_of(i0 + i)) : make_uint4(0u, 0u, 0u, 0u);
   }
-  const bool skip = bad_len || bad;
+  if (wrong) bad = 1;
+  bool skip = bad_len;   // (the same in every CTA of the cluster)
+  if (nc > 1) {
+    cluster_sync();
+    // (a lane a CTA: the remote reads are under way together)
+    skip |= __any_sync(0xffffffffu, static_cast<uint32_t>(lane) < nc && remote_u32(&bad, lane) != 0);
+  } else {
+    __syncthreads();
+    skip |= bad != 0;
+  }
+  if (skip && tid == 0 && g == 0 && rank == 0)
+    set_dev_err(p.err, bad_len ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_BLOCK);
   const int n = skip ? 0 : min(L, K);
-  for (int j = n + tid; j < p.kept_stride; j += kSelThreads) kept[j] = -1;
-  if (skip) return;
-  if (L <= K) {
-    for (int j = tid; j < L; j += kSelThreads) kept[j] = j;
+  for (int j = n + me; j < p.kept_stride; j += step) kept[j] = -1;
+  if (!skip && L <= K)
+    for (int j = me; j < L; j += step) kept[j] = j;
+  if (!skip && L > K) {
+    for (int j = me; j < n_sink; j += step) kept[j] = j;
+    for (int j = me; j < n_recent; j += step) kept[K - n_recent + j] = c1 + j;
+  }
+  if (skip || K >= L || m <= 0) {
+    if (nc > 1) cluster_sync();   // a CTA's shared memory outlives its readers
     return;
   }
-  const int n_recent = min(p.recent, K), n_sink = min(p.sink, K - n_recent);
-  const int c0 = n_sink, count = L - n_recent - n_sink;   // candidates [c0, c0 + count)
-  const int m = K - n_recent - n_sink;                    // of which m stay, m < count
-  for (int j = tid; j < n_sink; j += kSelThreads) kept[j] = j;
-  for (int j = tid; j < n_recent; j += kSelThreads) kept[K - n_recent + j] = L - n_recent + j;
-  if (m == 0) return;
-  auto read_key = [&](int i) {
-    const int t = c0 + i;
-    return mass_key(
-        p.mass[(static_cast<size_t>(table[t >> 4]) * p.Hkv + g) * kBlockTokens + (t & 15)]);
+
+  auto each_step = [&](auto &&f) {   // f(first token, keys), whole warps
+#pragma unroll 2
+    for (int i = 0; i < cached; ++i) f(t_of(i), keys_s[i * kSelThreads + tid]);
+#pragma unroll 1
+    for (int i = cached; i < per; ++i) {
+      const int t = t_of(i);
+      f(t, t < len ? keys4(weights(table[t >> 4], t), t) : make_uint4(0u, 0u, 0u, 0u));
+    }
   };
-  const int cached = min(count, p.cached);
-  for (int i = tid; i < cached; i += kSelThreads) keys_s[i] = read_key(i);
-  auto key_of = [&](int i) { return i < cached ? keys_s[i] : read_key(i); };
   // ---- the threshold: the m-th largest key ----
   uint32_t prefix = 0, mask = 0;   // the threshold's bits so far
-  int left = m;                    // its rank among the keys with that prefix
+  uint32_t left = m;               // its rank among the keys with that prefix
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t dm = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < count; i += kSelThreads) {
-      const uint32_t k = key_of(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & dm], 1u);
-    }
-    __syncthreads();
-    // bins from the top: thread i takes bins top - 4i .. top - 4i - 3
-    uint32_t c[kBins / kSelThreads];
-    unsigned long long sum = 0, total;
+    uint32_t *h = hist[pass & 1];
+    // (tokens that are no candidates count in the last bin, behind every weight's)
+    auto count = [&](uint32_t k) {
+      if ((k & mask) == prefix) atomicAdd(&h[kBins - 1 - ((k >> shift) & dm)], 1u);
+    };
+    each_step([&](int, const uint4 &x) {
+      count(x.x);
+      count(x.y);
+      count(x.z);
+      count(x.w);
+    });
+    if (nc > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    // The bins are shared out over the cluster (reading all of every CTA's histogram
+    // took 8 times as long): thread i of CTA r has nb bins of segment r.
+    // (a cluster of 16 leaves every second thread without a bin)
+    const int nb = max(1, kBinsPer / static_cast<int>(nc));
+    const bool busy = nc <= kBinsPer || tid < kSelThreads / 2;
+    const int first = nc <= kBinsPer ? (static_cast<int>(rank) * kSelThreads + tid) * nb
+                                     : static_cast<int>(rank) * (kSelThreads / 2) + (busy ? tid : 0);
+    uint32_t c[kBinsPer], sum = 0, total;
+    if (nc == 1) {
 #pragma unroll
-    for (int q = 0; q < kBins / kSelThreads; ++q) {
-      c[q] = hist[kBins - 1 - (tid * (kBins / kSelThreads) + q)];
-      sum += c[q];
-    }
-    unsigned long long above = block_scan(sum, warp_sums, &total);
+      for (int q = 0; q < kBinsPer; q += 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(&h[first + q]);
+        c[q] = x.x;
+        c[q + 1] = x.y;
+        c[q + 2] = x.z;
+        c[q + 3] = x.w;
+      }
+    } else {
 #pragma unroll
-    for (int q = 0; q < kBins / kSelThreads; ++q) {
-      if (above < static_cast<unsigned long long>(left) &&
-          above + c[q] >= static_cast<unsigned long long>(left)) {
-        digit_s = kBins - 1 - (tid * (kBins / kSelThreads) + q);
-        left_s = left - static_cast<int>(above);
+      for (int q = 0; q < kBinsPer; ++q) {
+        c[q] = 0;
+        if (q < nb && busy) {
+          uint32_t y[kMaxCluster];   // read together, then added
+          y[0] = h[first + q];
+#pragma unroll
+          for (int r = 1; r < kMaxCluster; ++r)
+            y[r] = r < static_cast<int>(nc) ? remote_u32(&h[first + q], (rank + r) % nc) : 0u;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) c[q] += y[r];
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBinsPer; ++q) sum += c[q];
+#pragma unroll
+    for (int q = 0; q < kBinsPer; q += 4)
+      *reinterpret_cast<uint4 *>(&hist[(pass & 1) ^ 1][kBinsPer * tid + q]) =
+          make_uint4(0u, 0u, 0u, 0u);
+    uint32_t above = block_scan(sum, warp_sums, &total);
+    if (nc > 1) {
+      if (tid == 0) segment = total;
+      cluster_sync();
+      above += __reduce_add_sync(0xffffffffu,
+                                 static_cast<uint32_t>(lane) < rank ? remote_u32(&segment, lane) : 0u);
+    }
+    uint32_t at = 0, rest = 0;   // (one thread of the cluster finds it)
+#pragma unroll
+    for (int q = 0; q < kBinsPer; ++q) {
+      if (above < left && above + c[q] >= left) {
+        at = kBins - 1 - (first + q);
+        rest = left - above;
       }
       above += c[q];
     }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(digit_s) << shift;
+    if (rest) {
+#pragma unroll 1
+      for (uint32_t r = 0; r < nc; ++r)
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote_addr(found, r)),
+                     "r"(at), "r"(rest)
+                     : "memory");
+    }
+    if (nc > 1)
+      cluster_sync();   // (and the histograms have been read)
+    else
+      __syncthreads();
+    prefix |= found[0] << shift;
     mask |= dm << shift;
-    left = left_s;
-    __syncthreads();
+    left = found[1];
   }
   // ---- kept indices in token order: above the threshold, and the first
   // `left` of those equal to it ----
-  int base_gt = 0, base_eq = 0;
-  for (int i0 = 0; i0 < count; i0 += kSelThreads * kScanPer) {
-    const int i1 = i0 + tid * kScanPer;
-    uint32_t gt = 0, eq = 0;   // bit q: token i1 + q
-#pragma unroll
-    for (int q = 0; q < kScanPer; ++q)
-      if (i1 + q < count) {
-        const uint32_t k = key_of(i1 + q);
-        gt |= (k > prefix ? 1u : 0u) << q;
-        eq |= (k == prefix ? 1u : 0u) << q;
-      }
-    unsigned long long total;
-    const unsigned long long v = static_cast<unsigned long long>(__popc(gt)) << 32 | __popc(eq);
-    const unsigned long long before = block_scan(v, warp_sums, &total);
-    int g_at = base_gt + static_cast<int>(before >> 32);
-    int e_at = base_eq + static_cast<int>(before & 0xffffffffu);
-#pragma unroll
-    for (int q = 0; q < kScanPer; ++q) {
-      const bool is_gt = gt >> q & 1u, is_eq = eq >> q & 1u;
-      if (is_gt || (is_eq && e_at < left))
-        kept[n_sink + g_at + min(e_at, left)] = c0 + i1 + q;
-      g_at += is_gt;
-      e_at += is_eq;
-    }
-    base_gt += static_cast<int>(total >> 32);
-    base_eq += static_cast<int>(total & 0xffffffffu);
+  uint32_t gt = 0, eq = 0;
+  each_step([&](int, const uint4 &x) {
+    gt += (x.x > prefix) + (x.y > prefix) + (x.z > prefix) + (x.w > prefix);
+    eq += (x.x == prefix) + (x.y == prefix) + (x.z == prefix) + (x.w == prefix);
+  });
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    counts[warp][0] = gt;
+    counts[warp][1] = eq;
   }
+  __syncthreads();
+  uint32_t g_at = 0, e_at = 0;   // above the threshold, and equal, ahead of this warp's tokens
+  if (nc > 1) {
+    if (tid < 2) {
+      uint32_t t = 0;
+      for (int w = 0; w < kWarps; ++w) t += counts[w][tid];
+      totals[tid] = t;
+    }
+    cluster_sync();
+    const bool ahead = static_cast<uint32_t>(lane) < rank;
+    g_at = __reduce_add_sync(0xffffffffu, ahead ? remote_u32(&totals[0], lane) : 0u);
+    e_at = __reduce_add_sync(0xffffffffu, ahead ? remote_u32(&totals[1], lane) : 0u);
+  }
+  for (int w = 0; w < warp; ++w) {
+    g_at += counts[w][0];
+    e_at += counts[w][1];
+  }
+  each_step([&](int t, const uint4 &x) {
+    const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+    uint32_t is_gt = 0, is_eq = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      is_gt |= (k[q] > prefix ? 1u : 0u) << q;
+      is_eq |= (k[q] == prefix ? 1u : 0u) << q;
+    }
+    const uint32_t v = __popc(is_gt) << 16 | __popc(is_eq);   // of at most 128 tokens
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+    uint32_t ga = g_at + ((incl - v) >> 16), ea = e_at + ((incl - v) & 0xffffu);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool one_gt = is_gt >> q & 1u, one_eq = is_eq >> q & 1u;
+      if (one_gt || (one_eq && ea < left)) kept[n_sink + ga + min(ea, left)] = t + q;
+      ga += one_gt;
+      ea += one_eq;
+    }
+    g_at += all >> 16;
+    e_at += all & 0xffffu;
+  });
+  if (nc > 1) cluster_sync();   // a CTA's shared memory outlives its readers
 }
 
-// CTA (row, head, part): part < 2 * slices moves column slice part / 2 of K (even)
-// or V (odd); part 2 * slices moves the weights.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
-  const int parts = 2 * p.slices + 1;
-  const int u = blockIdx.x / parts, part = blockIdx.x - u * parts;
+// CTA (row, head, part): part 0 walks K, 1 walks V, 2 the weights.
+__global__ void __launch_bounds__(kMoveThreads) evict_walk_kernel(const EvictParams p) {
+  pdl_wait();
+  const int u = blockIdx.x / 3, part = blockIdx.x - 3 * u;
   const int b = u / p.Hkv, g = u - b * p.Hkv;
   const int L = p.seq_lens[b], K = p.keep_lens[b];
   if (K >= L || K <= 0 || K > p.kept_stride) return;
   const int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
-  if (kept[0] < 0) return;   // the choice left this row alone (bad length or block)
+  if (kept[K - 1] < 0) return;   // the choice left this row alone (bad length or block)
   const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
   const int tid = threadIdx.x;
   auto row_of = [&](int t) {
     return (static_cast<size_t>(table[t >> 4]) * p.Hkv + g) * kBlockTokens + (t & 15);
   };
-  if (part == 2 * p.slices) {
-    for (int j0 = 0; j0 < K; j0 += kMoveThreads * kMoveBatch) {
-      float x[kMoveBatch];
-      bool go[kMoveBatch];
+  if (part == 2) {
+    for (int j0 = 0; j0 < K; j0 += kMoveThreads * kWalkVecs) {
+      float x[kWalkVecs];
+      bool go[kWalkVecs];
 #pragma unroll
-      for (int q = 0; q < kMoveBatch; ++q) {
+      for (int q = 0; q < kWalkVecs; ++q) {
         const int j = j0 + q * kMoveThreads + tid;
         const int s = j < K ? kept[j] : j;
         go[q] = s != j;
@@ -213,37 +412,185 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
       }
       __syncthreads();
 #pragma unroll
-      for (int q = 0; q < kMoveBatch; ++q) {
-        const int j = j0 + q * kMoveThreads + tid;
-        if (go[q]) p.mass[row_of(j)] = x[q];
-      }
+      for (int q = 0; q < kWalkVecs; ++q)
+        if (go[q]) p.mass[row_of(j0 + q * kMoveThreads + tid)] = x[q];
     }
     return;
   }
-  unsigned char *cache = (part & 1 ? p.v_cache : p.k_cache) +
-                         static_cast<size_t>(part >> 1) * p.slice_bytes;
-  const int width = min(p.slice_bytes, p.row_bytes - (part >> 1) * p.slice_bytes);
-  const int pieces = width / 16;                 // 16-byte pieces of a token's slice
+  unsigned char *cache = part ? p.v_cache : p.k_cache;
+  const int pieces = p.row_bytes / 16;           // 16-byte pieces of a token's row
   const int per = kMoveThreads / pieces;         // tokens in one round of the CTA
   const int lt = tid / pieces, lc = tid - lt * pieces;
   const bool on = lt < per;
-  for (int j0 = 0; j0 < K; j0 += per * kMoveBatch) {
-    uint4 x[kMoveBatch];
-    bool go[kMoveBatch];
+  for (int j0 = 0; j0 < K; j0 += per * kWalkVecs) {
+    uint4 x[kWalkVecs];
+    bool go[kWalkVecs];
 #pragma unroll
-    for (int q = 0; q < kMoveBatch; ++q) {
+    for (int q = 0; q < kWalkVecs; ++q) {
       const int j = j0 + q * per + lt;
       const int s = on && j < K ? kept[j] : j;
       go[q] = s != j;
       if (go[q]) x[q] = *reinterpret_cast<const uint4 *>(cache + row_of(s) * p.row_bytes + 16 * lc);
     }
-    __syncthreads();   // the chunk is read before any of it is written
+    __syncthreads();   // the step is read before any of it is written
 #pragma unroll
-    for (int q = 0; q < kMoveBatch; ++q) {
+    for (int q = 0; q < kWalkVecs; ++q) {
       const int j = j0 + q * per + lt;
       if (go[q]) *reinterpret_cast<uint4 *>(cache + row_of(j) * p.row_bytes + 16 * lc) = x[q];
     }
   }
+}
+
+// Lowest index in [0, n) of kept whose value is at least x (n if none), by a warp:
+// 32 probes a round.
+__device__ __forceinline__ int lower_bound(const int32_t *kept, int n, int x, int lane) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, at < hi && kept[at] < x));
+    if (below == 0) return lo;
+    hi = min(hi, lo + below * step);
+    lo += (below - 1) * step + 1;
+  }
+  return lo;
+}
+
+// One chunk of one (row, KV head): keys, values and weights.
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const EvictParams p) {
+  __shared__ int task_s, ok_s, range_s[2];
+  const int tid = threadIdx.x;
+  const int units = p.B * p.Hkv;
+  pdl_wait();
+  if (tid == 0) {
+    task_s = atomicAdd(p.ticket, 1);
+    ok_s = 1;
+  }
+  __syncthreads();
+  const int chunk = task_s / units, u = task_s - chunk * units;
+  const int b = u / p.Hkv, g = u - b * p.Hkv;
+  const int L = p.seq_lens[b], K = p.keep_lens[b];
+  const int j0 = chunk * p.chunk;
+  if (K >= L || j0 >= K || K > p.kept_stride) return;
+  const int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
+  const int nj = min(p.chunk, K - j0);
+  const int last = kept[j0 + nj - 1];
+  if (last < 0) return;   // the choice left this row alone (bad length or block)
+  int32_t *flags = p.flags + static_cast<size_t>(u) * p.chunks;
+  if (last == j0 + nj - 1) {   // every token up to here is where it belongs
+    if (tid == 0) asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flags + chunk) : "memory");
+    return;
+  }
+  const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
+  auto row_of = [&](int t) {
+    return (static_cast<size_t>(table[t >> 4]) * p.Hkv + g) * kBlockTokens + (t & 15);
+  };
+  const int pieces = p.row_bytes / 16;
+  uint4 xk[kMoveVecs], xv[kMoveVecs];
+  int dst[kMoveVecs];   // cache row, -1: nothing to move
+#pragma unroll
+  for (int q = 0; q < kMoveVecs; ++q) {
+    const int v = tid + q * kMoveThreads, j = v / pieces, c = v - j * pieces;
+    dst[q] = -1;
+    if (j < nj) {
+      const int s = kept[j0 + j];
+      if (s != j0 + j) {
+        const size_t at = row_of(s) * p.row_bytes + 16 * c;
+        xk[q] = __ldcg(reinterpret_cast<const uint4 *>(p.k_cache + at));
+        xv[q] = __ldcg(reinterpret_cast<const uint4 *>(p.v_cache + at));
+        dst[q] = static_cast<int>(row_of(j0 + j));
+      }
+    }
+  }
+  float xm[4];   // weights (a chunk has at most 1024 tokens)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int j = tid + q * kMoveThreads;
+    if (j < nj) xm[q] = __ldcg(p.mass + row_of(kept[j0 + j]));
+  }
+  // the chunks that read what lies in this chunk's slots: those of the kept tokens
+  // from there
+  if (tid < 64) {
+    const int at = lower_bound(kept, K, tid < 32 ? j0 : j0 + nj, tid & 31);
+    if ((tid & 31) == 0) range_s[tid >> 5] = at;
+  }
+  __threadfence();   // this thread's reads are done before the flag is seen
+  __syncthreads();
+  if (tid == 0) asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flags + chunk) : "memory");
+  int need = -1;
+  if (tid < 2 && range_s[0] < range_s[1]) {
+    need = (tid == 0 ? range_s[0] : range_s[1] - 1) / p.chunk;
+    if (need >= chunk) need = -1;   // (this one)
+  }
+  if (need >= 0) {
+    const long long t0 = clock64();
+    for (;;) {
+      int v;
+      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flags + need) : "memory");
+      if (v) break;
+      if (clock64() - t0 > kWaitCycles) {
+        set_dev_err(p.err, PKV_DEVERR_TIMEOUT);
+        ok_s = 0;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (!ok_s) return;
+#pragma unroll
+  for (int q = 0; q < kMoveVecs; ++q)
+    if (dst[q] >= 0) {
+      const size_t at =
+          static_cast<size_t>(dst[q]) * p.row_bytes + 16 * ((tid + q * kMoveThreads) % pieces);
+      *reinterpret_cast<uint4 *>(p.k_cache + at) = xk[q];
+      *reinterpret_cast<uint4 *>(p.v_cache + at) = xv[q];
+    }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int j = tid + q * kMoveThreads;
+    if (j < nj) p.mass[row_of(j0 + j)] = xm[q];
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int chunk_tokens(int row_bytes) { return kChunkBytes / row_bytes; }
+
+int check_sizes(int B, int Hkv, int d, int dtype, int kept_stride) {
+  PKV_REQUIRE(dtype_ok(dtype), PKV_ERR_UNSUPPORTED, "dtype %d", dtype);
+  PKV_REQUIRE(B >= 0 && B <= 65536 && Hkv > 0 && Hkv <= 4096, PKV_ERR_UNSUPPORTED,
+              "B = %d, Hkv = %d", B, Hkv);
+  const long long row_bytes = static_cast<long long>(d) * dtype_size(dtype);
+  PKV_REQUIRE(d > 0 && row_bytes % 16 == 0 && row_bytes <= 1024, PKV_ERR_UNSUPPORTED,
+              "head_dim * sizeof(dtype) must be a multiple of 16, at most 1024 (d=%d)", d);
+  PKV_REQUIRE(kept_stride > 0, PKV_ERR_INVALID_ARG, "kept_stride must be positive");
+  const long long chunks = (kept_stride + chunk_tokens(static_cast<int>(row_bytes)) - 1ll) /
+                           chunk_tokens(static_cast<int>(row_bytes));
+  PKV_REQUIRE(static_cast<long long>(B) * Hkv * chunks < (1ll << 31) &&
+                  static_cast<long long>(B) * Hkv * kMaxCluster < (1ll << 31),
+              PKV_ERR_UNSUPPORTED, "too many rows, heads and kept tokens");
+  return PKV_OK;
+}
+
+template <typename K>
+cudaError_t launch(K kern, long long grid, int threads, size_t smem, int cluster, bool dependent,
+                   const EvictParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (dependent) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
@@ -251,27 +598,42 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 using namespace pkv;
 
+extern "C" int pkv_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t d, int32_t dtype,
+                                         int32_t kept_stride, size_t *bytes) {
+  clear_error();
+  PKV_REQUIRE(bytes, PKV_ERR_INVALID_ARG, "bytes is NULL");
+  const int rc = check_sizes(B, Hkv, d, dtype, kept_stride);
+  if (rc != PKV_OK) return rc;
+  const int chunk = chunk_tokens(d * static_cast<int>(dtype_size(dtype)));
+  const size_t chunks = (kept_stride + chunk - 1ll) / chunk;
+  *bytes = 256 + align256(static_cast<size_t>(B) * Hkv * chunks * sizeof(int32_t));
+  return PKV_OK;
+}
+
 extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   clear_error();
   PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "args is NULL");
-  PKV_REQUIRE(dtype_ok(a->dtype), PKV_ERR_UNSUPPORTED, "dtype %d", a->dtype);
-  PKV_REQUIRE(a->B >= 0 && a->B <= 65536 && a->Hkv > 0 && a->Hkv <= 4096, PKV_ERR_UNSUPPORTED,
-              "B = %d, Hkv = %d", a->B, a->Hkv);
-  const long long row_bytes = static_cast<long long>(a->d) * dtype_size(a->dtype);
-  PKV_REQUIRE(a->d > 0 && row_bytes % 16 == 0 && row_bytes <= 1024, PKV_ERR_UNSUPPORTED,
-              "head_dim * sizeof(dtype) must be a multiple of 16, at most 1024 (d=%d)", a->d);
+  int rc = check_sizes(a->B, a->Hkv, a->d, a->dtype, a->kept_stride);
+  if (rc != PKV_OK) return rc;
   PKV_REQUIRE(a->sink >= 0 && a->recent >= 0, PKV_ERR_INVALID_ARG, "negative sink or recent");
   PKV_REQUIRE(a->num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
   PKV_REQUIRE(a->bt_stride > 0 && a->bt_stride < (1 << 26), PKV_ERR_INVALID_ARG, "bt_stride %d",
               a->bt_stride);
-  PKV_REQUIRE(a->kept_stride > 0, PKV_ERR_INVALID_ARG, "kept_stride must be positive");
   if (a->B == 0) return PKV_OK;
   PKV_REQUIRE(a->k_cache && a->v_cache && a->mass && a->block_tables && a->seq_lens &&
-                  a->keep_lens && a->kept,
+                  a->keep_lens && a->kept && a->workspace,
               PKV_ERR_INVALID_ARG, "NULL pointer");
-  PKV_REQUIRE((reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache)) %
+  PKV_REQUIRE((reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache) |
+               reinterpret_cast<uintptr_t>(a->mass)) %
                       16 == 0,
-              PKV_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+              PKV_ERR_INVALID_ARG, "caches and mass must be 16-byte aligned");
+  PKV_REQUIRE(reinterpret_cast<uintptr_t>(a->workspace) % 256 == 0, PKV_ERR_INVALID_ARG,
+              "workspace must be 256-byte aligned");
+  size_t need = 0;
+  rc = pkv_evict_workspace_bytes(a->B, a->Hkv, a->d, a->dtype, a->kept_stride, &need);
+  if (rc != PKV_OK) return rc;
+  PKV_REQUIRE(a->workspace_bytes >= need, PKV_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed",
+              a->workspace_bytes, need);
   EvictParams p;
   p.k_cache = static_cast<unsigned char *>(a->k_cache);
   p.v_cache = static_cast<unsigned char *>(a->v_cache);
@@ -281,6 +643,8 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   p.keep_lens = a->keep_lens;
   p.kept = a->kept;
   p.err = a->dev_err_flag;
+  p.ticket = static_cast<int32_t *>(a->workspace);
+  p.flags = p.ticket + 64;
   p.num_blocks = a->num_blocks;
   p.bt_stride = a->bt_stride;
   p.kept_stride = a->kept_stride;
@@ -288,29 +652,42 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   p.recent = a->recent;
   p.B = a->B;
   p.Hkv = a->Hkv;
-  p.row_bytes = static_cast<int>(row_bytes);
-  const long long longest = 16ll * a->bt_stride;
-  p.cached = static_cast<int>(longest < 40960 ? longest : 40960);
-  // column slices: split rows (down to a 32-byte sector) until the CTAs fill the GPU
+  p.row_bytes = a->d * static_cast<int>(dtype_size(a->dtype));
+  p.chunk = chunk_tokens(p.row_bytes);
+  p.chunks = static_cast<int>((a->kept_stride + p.chunk - 1ll) / p.chunk);
+  const long long rows = static_cast<long long>(a->num_blocks) * a->Hkv * kBlockTokens;
+  PKV_REQUIRE(rows < (1ll << 31), PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row numbers");
+  // CTAs per row and head: 8 steps of keys each for the longest row, and while the
+  // rows are few, enough to share it out (two steps at least)
   const long long units = static_cast<long long>(a->B) * a->Hkv;
-  p.slices = 1;
-  p.slice_bytes = p.row_bytes;
-  while (units * 2 * p.slices < 2 * 152 && p.slice_bytes % 64 == 0) {
-    p.slices *= 2;
-    p.slice_bytes /= 2;
-  }
-  const long long grid = units * (2 * p.slices + 1);
-  PKV_REQUIRE(grid < (1ll << 31), PKV_ERR_UNSUPPORTED, "too many rows and heads");
+  const long long longest = 16ll * a->bt_stride;
+  int cluster = 1;
+  while (cluster < kMaxCluster &&
+         (longest > 8ll * cluster * kTileTokens ||
+          (units * cluster < 152 && longest > 2ll * cluster * kTileTokens)))
+    cluster *= 2;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const long long tiles = ((longest + kTileTokens - 1) / kTileTokens + cluster - 1) / cluster;
+  p.cached = static_cast<int>(tiles < kMaxCached ? tiles : kMaxCached);
   static std::atomic<unsigned long long> attrs_set{0};
   PKV_CUDA_CHECK(set_attributes_once(attrs_set, [] {
-    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                40960 * 4);
+    for (auto kern : {evict_select_kernel<4>, evict_select_kernel<8>}) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMaxCached * kTileTokens * 4);
+      if (e == cudaSuccess)   // clusters of 16
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
   }));
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<static_cast<unsigned>(units), kSelThreads, p.cached * sizeof(uint32_t), s>>>(
-      p);
-  PKV_LAUNCH_CHECK("evict_select_kernel");
-  evict_move_kernel<<<static_cast<unsigned>(grid), kMoveThreads, 0, s>>>(p);
-  PKV_LAUNCH_CHECK("evict_move_kernel");
+  cudaError_t e = launch(tiles > 4 ? evict_select_kernel<8> : evict_select_kernel<4>, units * cluster, kSelThreads,
+                         static_cast<size_t>(p.cached) * kTileTokens * 4, cluster, false, p, s);
+  PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict_select_kernel launch: %s",
+              cudaGetErrorString(e));
+  if (units * 2 >= 152)
+    e = launch(evict_walk_kernel, units * 3, kMoveThreads, 0, 1, true, p, s);
+  else
+    e = launch(evict_chunk_kernel, units * p.chunks, kMoveThreads, 0, 1, true, p, s);
+  PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict compaction launch: %s", cudaGetErrorString(e));
   return PKV_OK;
 }

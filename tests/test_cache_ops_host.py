@@ -217,8 +217,10 @@ def fake(n=1 << 20):
 
 def evict_ok(b):
     a = b.EvictArgs()
-    for f in ("k_cache", "v_cache", "mass", "block_tables", "seq_lens", "keep_lens", "kept"):
+    for f in ("k_cache", "v_cache", "mass", "block_tables", "seq_lens", "keep_lens", "kept",
+              "workspace"):
         setattr(a, f, fake())
+    a.workspace_bytes = 1 << 30
     a.num_blocks, a.bt_stride, a.kept_stride, a.sink, a.recent = 8, 4, 16, 0, 0
     a.B, a.Hkv, a.d, a.dtype = 2, 2, 64, b.BF16
     return a
@@ -228,7 +230,9 @@ def evict_ok(b):
     ("k_cache", None), ("v_cache", None), ("mass", None), ("block_tables", None),
     ("seq_lens", None), ("keep_lens", None), ("kept", None), ("k_cache", fake((1 << 20) + 8)),
     ("num_blocks", 0), ("bt_stride", 0), ("kept_stride", 0), ("sink", -1), ("recent", -1),
-    ("B", -1), ("B", 70000), ("Hkv", 0), ("d", 0), ("d", 4), ("d", 1024), ("dtype", 5)])
+    ("B", -1), ("B", 70000), ("Hkv", 0), ("d", 0), ("d", 4), ("d", 1024), ("dtype", 5),
+    ("mass", fake((1 << 20) + 4)), ("workspace", None), ("workspace", fake((1 << 20) + 16)),
+    ("workspace_bytes", 256)])
 def test_evict_refuses(bind, field, value):
     a = evict_ok(bind)
     setattr(a, field, value)

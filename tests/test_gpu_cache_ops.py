@@ -485,10 +485,22 @@ def test_evict_head_shapes(Hkv, d, dtype):
     check_evict(c, 2, 10, 100)
 
 
-def test_evict_a_long_row():
-    """More candidates than the keys kept on chip."""
-    c = evict_case(1, 1, 64, "bf16", [50000], [20000], 3, ties=True)
-    check_evict(c, 4, 100, 20000)
+@pytest.mark.parametrize("L,K", [(3000, 1500), (9000, 8999), (16400, 3), (50000, 20000)])
+def test_evict_long_rows_shared_by_clusters(L, K):
+    c = evict_case(1, 1, 64, "bf16", [L], [K], 3, ties=True)
+    check_evict(c, 4, 100, K)
+
+
+def test_evict_a_row_longer_than_the_keys_kept_on_chip():
+    c = evict_case(1, 1, 8, "f32", [800001], [5000], 3, ties=True)
+    check_evict(c, 4, 100, 5000)
+
+
+def test_evict_many_rows_walk():
+    """Enough (row, head) pairs that each is walked by one CTA."""
+    lens = [(37 * i) % 300 for i in range(40)]
+    c = evict_case(40, 2, 64, "bf16", lens, [(11 * i) % 200 for i in range(40)], 17, ties=True)
+    check_evict(c, 3, 9, 200)
 
 
 def test_evict_leaves_bad_rows_alone():
