@@ -816,11 +816,18 @@ def _overlap(a, b):
 
 def _launch_on(args, stream):
     """The stream of a launch: ``stream`` or the current one, on the tensors' device."""
-    torch = _torch()
-    if torch.cuda.current_device() != args.device.index:
-        raise PkvError(ERR_INVALID_ARG, f"tensors are on {args.device}, the current device is "
-                                        f"cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    cuda = args.cuda
+    device = cuda.current_device()
+    if device != args.index:
+        raise PkvError(ERR_INVALID_ARG, f"tensors are on cuda:{args.index}, the current device is "
+                                        f"cuda:{device}")
+    return (cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _finish(args, device, keep):
+    """What a launch of the struct needs besides its fields."""
+    args.cuda, args.index, args.keep = _torch().cuda, device.index, keep
+    return args
 
 
 class Rotary:
@@ -888,9 +895,8 @@ def make_rotary_args(rotary, q, k, v, positions, q_out=None, k_out=None, slot_ma
         a.num_blocks = k_cache.shape[0]
     if err is not None:
         a.dev_err_flag = _want(err, "err", None, torch.int32, dev)
-    a.keep = (rotary, q, k, v, q_out, k_out, positions, slot_mapping, k_cache, v_cache, err)
-    a.device = dev
-    return a
+    return _finish(a, dev, (rotary, q, k, v, q_out, k_out, positions, slot_mapping, k_cache,
+                            v_cache, err))
 
 
 def rotary_append_args(args, stream=None):
@@ -1015,10 +1021,9 @@ def make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out
     if workspace is not None:
         a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)
         a.workspace_bytes = workspace.numel()
-    a.keep = (q_rot, k_cache, v_cache, block_tables, seq_lens, out, prefix_tables, prefix_plan, mass,
-              scores, mass_lens, lse, attn_bias, plan, workspace, err)
-    a.device = dev
-    return a
+    return _finish(a, dev, (q_rot, k_cache, v_cache, block_tables, seq_lens, out, prefix_tables,
+                            prefix_plan, mass, scores, mass_lens, lse, attn_bias, plan, workspace,
+                            err))
 
 
 def decode_attn_shared_args(args, stream=None):
@@ -1072,9 +1077,8 @@ def make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, k
                                 dtype=torch.uint8, device=dev)
     a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)
     a.workspace_bytes = workspace.numel()
-    a.keep = (k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, workspace, err)
-    a.device = dev
-    return a
+    return _finish(a, dev, (k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept,
+                            workspace, err))
 
 
 def evict_args(args, stream=None):
