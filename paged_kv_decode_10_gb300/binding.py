@@ -220,6 +220,8 @@ SIGNATURES = {
                                            _p_i32]),
     "pkv_shared_plan": (ctypes.c_int, [_p_i32, _c_i32, _p_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                        _c_i32, _c_i32, _p_i32, _c_i32, _p_i32, _p_i32]),
+    "pkv_shared_default_parts": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                                                _p_i32]),
     "pkv_shared_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                   ctypes.POINTER(_size_t)]),
     "pkv_decode_attn_shared": (ctypes.c_int, [ctypes.POINTER(SharedArgs), _vp]),
@@ -942,6 +944,14 @@ def shared_plan(row_prefix, prefix_lens, Hq, Hkv, d, dtype, num_ctas=0, out=None
     return out[:n.value]
 
 
+def shared_default_parts(B, Hq, Hkv, d, dtype, bt_stride):
+    """Partition of the own tokens that ``make_shared_args`` takes unless told."""
+    n = ctypes.c_int32()
+    _check(load().pkv_shared_default_parts(int(B), int(Hq), int(Hkv), int(d), int(dtype),
+                                           int(bt_stride), ctypes.byref(n)))
+    return n.value
+
+
 def shared_workspace_bytes(B, Hq, Hkv, d, num_parts, slots):
     n = _size_t()
     _check(load().pkv_shared_workspace_bytes(int(B), int(Hq), int(Hkv), int(d), int(num_parts),
@@ -1014,7 +1024,9 @@ def make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out
         a.lse_out = _want(lse, "lse", (B, Hq), f32, dev)
     if err is not None:
         a.dev_err_flag = _want(err, "err", None, i32, dev)
-    a.num_parts = int(num_parts) if num_parts is not None else default_parts(d, a.dtype, 0, Hq, Hkv)
+    if num_parts is None:
+        num_parts = shared_default_parts(B, Hq, Hkv, d, a.dtype, block_tables.shape[1])
+    a.num_parts = int(num_parts)
     if workspace is None and B > 0:
         nbytes = shared_workspace_bytes(B, Hq, Hkv, d, a.num_parts, a.slots)
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
