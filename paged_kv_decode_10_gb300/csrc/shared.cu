@@ -41,7 +41,7 @@ SharedSpace shared_space(size_t attn_bytes, int B, int Hq, int d, int slots) {
 // ---- prefix partials and own tokens joined -------------------------------------
 // out = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M) over the own tokens' partial
 // and the row's n prefix partials (merge_acc_add).  D / 4 lanes own one (row, head),
-// a float4 column each; the reads of four partials go out together.  Bound by L2:
+// a float4 column each; the reads of eight partials go out together.  Bound by L2:
 // the partials were just written.
 struct JoinParams {
   const int32_t *row_part;
@@ -55,7 +55,7 @@ struct JoinParams {
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   pdl_launch_dependents();
-  constexpr int LPR = D / 4, K = 4;
+  constexpr int LPR = D / 4, K = 8;
   const int u = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, d4 = threadIdx.x % LPR;
   if (u >= p.rows) {
     pdl_wait();

@@ -128,7 +128,10 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
       groups.push_back({p, rows, (rows + R - 1) / R, gr});
       longest = std::max(longest, gr);
     }
-    // time estimates, ns: a grain of tokens for one item, an item's fixed cost
+    // time estimates, ns: a grain of tokens for one item, an item's fixed cost.  (Half
+    // of what a grain takes alone on an SM: weighed at its full time, or with idle
+    // SMs credited, the choice came out longer ranges, which lost 4 % on 256 rows of
+    // five prefixes and nothing was gained elsewhere.)
     auto grain_ns = [&](int32_t rows) {
       const double q = static_cast<double>(rows) * G, w = d / 128.0;
       if (dtype == PKV_F32) return 500.0 * w * q;
