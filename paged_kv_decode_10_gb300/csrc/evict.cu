@@ -20,7 +20,8 @@
 //  * Few rows: chunks of T kept tokens go to CTAs of their own.  A chunk may be
 //    stored once every token that still lies in its T slots has been read; at most
 //    T kept tokens come from there, consecutive ones, so they belong to at most two
-//    chunks, earlier ones or itself: a chunk waits for two flags.  Chunks are taken
+//    chunks, earlier ones or itself: a chunk waits for two flags (the choice notes how
+//    many kept tokens lie below each chunk's first slot, which names them).  Chunks are taken
 //    by ticket in order and reading never waits, so every wait ends.
 // Both are memory bound: each kept row is read and written once.  The walk needs
 // no flags and keeps its steps back to back (64 rows of 8 heads: 89 us against
@@ -42,6 +43,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveVecs = 4;                       // 16-byte pieces of K (and of V) a thread moves
 constexpr int kChunkBytes = kMoveThreads * kMoveVecs * 16;
 constexpr int kWalkVecs = 8;                       // pieces a walking thread has in flight
+constexpr int kChunkUnits = 76;                    // (row, head) pairs from which rows are walked
 constexpr long long kWaitCycles = 1ll << 31;
 
 struct EvictParams {
@@ -50,6 +52,8 @@ struct EvictParams {
   const int32_t *block_tables, *seq_lens, *keep_lens;
   int32_t *kept, *err;
   int32_t *ticket, *flags;           // workspace: [1], [B * Hkv][chunks]
+  int32_t *below;                    // [B * Hkv][chunks + 1] kept tokens with index < chunk * c;
+                                     // NULL: rows are walked
   int num_blocks, bt_stride, kept_stride, sink, recent;
   int B, Hkv, row_bytes;
   int chunk, chunks;                 // tokens of a chunk, chunks of kept_stride tokens
@@ -88,15 +92,6 @@ __device__ __forceinline__ uint32_t remote_u32(const void *local, uint32_t rank)
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(local, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 remote_u128(const void *local, uint32_t rank) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(remote_addr(local, rank))
-               : "memory");
-  return v;
-}
-
 // Sum over the threads before this one of v, and the total (kSelThreads threads).
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -150,8 +145,12 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
   const bool bad_len = L < 0 || K < 0 || static_cast<long long>(L) > 16ll * p.bt_stride ||
                        min(L, K) > p.kept_stride;
   const int step = static_cast<int>(nc) * kSelThreads, me = static_cast<int>(rank) * kSelThreads + tid;
-  // the compaction's flags and ticket
-  for (int j = me; j < p.chunks; j += step) p.flags[static_cast<size_t>(u) * p.chunks + j] = 0;
+  // what the chunks need: flags and ticket
+  int32_t *below = nullptr;
+  if (p.below) {
+    for (int j = me; j < p.chunks; j += step) p.flags[static_cast<size_t>(u) * p.chunks + j] = 0;
+    below = p.below + static_cast<size_t>(u) * (p.chunks + 1);
+  }
   if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
   for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0;
   if (tid == 0) bad = 0;
@@ -219,6 +218,15 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
   if (!skip && L > K) {
     for (int j = me; j < n_sink; j += step) kept[j] = j;
     for (int j = me; j < n_recent; j += step) kept[K - n_recent + j] = c1 + j;
+    // below, where the choice has no say: among the first and the last tokens, or
+    // where all between go
+    for (int c = below ? me : p.chunks + 1; c <= p.chunks; c += step) {
+      const long long x = static_cast<long long>(c) * p.chunk;
+      if (x <= c0 || x >= c1 || m <= 0)
+        below[c] = static_cast<int>(x <= c0   ? x
+                                    : x >= c1 ? min(static_cast<long long>(K), K - n_recent + (x - c1))
+                                              : n_sink);
+    }
   }
   if (skip || K >= L || m <= 0) {
     if (nc > 1) cluster_sync();   // a CTA's shared memory outlives its readers
@@ -372,8 +380,12 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
     }
     const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
     uint32_t ga = g_at + ((incl - v) >> 16), ea = e_at + ((incl - v) & 0xffffu);
+    const int c = below ? (t + 3) / p.chunk : 0;   // a chunk's first slot among these?
+    const int edge = c * p.chunk;
+    const bool mark = below && edge >= t && edge > c0 && edge < c1 && c <= p.chunks;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+      if (mark && edge == t + q) below[c] = static_cast<int>(n_sink + ga + min(ea, left));
       const bool one_gt = is_gt >> q & 1u, one_eq = is_eq >> q & 1u;
       if (one_gt || (one_eq && ea < left)) kept[n_sink + ga + min(ea, left)] = t + q;
       ga += one_gt;
@@ -396,24 +408,30 @@ __global__ void __launch_bounds__(kMoveThreads) evict_walk_kernel(const EvictPar
   if (kept[K - 1] < 0) return;   // the choice left this row alone (bad length or block)
   const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
   const int tid = threadIdx.x;
-  auto row_of = [&](int t) {
-    return (static_cast<size_t>(table[t >> 4]) * p.Hkv + g) * kBlockTokens + (t & 15);
+  auto row_of = [&](int t) {   // (the pool has fewer than 2^31 rows)
+    return (table[t >> 4] * p.Hkv + g) * kBlockTokens + (t & 15);
   };
+  // Each kind of read (indices, table, rows) for all of a step's pieces before the
+  // next kind, without branches between: a round trip serves them all.
   if (part == 2) {
     for (int j0 = 0; j0 < K; j0 += kMoveThreads * kWalkVecs) {
       float x[kWalkVecs];
-      bool go[kWalkVecs];
+      int from[kWalkVecs], to[kWalkVecs];   // cache rows; to -1: nothing to move
+#pragma unroll
+      for (int q = 0; q < kWalkVecs; ++q) from[q] = kept[min(j0 + q * kMoveThreads + tid, K - 1)];
 #pragma unroll
       for (int q = 0; q < kWalkVecs; ++q) {
-        const int j = j0 + q * kMoveThreads + tid;
-        const int s = j < K ? kept[j] : j;
-        go[q] = s != j;
-        if (go[q]) x[q] = p.mass[row_of(s)];
+        const int j = j0 + q * kMoveThreads + tid, row = row_of(min(j, K - 1));
+        to[q] = j < K && from[q] != j ? row : -1;
+        from[q] = row_of(from[q]);
       }
+#pragma unroll
+      for (int q = 0; q < kWalkVecs; ++q)
+        if (to[q] >= 0) x[q] = p.mass[from[q]];
       __syncthreads();
 #pragma unroll
       for (int q = 0; q < kWalkVecs; ++q)
-        if (go[q]) p.mass[row_of(j0 + q * kMoveThreads + tid)] = x[q];
+        if (to[q] >= 0) p.mass[to[q]] = x[q];
     }
     return;
   }
@@ -422,44 +440,38 @@ __global__ void __launch_bounds__(kMoveThreads) evict_walk_kernel(const EvictPar
   const int per = kMoveThreads / pieces;         // tokens in one round of the CTA
   const int lt = tid / pieces, lc = tid - lt * pieces;
   const bool on = lt < per;
+  cache += 16 * lc;
   for (int j0 = 0; j0 < K; j0 += per * kWalkVecs) {
     uint4 x[kWalkVecs];
-    bool go[kWalkVecs];
+    int from[kWalkVecs], to[kWalkVecs];
+#pragma unroll
+    for (int q = 0; q < kWalkVecs; ++q) from[q] = kept[min(j0 + q * per + lt, K - 1)];
 #pragma unroll
     for (int q = 0; q < kWalkVecs; ++q) {
-      const int j = j0 + q * per + lt;
-      const int s = on && j < K ? kept[j] : j;
-      go[q] = s != j;
-      if (go[q]) x[q] = *reinterpret_cast<const uint4 *>(cache + row_of(s) * p.row_bytes + 16 * lc);
+      const int j = j0 + q * per + lt, row = row_of(min(j, K - 1));
+      to[q] = on && j < K && from[q] != j ? row : -1;
+      from[q] = row_of(from[q]);
     }
+#pragma unroll
+    for (int q = 0; q < kWalkVecs; ++q)
+      if (to[q] >= 0)
+        x[q] = *reinterpret_cast<const uint4 *>(cache + static_cast<size_t>(from[q]) * p.row_bytes);
     __syncthreads();   // the step is read before any of it is written
 #pragma unroll
-    for (int q = 0; q < kWalkVecs; ++q) {
-      const int j = j0 + q * per + lt;
-      if (go[q]) *reinterpret_cast<uint4 *>(cache + row_of(j) * p.row_bytes + 16 * lc) = x[q];
-    }
+    for (int q = 0; q < kWalkVecs; ++q)
+      if (to[q] >= 0)
+        *reinterpret_cast<uint4 *>(cache + static_cast<size_t>(to[q]) * p.row_bytes) = x[q];
   }
-}
-
-// Lowest index in [0, n) of kept whose value is at least x (n if none), by a warp:
-// 32 probes a round.
-__device__ __forceinline__ int lower_bound(const int32_t *kept, int n, int x, int lane) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const int below = __popc(__ballot_sync(0xffffffffu, at < hi && kept[at] < x));
-    if (below == 0) return lo;
-    hi = min(hi, lo + below * step);
-    lo += (below - 1) * step + 1;
-  }
-  return lo;
 }
 
 // One chunk of one (row, KV head): keys, values and weights.
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const EvictParams p) {
-  __shared__ int task_s, ok_s, range_s[2];
+  __shared__ int task_s, ok_s;
+  __shared__ int2 lens_s[kChunkUnits];
   const int tid = threadIdx.x;
   const int units = p.B * p.Hkv;
+  // (every row's lengths, so that they need not wait for the ticket)
+  if (tid < p.B) lens_s[tid] = make_int2(p.seq_lens[tid], p.keep_lens[tid]);
   pdl_wait();
   if (tid == 0) {
     task_s = atomicAdd(p.ticket, 1);
@@ -468,12 +480,24 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const Evic
   __syncthreads();
   const int chunk = task_s / units, u = task_s - chunk * units;
   const int b = u / p.Hkv, g = u - b * p.Hkv;
-  const int L = p.seq_lens[b], K = p.keep_lens[b];
+  const int L = lens_s[b].x, K = lens_s[b].y;
   const int j0 = chunk * p.chunk;
   if (K >= L || j0 >= K || K > p.kept_stride) return;
   const int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
   const int nj = min(p.chunk, K - j0);
+  const int pieces = p.row_bytes / 16;
+  int src[kMoveVecs];   // where this thread's pieces come from (read beside what follows)
+#pragma unroll
+  for (int q = 0; q < kMoveVecs; ++q)
+    src[q] = kept[j0 + min((tid + q * kMoveThreads) / pieces, nj - 1)];
   const int last = kept[j0 + nj - 1];
+  // the chunks whose tokens lie in this chunk's slots (threads 0 and 1)
+  int lo = 0, hi = 0;
+  if (tid < 2) {
+    const int32_t *below = p.below + static_cast<size_t>(u) * (p.chunks + 1) + chunk;
+    lo = below[0];
+    hi = below[1];
+  }
   if (last < 0) return;   // the choice left this row alone (bad length or block)
   int32_t *flags = p.flags + static_cast<size_t>(u) * p.chunks;
   if (last == j0 + nj - 1) {   // every token up to here is where it belongs
@@ -484,49 +508,53 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const Evic
   auto row_of = [&](int t) {
     return (static_cast<size_t>(table[t >> 4]) * p.Hkv + g) * kBlockTokens + (t & 15);
   };
-  const int pieces = p.row_bytes / 16;
   uint4 xk[kMoveVecs], xv[kMoveVecs];
   int dst[kMoveVecs];   // cache row, -1: nothing to move
+  float xm[4];          // weights (a chunk has at most 1024 tokens)
+  int msrc[4];
+  // (each kind of read for all pieces before the next kind, and no branch between, so
+  // that a round trip serves them all: one by one this phase took 3 to 6 us of a CTA's 7)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) msrc[q] = kept[j0 + min(tid + q * kMoveThreads, nj - 1)];
+  int from[kMoveVecs];
 #pragma unroll
   for (int q = 0; q < kMoveVecs; ++q) {
-    const int v = tid + q * kMoveThreads, j = v / pieces, c = v - j * pieces;
-    dst[q] = -1;
-    if (j < nj) {
-      const int s = kept[j0 + j];
-      if (s != j0 + j) {
-        const size_t at = row_of(s) * p.row_bytes + 16 * c;
-        xk[q] = __ldcg(reinterpret_cast<const uint4 *>(p.k_cache + at));
-        xv[q] = __ldcg(reinterpret_cast<const uint4 *>(p.v_cache + at));
-        dst[q] = static_cast<int>(row_of(j0 + j));
-      }
+    const int j = (tid + q * kMoveThreads) / pieces;
+    from[q] = static_cast<int>(row_of(src[q]));
+    const int to = static_cast<int>(row_of(j0 + min(j, nj - 1)));
+    dst[q] = j < nj && src[q] != j0 + j ? to : -1;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) msrc[q] = static_cast<int>(row_of(msrc[q]));
+#pragma unroll
+  for (int q = 0; q < kMoveVecs; ++q) {
+    const size_t at =
+        static_cast<size_t>(from[q]) * p.row_bytes + 16 * ((tid + q * kMoveThreads) % pieces);
+    if (dst[q] >= 0) {
+      xk[q] = __ldcg(reinterpret_cast<const uint4 *>(p.k_cache + at));
+      xv[q] = __ldcg(reinterpret_cast<const uint4 *>(p.v_cache + at));
     }
   }
-  float xm[4];   // weights (a chunk has at most 1024 tokens)
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int j = tid + q * kMoveThreads;
-    if (j < nj) xm[q] = __ldcg(p.mass + row_of(kept[j0 + j]));
-  }
-  // the chunks that read what lies in this chunk's slots: those of the kept tokens
-  // from there
-  if (tid < 64) {
-    const int at = lower_bound(kept, K, tid < 32 ? j0 : j0 + nj, tid & 31);
-    if ((tid & 31) == 0) range_s[tid >> 5] = at;
-  }
+  for (int q = 0; q < 4; ++q)
+    if (tid + q * kMoveThreads < nj) xm[q] = __ldcg(p.mass + msrc[q]);
+  // the chunks that have to have been read: mostly they were long ago, so a first
+  // look goes out beside the reads
+  int need = lo < hi ? (tid == 0 ? lo : hi - 1) / p.chunk : -1;
+  if (need >= chunk) need = -1;   // (this one)
+  auto is_read = [&]() {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flags + need) : "memory");
+    return v != 0;
+  };
+  if (need >= 0 && is_read()) need = -1;
   __threadfence();   // this thread's reads are done before the flag is seen
   __syncthreads();
-  if (tid == 0) asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flags + chunk) : "memory");
-  int need = -1;
-  if (tid < 2 && range_s[0] < range_s[1]) {
-    need = (tid == 0 ? range_s[0] : range_s[1] - 1) / p.chunk;
-    if (need >= chunk) need = -1;   // (this one)
-  }
+  // (the flag before any wait: what has been read never waits)
+  if (tid == 0) asm volatile("st.relaxed.gpu.global.s32 [%0], 1;" ::"l"(flags + chunk) : "memory");
   if (need >= 0) {
     const long long t0 = clock64();
-    for (;;) {
-      int v;
-      asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flags + need) : "memory");
-      if (v) break;
+    while (!is_read()) {
       if (clock64() - t0 > kWaitCycles) {
         set_dev_err(p.err, PKV_DEVERR_TIMEOUT);
         ok_s = 0;
@@ -606,7 +634,7 @@ extern "C" int pkv_evict_workspace_bytes(int32_t B, int32_t Hkv, int32_t d, int3
   if (rc != PKV_OK) return rc;
   const int chunk = chunk_tokens(d * static_cast<int>(dtype_size(dtype)));
   const size_t chunks = (kept_stride + chunk - 1ll) / chunk;
-  *bytes = 256 + align256(static_cast<size_t>(B) * Hkv * chunks * sizeof(int32_t));
+  *bytes = 256 + align256(static_cast<size_t>(B) * Hkv * (2 * chunks + 1) * sizeof(int32_t));
   return PKV_OK;
 }
 
@@ -645,6 +673,9 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   p.err = a->dev_err_flag;
   p.ticket = static_cast<int32_t *>(a->workspace);
   p.flags = p.ticket + 64;
+  p.chunk = chunk_tokens(a->d * static_cast<int>(dtype_size(a->dtype)));
+  p.chunks = static_cast<int>((a->kept_stride + p.chunk - 1ll) / p.chunk);
+  p.below = p.flags + static_cast<size_t>(a->B) * a->Hkv * p.chunks;
   p.num_blocks = a->num_blocks;
   p.bt_stride = a->bt_stride;
   p.kept_stride = a->kept_stride;
@@ -653,8 +684,6 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   p.B = a->B;
   p.Hkv = a->Hkv;
   p.row_bytes = a->d * static_cast<int>(dtype_size(a->dtype));
-  p.chunk = chunk_tokens(p.row_bytes);
-  p.chunks = static_cast<int>((a->kept_stride + p.chunk - 1ll) / p.chunk);
   const long long rows = static_cast<long long>(a->num_blocks) * a->Hkv * kBlockTokens;
   PKV_REQUIRE(rows < (1ll << 31), PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row numbers");
   // CTAs per row and head: 8 steps of keys each for the longest row, and while the
@@ -666,6 +695,8 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
          (longest > 8ll * cluster * kTileTokens ||
           (units * cluster < 152 && longest > 2ll * cluster * kTileTokens)))
     cluster *= 2;
+  const bool walk = units >= kChunkUnits;   // two CTAs a pair (K, V) fill the GPU
+  if (walk) p.below = nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long tiles = ((longest + kTileTokens - 1) / kTileTokens + cluster - 1) / cluster;
   p.cached = static_cast<int>(tiles < kMaxCached ? tiles : kMaxCached);
@@ -684,7 +715,7 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
                          static_cast<size_t>(p.cached) * kTileTokens * 4, cluster, false, p, s);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict_select_kernel launch: %s",
               cudaGetErrorString(e));
-  if (units * 2 >= 152)
+  if (walk)
     e = launch(evict_walk_kernel, units * 3, kMoveThreads, 0, 1, true, p, s);
   else
     e = launch(evict_chunk_kernel, units * p.chunks, kMoveThreads, 0, 1, true, p, s);
