@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
   // a kernel launched after this one as a programmatic dependent (the next
   // layer's RoPE/append) may start now; it waits for this grid before it reads
   // anything this grid produces
-  if (!FUSE) pdl_launch_dependents();
+  if (!FUSE && !EXT) pdl_launch_dependents();
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -1040,6 +1040,13 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
   if (warp == NW && lane == 0) {
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
+  }
+  if constexpr (EXT) {
+    // behind the prefix kernel everything else was there before that one's wait was
+    // over; otherwise this kernel waits itself.  Either way what starts after the
+    // trigger may read what was there before.
+    if (!p.ext.dependent) pdl_wait();
+    pdl_launch_dependents();
   }
   if constexpr (FUSE) {   // read after the block-wide barrier below
     for (int i = tid; i < D / 2; i += Q::kThreads) turns_s[i] = p.turns[i];
@@ -1164,7 +1171,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     }
   }
   if (start >= end) {
-    if constexpr (EXT) pdl_wait();
+    pdl_wait();   // (a grid that ends has waited for the one before it, pages or not)
     return;
   }
   if (use_plan && rec_h.x >= p.B) {   // a record naming no row: never read outside seq_lens
@@ -1777,7 +1784,7 @@ struct AttnLauncher {
       attr[na].id = cudaLaunchAttributeCooperative;
       attr[na++].val.cooperative = 1;
     }
-    if (EXT ? p.ext.dependent != 0 : !FUSE) {
+    if (!FUSE) {
       attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attr[na++].val.programmaticStreamSerializationAllowed = 1;
     }

@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <utility>
 
 #include "pkv.h"
 #include "status.h"
@@ -228,6 +229,24 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // Waits until every prerequisite grid has finished and its writes are visible
 // (returns at once when the kernel was not launched as a dependent).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that calls pdl_wait() before it touches memory: its launch
+// and set-up overlap the end of whatever kernel is ahead of it on the stream.
+template <typename... P, typename... A>
+inline cudaError_t launch_waiting(void (*kern)(P...), unsigned grid, int threads, size_t smem,
+                                  cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
+}
 
 __device__ __forceinline__ void set_dev_err(int32_t *flag, int bits) {
   if (flag) atomicOr(flag, bits);

@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
   __shared__ __align__(8) uint32_t found[2]; 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), nc = cluster_size();
+  pdl_wait();
   pdl_launch_dependents();
   const int u = blockIdx.x / nc;
   const int b = u / p.Hkv, g = u - b * p.Hkv;
@@ -470,7 +471,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const Evic
   __shared__ int2 lens_s[kChunkUnits];
   const int tid = threadIdx.x;
   const int units = p.B * p.Hkv;
-  // (every row's lengths, so that they need not wait for the ticket)
+  // (every row's lengths, so that they need not wait for the ticket; the choice's own
+  // wait is over)
   if (tid < p.B) lens_s[tid] = make_int2(p.seq_lens[tid], p.keep_lens[tid]);
   pdl_wait();
   if (tid == 0) {
@@ -600,24 +602,21 @@ int check_sizes(int B, int Hkv, int d, int dtype, int kept_stride) {
 }
 
 template <typename K>
-cudaError_t launch(K kern, long long grid, int threads, size_t smem, int cluster, bool dependent,
+cudaError_t launch(K kern, long long grid, int threads, size_t smem, int cluster,
                    const EvictParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (dependent) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  }
+  cudaLaunchAttribute attr[2];   // (every kernel here waits before it touches memory)
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -712,13 +711,13 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
     return cudaSuccess;
   }));
   cudaError_t e = launch(tiles > 4 ? evict_select_kernel<8> : evict_select_kernel<4>, units * cluster, kSelThreads,
-                         static_cast<size_t>(p.cached) * kTileTokens * 4, cluster, false, p, s);
+                         static_cast<size_t>(p.cached) * kTileTokens * 4, cluster, p, s);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict_select_kernel launch: %s",
               cudaGetErrorString(e));
   if (walk)
-    e = launch(evict_walk_kernel, units * 3, kMoveThreads, 0, 1, true, p, s);
+    e = launch(evict_walk_kernel, units * 3, kMoveThreads, 0, 1, p, s);
   else
-    e = launch(evict_chunk_kernel, units * p.chunks, kMoveThreads, 0, 1, true, p, s);
+    e = launch(evict_chunk_kernel, units * p.chunks, kMoveThreads, 0, 1, p, s);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict compaction launch: %s", cudaGetErrorString(e));
   return PKV_OK;
 }

@@ -235,14 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);   // abort, tmem, bad pages [2]
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  pdl_launch_dependents();
-  // the plan's header and this CTA's items (under way while the CTA is set up)
-  const int *ctas = p.plan + plan_ctas_at(p.B);
-  int n_planned, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
-  const bool plan_ok = prefix_plan_ok(p, &n_planned);
-  i0 = uniform(plan_ok ? max(0, i0) : 0);
-  i1 = uniform(plan_ok ? min(n_planned, i1) : 0);
-  if (!plan_ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -277,6 +269,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
+  pdl_wait();
+  pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
+  // the plan's header and this CTA's items
+  const int *ctas = p.plan + plan_ctas_at(p.B);
+  int n_planned, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
+  const bool plan_ok = prefix_plan_ok(p, &n_planned);
+  i0 = uniform(plan_ok ? max(0, i0) : 0);
+  i1 = uniform(plan_ok ? min(n_planned, i1) : 0);
+  if (!plan_ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(static_cast<uint32_t>(misc[1]));
@@ -715,8 +716,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixPar
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  kern<<<p.C, kThreads, Lay<D>::kBytes, s>>>(tk, tv, p);
-  return cudaGetLastError();
+  return launch_waiting(kern, p.C, kThreads, Lay<D>::kBytes, s, tk, tv, p);
 }
 
 }  // namespace

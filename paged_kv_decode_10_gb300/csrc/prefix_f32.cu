@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_f32_kernel(const PrefixPar
   int *rows = reinterpret_cast<int *>(sm + L::kRow), *slots = rows + kRows;
   const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int *ctas = p.plan + plan_ctas_at(p.B);
   int n_items, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
   if (!prefix_plan_ok(p, &n_items)) {
@@ -215,8 +216,7 @@ cudaError_t launch(const PrefixParams &p, cudaStream_t s) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
-  kern<<<p.C, kWarps * 32, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_waiting(kern, p.C, kWarps * 32, smem, s, p);
 }
 
 }  // namespace

@@ -103,6 +103,7 @@ template <typename T, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   extern __shared__ float2 cs[];
   constexpr int VEC = 16 / static_cast<int>(sizeof(T)), kBatch = 2;
+  pdl_wait();
   const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
   const int half = p.rot >> 1, H = p.Hq + p.Hkv, heads = H + (p.slots ? p.Hkv : 0);
   const int c = threadIdx.x % p.per_head, first = threadIdx.x / p.per_head;
@@ -195,6 +196,7 @@ template <typename T, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_any_kernel(
     const __grid_constant__ RotaryParams p) {
   extern __shared__ float2 cs[];
+  pdl_wait();
   const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
   const int half = p.rot >> 1, pairs = p.d >> 1;
   const int H = p.Hq + p.Hkv, heads = H + (p.slots ? p.Hkv : 0);
@@ -238,13 +240,11 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(
 }
 
 template <typename T>
-void launch(const RotaryParams &p, bool wide, bool il, unsigned grid, size_t smem, cudaStream_t s) {
-  if (wide)
-    il ? rotary_kernel<T, true><<<grid, kThreads, smem, s>>>(p)
-       : rotary_kernel<T, false><<<grid, kThreads, smem, s>>>(p);
-  else
-    il ? rotary_any_kernel<T, true><<<grid, kThreads, smem, s>>>(p)
-       : rotary_any_kernel<T, false><<<grid, kThreads, smem, s>>>(p);
+cudaError_t launch(const RotaryParams &p, bool wide, bool il, unsigned grid, size_t smem,
+                   cudaStream_t s) {
+  auto kern = wide ? (il ? rotary_kernel<T, true> : rotary_kernel<T, false>)
+                   : (il ? rotary_any_kernel<T, true> : rotary_any_kernel<T, false>);
+  return launch_waiting(kern, grid, kThreads, smem, s, p);
 }
 
 }  // namespace
@@ -410,10 +410,8 @@ extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
   const size_t smem = static_cast<size_t>(tb) * (r.rot_dim / 2) * sizeof(float2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool il = r.layout == PKV_ROTARY_INTERLEAVED;
-  if (a->dtype == PKV_BF16)
-    launch<__nv_bfloat16>(p, wide, il, grid, smem, s);
-  else
-    launch<float>(p, wide, il, grid, smem, s);
-  PKV_LAUNCH_CHECK("rotary_kernel");
+  const cudaError_t e = a->dtype == PKV_BF16 ? launch<__nv_bfloat16>(p, wide, il, grid, smem, s)
+                                             : launch<float>(p, wide, il, grid, smem, s);
+  PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "rotary_kernel launch: %s", cudaGetErrorString(e));
   return PKV_OK;
 }

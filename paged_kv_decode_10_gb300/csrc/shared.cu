@@ -7,6 +7,9 @@
 // SMs that one leaves), the merge of the two and, with mass, the fold of the
 // scores.  Without prefixes only the second and the last.
 //
+// Each kernel is launched behind the one before as its programmatic dependent and
+// waits for it before it reads what it left.
+//
 // The merge is a kernel of its own because joining the partials in the split-KV
 // kernel's epilogue made its consumers wait, first for the prefix kernel and then
 // for chains of partial reads, while no page was streamed: that took 31 us of the
@@ -91,20 +94,6 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     if (p.lse2) p.lse2[u] = l2;
     if (p.lse_out) p.lse_out[u] = l2 * 0.6931471805599453f;
   }
-}
-
-template <typename K, typename P>
-cudaError_t launch_dependent(K kern, unsigned grid, const P &p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // ---- the weights of the own tokens --------------------------------------------
@@ -353,10 +342,10 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     const unsigned grid = static_cast<unsigned>((j.rows + per_cta - 1) / per_cta);
     const cudaError_t e =
         a->dtype == PKV_BF16
-            ? (a->d == 64 ? launch_dependent(join_kernel<__nv_bfloat16, 64>, grid, j, s)
-                          : launch_dependent(join_kernel<__nv_bfloat16, 128>, grid, j, s))
-            : (a->d == 64 ? launch_dependent(join_kernel<float, 64>, grid, j, s)
-                          : launch_dependent(join_kernel<float, 128>, grid, j, s));
+            ? (a->d == 64 ? launch_waiting(join_kernel<__nv_bfloat16, 64>, grid, 256, 0, s, j)
+                          : launch_waiting(join_kernel<__nv_bfloat16, 128>, grid, 256, 0, s, j))
+            : (a->d == 64 ? launch_waiting(join_kernel<float, 64>, grid, 256, 0, s, j)
+                          : launch_waiting(join_kernel<float, 128>, grid, 256, 0, s, j));
     PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "join kernel launch: %s", cudaGetErrorString(e));
   }
   if (a->mass) {
@@ -379,10 +368,10 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     const int most = a->B >= 64 ? 64 : 4096 / a->B;
     m.chunks = chunks < most ? chunks : most;
     const unsigned grid = static_cast<unsigned>(a->B) * m.chunks;
-    const cudaError_t e = G == 1   ? launch_dependent(mass_kernel<1>, grid, m, s)
-                          : G == 2 ? launch_dependent(mass_kernel<2>, grid, m, s)
-                          : G == 4 ? launch_dependent(mass_kernel<4>, grid, m, s)
-                                   : launch_dependent(mass_kernel<8>, grid, m, s);
+    const cudaError_t e = G == 1   ? launch_waiting(mass_kernel<1>, grid, 256, 0, s, m)
+                          : G == 2 ? launch_waiting(mass_kernel<2>, grid, 256, 0, s, m)
+                          : G == 4 ? launch_waiting(mass_kernel<4>, grid, 256, 0, s, m)
+                                   : launch_waiting(mass_kernel<8>, grid, 256, 0, s, m);
     PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "mass kernel launch: %s", cudaGetErrorString(e));
   }
   return PKV_OK;
