@@ -35,7 +35,11 @@ struct RotaryParams {
   unsigned long long turns[128];
 };
 
-// The angles of the CTA's tokens: cs [tokens][rot/2] = amplitude * (cos, sin).
+// The angles of the CTA's tokens, amplitude * (cos, sin): cs [tokens][rot/2], or with
+// VEC > 1 [tokens][VEC/2][rot/2/VEC][2], so that threads of neighbouring items (VEC
+// pairs each) read two pairs from neighbouring 16 bytes (pair after pair, eight
+// threads met in the same banks four times over).
+template <int VEC>
 __device__ __forceinline__ void fill_angles(const RotaryParams &p, float2 *cs, int t0, int nt) {
   const int half = p.rot >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -45,20 +49,22 @@ __device__ __forceinline__ void fill_angles(const RotaryParams &p, float2 *cs, i
     float s, co;
     // the signed fraction of a turn times 2 pi / 2^64
     sincosf(static_cast<float>(static_cast<long long>(ph)) * 3.4061215800865545e-19f, &s, &co);
-    cs[i] = make_float2(co * p.amplitude, s * p.amplitude);
+    const int at = VEC == 1 ? i : 2 * ((t * (VEC / 2) + c % VEC / 2) * (half / VEC) + c / VEC) + c % 2;
+    cs[at] = make_float2(co * p.amplitude, s * p.amplitude);
   }
   if (p.slots && threadIdx.x < nt && p.slots[t0 + threadIdx.x] >= p.num_slots)
     set_dev_err(p.err, PKV_DEVERR_BAD_SLOT);
 }
 
-// The pairs of one item turned in place; w holds two pairs' (cos, sin) each.
+// The pairs of one item turned in place; w[i * step] holds the (cos, sin) of pairs 2i
+// and 2i + 1.
 template <typename T, bool IL>
-__device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w) {
+__device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w, int step) {
   uint32_t *x = &a.x, *y = &b.x;
   if constexpr (sizeof(T) == 2) {   // a word holds two elements
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 c = w[i];   // pairs 2i and 2i + 1
+      const float4 c = w[i * step];
       float u1, u2, v1, v2;
       if constexpr (IL) {   // a pair is a word: the first four in a, the others in b
         uint32_t *p = i < 2 ? x + 2 * i : y + (2 * i - 4);
@@ -76,7 +82,7 @@ __device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w)
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 c = w[i];
+      const float4 c = w[i * step];
       float *p = reinterpret_cast<float *>(x), *q = reinterpret_cast<float *>(y);
       if constexpr (IL) {
         float *r = i == 0 ? p : q;
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     }
   };
   load_batch(t, h);
-  fill_angles(p, cs, t0, nt);
+  fill_angles<VEC>(p, cs, t0, nt);
   __syncthreads();
   bool again = false;
   while (t < nt) {
@@ -160,7 +166,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       if (t < nt) {
         const long long tok = t0 + t;
         if (rot && h < H)
-          rotate_item<T, IL>(a[u], b[u], reinterpret_cast<const float4 *>(cs + t * half + VEC * c));
+          rotate_item<T, IL>(a[u], b[u],
+                             reinterpret_cast<const float4 *>(cs + t * half) + c, half / VEC);
         if (h < p.Hq) {
           T *dst = static_cast<T *>(p.q_out) + tok * p.q_out_stride + h * p.d + off;
           *reinterpret_cast<uint4 *>(dst) = a[u];
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(
   const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
   const int half = p.rot >> 1, pairs = p.d >> 1;
   const int H = p.Hq + p.Hkv, heads = H + (p.slots ? p.Hkv : 0);
-  fill_angles(p, cs, t0, nt);
+  fill_angles<1>(p, cs, t0, nt);
   __syncthreads();
   for (int e = threadIdx.x; e < nt * heads * pairs; e += kThreads) {
     const int t = e / (heads * pairs), r = e - t * heads * pairs, h = r / pairs, i = r - h * pairs;

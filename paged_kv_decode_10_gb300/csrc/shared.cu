@@ -124,21 +124,28 @@ __global__ void __launch_bounds__(256, 5) mass_kernel(const MassParams p) {
   const int per_page = p.Hkv * kBlockTokens;
   bool waited = false;
   for (int j0 = chunk * kMassPages; j0 < n; j0 += p.chunks * kMassPages) {
-    const int items = min(kMassPages, n - j0) * per_page;
-    for (int e0 = threadIdx.x; e0 < items; e0 += kBatch * 256) {
+    const int j1 = min(n, j0 + kMassPages);
+    // this thread's items, 256 apart, by page and place (no division in the loop)
+    int j = j0 + threadIdx.x / per_page, r = threadIdx.x % per_page;
+    while (j < j1) {
+      int heads[kBatch];
       int at[kBatch];   // cache row of the item, -1: nothing to do
       float old[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int e = e0 + u * 256;
         at[u] = -1;
-        if (e >= items) continue;
-        const int j = j0 + e / per_page, r = e % per_page;
+        heads[u] = r / kBlockTokens;
         const int t = j * kBlockTokens + r % kBlockTokens;
-        const int blk = table[j];
-        if (t >= L || blk < 0 || blk >= p.num_blocks) continue;   // (flagged by the attention kernel)
-        at[u] = blk * per_page + r;   // (the pool has fewer than 2^31 rows)
-        old[u] = t < known ? p.decay * p.mass[at[u]] : 0.f;
+        const int blk = j < j1 ? table[j] : -1;
+        if (t < L && blk >= 0 && blk < p.num_blocks) {   // (others: flagged by the attention kernel)
+          at[u] = blk * per_page + r;   // (the pool has fewer than 2^31 rows)
+          old[u] = t < known ? p.decay * p.mass[at[u]] : 0.f;
+        }
+        r += 256;
+        while (r >= per_page) {
+          r -= per_page;
+          ++j;
+        }
       }
       if (!waited) pdl_wait();   // scores and row sums come from the kernels before this one
       waited = true;
@@ -159,8 +166,7 @@ __global__ void __launch_bounds__(256, 5) mass_kernel(const MassParams p) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (at[u] < 0) continue;
-        const int g = (e0 + u * 256) % per_page / kBlockTokens;
-        const float *l = p.lse2 + static_cast<size_t>(b) * p.Hq + g * G;
+        const float *l = p.lse2 + static_cast<size_t>(b) * p.Hq + heads[u] * G;
         float w = 0.f;
 #pragma unroll
         for (int q = 0; q < G; ++q) {
