@@ -492,11 +492,13 @@ int pkv_rotary_append(const pkv_rotary_args *args, void *stream);
  * row_prefix[b] followed by its own seq_lens[b] tokens, which are all that its
  * block table names.  Each prefix's keys and values are read once for all of its
  * rows, as matrix products over the rows' queries; the rows' own tokens go
- * through the split-KV kernel, whose epilogue merges the two by log-sum-exp:
+ * through the split-KV kernel, and the two are joined by log-sum-exp:
  *   out[b,h] = sum_t softmax_t(q_rot[b,h] . k_t * scale + bias_t) v_t
  * over t in prefix ++ own (the bias, if any, covers own tokens only; -inf, or a
- * value below -2.35e38 such as float32's lowest, excludes a token).  A row with no
- * token at all, or none that is not excluded, outputs zeros and lse = -inf.
+ * value below -2.35e38 such as float32's lowest, excludes a token, whatever its key
+ * and value hold).  A row with no token at all, or none that is not excluded, outputs
+ * zeros and lse = -inf; a query, key or value of NaN or infinity in what counts gives
+ * NaN where the formula does.
  *
  * Positions are the caller's: a row's own token i sits at position
  * prefix length + i (pkv_seq_set_offset lets the allocator count that way).
@@ -524,8 +526,9 @@ int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int3
                              int32_t bt_stride, int32_t *num_parts);
 /* Workspace of pkv_decode_attn_shared: the bytes of pkv_attn_workspace_bytes plus
  * the row sums and the partials of `slots` (0 without prefixes; max_slots above
- * serves every plan of those sizes).  Same rules: 256-byte aligned, zero-filled
- * once, calls that share it must not overlap. */
+ * serves every plan of those sizes).  Same rules: 256-byte aligned, zero-filled once
+ * for a given B and num_parts (the counters' places follow from them, so again before
+ * calls with others), calls that share it, or scores, must not overlap. */
 int pkv_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                                int32_t num_parts, int32_t slots, size_t *bytes);
 
@@ -561,8 +564,8 @@ typedef struct pkv_shared_args {
  * zero, whatever its block held before).  The weights are relative to prefix and
  * own tokens together.  A block may then belong to one row only.
  *
- * Sizes as pkv_decode_attn_split; flags: PKV_ATTN_SIMT (own tokens),
- * PKV_ATTN_CHECK_PLAN, PKV_ATTN_SHORT_WAITS.  A block id outside the pool sets
+ * Sizes as pkv_decode_attn_split; flags: PKV_ATTN_CHECK_PLAN,
+ * PKV_ATTN_SHORT_WAITS.  out must not overlap q_rot.  A block id outside the pool sets
  * PKV_DEVERR_BAD_BLOCK and its tokens are left out; plan records that do not
  * fit the call set PKV_DEVERR_BAD_PLAN and are skipped.  plan_ints, slots and
  * num_ctas are pkv_shared_plan's.

@@ -297,20 +297,30 @@ __device__ __forceinline__ void merge_store(T *out_rows, int col, int D, const M
   store4<T>(out_rows + h * D + 4 * d4, o);
 }
 
+// A joined result for storing: merge_store takes zeros for a denominator that is not
+// positive.
+__device__ __forceinline__ void keep_nan(MergeAcc &a) {
+  if (a.den == a.den) return;
+  a.den = 1.f;
+  a.acc.x = a.acc.y = a.acc.z = a.acc.w = a.M = __int_as_float(0x7fffffff);
+}
+
 // EXT: stores a column of the own tokens' result (row b, head hq of the whole row)
 // and the row sums.
 template <typename T>
-__device__ __forceinline__ void ext_store(const MergeAcc &a, const AttnParams &p, int b, int hq,
+__device__ __forceinline__ void ext_store(MergeAcc a, const AttnParams &p, int b, int hq,
                                           int d4, int D) {
   const size_t at = static_cast<size_t>(b) * p.Hq + hq;
+  const float part = part_lse(a.M, a.den);   // before NaN is spelled out
+  keep_nan(a);
   if (p.ext.own_o)
     merge_store<float>(p.ext.own_o + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D, a);
   else
     merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(b) * p.Hq * D, hq * (D / 4) + d4, D,
                    a);
   if (d4 == 0) {
-    const float l2 = a.den > 0.f ? a.M + log2f(a.den) : -INFINITY;
-    if (p.ext.lse2) p.ext.lse2[at] = l2;
+    const float l2 = part == INFINITY ? a.M : part;
+    if (p.ext.lse2) p.ext.lse2[at] = p.ext.own_o ? part : l2;
     if (p.ext.lse_out) p.ext.lse_out[at] = l2 * 0.6931471805599453f;
   }
 }
@@ -555,17 +565,27 @@ __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, ui
 #pragma unroll
   for (int e = 0; e < 4; ++e) sc[e] = (sa[e] + sb[e]) * p.scale_log2;
   // sc[0]: (token r, head 2c)  sc[1]: (r, 2c+1)  sc[2]: (r+8, 2c)  sc[3]: (r+8, 2c+1)
+  uint32_t out_lo = 0u, out_hi = 0u;   // EXT: bit 4 t: token t (t + 8) is excluded by the mask
   if (may_bias && p.bias) {
     const float *bias = p.bias + static_cast<size_t>(b) * p.bias_stride + t0;
+    bool ex0 = false, ex1 = false;
     if (r < valid) {
       const float x = bias[r] * kLog2e;
+      ex0 = x == -INFINITY;
       sc[0] += x;
       sc[1] += x;
     }
     if (r + 8 < valid) {
       const float x = bias[r + 8] * kLog2e;
+      ex1 = x == -INFINITY;
       sc[2] += x;
       sc[3] += x;
+    }
+    if constexpr (EXT) {   // whatever an excluded token holds, NaN included, does not count
+      if (ex0) sc[0] = sc[1] = -INFINITY;
+      if (ex1) sc[2] = sc[3] = -INFINITY;
+      out_lo = __ballot_sync(0xffffffffu, ex0);
+      out_hi = __ballot_sync(0xffffffffu, ex1);
     }
   }
   if (r >= valid) sc[0] = sc[1] = -INFINITY;
@@ -624,6 +644,14 @@ __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, ui
   if (valid < kBlockTokens) {
     mlo = (2 * c < valid ? 0x0000ffffu : 0u) | (2 * c + 1 < valid ? 0xffff0000u : 0u);
     mhi = (2 * c + 8 < valid ? 0x0000ffffu : 0u) | (2 * c + 9 < valid ? 0xffff0000u : 0u);
+  }
+  if constexpr (EXT) {
+    if (out_lo | out_hi) {
+      mlo &= (out_lo >> (8 * c) & 1u ? 0u : 0x0000ffffu) |
+             (out_lo >> (8 * c + 4) & 1u ? 0u : 0xffff0000u);
+      mhi &= (out_hi >> (8 * c) & 1u ? 0u : 0x0000ffffu) |
+             (out_hi >> (8 * c + 4) & 1u ? 0u : 0xffff0000u);
+    }
   }
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) {
@@ -905,10 +933,18 @@ __device__ __forceinline__ void simt_page(SimtState<T, D, G> &s, const AttnParam
   const float *bias =
       may_bias && p.bias ? p.bias + static_cast<size_t>(b) * p.bias_stride + t0 : nullptr;
   float mx = -INFINITY;
+  uint32_t out = 0u;   // EXT: tokens excluded by the mask
 #pragma unroll
   for (int i = 0; i < kBlockTokens; ++i) {
     if (i < valid) {
-      if (bias) sc[i] += bias[i] * kLog2e;
+      if (bias) {
+        const float x = bias[i] * kLog2e;
+        sc[i] += x;
+        if (EXT && x == -INFINITY) {   // whatever it holds, NaN included
+          sc[i] = -INFINITY;
+          out |= 1u << i;
+        }
+      }
     } else {
       sc[i] = -INFINITY;
     }
@@ -944,6 +980,7 @@ __device__ __forceinline__ void simt_page(SimtState<T, D, G> &s, const AttnParam
     for (int e = 0; e < DPL; ++e) s.acc[h][e] *= a;
   }
   for (int i = 0; i < valid; ++i) {
+    if (EXT && (out >> i & 1u)) continue;
     float v[DPL];
     simt_load_row<T, DPL>(vtile, i, lane, v);
 #pragma unroll
@@ -1608,7 +1645,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       o.z *= inv;
       o.w *= inv;
       if (EXT && nseg == 1) {
-        ext_store<T>(MergeAcc{den > 0.f ? M + log2f(den) : -INFINITY, den > 0.f ? 1.f : 0.f, o}, p,
+        ext_store<T>(MergeAcc{den > 0.f ? M + log2f(den) : -INFINITY, den > 0.f ? 1.f : den, o}, p,
                      u.b, u.g * gq + h, d4, D);
       } else if (nseg == 1) {
         store4<T>(static_cast<T *>(p.out) + (static_cast<size_t>(u.b) * p.Hq + u.g * gq + h) * D +
@@ -1618,7 +1655,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
         const size_t idx = static_cast<size_t>(u_idx) + blockIdx.x;
         *reinterpret_cast<float4 *>(p.o_part + (idx * gq + h) * D + 4 * d4) = o;
         if (d4 == 0)
-          p.lse_part[idx * gq + h] = den > 0.f ? M + (EXT ? log2f(den) : lg2(den)) : -INFINITY;
+          p.lse_part[idx * gq + h] =
+              EXT ? part_lse(M, den) : den > 0.f ? M + lg2(den) : -INFINITY;
       }
     }
     if (tid == 0 && j0 == 0) {

@@ -230,6 +230,25 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // (returns at once when the kernel was not launched as a dependent).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Base-2 log-sum-exp of a partial of pkv_decode_attn_shared.  NaN weights (a query,
+// key or score that is not finite) make it +inf, which makes NaN of whatever it is
+// joined with (2^(inf - inf)), as the formula does; -inf stands for no token.
+__device__ __forceinline__ float part_lse(float M, float den) {
+  return den > 0.f ? M + log2f(den) : den == 0.f ? -INFINITY : INFINITY;
+}
+
+// Whether two tensors of T rows overlap: rows of la and lb bytes, sa and sb bytes apart.
+// Rows that interleave (slices of one buffer, equal strides) do not.
+inline bool rows_overlap(const void *a, long long sa, long long la, const void *b, long long sb,
+                         long long lb, long long T) {
+  const long long a0 = reinterpret_cast<long long>(a), b0 = reinterpret_cast<long long>(b);
+  if (T <= 0 || la <= 0 || lb <= 0) return false;
+  if (a0 >= b0 + (T - 1) * sb + lb || b0 >= a0 + (T - 1) * sa + la) return false;
+  if (T == 1 || sa != sb) return true;
+  const long long off = ((b0 - a0) % sa + sa) % sa;   // of b's rows behind a's
+  return off < la || sa - off < lb;
+}
+
 // Launches a kernel that calls pdl_wait() before it touches memory: its launch
 // and set-up overlap the end of whatever kernel is ahead of it on the stream.
 template <typename... P, typename... A>

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
   __shared__ uint32_t warp_sums[kWarps];
   __shared__ uint32_t counts[kWarps][2], totals[2];
   __shared__ uint32_t bad, segment;
-  __shared__ __align__(8) uint32_t found[2]; 
+  __shared__ __align__(8) uint32_t found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank(), nc = cluster_size();
   pdl_wait();
@@ -685,6 +685,8 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
   p.row_bytes = a->d * static_cast<int>(dtype_size(a->dtype));
   const long long rows = static_cast<long long>(a->num_blocks) * a->Hkv * kBlockTokens;
   PKV_REQUIRE(rows < (1ll << 31), PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row numbers");
+  PKV_REQUIRE(!rows_overlap(a->k_cache, 0, rows * p.row_bytes, a->v_cache, 0, rows * p.row_bytes, 1),
+              PKV_ERR_INVALID_ARG, "the caches overlap");
   // CTAs per row and head: 8 steps of keys each for the longest row, and while the
   // rows are few, enough to share it out (two steps at least)
   const long long units = static_cast<long long>(a->B) * a->Hkv;
@@ -710,7 +712,8 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
     }
     return cudaSuccess;
   }));
-  cudaError_t e = launch(tiles > 4 ? evict_select_kernel<8> : evict_select_kernel<4>, units * cluster, kSelThreads,
+  cudaError_t e = launch(tiles > 4 ? evict_select_kernel<8> : evict_select_kernel<4>,
+                         units * cluster, kSelThreads,
                          static_cast<size_t>(p.cached) * kTileTokens * 4, cluster, p, s);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict_select_kernel launch: %s",
               cudaGetErrorString(e));

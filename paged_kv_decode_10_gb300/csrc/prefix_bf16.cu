@@ -458,8 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       x += tiles;
     }
-    // every product is done before tensor memory is given back
-    if (lane == 0) mma_commit(drain);
+    // every product is done before tensor memory is given back (the lane that issued
+    // them commits)
+    if (elect_one()) mma_commit(drain);
     __syncwarp();
     mbar_wait_bounded(drain, 0, kDrainCycles);
   }
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = den > 0.f ? 1.f / den : 0.f;
             w0 *= inv;
             w1 *= inv;
-            if (at >= 0) p.lse[at] = den > 0.f ? mx + log2f(den) : -INFINITY;
+            if (at >= 0) p.lse[at] = part_lse(mx, den);
           }
 #pragma unroll
           for (int q = 0; q < D / 64; ++q) {

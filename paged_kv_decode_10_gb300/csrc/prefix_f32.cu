@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_f32_kernel(const PrefixPar
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) p.o[at * D + e * 32 + lane] = st.acc[r][e] * inv;
-      if (lane == 0) p.lse[at] = sum > 0.f ? st.mx[r] + log2f(sum) : -INFINITY;
+      if (lane == 0) p.lse[at] = part_lse(st.mx[r], sum);
     }
   }
 }

@@ -348,6 +348,22 @@ extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
                    a->k_stride == a->k_out_stride),
               PKV_ERR_INVALID_ARG, "in place needs equal strides");
   const int elem = static_cast<int>(dtype_size(a->dtype));
+  {
+    // outputs may be their own inputs, and overlap nothing else
+    const long long qs = a->q_stride * elem, ks = a->k_stride * elem, vs = a->v_stride * elem,
+                    qos = a->q_out_stride * elem, kos = a->k_out_stride * elem;
+    const long long ql = qrow * elem, kl = krow * elem, vl = append ? kl : 0,
+                    kol = a->k_out ? kl : 0, T = a->T;
+    const bool clash =
+        (a->q_out != a->q && rows_overlap(a->q_out, qos, ql, a->q, qs, ql, T)) ||
+        rows_overlap(a->q_out, qos, ql, a->k, ks, kl, T) ||
+        rows_overlap(a->q_out, qos, ql, a->v, vs, vl, T) ||
+        rows_overlap(a->q_out, qos, ql, a->k_out, kos, kol, T) ||
+        (a->k_out != a->k && rows_overlap(a->k_out, kos, kol, a->k, ks, kl, T)) ||
+        rows_overlap(a->k_out, kos, kol, a->q, qs, ql, T) ||
+        rows_overlap(a->k_out, kos, kol, a->v, vs, vl, T);
+    PKV_REQUIRE(!clash, PKV_ERR_INVALID_ARG, "an output overlaps another tensor");
+  }
   const uintptr_t cache_addr =
       append ? reinterpret_cast<uintptr_t>(a->k_cache) | reinterpret_cast<uintptr_t>(a->v_cache) : 0;
   if (append) {
@@ -355,6 +371,9 @@ extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
                 "NULL append argument");
     PKV_REQUIRE(a->d * elem % 16 == 0 && cache_addr % 16 == 0, PKV_ERR_INVALID_ARG,
                 "append needs 16-byte rows and 16-byte aligned caches");
+    const long long bytes = static_cast<long long>(a->num_blocks) * kBlockTokens * krow * elem;
+    PKV_REQUIRE(!rows_overlap(a->k_cache, 0, bytes, a->v_cache, 0, bytes, 1), PKV_ERR_INVALID_ARG,
+                "the caches overlap");
   }
   uintptr_t addr = 0;
   long long strides = 0;

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     merge_acc_add<K>(a, l, v);
   }
   merge_acc_add<1>(a, l1, v1);
+  keep_nan(a);
   merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(u) * D, d4, D, a);
   if (d4 == 0) {
     const float l2 = a.den > 0.f ? a.M + log2f(a.den) : -INFINITY;
@@ -229,7 +230,11 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
   PKV_REQUIRE(a->q_rot && a->k_cache && a->v_cache && a->block_tables && a->seq_lens && a->out &&
                   a->workspace,
               PKV_ERR_INVALID_ARG, "NULL pointer");
-  PKV_REQUIRE(a->out != a->q_rot, PKV_ERR_INVALID_ARG, "out must not be q_rot");
+  const long long out_bytes =
+      static_cast<long long>(a->B) * a->Hq * a->d * static_cast<long long>(dtype_size(a->dtype));
+  PKV_REQUIRE(!rows_overlap(a->out, 0, out_bytes, a->q_rot, 0, out_bytes, 1), PKV_ERR_INVALID_ARG,
+              "out must not overlap q_rot");
+  PKV_REQUIRE(std::isfinite(a->scale), PKV_ERR_INVALID_ARG, "scale must be finite");
   PKV_REQUIRE(a->num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
   PKV_REQUIRE((reinterpret_cast<uintptr_t>(a->k_cache) & 15) == 0 &&
                   (reinterpret_cast<uintptr_t>(a->v_cache) & 15) == 0 &&
@@ -244,6 +249,8 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
   PKV_REQUIRE(!a->plan || (reinterpret_cast<uintptr_t>(a->plan) & 15) == 0, PKV_ERR_INVALID_ARG,
               "plan must be 16-byte aligned");
   PKV_REQUIRE(!a->mass || a->scores, PKV_ERR_INVALID_ARG, "mass needs the scores buffer");
+  PKV_REQUIRE(!a->mass || std::isfinite(a->mass_decay), PKV_ERR_INVALID_ARG,
+              "mass_decay must be finite");
   PKV_REQUIRE(!a->mass || (reinterpret_cast<uintptr_t>(a->scores) & 15) == 0, PKV_ERR_INVALID_ARG,
               "scores must be 16-byte aligned");
   int num_parts = a->num_parts;

@@ -220,6 +220,7 @@ def evict_ok(b):
     for f in ("k_cache", "v_cache", "mass", "block_tables", "seq_lens", "keep_lens", "kept",
               "workspace"):
         setattr(a, f, fake())
+    a.v_cache = fake(1 << 22)
     a.workspace_bytes = 1 << 30
     a.num_blocks, a.bt_stride, a.kept_stride, a.sink, a.recent = 8, 4, 16, 0, 0
     a.B, a.Hkv, a.d, a.dtype = 2, 2, 64, b.BF16
@@ -232,7 +233,8 @@ def evict_ok(b):
     ("num_blocks", 0), ("bt_stride", 0), ("kept_stride", 0), ("sink", -1), ("recent", -1),
     ("B", -1), ("B", 70000), ("Hkv", 0), ("d", 0), ("d", 4), ("d", 1024), ("dtype", 5),
     ("mass", fake((1 << 20) + 4)), ("workspace", None), ("workspace", fake((1 << 20) + 16)),
-    ("workspace_bytes", 256)])
+    ("workspace_bytes", 256), ("v_cache", fake()), ("v_cache", fake((1 << 20) + 4096)),
+    ("k_cache", fake((1 << 22) + 8 * 2 * 16 * 64 * 2 - 16))])
 def test_evict_refuses(bind, field, value):
     a = evict_ok(bind)
     setattr(a, field, value)
@@ -269,7 +271,7 @@ def shared_ok(b):
     a.num_blocks, a.bt_stride, a.n_prefixes, a.pt_stride = 8, 4, 1, 4
     a.plan_ints, a.slots, a.num_ctas = 4096, 4, 4
     a.B, a.Hq, a.Hkv, a.d, a.dtype, a.num_parts = 2, 8, 2, 64, b.BF16, 8
-    a.scale = 0.125
+    a.scale, a.mass_decay = 0.125, 1.0
     return a
 
 
@@ -282,7 +284,8 @@ def shared_ok(b):
     ("pt_stride", 0), ("bt_stride", 0), ("num_blocks", 0), ("num_blocks", 1 << 27),
     ("scores", None), ("scores", fake((1 << 20) + 4)), ("flags", 1), ("flags", 2), ("flags", 4),
     ("attn_bias", fake()), ("Hq", 7), ("Hq", 6), ("Hkv", 0), ("d", 96), ("dtype", 3), ("B", 70000),
-    ("num_parts", 5000)])
+    ("num_parts", 5000), ("out", fake((1 << 20) + 2 * 8 * 64 * 2 - 16)), ("scale", float("nan")),
+    ("scale", float("inf")), ("mass_decay", float("nan"))])
 def test_shared_attention_refuses(bind, field, value):
     a = shared_ok(bind)
     setattr(a, field, value)
@@ -299,8 +302,9 @@ def rotary_ok(b):
     KEEP.append(r)
     a = b.RotaryArgs()
     a.rotary = ctypes.pointer(r.table)
-    for f in ("q", "k", "v", "q_out", "k_out", "positions", "slot_mapping", "k_cache", "v_cache"):
-        setattr(a, f, fake())
+    for i, f in enumerate(("q", "k", "v", "positions", "slot_mapping", "k_cache", "v_cache")):
+        setattr(a, f, fake(1 + i << 20))
+    a.q_out, a.k_out = a.q, a.k
     a.q_stride = a.q_out_stride = 8 * 64
     a.k_stride = a.v_stride = a.k_out_stride = 2 * 64
     a.num_blocks, a.T, a.Hq, a.Hkv, a.d, a.dtype = 8, 4, 8, 2, 64, b.BF16
@@ -312,13 +316,37 @@ def rotary_ok(b):
     ("k_cache", None), ("v_cache", None), ("k_cache", fake((1 << 20) + 8)), ("d", 128),
     ("dtype", 9), ("T", -1), ("Hq", -1), ("Hkv", -1), ("q_stride", 64), ("k_stride", 64),
     ("v_stride", 64), ("k_out_stride", 64), ("q_stride", 1024), ("q", fake((1 << 20) + 1)),
-    ("num_blocks", -1), ("Hq", 1 << 20)])
+    ("num_blocks", -1), ("Hq", 1 << 20),
+    # outputs over other tensors, or over their own inputs but not in place
+    ("q_out", fake(2 << 20)), ("q_out", fake(3 << 20)), ("k_out", fake(1 << 20)),
+    ("k_out", fake(3 << 20)), ("q_out", fake((1 << 20) + 1024)), ("q_out", fake((1 << 20) - 1024)),
+    ("k_out", fake((2 << 20) + 16)), ("k", fake((1 << 20) + 4096 - 16)), ("v_cache", fake(6 << 20)),
+    ("k_cache", fake((7 << 20) + 16))])
 def test_rotary_append_refuses(bind, field, value):
     a = rotary_ok(bind)
     setattr(a, field, value)
     assert bind.load().pkv_rotary_append(ctypes.byref(a), None) in (bind.ERR_INVALID_ARG,
                                                                     bind.ERR_UNSUPPORTED)
     assert bind.load().pkv_last_error()
+
+
+def test_rotary_append_tells_interleaved_rows_from_overlapping_ones(bind):
+    """q, k and v as slices of one projection's output, q rotated where it lies: refused
+    only from the step on at which a slice reaches the next (by the argument that is
+    checked after the overlaps: there is nothing to launch on)."""
+    def why(k_at, T=4, hq=8, row=768):
+        a = rotary_ok(bind)
+        a.T, a.Hq = T, hq
+        a.q = a.q_out = fake(1 << 20)
+        a.k, a.v = fake((1 << 20) + 2 * k_at), fake((1 << 20) + 2 * (k_at + 128))
+        a.k_out = fake(9 << 20)
+        a.q_stride = a.q_out_stride = a.k_stride = a.v_stride = row
+        a.d, a.num_blocks = 64, -1
+        assert bind.load().pkv_rotary_append(ctypes.byref(a), None) == bind.ERR_INVALID_ARG
+        return bind.load().pkv_last_error().decode()
+    assert "append" in why(512) and "append" in why(512 + 768) and "append" in why(512, T=1)
+    assert "overlap" in why(504) and "overlap" in why(520) and "overlap" in why(504, T=1)
+    assert "overlap" in why(512 + 768 - 8)
 
 
 def test_rotary_append_needs_an_initialised_table(bind):

@@ -540,3 +540,198 @@ def test_evict_in_a_graph():
     torch.cuda.synchronize()
     for x, y in zip([c[k] for k in ("kc", "vc", "mass")] + [kept], want):
         assert torch.equal(x, y)
+
+
+def test_evict_behind_tables_for_millions_of_tokens():
+    """The launch follows the tables' width, not the rows' lengths."""
+    c = evict_case(1, 2, 64, "bf16", [70], [33], 23)
+    wide = np.full((1, 1 << 17), -1, np.int32)
+    wide[:, :c["tab"].shape[1]] = c["tab"]
+    check_evict(dict(c, tab=wide), 2, 5, 40)
+
+
+# --------------------------------------------------------------------------- where it can go wrong
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("plens", [[], [64]])
+@pytest.mark.parametrize("parts", [None, 7])
+def test_excluded_tokens_may_hold_anything(dtype, plens, parts):
+    lens = [40, 33, 1, 16, 100]
+    c = make_case(5, 8, 2, 64, dtype, lens, plens, [0, -1, 0, 0, 0], 71, bias=True, mass=True)
+    rng = np.random.default_rng(5)
+    mass0 = f64(c["mass"])
+    for b, n in enumerate(lens):
+        x = excluded(c["bias"])[b, :n]
+        for t in np.flatnonzero(np.isneginf(x)):
+            for cache in (c["kc"], c["vc"]):
+                cache[int(c["tab"][b, t // 16]), :, t % 16] = \
+                    float(rng.choice([np.nan, np.inf, -np.inf]))
+    out, lse, err, _ = run_case(c, num_parts=parts)
+    # (the oracle multiplies what is excluded by zero: it gets zeros there)
+    for cache in ("kc", "vc"):
+        c[cache] = torch.nan_to_num(c[cache], 0.0, 0.0, 0.0)
+    check_case(c, out, lse, mass0, err=err)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows_of", [1, 24])
+@pytest.mark.parametrize("parts", [None, 7])
+def test_nan_spreads_as_in_the_formula(dtype, rows_of, parts):
+    """NaN or infinity in what counts: the rows (heads, columns) that the formula makes NaN
+    are NaN, and no others change."""
+    B, Hq, Hkv, d, G = 6 * rows_of, 8, 2, 64, 4
+    lens, rows = [40, 0, 100, 33, 5, 20] * rows_of, [0, 0, 1, -1, 1, 0] * rows_of
+    c = make_case(B, Hq, Hkv, d, dtype, lens, [300, 50], rows, 81, mass=True)
+    before = {k: c[k].clone() for k in ("q", "kc", "vc", "mass")}
+    want, want_lse, err, _ = run_case(c, num_parts=parts)
+    want_mass = c["mass"].clone()
+    nan = torch.zeros((B, Hq, d), dtype=torch.bool)
+    c["mass"].copy_(before["mass"])
+    c["q"][0, 1] = float("nan")                                    # a query head, prefix and own
+    nan[0, 1] = True
+    c["q"][1, 6, 3] = float("inf")                                 # a row with a prefix alone
+    nan[1, 6] = True
+    c["kc"][int(c["tab"][3, 1]), 0, 2, 5] = float("nan")           # own key, KV head 0
+    nan[3, :G] = True
+    c["kc"][int(c["ptab"][1, 2]), 1, 7, 0] = float("nan")          # key of prefix 1, KV head 1
+    nan[torch.tensor(rows) == 1, G:] = True
+    c["vc"][int(c["ptab"][0, 0]), 0, 0, 9] = float("inf")          # value of prefix 0: no NaN
+    c["vc"][int(c["tab"][5, 0]), 1, 3, 8] = float("nan")           # own value: one column
+    nan[5, G:, 8] = True
+    inf = torch.zeros_like(nan)
+    inf[torch.tensor(rows) == 0, :G, 9] = True
+    out, lse, err, _ = run_case(c, num_parts=parts)
+    assert err == 0
+    o, w = out.float().cpu(), want.float().cpu()
+    inf &= ~nan
+    assert torch.equal(o.isnan(), nan)
+    assert (o[inf] == float("inf")).all()
+    assert torch.equal(o[~nan & ~inf], w[~nan & ~inf])
+    whole = nan.all(-1)
+    assert torch.equal(lse.isnan().cpu(), whole)
+    assert torch.equal(lse.cpu()[~whole], want_lse.cpu()[~whole])
+    # weights: those of a KV head with a NaN query head or key are NaN, the others are as before
+    heads = whole.view(B, Hkv, G).any(-1)
+    for b in range(B):
+        for t in range(0, lens[b]):
+            at = (int(c["tab"][b, t // 16]), slice(None), t % 16)
+            got, old = c["mass"][at].cpu(), want_mass[at].cpu()
+            assert torch.equal(got.isnan(), heads[b]) and torch.equal(got[~heads[b]], old[~heads[b]])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prefix_waits_that_give_up_report_a_timeout(dtype):
+    """Waits of 64 clocks end long before a copy lands: the call flags it, ends, and after the
+    workspace is zero-filled again the next call is exact."""
+    c = make_case(9, 8, 2, 128, dtype, [40, 3, 0, 17, 90, 1, 64, 200, 33], [1000, 130],
+                  [i % 3 - 1 for i in range(9)], 91)
+    want, want_lse, err, a = run_case(c)
+    assert err == 0
+    space = torch.zeros(a.workspace_bytes, dtype=torch.uint8, device=dev())
+    out, lse, err, b = run_case(c, workspace=space, flags=binding.ATTN_SHORT_WAITS)
+    assert err & binding.DEVERR_TIMEOUT and not err & ~binding.DEVERR_TIMEOUT
+    space.zero_()
+    out, lse, err, _ = run_case(c, workspace=space)
+    assert err == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_a_captured_call_follows_the_plan_in_its_buffer():
+    """One graph, a plan buffer and a workspace for the largest plan of its sizes: new
+    prefixes of the rows and new lengths go in by overwriting the buffers."""
+    B, Hq, Hkv, d, P = 12, 8, 2, 64, 3
+    c = make_case(B, Hq, Hkv, d, "bf16", [50 - 4 * i for i in range(B)], [700, 90, 300], [0] * B, 95)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cap, most = binding.shared_plan_cap(B, P, Hq, Hkv, sms)
+    buf, lens = torch.zeros(cap, dtype=torch.int32, device=dev()), i32(c["lens"])
+    ptab = torch.from_numpy(c["ptab"]).to(dev())
+    out, lse = torch.empty_like(c["q"]), torch.empty((B, Hq), device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    a = binding.make_shared_args(c["q"], c["kc"], c["vc"], torch.from_numpy(c["tab"]).to(dev()), lens,
+                                 c["scale"], out, prefix_tables=ptab, prefix_plan=buf, slots=most,
+                                 num_ctas=sms, lse=lse, err=err)
+
+    def put(rows, plens, own):
+        plan = binding.shared_plan(rows, plens, Hq, Hkv, d, binding.BF16, sms)
+        buf.zero_()
+        buf[:len(plan)].copy_(torch.from_numpy(plan))
+        lens.copy_(i32(own))
+        c.update(rows=rows, plens=plens, lens=np.asarray(own))
+
+    put([0] * B, [700, 90, 300], c["lens"])
+    binding.decode_attn_shared_args(a)
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        binding.decode_attn_shared_args(a, side)
+    for rows, plens, own in (([0] * B, [700, 90, 300], c["lens"].tolist()),
+                             ([i % 3 for i in range(B)], [700, 90, 300], [0] * B),
+                             ([i % 4 - 1 for i in range(B)], [160, 90, 0], [1] * B),
+                             ([-1] * B, [700, 90, 300], [3] * B)):
+        put(rows, plens, own)
+        out.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check_case(c, out, lse, err=int(err))
+
+
+def test_caches_beyond_32_bit_offsets():
+    """Blocks whose elements and bytes lie behind 2^32: append, attention, weights, eviction."""
+    Hq, Hkv, d, dtype = 16, 8, 128, "bf16"
+    nb = (1 << 32) // (Hkv * 16 * d) + 64                  # 2^32 elements: 8.6 GB a cache
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    rng = np.random.default_rng(7)
+    high = list(nb - 1 - rng.permutation(60))
+    kc = torch.empty((nb, Hkv, 16, d), dtype=TD[dtype], device=dev())
+    vc = torch.empty_like(kc)
+    mass = torch.empty((nb, Hkv, 16), device=dev())
+    n, plen = 200, 300
+    ptab = np.array([[high.pop() for _ in range(19)]], np.int32)
+    tab = np.array([[high.pop() for _ in range(13)]], np.int32)
+    rot = binding.Rotary(d)
+    kv = [normal((n + plen, Hkv, d), dtype, 1), normal((n + plen, Hkv, d), dtype, 2)]
+    pos = np.arange(n + plen)
+    slots = np.concatenate([ptab[0][np.arange(plen) // 16].astype(np.int64) * 16 + np.arange(plen) % 16,
+                            tab[0][np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16])
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    _, k_rot = binding.rotary_append(rot, None, kv[0], kv[1], i32(pos), torch.from_numpy(slots).to(dev()),
+                                     kc, vc, err=err)
+    q = normal((1, Hq, d), dtype, 3)
+    # the same in small caches
+    small = dict(B=1, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, lens=np.array([n]), plens=[plen], rows=[0],
+                 nb=32, ptab=np.arange(19, dtype=np.int32)[None],
+                 tab=np.arange(19, 32, dtype=np.int32)[None], q=q, scale=d**-0.5, bias=None)
+    used = torch.from_numpy(np.concatenate([ptab[0], tab[0]]).astype(np.int64)).to(dev())
+    small["kc"], small["vc"] = kc[used], vc[used]
+    for x, src in ((small["kc"], k_rot), (small["vc"], kv[1])):
+        flat = x.transpose(1, 2).reshape(32 * 16, Hkv, d)
+        assert torch.equal(flat[:plen], src[:plen]) and torch.equal(flat[304:304 + n], src[plen:])
+    out, lse = torch.empty_like(q), torch.empty((1, Hq), device=dev())
+    plan = torch.from_numpy(binding.shared_plan([0], [plen], Hq, Hkv, d, binding.BF16)).to(dev())
+    scores = binding.alloc_scores(nb, Hq)
+    a = binding.make_shared_args(q, kc, vc, torch.from_numpy(tab).to(dev()), i32([n]), d**-0.5, out,
+                                 prefix_tables=torch.from_numpy(ptab).to(dev()), prefix_plan=plan,
+                                 mass=mass, scores=scores, mass_lens=i32([0]), lse=lse, err=err)
+    binding.decode_attn_shared_args(a)
+    torch.cuda.synchronize()
+    small["mass"], small["known"] = mass[used], [0]
+    unused = np.zeros((32, Hkv, 16))
+    m = f64(small["mass"])
+    own = np.zeros((32, 16), bool)
+    t = np.arange(n)
+    own[19 + t // 16, t % 16] = True
+    m[~own[:, None, :].repeat(Hkv, 1)] = 0
+    small["mass"] = torch.from_numpy(m)
+    check_case(small, out, lse, unused, err=int(err))
+    big = [bits(x[used]) for x in (kc, vc, mass)]
+    kept = binding.evict(kc, vc, mass, torch.from_numpy(tab).to(dev()), i32([n]), i32([90]), 90, 3, 10,
+                         err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    src = kept.cpu().numpy()[0]
+    new = [x.copy() for x in big]
+    j = np.arange(90)
+    for g in range(Hkv):
+        for x, o in zip(new, big):
+            x[19 + j // 16, g, j % 16] = o[19 + src[g] // 16, g, src[g] % 16]
+    for x, y in zip(new, (kc, vc, mass)):
+        np.testing.assert_array_equal(x, bits(y[used]))
