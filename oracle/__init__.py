@@ -31,7 +31,10 @@ Modules
 ``step``       one whole decode step (RoPE, slot append, attention) and the
                joiners' prefix write (RoPE of each prefix key, slot write).
 ``dense``      the right-padded dense batch: assemble, extract a row, gap mask.
+``cache_ops``  rotary layouts and scalings, attention over shared prefixes with
+               the weights of the own tokens, eviction by those weights.
 
-Every function is pinned by tests in ``tests/test_oracle_pins.py`` against
-closed forms, hand-worked values, library routines or brute force.
+Every function is pinned by tests in ``tests/test_oracle_pins.py`` (``cache_ops``:
+``tests/test_oracle_cache_ops.py``) against closed forms, hand-worked values,
+library routines or brute force.
 """

@@ -102,9 +102,9 @@ __device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w,
 // per_head items; a thread keeps its item number c within the head and goes through
 // the CTA's (token, head) pairs kThreads / per_head at a time, kBatch of them with
 // their loads in flight together; the first batch's go out before the angles are
-// formed.  Two pairs at a time and more CTAs on an SM beat four (72 against 76 us for
-// 16384 tokens of 32 + 8 heads of 128 in bf16, whole heads turned: 5.6 TB/s; float32
-// 121 us, 6.7 TB/s).
+// formed.  16384 tokens of 32 + 8 heads of 128 in bf16, whole heads turned: 64 us, 6.3
+// TB/s (float32 121 us, 6.7 TB/s); four pairs at a time, with fewer CTAs on an SM, took
+// 5 % longer.
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   extern __shared__ float2 cs[];
