@@ -901,6 +901,23 @@ def make_rotary_args(rotary, q, k, v, positions, q_out=None, k_out=None, slot_ma
                             v_cache, err))
 
 
+def set_rotary_inputs(layers, q, k, v):
+    """Puts ``q [L,T,Hq,d]``, ``k``, ``v [L,T,Hkv,d]`` into prepared ``RotaryArgs``, one per
+    layer, made for inputs of the same shapes, type and device (all three of them)."""
+    for x, name, at in ((q, "q", 1), (k, "k", 2), (v, "v", 3)):
+        old = layers[0].keep[at]
+        if x.dim() != 4 or x.shape[0] != len(layers) or x.shape[1:] != old.shape:
+            raise PkvError(ERR_INVALID_ARG, f"{name}: shape {tuple(x.shape)}, the calls were made for "
+                                            f"{len(layers)} x {tuple(old.shape)}")
+        first, stride = _heads(x[0], name, old.shape[0], old.shape[2], old.dtype, old.device)
+        addr, step = first.value or 0, x.stride(0) * x.element_size()
+        for i, a in enumerate(layers):
+            setattr(a, name, addr + i * step)
+            setattr(a, name + "_stride", stride)
+    for a in layers:
+        a.inputs = (q, k, v)
+
+
 def rotary_append_args(args, stream=None):
     """Runs ``pkv_rotary_append`` from prepared ``RotaryArgs``."""
     _check(load().pkv_rotary_append(ctypes.byref(args), _launch_on(args, stream)))

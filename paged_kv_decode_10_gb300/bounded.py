@@ -62,10 +62,12 @@ class BoundedDecoder(PagedDecoder):
         self._prefix_of = {}     # sequence id -> prefix id or None
         self._prefixes = {}      # prefix id (a sequence of the allocator) -> tokens
         self._known = {}         # sequence id -> leading own tokens whose weight is known
+        self._held = {}          # sequence id -> own tokens
         self._plan_key = None
+        self._rows_now = None    # sequences of the last step (None: their prefixes may have changed)
         self._prefix_args = {}
         self._space = None
-        self._rows_now = []
+        self._calls = {}         # metadata buffer -> prepared calls of every layer, for this plan
 
     def _on(self, stream):
         """The stream of a call as torch's current one, so that the call's copies and
@@ -114,7 +116,7 @@ class BoundedDecoder(PagedDecoder):
             raise ValueError(f"prefix {pid} is in use")
         self.alloc.leave(pid)
         del self._prefixes[pid]
-        self._plan_key = None    # (the id may come back as another prefix)
+        self._plan_key = self._rows_now = None    # (the id may come back as another prefix)
 
     def join(self, prefix_len=0, prefix=None, k=None, v=None, stream=None):
         """A new sequence behind ``prefix`` (an id of ``add_prefix``, or None) with
@@ -138,14 +140,16 @@ class BoundedDecoder(PagedDecoder):
         except Exception:
             self.alloc.leave(sid)
             raise
-        self._prefix_of[sid], self._known[sid] = prefix, 0
+        self._prefix_of[sid], self._known[sid], self._held[sid] = prefix, 0, int(prefix_len)
+        self._rows_now = None
         return sid
 
     def leave(self, seq_id):
         if seq_id not in self._prefix_of:
             raise binding.UnknownSequence(binding.ERR_UNKNOWN_SEQ, f"sequence {seq_id} is not live")
         self.alloc.leave(seq_id)
-        del self._prefix_of[seq_id], self._known[seq_id]
+        del self._prefix_of[seq_id], self._known[seq_id], self._held[seq_id]
+        self._rows_now = None
 
     # -- eviction -------------------------------------------------------------------
     def evict(self, seq_ids, keep=None, stream=None):
@@ -169,7 +173,7 @@ class BoundedDecoder(PagedDecoder):
                           device=self.device)
         if n == 0:
             return kept
-        lens = np.array([self.alloc.seq_len(s) for s in seq_ids], np.int32)
+        lens = np.array([self._held[s] for s in seq_ids], np.int32)
         blocks = [self.alloc.seq_blocks(s) for s in seq_ids]
         tables = np.full((n, max(1, max(len(b) for b in blocks))), -1, np.int32)
         for i, b in enumerate(blocks):
@@ -189,7 +193,7 @@ class BoundedDecoder(PagedDecoder):
                 kept[layer], self.sink, self.recent, err=self.err))
         self.alloc.evict_many(seq_ids, np.full(n, keep, np.int32))
         for s in seq_ids:
-            self._known[s] = min(self._known[s], keep)
+            self._known[s], self._held[s] = min(self._known[s], keep), min(self._held[s], keep)
         return kept
 
     # -- the step -------------------------------------------------------------------
@@ -197,10 +201,13 @@ class BoundedDecoder(PagedDecoder):
         """Plan, prefix tables and workspace for these rows (kept while the rows'
         prefixes stay the same)."""
         torch = self.torch
+        if seq_ids == self._rows_now:
+            return
         rows = tuple(self._prefix_of[s] for s in seq_ids)
         used = sorted({p for p in rows if p is not None and self._prefixes[p] > 0})
         key = (rows, tuple(used))
         if key == self._plan_key:
+            self._rows_now = seq_ids
             return
         slots, self._prefix_args = 0, {}
         if used:
@@ -221,7 +228,24 @@ class BoundedDecoder(PagedDecoder):
         # a workspace of these rows' own, zero-filled once: the counters' place in it
         # depends on the number of rows
         self._space = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        self._plan_key = key
+        self._plan_key, self._calls, self._rows_now = key, {}, seq_ids
+
+    def _prepared(self, B, q, k, v):
+        """The calls of every layer on the metadata buffer of this step, made once for
+        each buffer and plan; the step's own tensors are put in by ``_launch``."""
+        key = self.positions.data_ptr()     # (one of the decoder's own buffers)
+        if key not in self._calls:
+            self._calls[key] = [(binding.make_rotary_args(
+                self.rotary, q[layer], k[layer], v[layer], self.positions,
+                q_out=self.q_rots[layer, :B], k_out=self.k_rots[layer, :B],
+                slot_mapping=self.slots, k_cache=self.k_caches[layer],
+                v_cache=self.v_caches[layer], err=self.err), binding.make_shared_args(
+                self.q_rots[layer, :B], self.k_caches[layer], self.v_caches[layer], self.tables,
+                self.seq_lens, self.scale, self.outs[layer, :B], mass=self.masses[layer],
+                scores=self.scores, decay=self.decay, plan=self.plan, num_parts=self.num_parts,
+                workspace=self._space, err=self.err, **self._prefix_args))
+                for layer in range(self.n_layers)]
+        return self._calls[key]
 
     def _launch(self, B, q, k, v, attn_bias, stream):
         torch = self.torch
@@ -232,18 +256,12 @@ class BoundedDecoder(PagedDecoder):
         fresh = None
         if not np.array_equal(known, lens - 1):
             fresh = torch.from_numpy(known).to(self.device)
-        for layer in range(self.n_layers):
-            binding.rotary_append_args(binding.make_rotary_args(
-                self.rotary, q[layer], k[layer], v[layer], self.positions,
-                q_out=self.q_rots[layer, :B], k_out=self.k_rots[layer, :B],
-                slot_mapping=self.slots, k_cache=self.k_caches[layer],
-                v_cache=self.v_caches[layer], err=self.err))
-            binding.decode_attn_shared_args(binding.make_shared_args(
-                self.q_rots[layer, :B], self.k_caches[layer], self.v_caches[layer], self.tables,
-                self.seq_lens, self.scale, self.outs[layer, :B], mass=self.masses[layer],
-                scores=self.scores, mass_lens=fresh, decay=self.decay, plan=self.plan,
-                num_parts=self.num_parts, workspace=self._space, err=self.err,
-                **self._prefix_args))
+        calls = self._prepared(B, q, k, v)
+        binding.set_rotary_inputs([rotary for rotary, _ in calls], q, k, v)
+        for rotary, attend in calls:
+            attend.mass_lens = None if fresh is None else fresh.data_ptr()
+            binding.rotary_append_args(rotary, stream)
+            binding.decode_attn_shared_args(attend, stream)
 
     def step(self, seq_ids, q, k, v, attn_bias=None, stream=None):
         """One decode step for the listed sequences (cutting back those at their bound
@@ -270,14 +288,18 @@ class BoundedDecoder(PagedDecoder):
         torch = self.torch
         run = stream if stream is not None else torch.cuda.current_stream(self.device)
         with torch.cuda.stream(run):   # (copies and launches in one order)
-            full = [s for s in seq_ids if self.alloc.seq_len(s) >= self.budget + self.slack]
+            full = [s for s in seq_ids if self._held[s] >= self.budget + self.slack]
             if full:
                 self.evict(full)
             self._prefix_state(seq_ids)
-            self._rows_now = seq_ids
-            out = super().step(seq_ids, q, k, v, None, run)
-        for s, n in zip(seq_ids, self.last_metadata[2]):
-            self._known[s] = int(n)
+            try:
+                out = super().step(seq_ids, q, k, v, None, run)
+            except Exception:
+                for s in seq_ids:
+                    self._held[s] = self.alloc.seq_len(s)
+                raise
+        for s, n in zip(seq_ids, self.last_metadata[2].tolist()):
+            self._known[s] = self._held[s] = n
         return out
 
     def capture(self, *args, **kw):

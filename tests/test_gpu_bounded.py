@@ -249,3 +249,66 @@ def test_eviction_before_the_first_step_on_another_stream():
     assert kept[0, 0].tolist() == [list(range(8)) + [29, 30]] * 2
     assert dec.alloc.seq_len(s) == 11 and int(dec.last_metadata[0][0]) == 31
     assert bool(out.float().isfinite().all()) and dec.device_errors() == 0
+
+
+def test_a_step_that_runs_out_of_blocks_changes_nothing():
+    """Blocks for two of three rows: the step raises, and runs after a sequence has left."""
+    dec = BoundedDecoder(5, 4, 2, 64, "f32", 3, 40, 8, device=dev())
+    draw = (workloads.normal((16, 2, 64), "f32", i).to(dev()) for i in range(8))
+    ids = [dec.join(n, None, next(draw)[:n], next(draw)[:n]) for n in (16, 16, 4)]
+    x = [workloads.normal((3, h, 64), "f32", 20 + h + i).to(dev()) for i, h in enumerate((4, 2, 2))]
+    first = [t[2:] for t in x]
+    with pytest.raises(binding.OutOfBlocks):
+        for _ in range(40):
+            dec.step(ids, *x)
+    lens = [dec.alloc.seq_len(s) for s in ids]
+    assert lens[0] == lens[1] == 32 and lens[2] == 20 or max(lens) <= 48
+    assert lens == [dec._held[s] for s in ids]
+    dec.leave(ids[0])
+    out = dec.step(ids[1:], *(t[1:] for t in x)).clone()
+    # the same sequence alone, whole
+    ref = BoundedDecoder(5, 4, 2, 64, "f32", 3, 40, 8, device=dev())
+    draw = [workloads.normal((16, 2, 64), "f32", i).to(dev()) for i in (4, 5)]
+    one = ref.join(4, None, draw[0][:4], draw[1][:4])
+    for _ in range(lens[2] - 4 + 1):
+        want = ref.step([one], *first)
+    torch.cuda.synchronize()
+    assert dec.device_errors() == 0
+    torch.testing.assert_close(out[1], want[0], rtol=2.0**-18, atol=2.0**-18)
+
+
+def test_steps_in_other_orders_reuse_prepared_calls():
+    """The same batch in either order, strided inputs, and one metadata buffer in turn after
+    the other give each row the same output as a batch of its own."""
+    made = []
+    for metadata in ("copy", "mapped"):
+        dec = BoundedDecoder(40, 8, 2, 64, "bf16", 4, 24, 8, device=dev(), metadata=metadata)
+        x = workloads.normal((40, 2, 64), "bf16", 1).to(dev())
+        p = dec.add_prefix(x, x.flip(0))
+        ids = [dec.join(prefix=p), dec.join(), dec.join(5, p, x[:5], x[5:10])]
+        outs = []
+        for step in range(9):
+            qkv = workloads.normal((3, 12, 64), "bf16", 50 + step).to(dev())
+            order = [0, 1, 2] if step % 2 else [2, 0, 1]
+            if step == 6:
+                order = [1]
+            rows = qkv[torch.tensor(order, device=dev())]
+            if step % 3 == 0:       # slices of one projection's output
+                q, k, v = rows[:, :8], rows[:, 8:10], rows[:, 10:]
+            else:
+                q, k, v = (t.contiguous() for t in (rows[:, :8], rows[:, 8:10], rows[:, 10:]))
+            out = dec.step([ids[i] for i in order], q, k, v)
+            outs.append({i: out[b].clone() for b, i in enumerate(order)})
+        torch.cuda.synchronize()
+        assert dec.device_errors() == 0
+        made.append(outs)
+    for a, b in zip(*made):
+        for i in a:
+            assert torch.equal(a[i], b[i])
+    # sequence 1 alone
+    dec = BoundedDecoder(40, 8, 2, 64, "bf16", 1, 24, 8, device=dev())
+    s = dec.join()
+    for step in range(9):
+        qkv = workloads.normal((3, 12, 64), "bf16", 50 + step).to(dev())[1:2]
+        out = dec.step([s], qkv[:, :8], qkv[:, 8:10], qkv[:, 10:])
+        torch.testing.assert_close(out[0].float(), made[0][step][1].float(), rtol=2.0**-6, atol=2.0**-6)
