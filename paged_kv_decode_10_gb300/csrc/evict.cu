@@ -23,9 +23,10 @@
 //    chunks, earlier ones or itself: a chunk waits for two flags (the choice notes how
 //    many kept tokens lie below each chunk's first slot, which names them).  Chunks are taken
 //    by ticket in order and reading never waits, so every wait ends.
-// Both are memory bound: each kept row is read and written once.  The walk needs
+//  * Short rows: one CTA chooses and compacts (evict_small_kernel).
+// The first two are memory bound: each kept row is read and written once.  The walk needs
 // no flags and keeps its steps back to back (64 rows of 8 heads, 1500..2600 tokens of 128
-// down to 1024, bf16: 87 us, 5.4 TB/s, against 150 us in chunks, the choice before it
+// down to 1024, bf16: 80 us, 5.8 TB/s, against 150 us in chunks, the choice before it
 // 17 us); with 4 (row, head) pairs it leaves the GPU empty (131072 tokens down to 32768:
 // 130 us against 31 us in chunks, the choice 23 us).
 #include <cstdint>
@@ -43,7 +44,8 @@ constexpr int kMaxCluster = 16, kMaxCached = 48;   // CTAs, steps (of 4 KB of ke
 constexpr int kMoveThreads = 256;
 constexpr int kMoveVecs = 4;                       // 16-byte pieces of K (and of V) a thread moves
 constexpr int kChunkBytes = kMoveThreads * kMoveVecs * 16;
-constexpr int kWalkVecs = 8;                       // pieces a walking thread has in flight
+constexpr int kWalkVecs = 4;                       // pieces of a walking thread's step
+constexpr int kWalkTokens = 1024;                  // tokens of its list
 constexpr int kChunkUnits = 76;                    // (row, head) pairs from which rows are walked
 constexpr long long kWaitCycles = 1ll << 31;
 
@@ -399,70 +401,190 @@ __global__ void __launch_bounds__(kSelThreads, kRead > 4 ? 2 : 4)
   if (nc > 1) cluster_sync();   // a CTA's shared memory outlives its readers
 }
 
+// Rows of up to NT tokens: choice and compaction by one CTA per (row, KV head), a token
+// a thread.  A candidate stays if fewer than m candidates come before it in order of
+// weight (ties: of index), which a thread counts over all keys in shared memory; the
+// places follow from a scan of the ballots.  Every weight is in a register and every
+// step's keys and values are read before anything is written where they lay.  Bound by
+// latency and, for many rows, by the keys' n^2 comparisons.  8 heads of 128 in bf16, half
+// kept: 1 row of 256 tokens 5.5 us (choice and compaction apart 11.3), 64 rows 11.5
+// (19.9); 512 tokens: 1 row 10.0 (12.6), 64 rows 31.5 (29.1).
+template <int NT>
+__global__ void __launch_bounds__(NT) evict_small_kernel(const EvictParams p) {
+  __shared__ __align__(16) uint32_t keys[NT];
+  __shared__ int table_s[NT / kBlockTokens], from_s[NT];
+  __shared__ int counts[NT / 32];
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = blockIdx.x, b = u / p.Hkv, g = u - b * p.Hkv;
+  const int L = p.seq_lens[b], K = p.keep_lens[b];
+  int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
+  const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
+  const bool bad_len = L < 0 || K < 0 || L > kBlockTokens * p.bt_stride ||
+                       min(L, K) > p.kept_stride;
+  const int len = bad_len ? 0 : L;   // (at most NT)
+  const int blk = tid < len ? table[tid >> 4] : -1;
+  const bool there = blk >= 0 && blk < p.num_blocks;
+  const bool skip = __syncthreads_or(tid < len && !there) || bad_len;
+  if (skip && tid == 0 && g == 0)
+    set_dev_err(p.err, bad_len ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_BLOCK);
+  const int n = skip ? 0 : min(L, K);
+  for (int j = n + tid; j < p.kept_stride; j += NT) kept[j] = -1;
+  if (skip || L <= K) {
+    if (tid < n) kept[tid] = tid;
+    return;
+  }
+  const int n_recent = min(p.recent, K), n_sink = min(p.sink, K - n_recent);
+  const int c0 = n_sink, c1 = L - n_recent;            // candidates [c0, c1)
+  const int m = K - n_recent - n_sink;                 // of which m stay
+  const int row = there ? (blk * p.Hkv + g) * kBlockTokens + (tid & 15) : 0;
+  const float x = there ? p.mass[row] : 0.f;
+  const bool candidate = tid >= c0 && tid < c1;
+  const uint32_t key = candidate ? mass_key(x) : 0u;
+  keys[tid] = key;
+  if (there && (tid & 15) == 0) table_s[tid >> 4] = blk;
+  __syncthreads();
+  // rank: keys ahead of this warp's count from equal on, those behind it from larger on
+  int rank = 0;
+  const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
+  const int w0 = 8 * warp, w1 = w0 + 8, end = (c1 + 3) / 4;
+  for (int i = c0 / 4; i < min(w0, end); ++i) {
+    const uint4 k = k4[i];
+    rank += (k.x >= key) + (k.y >= key) + (k.z >= key) + (k.w >= key);
+  }
+  for (int i = max(w0, c0 / 4); i < min(w1, end); ++i) {
+    const uint4 k = k4[i];
+    rank += (k.x > key || (k.x == key && 4 * i < tid)) + (k.y > key || (k.y == key && 4 * i + 1 < tid)) +
+            (k.z > key || (k.z == key && 4 * i + 2 < tid)) +
+            (k.w > key || (k.w == key && 4 * i + 3 < tid));
+  }
+  for (int i = max(w1, c0 / 4); i < end; ++i) {
+    const uint4 k = k4[i];
+    rank += (k.x > key) + (k.y > key) + (k.z > key) + (k.w > key);
+  }
+  const bool stays = tid < len && (candidate ? rank < m : true);
+  const uint32_t votes = __ballot_sync(0xffffffffu, stays);
+  if (lane == 0) counts[warp] = __popc(votes);
+  __syncthreads();
+  int at = __popc(votes & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) at += counts[w];
+  auto row_at = [&](int j) { return (table_s[j >> 4] * p.Hkv + g) * kBlockTokens + (j & 15); };
+  if (stays) {
+    kept[at] = tid;
+    from_s[at] = row;
+    if (at != tid) p.mass[row_at(at)] = x;   // (every weight has been read)
+  }
+  __syncthreads();
+  const int pieces = p.row_bytes / 16, per = NT / pieces;
+  const int lt = tid / pieces, lc = tid - lt * pieces;
+  for (int j0 = 0; j0 < K; j0 += per * kWalkVecs) {
+    uint4 xk[kWalkVecs], xv[kWalkVecs];
+    int to[kWalkVecs];
+#pragma unroll
+    for (int q = 0; q < kWalkVecs; ++q) {
+      const int j = j0 + q * per + lt, jc = min(j, K - 1);
+      const int from = from_s[jc];
+      to[q] = row_at(jc);
+      if (lt >= per || j >= K || from == to[q]) to[q] = -1;
+      if (to[q] >= 0) {
+        const size_t off = static_cast<size_t>(from) * p.row_bytes + 16 * lc;
+        xk[q] = *reinterpret_cast<const uint4 *>(p.k_cache + off);
+        xv[q] = *reinterpret_cast<const uint4 *>(p.v_cache + off);
+      }
+    }
+    __syncthreads();   // the step is read before any of it is written
+#pragma unroll
+    for (int q = 0; q < kWalkVecs; ++q)
+      if (to[q] >= 0) {
+        const size_t off = static_cast<size_t>(to[q]) * p.row_bytes + 16 * lc;
+        *reinterpret_cast<uint4 *>(p.k_cache + off) = xk[q];
+        *reinterpret_cast<uint4 *>(p.v_cache + off) = xv[q];
+      }
+  }
+}
+
 // CTA (row, head, part): part 0 walks K, 1 walks V, 2 the weights.
-__global__ void __launch_bounds__(kMoveThreads) evict_walk_kernel(const EvictParams p) {
+//
+// The kept tokens ahead of the first dropped one stay where they are: one round of
+// probes finds where they end.  From there on, kWalkTokens at a time, the cache rows
+// they come from and go to are listed in shared memory (two round trips for all of
+// them; looked up step by step they were two of every step's three), and while a step
+// is stored the next one's reads are under way.
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_walk_kernel(const EvictParams p) {
+  __shared__ int2 list[kWalkTokens];   // cache rows: from, to
   pdl_wait();
   const int u = blockIdx.x / 3, part = blockIdx.x - 3 * u;
   const int b = u / p.Hkv, g = u - b * p.Hkv;
   const int L = p.seq_lens[b], K = p.keep_lens[b];
   if (K >= L || K <= 0 || K > p.kept_stride) return;
   const int32_t *kept = p.kept + static_cast<size_t>(u) * p.kept_stride;
-  if (kept[K - 1] < 0) return;   // the choice left this row alone (bad length or block)
-  const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
   const int tid = threadIdx.x;
+  const int span = (K + kMoveThreads - 1) / kMoveThreads;
+  const int probe = min((tid + 1) * span, K) - 1, last = kept[K - 1];
+  const int stay = __syncthreads_count(kept[probe] == probe) * span;   // (kept[j] - j never falls)
+  // (last < 0: the choice left this row alone, for a bad length or block)
+  if (last < 0 || stay >= K) return;
+  const int32_t *table = p.block_tables + static_cast<size_t>(b) * p.bt_stride;
   auto row_of = [&](int t) {   // (the pool has fewer than 2^31 rows)
     return (table[t >> 4] * p.Hkv + g) * kBlockTokens + (t & 15);
   };
-  // Each kind of read (indices, table, rows) for all of a step's pieces before the
-  // next kind, without branches between: a round trip serves them all.
-  if (part == 2) {
-    for (int j0 = 0; j0 < K; j0 += kMoveThreads * kWalkVecs) {
-      float x[kWalkVecs];
-      int from[kWalkVecs], to[kWalkVecs];   // cache rows; to -1: nothing to move
-#pragma unroll
-      for (int q = 0; q < kWalkVecs; ++q) from[q] = kept[min(j0 + q * kMoveThreads + tid, K - 1)];
-#pragma unroll
-      for (int q = 0; q < kWalkVecs; ++q) {
-        const int j = j0 + q * kMoveThreads + tid, row = row_of(min(j, K - 1));
-        to[q] = j < K && from[q] != j ? row : -1;
-        from[q] = row_of(from[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < kWalkVecs; ++q)
-        if (to[q] >= 0) x[q] = p.mass[from[q]];
-      __syncthreads();
-#pragma unroll
-      for (int q = 0; q < kWalkVecs; ++q)
-        if (to[q] >= 0) p.mass[to[q]] = x[q];
-    }
-    return;
-  }
-  unsigned char *cache = part ? p.v_cache : p.k_cache;
+  unsigned char *cache = part == 0 ? p.k_cache : p.v_cache;
   const int pieces = p.row_bytes / 16;           // 16-byte pieces of a token's row
   const int per = kMoveThreads / pieces;         // tokens in one round of the CTA
   const int lt = tid / pieces, lc = tid - lt * pieces;
-  const bool on = lt < per;
   cache += 16 * lc;
-  for (int j0 = 0; j0 < K; j0 += per * kWalkVecs) {
-    uint4 x[kWalkVecs];
-    int from[kWalkVecs], to[kWalkVecs];
+  for (int j0 = stay; j0 < K; j0 += kWalkTokens) {
+    const int n = min(kWalkTokens, K - j0);
+    constexpr int kPer = kWalkTokens / kMoveThreads;
+    int src[kPer], to[kPer];
 #pragma unroll
-    for (int q = 0; q < kWalkVecs; ++q) from[q] = kept[min(j0 + q * per + lt, K - 1)];
+    for (int q = 0; q < kPer; ++q) src[q] = kept[j0 + min(q * kMoveThreads + tid, n - 1)];
 #pragma unroll
-    for (int q = 0; q < kWalkVecs; ++q) {
-      const int j = j0 + q * per + lt, row = row_of(min(j, K - 1));
-      to[q] = on && j < K && from[q] != j ? row : -1;
-      from[q] = row_of(from[q]);
+    for (int q = 0; q < kPer; ++q) to[q] = row_of(j0 + min(q * kMoveThreads + tid, n - 1));
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) src[q] = row_of(src[q]);
+    if (part == 2) {
+      float x[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) x[q] = p.mass[src[q]];
+      __syncthreads();   // read before any of it is written
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        if (q * kMoveThreads + tid < n) p.mass[to[q]] = x[q];
+      continue;
     }
+    __syncthreads();   // (the list before is done with)
 #pragma unroll
-    for (int q = 0; q < kWalkVecs; ++q)
-      if (to[q] >= 0)
-        x[q] = *reinterpret_cast<const uint4 *>(cache + static_cast<size_t>(from[q]) * p.row_bytes);
-    __syncthreads();   // the step is read before any of it is written
+    for (int q = 0; q < kPer; ++q) list[q * kMoveThreads + tid] = make_int2(src[q], to[q]);
+    __syncthreads();
+    const int step = per * kWalkVecs;
+    auto load = [&](uint4(&x)[kWalkVecs], int(&dst)[kWalkVecs], int i0) {
 #pragma unroll
-    for (int q = 0; q < kWalkVecs; ++q)
-      if (to[q] >= 0)
-        *reinterpret_cast<uint4 *>(cache + static_cast<size_t>(to[q]) * p.row_bytes) = x[q];
+      for (int q = 0; q < kWalkVecs; ++q) {
+        const int i = i0 + q * per + lt;
+        const int2 r = list[min(i, kWalkTokens - 1)];
+        dst[q] = lt < per && i < n && r.x != r.y ? r.y : -1;
+        if (dst[q] >= 0)
+          x[q] = *reinterpret_cast<const uint4 *>(cache + static_cast<size_t>(r.x) * p.row_bytes);
+      }
+    };
+    auto store = [&](const uint4(&x)[kWalkVecs], const int(&dst)[kWalkVecs]) {
+#pragma unroll
+      for (int q = 0; q < kWalkVecs; ++q)
+        if (dst[q] >= 0)
+          *reinterpret_cast<uint4 *>(cache + static_cast<size_t>(dst[q]) * p.row_bytes) = x[q];
+    };
+    uint4 x[kWalkVecs], y[kWalkVecs];
+    int dx[kWalkVecs], dy[kWalkVecs];
+    load(x, dx, 0);
+    for (int i = 0; i < n; i += 2 * step) {
+      load(y, dy, i + step);   // (its tokens lie behind every slot that is written by then)
+      __syncthreads();         // a step is read before any of it is written
+      store(x, dx);
+      load(x, dx, i + 2 * step);
+      __syncthreads();
+      store(y, dy);
+    }
   }
 }
 
@@ -697,9 +819,17 @@ extern "C" int pkv_evict(const pkv_evict_args *a, void *stream) {
          (longest > 8ll * cluster * kTileTokens ||
           (units * cluster < 152 && longest > 2ll * cluster * kTileTokens)))
     cluster *= 2;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (longest <= 256 || (longest <= 512 && units <= 152)) {   // (512: a CTA to an SM)
+    const cudaError_t e = longest <= 256
+                              ? launch(evict_small_kernel<256>, units, 256, 0, 1, p, s)
+                              : launch(evict_small_kernel<512>, units, 512, 0, 1, p, s);
+    PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "evict_small_kernel launch: %s",
+                cudaGetErrorString(e));
+    return PKV_OK;
+  }
   const bool walk = units >= kChunkUnits;   // two CTAs a pair (K, V) fill the GPU
   if (walk) p.below = nullptr;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long tiles = ((longest + kTileTokens - 1) / kTileTokens + cluster - 1) / cluster;
   p.cached = static_cast<int>(tiles < kMaxCached ? tiles : kMaxCached);
   static std::atomic<unsigned long long> attrs_set{0};

@@ -503,13 +503,40 @@ def test_evict_many_rows_walk():
     check_evict(c, 3, 9, 200)
 
 
-def test_evict_leaves_bad_rows_alone():
-    c = evict_case(5, 2, 64, "bf16", [40, 40, 40, 40, 40], [8, 8, 8, -1, 30], 9)
+def widened(c, pages):
+    """The case behind tables of `pages` entries (the kernels are chosen by their width)."""
+    tab = np.full((c["tab"].shape[0], pages), -1, np.int32)
+    tab[:, :c["tab"].shape[1]] = c["tab"]
+    return dict(c, tab=tab)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pages", [16, 17, 32, 33, 70])
+@pytest.mark.parametrize("B", [1, 5, 77])
+def test_evict_short_rows_by_every_kernel(dtype, pages, B):
+    lens = [(53 * i + 200) % 257 for i in range(B)]
+    keeps = [(29 * i + 100) % 200 for i in range(B)]
+    c = widened(evict_case(B, 1 + B % 2, 64, dtype, lens, keeps, 7 * B + pages, ties=B != 5), pages)
+    check_evict(c, 3, 9, 200)
+
+
+@pytest.mark.parametrize("L,K,sink,recent", [(256, 255, 0, 0), (256, 1, 0, 0), (256, 128, 128, 0),
+                                             (255, 128, 0, 128), (241, 240, 1, 1), (512, 256, 4, 16),
+                                             (512, 511, 0, 0), (497, 3, 1, 1)])
+def test_evict_at_the_ends_of_a_short_row(L, K, sink, recent):
+    check_evict(evict_case(2, 3, 128, "bf16", [L, L - 1], [K, K], L + K, ties=True), sink, recent, K)
+    check_evict(evict_case(2, 3, 128, "bf16", [L, 5], [K, K], L + K), sink, recent, K + 1)
+
+
+@pytest.mark.parametrize("pages,copies", [(3, 1), (40, 1), (40, 20)])   # one CTA, chunks, walks
+def test_evict_leaves_bad_rows_alone(pages, copies):
+    c = evict_case(5 * copies, 2, 64, "bf16", [40] * 5 * copies, [8, 8, 8, -1, 30] * copies, 9)
+    assert c["tab"].shape[1] == 3
     before = [bits(c[k]).copy() for k in ("kc", "vc", "mass")]
-    tab = c["tab"].copy()
-    tab[0, 1] = c["nb"]                       # a block outside the pool
-    tab[1, 2] = -1
-    lens = np.array([40, 40, 49, 40, 40])     # row 2: longer than its table
+    tab = widened(c, pages)["tab"]
+    tab[0::5, 1] = c["nb"]                    # a block outside the pool
+    tab[1::5, 2] = -1
+    lens = np.array([40, 40, 16 * pages + 1, 40, 40] * copies)     # row 2: longer than its table
     err = torch.zeros(1, dtype=torch.int32, device=dev())
     # row 3 keeps a negative number, row 4 more than kept holds
     kept = binding.evict(c["kc"], c["vc"], c["mass"], torch.from_numpy(tab).to(dev()), i32(lens),
