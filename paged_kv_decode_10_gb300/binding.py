@@ -222,6 +222,7 @@ SIGNATURES = {
                                        _c_i32, _c_i32, _p_i32, _c_i32, _p_i32, _p_i32]),
     "pkv_shared_default_parts": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                 _p_i32]),
+    "pkv_shared_short": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _p_i32]),
     "pkv_shared_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                   ctypes.POINTER(_size_t)]),
     "pkv_decode_attn_shared": (ctypes.c_int, [ctypes.POINTER(SharedArgs), _vp]),
@@ -969,6 +970,14 @@ def shared_default_parts(B, Hq, Hkv, d, dtype, bt_stride):
     return n.value
 
 
+def shared_short(B, Hkv, pages):
+    """Whether a call without ``num_parts``, ``plan`` and flags takes the one-kernel form for
+    short contexts (``pages``: the tables' widths added)."""
+    n = ctypes.c_int32()
+    _check(load().pkv_shared_short(int(B), int(Hkv), int(pages), ctypes.byref(n)))
+    return bool(n.value)
+
+
 def shared_workspace_bytes(B, Hq, Hkv, d, num_parts, slots):
     n = _size_t()
     _check(load().pkv_shared_workspace_bytes(int(B), int(Hq), int(Hkv), int(d), int(num_parts),
@@ -989,7 +998,8 @@ def make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out
     """``pkv_shared_args``.  ``prefix_plan`` is ``shared_plan``'s output on the
     device (or pinned); ``slots`` and ``num_ctas`` are read from it once unless
     given (give them, with a workspace for ``slots``, when the buffer will later
-    hold other plans)."""
+    hold other plans).  Without ``num_parts`` and ``plan`` short contexts are computed
+    by one kernel (``shared_short``), the rest in ``shared_default_parts`` parts."""
     torch = _torch()
     if q_rot.dim() != 3 or k_cache.dim() != 4 or not q_rot.is_cuda:
         raise PkvError(ERR_INVALID_ARG, "q_rot must be [B,Hq,d] and the caches [blocks,Hkv,16,d], "
@@ -1041,11 +1051,10 @@ def make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out
         a.lse_out = _want(lse, "lse", (B, Hq), f32, dev)
     if err is not None:
         a.dev_err_flag = _want(err, "err", None, i32, dev)
-    if num_parts is None:
-        num_parts = shared_default_parts(B, Hq, Hkv, d, a.dtype, block_tables.shape[1])
-    a.num_parts = int(num_parts)
+    a.num_parts = int(num_parts or 0)
     if workspace is None and B > 0:
-        nbytes = shared_workspace_bytes(B, Hq, Hkv, d, a.num_parts, a.slots)
+        parts = a.num_parts or shared_default_parts(B, Hq, Hkv, d, a.dtype, block_tables.shape[1])
+        nbytes = shared_workspace_bytes(B, Hq, Hkv, d, parts, a.slots)
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
     if workspace is not None:
         a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)

@@ -223,8 +223,9 @@ class BoundedDecoder(PagedDecoder):
             self._prefix_args = dict(prefix_tables=torch.from_numpy(tables).to(self.device),
                                      prefix_plan=torch.from_numpy(plan).to(self.device),
                                      slots=slots, num_ctas=int(plan[4]))
-        need = binding.shared_workspace_bytes(len(rows), self.Hq, self.Hkv, self.d, self.num_parts,
-                                              slots)
+        parts = max(self.num_parts, binding.shared_default_parts(
+            len(rows), self.Hq, self.Hkv, self.d, self._code, self.bt_stride))
+        need = binding.shared_workspace_bytes(len(rows), self.Hq, self.Hkv, self.d, parts, slots)
         # a workspace of these rows' own, zero-filled once: the counters' place in it
         # depends on the number of rows
         self._space = torch.zeros(need, dtype=torch.uint8, device=self.device)
@@ -235,6 +236,10 @@ class BoundedDecoder(PagedDecoder):
         each buffer and plan; the step's own tensors are put in by ``_launch``."""
         key = self.positions.data_ptr()     # (one of the decoder's own buffers)
         if key not in self._calls:
+            ptab = self._prefix_args.get("prefix_tables")
+            pages = self.bt_stride + (0 if ptab is None else ptab.shape[1])
+            parts = ({} if binding.shared_short(B, self.Hkv, pages) else
+                     dict(plan=self.plan, num_parts=self.num_parts))
             self._calls[key] = [(binding.make_rotary_args(
                 self.rotary, q[layer], k[layer], v[layer], self.positions,
                 q_out=self.q_rots[layer, :B], k_out=self.k_rots[layer, :B],
@@ -242,8 +247,8 @@ class BoundedDecoder(PagedDecoder):
                 v_cache=self.v_caches[layer], err=self.err), binding.make_shared_args(
                 self.q_rots[layer, :B], self.k_caches[layer], self.v_caches[layer], self.tables,
                 self.seq_lens, self.scale, self.outs[layer, :B], mass=self.masses[layer],
-                scores=self.scores, decay=self.decay, plan=self.plan, num_parts=self.num_parts,
-                workspace=self._space, err=self.err, **self._prefix_args))
+                scores=self.scores, decay=self.decay, workspace=self._space, err=self.err, **parts,
+                **self._prefix_args))
                 for layer in range(self.n_layers)]
         return self._calls[key]
 

@@ -53,6 +53,22 @@ __device__ __forceinline__ int prefix_row(const PrefixParams &p, const PrefixIte
   return ok ? w.x : -1;
 }
 
+// The form of the whole call for short contexts (shared_short.cu).
+struct ShortParams {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_tables, *seq_lens, *prefix_tables, *plan, *mass_lens;   // plan: nullable
+  const float *bias;
+  float *mass, *lse_out;
+  void *out;
+  int32_t *err;
+  int B, Hq, Hkv, C, num_blocks, n_prefixes, pt_stride, bt_stride, bias_stride;
+  int cluster, pages;            // CTAs to a (row, KV head), pages one of them may get
+  float scale_log2, decay;
+};
+constexpr int kShortMaxSmem = 160 * 1024;
+int shared_short_cluster(long long units, long long pages, int *per_cta);
+cudaError_t launch_shared_short(const ShortParams &p, int D, int G, int dtype, cudaStream_t s);
+
 cudaError_t launch_prefix_f32(const PrefixParams &p, int D, cudaStream_t s);
 cudaError_t launch_prefix_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
                                int D, cudaStream_t s);

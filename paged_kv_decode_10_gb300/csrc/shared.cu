@@ -5,7 +5,8 @@
 // build of the split-KV kernel over the rows' own tokens (a programmatic
 // dependent of the prefix kernel that reads nothing of it, so it fills whatever
 // SMs that one leaves), the merge of the two and, with mass, the fold of the
-// scores.  Without prefixes only the second and the last.
+// scores.  Without prefixes only the second and the last.  Short contexts take one
+// launch of another kernel (shared_short.cu).
 //
 // Each kernel is launched behind the one before as its programmatic dependent and
 // waits for it before it reads what it left.
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     return;
   }
   const int b = u / p.Hq, h = u - b * p.Hq;
-  const int2 part = *reinterpret_cast<const int2 *>(p.row_part + 2 * b);
+  const int2 part = *reinterpret_cast<const int2 *>(p.row_part + 4 * b);
   int n = part.y;
   if (n < 0 || part.x < 0 || n > p.slots - part.x) {   // never read outside the workspace
     if (n != 0 && d4 == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
@@ -210,6 +211,16 @@ extern "C" int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int3
   return PKV_OK;
 }
 
+extern "C" int pkv_shared_short(int32_t B, int32_t Hkv, int32_t pages, int32_t *short_form) {
+  clear_error();
+  PKV_REQUIRE(short_form, PKV_ERR_INVALID_ARG, "short_form is NULL");
+  PKV_REQUIRE(B >= 0 && Hkv > 0 && pages >= 0, PKV_ERR_INVALID_ARG, "B = %d, Hkv = %d, pages = %d",
+              B, Hkv, pages);
+  int per_cta = 0;
+  *short_form = shared_short_cluster(static_cast<long long>(B) * Hkv, pages, &per_cta) > 0;
+  return PKV_OK;
+}
+
 extern "C" int pkv_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                                           int32_t num_parts, int32_t slots, size_t *bytes) {
   size_t attn = 0;
@@ -294,6 +305,41 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
               "pool too large for 32-bit TMA row coordinates");
   unsigned char *ws = static_cast<unsigned char *>(a->workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->num_parts <= 0 && a->flags == 0) {   // short contexts: one launch
+    ShortParams p = {};
+    const long long pages = static_cast<long long>(a->bt_stride) + (prefixes ? a->pt_stride : 0);
+    p.cluster = shared_short_cluster(static_cast<long long>(a->B) * a->Hkv, pages, &p.pages);
+    if (p.cluster > 0) {
+      p.q = a->q_rot;
+      p.k_cache = a->k_cache;
+      p.v_cache = a->v_cache;
+      p.block_tables = a->block_tables;
+      p.seq_lens = a->seq_lens;
+      p.prefix_tables = prefixes ? a->prefix_tables : a->block_tables;
+      p.plan = prefixes ? a->prefix_plan : nullptr;
+      p.mass_lens = a->mass_lens;
+      p.bias = a->attn_bias;
+      p.mass = a->mass;
+      p.lse_out = a->lse_out;
+      p.out = a->out;
+      p.err = a->dev_err_flag;
+      p.B = a->B;
+      p.Hq = a->Hq;
+      p.Hkv = a->Hkv;
+      p.C = C;
+      p.num_blocks = a->num_blocks;
+      p.n_prefixes = a->n_prefixes;
+      p.pt_stride = prefixes ? a->pt_stride : 0;
+      p.bt_stride = a->bt_stride;
+      p.bias_stride = a->attn_bias ? a->bias_stride : 0;
+      p.scale_log2 = a->scale * kLog2e;
+      p.decay = a->mass_decay;
+      const cudaError_t e = launch_shared_short(p, a->d, G, a->dtype, s);
+      PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "shared_short_kernel launch: %s",
+                  cudaGetErrorString(e));
+      return PKV_OK;
+    }
+  }
   AttnExt ext = {};
   ext.scores = a->mass ? a->scores : nullptr;
   ext.lse2 = a->mass ? reinterpret_cast<float *>(ws + sp.lse2) : nullptr;

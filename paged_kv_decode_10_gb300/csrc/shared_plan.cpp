@@ -191,15 +191,20 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
     };
     std::vector<Item> items;
     int32_t *rows_out = plan + pkv::plan_rows_at();
-    for (int32_t b = 0; b < B; ++b) rows_out[2 * b] = rows_out[2 * b + 1] = 0;
+    for (int32_t b = 0; b < B; ++b) {
+      const int32_t len = row_prefix[b] < 0 ? 0 : prefix_lens[row_prefix[b]];
+      rows_out[4 * b] = rows_out[4 * b + 1] = 0;
+      rows_out[4 * b + 2] = len > 0 ? row_prefix[b] : -1;
+      rows_out[4 * b + 3] = len;
+    }
     int64_t slot = 0;
     for (const Group &g : groups) {
       const int32_t s = (g.grains + best_c - 1) / best_c;
       const int32_t L = prefix_lens[g.p];
       for (int32_t i = 0; i < g.rows; ++i) {
         const int32_t b = order[first[g.p] + i];
-        rows_out[2 * b] = static_cast<int32_t>(slot);
-        rows_out[2 * b + 1] = s;
+        rows_out[4 * b] = static_cast<int32_t>(slot);
+        rows_out[4 * b + 1] = s;
         slot += s;
       }
       for (int32_t t = 0; t < g.tiles; ++t) {
@@ -240,7 +245,7 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
     for (int32_t i = 0; i < B; ++i) {
       const int32_t b = i < static_cast<int32_t>(order.size()) ? order[i] : -1;
       order_out[2 * i] = b;
-      order_out[2 * i + 1] = b < 0 ? 0 : rows_out[2 * b];
+      order_out[2 * i + 1] = b < 0 ? 0 : rows_out[4 * b];
     }
     int32_t *ctas = plan + pkv::plan_ctas_at(B);
     int32_t *out = plan + items_at;

@@ -53,10 +53,10 @@ def test_rotary_refuses_head_sizes(bind, d):
 # --------------------------------------------------------------------------- planner
 def read_plan(plan):
     magic, n, B, slots, C, Hkv, G, R = plan[:8]
-    rows = plan[16:16 + 2 * B].reshape(B, 2)
-    order = plan[16 + 2 * B:16 + 4 * B].reshape(B, 2)
-    ctas = plan[16 + 4 * B:16 + 4 * B + C + 1]
-    at = (16 + 4 * B + C + 1 + 3) // 4 * 4
+    rows = plan[16:16 + 4 * B].reshape(B, 4)
+    order = plan[16 + 4 * B:16 + 6 * B].reshape(B, 2)
+    ctas = plan[16 + 6 * B:16 + 6 * B + C + 1]
+    at = (16 + 6 * B + C + 1 + 3) // 4 * 4
     items = plan[at:].reshape(-1, 8)
     assert len(items) == n and ctas[0] == 0 and ctas[-1] == n and (np.diff(ctas) >= 0).all()
     return rows, order, ctas, items, slots, R
@@ -90,6 +90,7 @@ def test_shared_plan_covers_every_token_once(bind, dtype, B, Hq, Hkv, lens, seed
     for b in range(B):
         has = prefix[b] >= 0 and lens[prefix[b]] > 0
         assert (rows[b, 1] > 0) == has
+        assert rows[b, 2:].tolist() == ([prefix[b], lens[prefix[b]]] if has else [-1, 0])
         for g in range(Hkv):
             parts = sorted(seen.get((b, g), []))
             assert len(parts) == rows[b, 1]
@@ -116,6 +117,15 @@ def test_shared_plan_refuses(bind):
                 dict(out=np.empty(512, np.int64))):
         with pytest.raises(bind.PkvError):
             bind.shared_plan(**{**ok, **bad})
+
+
+def test_short_contexts_are_few_rows_of_few_pages(bind):
+    short = bind.shared_short
+    assert short(1, 1, 1) and short(14, 1, 128) and short(2, 17, 64) and short(76, 1, 32)
+    assert short(19, 8, 16) and not short(19, 8, 17) and not short(153, 1, 1)
+    assert not short(1, 1, 129) and not short(15, 1, 65) and not short(35, 1, 33)
+    with pytest.raises(bind.PkvError):
+        short(1, 0, 4)
 
 
 def test_shared_workspace_grows_with_slots(bind):

@@ -99,15 +99,16 @@ class Replay:
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("L,metadata", [(1, "copy"), (2, "mapped")])
-def test_bounded_decoding_against_a_replay(dtype, L, metadata):
+@pytest.mark.parametrize("L,metadata,width", [(1, "copy", 3), (2, "mapped", 3), (1, "mapped", 150),
+                                              (2, "copy", 150)])   # (150: not a short context)
+def test_bounded_decoding_against_a_replay(dtype, L, metadata, width):
     Hq, Hkv, d, budget, slack = 8, 2, 64, 24, 9
     rot = binding.Rotary(d, rot_dim=32, layout="interleaved", scaling="bands", factor=4.0, low=1.0,
                          high=4.0, original_len=64)
     spec = dict(freq=cache_ops.rotary_frequencies(32, "bands", factor=4.0, low=1.0, high=4.0,
                                                   original_len=64), layout="interleaved")
     dec = BoundedDecoder(96, Hq, Hkv, d, dtype, 6, budget, slack, sink=2, recent=5, rotary=rot,
-                         decay=0.95, n_layers=L, metadata=metadata, device=dev(),
+                         decay=0.95, n_layers=L, metadata=metadata, device=dev(), max_blocks_per_seq=width,
                          initial_free=np.random.default_rng(1).permutation(96).astype(np.int32))
     free0 = dec.alloc.num_free()
 

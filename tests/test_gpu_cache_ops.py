@@ -195,6 +195,9 @@ def run_case(c, out=None, **kw):
     B = c["B"]
     err = torch.zeros(1, dtype=torch.int32, device=dev())
     lse = torch.empty((B, c["Hq"]), device=dev())
+    if kw.pop("general", False):   # a stated number of parts: not the form for short contexts
+        kw["num_parts"] = binding.shared_default_parts(B, c["Hq"], c["kc"].shape[1], c["d"],
+                                                       binding.dtype_code(c["q"]), c["tab"].shape[1])
     out = torch.full_like(c["q"], 7.0) if out is None else out
     if len(c["plens"]):
         plan = binding.shared_plan(c["rows"], c["plens"], c["Hq"], c["Hkv"], c["d"],
@@ -273,11 +276,12 @@ SHARED = [
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("general", [False, True])
 @pytest.mark.parametrize("i", range(len(SHARED)))
-def test_shared_attention(dtype, i):
+def test_shared_attention(dtype, i, general):
     B, Hq, Hkv, d, lens, plens, rows = SHARED[i]
     c = make_case(B, Hq, Hkv, d, dtype, lens, plens, rows, 11 * i)
-    out, lse, err, _ = run_case(c)
+    out, lse, err, _ = run_case(c, general=general)
     check_case(c, out, lse, err=err)
 
 
@@ -292,14 +296,15 @@ def test_shared_attention_under_other_partitions(dtype, ctas, parts):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("general", [False, True])
 @pytest.mark.parametrize("plens", [[], [90, 300]])
-def test_weights_are_accumulated(dtype, G, plens):
+def test_weights_are_accumulated(dtype, G, plens, general):
     B = 7
     rows = [-1, 0, 1, 0, 1, 0, -1] if plens else [-1] * B
     c = make_case(B, 2 * G, 2, 64 if G < 4 else 128, dtype, [0, 1, 2, 17, 64, 200, 33], plens, rows, G,
                   mass=True)
     m0 = f64(c["mass"])
-    out, lse, err, a = run_case(c)
+    out, lse, err, a = run_case(c, general=general)
     check_case(c, out, lse, m0, err=err)
     # a second call goes on from there
     m1 = f64(c["mass"])
@@ -309,11 +314,12 @@ def test_weights_are_accumulated(dtype, G, plens):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("general", [False, True])
 @pytest.mark.parametrize("plens", [[], [64]])
-def test_masks_on_own_tokens(dtype, plens):
+def test_masks_on_own_tokens(dtype, plens, general):
     c = make_case(5, 8, 2, 64, dtype, [20, 33, 16, 1, 50], plens, [0, 0, -1, 0, 0], 5, bias=True, mass=True)
     m0 = f64(c["mass"])
-    out, lse, err, _ = run_case(c)
+    out, lse, err, _ = run_case(c, general=general)
     check_case(c, out, lse, m0, err=err)
 
 
@@ -345,10 +351,11 @@ def test_default_new_token_and_planned_partition(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_a_row_alone_equals_the_batch_without_sharing(dtype):
+@pytest.mark.parametrize("general", [False, True])
+def test_a_row_alone_equals_the_batch_without_sharing(dtype, general):
     """The same tokens as one long own sequence, through the framework's attention."""
     c = make_case(4, 8, 2, 128, dtype, [33, 1, 16, 70], [160], [0] * 4, 31)
-    out, lse, err, _ = run_case(c)
+    out, lse, err, _ = run_case(c, general=general)
     joined = np.full((4, 10 + 5), -1, np.int32)
     for b in range(4):
         n = -(-int(c["lens"][b]) // 16)
@@ -362,11 +369,12 @@ def test_a_row_alone_equals_the_batch_without_sharing(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_bad_blocks_and_plans_are_flagged(dtype):
+@pytest.mark.parametrize("general", [False, True])
+def test_bad_blocks_and_plans_are_flagged(dtype, general):
     c = make_case(3, 8, 2, 64, dtype, [5, 40, 20], [100, 40], [0, 0, 1], 41)
     good = c["ptab"].copy()
     c["ptab"][0, 3] = c["nb"]          # tokens 48..63 of prefix 0 drop out
-    out, lse, err, _ = run_case(c)
+    out, lse, err, _ = run_case(c, general=general)
     assert err == binding.DEVERR_BAD_BLOCK
     # the same as a prefix without that page
     c2 = dict(c, ptab=np.full((2, 7), -1, np.int32), plens=[84, 40])
@@ -382,7 +390,8 @@ def test_bad_blocks_and_plans_are_flagged(dtype):
     a = binding.make_shared_args(c["q"], c["kc"], c["vc"], torch.from_numpy(c["tab"]).to(dev()),
                                  i32(c["lens"]), c["scale"], out,
                                  prefix_tables=torch.from_numpy(c["ptab"]).to(dev()),
-                                 prefix_plan=torch.from_numpy(pad).to(dev()), err=e)
+                                 prefix_plan=torch.from_numpy(pad).to(dev()), err=e,
+                                 num_parts=4 if general else None)
     binding.decode_attn_shared_args(a)
     torch.cuda.synchronize()
     assert int(e) & binding.DEVERR_BAD_PLAN
@@ -401,10 +410,11 @@ def test_repeated_calls_are_bit_identical(dtype):
     check_case(c, out, lse, err=err)
 
 
-def test_shared_attention_in_a_graph_and_on_another_stream():
+@pytest.mark.parametrize("general", [False, True])
+def test_shared_attention_in_a_graph_and_on_another_stream(general):
     c = make_case(6, 8, 2, 64, "bf16", [3, 50, 16, 1, 0, 20], [300], [0, 0, 0, -1, 0, 0], 61, mass=True)
     first = c["mass"].clone()
-    out, lse, err, a = run_case(c)
+    out, lse, err, a = run_case(c, general=general)
     want, want_mass = out.clone(), c["mass"].clone()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -661,7 +671,8 @@ def test_prefix_waits_that_give_up_report_a_timeout(dtype):
     assert err == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
-def test_a_captured_call_follows_the_plan_in_its_buffer():
+@pytest.mark.parametrize("general", [False, True])
+def test_a_captured_call_follows_the_plan_in_its_buffer(general):
     """One graph, a plan buffer and a workspace for the largest plan of its sizes: new
     prefixes of the rows and new lengths go in by overwriting the buffers."""
     B, Hq, Hkv, d, P = 12, 8, 2, 64, 3
@@ -674,7 +685,7 @@ def test_a_captured_call_follows_the_plan_in_its_buffer():
     err = torch.zeros(1, dtype=torch.int32, device=dev())
     a = binding.make_shared_args(c["q"], c["kc"], c["vc"], torch.from_numpy(c["tab"]).to(dev()), lens,
                                  c["scale"], out, prefix_tables=ptab, prefix_plan=buf, slots=most,
-                                 num_ctas=sms, lse=lse, err=err)
+                                 num_ctas=sms, lse=lse, err=err, num_parts=24 if general else None)
 
     def put(rows, plens, own):
         plan = binding.shared_plan(rows, plens, Hq, Hkv, d, binding.BF16, sms)
@@ -762,3 +773,37 @@ def test_caches_beyond_32_bit_offsets():
             x[19 + j // 16, g, j % 16] = o[19 + src[g] // 16, g, src[g] % 16]
     for x, y in zip(new, (kc, vc, mass)):
         np.testing.assert_array_equal(x, bits(y[used]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("B,pages", [(1, 1), (1, 40), (3, 22), (8, 40), (19, 20), (38, 10)])
+def test_short_contexts_in_one_launch(dtype, d, G, B, pages):
+    """One CTA or a cluster of up to eight to a (row, KV head), shares that hold no page
+    among them, against the oracle."""
+    Hkv = 4
+    lens = [(37 * b + 16 * pages - 3) % (16 * pages + 1) for b in range(B)]
+    lens[-1] = 16 * pages
+    plens = [] if pages == 1 else [min(16 * 24, 5 * pages), 1]
+    rows = [b % 3 - 1 if plens else -1 for b in range(B)]
+    c = make_case(B, Hkv * G, Hkv, d, dtype, lens, plens, rows, 3 * B + G, bias=B == 3, mass=True)
+    m0 = f64(c["mass"])
+    out, lse, err, a = run_case(c)
+    assert a.num_parts == 0 and binding.shared_short(B, Hkv, a.bt_stride + a.pt_stride)
+    check_case(c, out, lse, m0, err=err)
+
+
+@pytest.mark.parametrize("general", [False, True])
+def test_lengths_that_do_not_fit_are_flagged(general):
+    """A row longer than its table, or of negative length, has no own tokens."""
+    c = make_case(3, 8, 2, 64, "bf16", [20, 20, 20], [40], [0, -1, 0], 17, mass=True)
+    c["known"] = [0, 0, 0]
+    before = c["mass"].clone()
+    lens = c["lens"].copy()
+    c["lens"] = np.array([33, -1, 20])
+    out, lse, err, _ = run_case(c, general=general)
+    assert err == binding.DEVERR_BAD_LEN
+    c["lens"] = np.array([0, 0, 20])
+    m0 = f64(before)
+    check_case(c, out, lse, m0)
