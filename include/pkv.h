@@ -520,7 +520,7 @@ int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32_t *prefix_
                     int32_t num_ctas, int32_t *plan, int32_t plan_cap, int32_t *plan_ints,
                     int32_t *slots);
 /* The partition pkv_decode_attn_shared takes for num_parts <= 0 where the contexts are
- * not short (pkv_shared_short): that of
+ * not short (pkv_shared_short; in float32 behind prefixes at most one part to an SM): that of
  * pkv_attn_default_parts, but at least 8 positions (pages and unit boundaries, see
  * pkv_attn_default_parts' partition) to a part if every table were full. */
 int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,

@@ -275,6 +275,15 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
   }
   // (a plan without partials -- no row has a prefix -- leaves the own tokens alone)
   const bool prefixes = a->prefix_tables != nullptr && a->n_prefixes > 0 && a->slots > 0;
+  if (a->num_parts <= 0 && prefixes && a->dtype == PKV_F32) {
+    // One part to an SM leaves room for a CTA of the float32 prefix kernel beside it; with
+    // two the kernels follow one another (24 rows of 300 tokens, 16/8 heads of 64, behind
+    // 1000: 28 us against 40; behind 300: 25 against 30).
+    int sms = 0;
+    rc = current_sms(&sms);
+    if (rc != PKV_OK) return rc;
+    if (num_parts > sms) num_parts = sms;
+  }
   int C = a->num_ctas;
   if (prefixes) {
     if (C <= 0) {

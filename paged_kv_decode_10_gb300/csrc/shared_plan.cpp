@@ -100,6 +100,7 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
                 row_prefix[b], n_prefixes);
   const int32_t C = num_ctas, G = Hq / Hkv;
   const int32_t R = (dtype == PKV_BF16 ? pkv::kTileRowsBf16 : pkv::kTileRowsF32) / G;
+  const int32_t grain = dtype == PKV_BF16 ? pkv::kSplitTokens : pkv::kSplitTokensF32;
   const Bounds bd = bounds(B, n_prefixes, Hq, Hkv, C);
   const int64_t items_at = pkv::plan_items_at(B, C);
   PKV_REQUIRE(plan_cap >= items_at, PKV_ERR_INVALID_ARG, "plan_cap %d < %lld", plan_cap,
@@ -124,7 +125,7 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
     for (int32_t p = 0; p < n_prefixes; ++p) {
       const int32_t rows = first[p + 1] - first[p];
       if (rows == 0) continue;
-      const int32_t gr = (prefix_lens[p] + pkv::kSplitTokens - 1) / pkv::kSplitTokens;
+      const int32_t gr = (prefix_lens[p] + grain - 1) / grain;
       groups.push_back({p, rows, (rows + R - 1) / R, gr});
       longest = std::max(longest, gr);
     }
@@ -134,7 +135,7 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
     // five prefixes and nothing was gained elsewhere.)
     auto grain_ns = [&](int32_t rows) {
       const double q = static_cast<double>(rows) * G, w = d / 128.0;
-      if (dtype == PKV_F32) return 500.0 * w * q;
+      if (dtype == PKV_F32) return 500.0 / (pkv::kSplitTokens / pkv::kSplitTokensF32) * w * q;
       return (q > 128 ? 1100.0 : 700.0) * (d == 128 ? 1.0 : 0.7);
     };
     const double fixed_ns = 3000.0;
@@ -213,8 +214,8 @@ extern "C" int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32
           const int32_t a = static_cast<int32_t>(static_cast<int64_t>(g.grains) * k / s);
           const int32_t e = static_cast<int32_t>(static_cast<int64_t>(g.grains) * (k + 1) / s);
           for (int32_t h = 0; h < Hkv; ++h) {
-            Item it{{g.p, h, first[g.p] + r.first, r.second - r.first, a * pkv::kSplitTokens,
-                     std::min(L, e * pkv::kSplitTokens), k, 0},
+            Item it{{g.p, h, first[g.p] + r.first, r.second - r.first, a * grain,
+                     std::min(L, e * grain), k, 0},
                     fixed_ns + (e - a) * grain_ns(r.second - r.first)};
             items.push_back(it);
           }

@@ -22,7 +22,8 @@ inline __host__ __device__ int plan_items_at(int B, int C) {
 // Query rows (batch rows x group heads) one work item covers at most.
 constexpr int kTileRowsBf16 = 256;
 constexpr int kTileRowsF32 = 64;
-// Prefixes are split at multiples of this many tokens.
+// Prefixes are split at multiples of this many tokens (a step of the kernels).
 constexpr int kSplitTokens = 128;
+constexpr int kSplitTokensF32 = 32;
 
 }  // namespace pkv
