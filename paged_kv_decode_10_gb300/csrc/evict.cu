@@ -26,7 +26,7 @@
 //  * Short rows: one CTA chooses and compacts (evict_small_kernel).
 // The first two are memory bound: each kept row is read and written once.  The walk needs
 // no flags and keeps its steps back to back (64 rows of 8 heads, 1500..2600 tokens of 128
-// down to 1024, bf16: 80 us, 5.8 TB/s, against 150 us in chunks, the choice before it
+// down to 1024, bf16: 78 us, 5.9 TB/s, against 150 us in chunks, the choice before it
 // 17 us); with 4 (row, head) pairs it leaves the GPU empty (131072 tokens down to 32768:
 // 130 us against 31 us in chunks, the choice 23 us).
 #include <cstdint>
