@@ -526,9 +526,10 @@ int pkv_shared_plan(const int32_t *row_prefix, int32_t B, const int32_t *prefix_
 int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                              int32_t bt_stride, int32_t *num_parts);
 /* Whether pkv_decode_attn_shared with num_parts <= 0 and no flags takes its one-kernel
- * form for short contexts: few (row, KV head) pairs and at most `pages` 16-token pages
- * to a row (bt_stride + pt_stride). */
-int pkv_shared_short(int32_t B, int32_t Hkv, int32_t pages, int32_t *short_form);
+ * form for short contexts: few (row, KV head) pairs whose tables have few entries
+ * (pt_stride 0: no prefixes). */
+int pkv_shared_short(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                     int32_t bt_stride, int32_t pt_stride, int32_t *short_form);
 /* Workspace of pkv_decode_attn_shared: the bytes of pkv_attn_workspace_bytes plus
  * the row sums and the partials of `slots` (0 without prefixes; max_slots above
  * serves every plan of those sizes).  Same rules: 256-byte aligned, zero-filled once

@@ -222,7 +222,7 @@ SIGNATURES = {
                                        _c_i32, _c_i32, _p_i32, _c_i32, _p_i32, _p_i32]),
     "pkv_shared_default_parts": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                 _p_i32]),
-    "pkv_shared_short": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _p_i32]),
+    "pkv_shared_short": (ctypes.c_int, [_c_i32] * 7 + [_p_i32]),
     "pkv_shared_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                   ctypes.POINTER(_size_t)]),
     "pkv_decode_attn_shared": (ctypes.c_int, [ctypes.POINTER(SharedArgs), _vp]),
@@ -975,11 +975,12 @@ def shared_default_parts(B, Hq, Hkv, d, dtype, bt_stride):
     return n.value
 
 
-def shared_short(B, Hkv, pages):
+def shared_short(B, Hq, Hkv, d, dtype, bt_stride, pt_stride=0):
     """Whether a call without ``num_parts``, ``plan`` and flags takes the one-kernel form for
-    short contexts (``pages``: the tables' widths added)."""
+    short contexts (``pt_stride`` 0: no prefixes)."""
     n = ctypes.c_int32()
-    _check(load().pkv_shared_short(int(B), int(Hkv), int(pages), ctypes.byref(n)))
+    _check(load().pkv_shared_short(int(B), int(Hq), int(Hkv), int(d), int(dtype), int(bt_stride),
+                                   int(pt_stride), ctypes.byref(n)))
     return bool(n.value)
 
 

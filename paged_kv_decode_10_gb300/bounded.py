@@ -237,9 +237,9 @@ class BoundedDecoder(PagedDecoder):
         key = self.positions.data_ptr()     # (one of the decoder's own buffers)
         if key not in self._calls:
             ptab = self._prefix_args.get("prefix_tables")
-            pages = self.bt_stride + (0 if ptab is None else ptab.shape[1])
-            parts = ({} if binding.shared_short(B, self.Hkv, pages) else
-                     dict(plan=self.plan, num_parts=self.num_parts))
+            short = binding.shared_short(B, self.Hq, self.Hkv, self.d, self._code, self.bt_stride,
+                                         0 if ptab is None else ptab.shape[1])
+            parts = {} if short else dict(plan=self.plan, num_parts=self.num_parts)
             self._calls[key] = [(binding.make_rotary_args(
                 self.rotary, q[layer], k[layer], v[layer], self.positions,
                 q_out=self.q_rots[layer, :B], k_out=self.k_rots[layer, :B],

@@ -66,7 +66,7 @@ struct ShortParams {
   float scale_log2, decay;
 };
 constexpr int kShortMaxSmem = 160 * 1024;
-int shared_short_cluster(long long units, long long pages, int *per_cta);
+int shared_short_cluster(const pkv_shared_args &a, bool prefixes, int *per_cta);
 cudaError_t launch_shared_short(const ShortParams &p, int D, int G, int dtype, cudaStream_t s);
 
 cudaError_t launch_prefix_f32(const PrefixParams &p, int D, cudaStream_t s);

@@ -211,13 +211,23 @@ extern "C" int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int3
   return PKV_OK;
 }
 
-extern "C" int pkv_shared_short(int32_t B, int32_t Hkv, int32_t pages, int32_t *short_form) {
+extern "C" int pkv_shared_short(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
+                                int32_t bt_stride, int32_t pt_stride, int32_t *short_form) {
   clear_error();
   PKV_REQUIRE(short_form, PKV_ERR_INVALID_ARG, "short_form is NULL");
-  PKV_REQUIRE(B >= 0 && Hkv > 0 && pages >= 0, PKV_ERR_INVALID_ARG, "B = %d, Hkv = %d, pages = %d",
-              B, Hkv, pages);
+  const int rc = check_shapes(B, Hq, Hkv, d, dtype);
+  if (rc != PKV_OK) return rc;
+  PKV_REQUIRE(bt_stride >= 0 && pt_stride >= 0, PKV_ERR_INVALID_ARG, "negative width");
+  pkv_shared_args a = {};
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.dtype = dtype;
+  a.bt_stride = bt_stride;
+  a.pt_stride = pt_stride;
   int per_cta = 0;
-  *short_form = shared_short_cluster(static_cast<long long>(B) * Hkv, pages, &per_cta) > 0;
+  *short_form = shared_short_cluster(a, pt_stride > 0, &per_cta) > 0;
   return PKV_OK;
 }
 
@@ -316,8 +326,7 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->num_parts <= 0 && a->flags == 0) {   // short contexts: one launch
     ShortParams p = {};
-    const long long pages = static_cast<long long>(a->bt_stride) + (prefixes ? a->pt_stride : 0);
-    p.cluster = shared_short_cluster(static_cast<long long>(a->B) * a->Hkv, pages, &p.pages);
+    p.cluster = shared_short_cluster(*a, prefixes, &p.pages);
     if (p.cluster > 0) {
       p.q = a->q_rot;
       p.k_cache = a->k_cache;

@@ -62,8 +62,14 @@ struct Piece {
   }
 };
 
+// CTAs that fit an SM by registers (a page's keys and values and the accumulators of the
+// group are held in them).
+constexpr int resident(int elem, int d, int G) {
+  return elem * d * (G < 4 ? 1 : G / 2) <= 256 ? 2 : 1;
+}
+
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, resident(sizeof(T), D, G))
     shared_short_kernel(const __grid_constant__ ShortParams p) {
   constexpr int DPL = D / 32, QS = D + 8;   // (the halves of a query 4 floats apart: other banks)
   extern __shared__ __align__(16) float sm[];
@@ -327,17 +333,27 @@ cudaError_t launch_g(const ShortParams &p, int G, cudaStream_t s) {
 }  // namespace
 
 // CTAs to a (row, KV head) and the pages one of them may get; 0: the other form.
-// A CTA has an SM to itself, and as many clusters of S are on the GPU at once as its
-// groups of SMs hold (152, 76, 36 and 15).  Up to two pages a warp this form wins (4
-// heads of 128 to a KV head, bf16: 1 row of 4 KV heads and 512 tokens 6.4 us against
-// 10.5 in parts, 16 rows behind 448 shared tokens 9.6 against 15.2; 8 heads to a KV head
-// with weights 13.3 against 18.8); at four they are even, and beyond it loses.
-int shared_short_cluster(long long units, long long pages, int *per_cta) {
+// As many clusters of S are on the GPU at once as its groups of SMs hold (152, 76, 36 and
+// 15 with a CTA to an SM).  Up to two pages a warp this form wins (4 heads of 128 to a KV
+// head, bf16: 1 row of 4 KV heads and 512 tokens 6.4 us against 10.5 in parts, 16 rows
+// behind 448 shared tokens 9.6 against 15.2; 8 heads to a KV head with weights 13.3
+// against 18.8); at four they are even, and beyond it loses.  One CTA to a pair may also
+// take several waves, where the other form pays for more kernels (prefixes) or for its
+// partition (float32): 608 pairs of 16 own tokens behind 40, bf16, 4 heads of 64: 8.6
+// against 18.3; 250 tokens, float32, 4 heads of 128: 51 against 64.  Two waves of the
+// bf16 form without prefixes lose (304 pairs of 100 tokens, heads of 128: 12 against 7).
+int shared_short_cluster(const pkv_shared_args &a, bool prefixes, int *per_cta) {
   constexpr int kMostUnits[4] = {152, 76, 34, 14};
+  const long long units = static_cast<long long>(a.B) * a.Hkv;
+  const long long pages = static_cast<long long>(a.bt_stride) + (prefixes ? a.pt_stride : 0);
   int i = 0;
   while (i < 3 && units <= kMostUnits[i + 1] && pages > static_cast<long long>(kWarps) << i) ++i;
   const long long s = 1ll << i;
-  if (units > kMostUnits[i] || pages > 2 * kWarps * s) return 0;
+  const long long rounds = (pages + kWarps * s - 1) / (kWarps * s);   // pages of a warp
+  const int r = resident(static_cast<int>(dtype_size(a.dtype)), a.d, a.Hq / a.Hkv);
+  const long long waves = i > 0 ? 1 : (units + 152 * r - 1) / (152 * r);
+  const int most = i > 0 ? 2 : a.dtype == PKV_F32 ? 8 / r : prefixes ? 2 * r : 2;
+  if (rounds > 2 || waves * rounds > most || (waves > 1 && !prefixes && a.dtype == PKV_BF16)) return 0;
   *per_cta = static_cast<int>((pages + s - 1) / s);
   return static_cast<int>(s);
 }

@@ -120,12 +120,19 @@ def test_shared_plan_refuses(bind):
 
 
 def test_short_contexts_are_few_rows_of_few_pages(bind):
-    short = bind.shared_short
+    def short(B, Hkv, own, pre=0, G=4, d=128, dtype=bind.BF16):
+        return bind.shared_short(B, Hkv * G, Hkv, d, dtype, own, pre)
     assert short(1, 1, 1) and short(14, 1, 128) and short(2, 17, 64) and short(76, 1, 32)
     assert short(19, 8, 16) and not short(19, 8, 17) and not short(153, 1, 1)
     assert not short(1, 1, 129) and not short(15, 1, 65) and not short(35, 1, 33)
-    with pytest.raises(bind.PkvError):
-        short(1, 0, 4)
+    # several waves where the other form has more kernels or a costly partition
+    assert short(38, 8, 4, 4) and not short(38, 8, 8, 8) and not short(77, 8, 4, 4)
+    assert short(76, 8, 8, 8, d=64) and short(152, 8, 4, 4, d=64) and not short(152, 8, 8, 8, d=64)
+    assert short(76, 8, 16, dtype=bind.F32) and not short(152, 8, 16, dtype=bind.F32)
+    assert not short(65536, 8, 1) and not short(1, 1, (1 << 26) - 1, 1 << 25)
+    for bad in ((1, 0, 4), (1, 1, -1), (1, 1, 1, -1), (1, 1, 1, 0, 3), (1, 1, 1, 0, 4, 96)):
+        with pytest.raises(bind.PkvError):
+            short(*bad)
 
 
 def test_shared_workspace_grows_with_slots(bind):

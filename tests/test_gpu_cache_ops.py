@@ -778,7 +778,7 @@ def test_caches_beyond_32_bit_offsets():
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
-@pytest.mark.parametrize("B,pages", [(1, 1), (1, 40), (3, 22), (8, 40), (19, 20), (38, 10)])
+@pytest.mark.parametrize("B,pages", [(1, 1), (1, 40), (3, 22), (8, 40), (19, 20), (38, 10), (70, 4)])
 def test_short_contexts_in_one_launch(dtype, d, G, B, pages):
     """One CTA or a cluster of up to eight to a (row, KV head), shares that hold no page
     among them, against the oracle."""
@@ -790,7 +790,8 @@ def test_short_contexts_in_one_launch(dtype, d, G, B, pages):
     c = make_case(B, Hkv * G, Hkv, d, dtype, lens, plens, rows, 3 * B + G, bias=B == 3, mass=True)
     m0 = f64(c["mass"])
     out, lse, err, a = run_case(c)
-    assert a.num_parts == 0 and binding.shared_short(B, Hkv, a.bt_stride + a.pt_stride)
+    assert a.num_parts == 0 and binding.shared_short(B, Hkv * G, Hkv, d, a.dtype, a.bt_stride,
+                                                     a.pt_stride)
     check_case(c, out, lse, m0, err=err)
 
 
