@@ -22,7 +22,7 @@ from .engine import PagedDecoder
 class BoundedDecoder(PagedDecoder):
     """``budget``: own tokens a sequence keeps when it is cut back, which happens before
     the step that would append to ``budget + slack`` tokens.  ``rotary``: a
-    ``binding.Rotary`` (default: the whole head, plain).  ``decay``: factor on the
+    ``binding.Rotary`` (default: the whole head, plain, at ``rope_base``).  ``decay``: factor on the
     weight accumulated so far at every step.  ``max_prefixes`` prefixes of up to
     ``max_prefix_len`` tokens may be live.  The rest as ``PagedDecoder``; its captured
     forms and additive masks are not offered here."""
@@ -37,6 +37,8 @@ class BoundedDecoder(PagedDecoder):
             raise ValueError("sink and recent must not be negative")
         if max_prefixes < 0 or max_prefix_len < 0:
             raise ValueError("max_prefixes and max_prefix_len must not be negative")
+        if rotary is not None and kw.get("rope_base") is not None:
+            raise ValueError("rotary states its own base: give rope_base or rotary")
         need = -(-(budget + slack) // binding.BLOCK_SIZE)
         bt = kw.pop("max_blocks_per_seq", need)
         if bt < need:
@@ -52,7 +54,7 @@ class BoundedDecoder(PagedDecoder):
         self.alloc = binding.BlockAllocator(num_blocks, max_seqs + max_prefixes, width,
                                             kw.get("initial_free"))
         self.budget, self.slack, self.sink, self.recent = budget, slack, sink, recent
-        self.rotary = binding.Rotary(d) if rotary is None else rotary
+        self.rotary = binding.Rotary(d, base=self.rope_base) if rotary is None else rotary
         if self.rotary.d != d:
             raise ValueError(f"rotary was made for heads of {self.rotary.d}, not {d}")
         self.decay = float(decay)

@@ -1,0 +1,51 @@
+"""``BoundedDecoder``'s arguments and its states between steps, on the GPU.
+
+Tolerance of an output against the float64 replay: as in test_gpu_bounded."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import dev, f64
+from oracle import cache_ops
+from paged_kv_decode_10_gb300 import workloads
+from paged_kv_decode_10_gb300.bounded import BoundedDecoder
+from test_gpu_bounded import Replay
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib(cuda_lib):
+    return cuda_lib
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rope_base_against_a_replay(dtype):
+    """The default rotary turns at the decoder's ``rope_base``."""
+    Hq, Hkv, d, base = 8, 2, 64, 500000.0
+    dec = BoundedDecoder(16, Hq, Hkv, d, dtype, 1, 64, 16, rope_base=base, device=dev())
+    spec = dict(freq=cache_ops.rotary_frequencies(d, "plain", base=base), layout="half")
+    ref = Replay(dec, spec, dtype)
+
+    def draw(n, heads, seed):
+        x = workloads.normal((n, heads, d), dtype, seed)
+        return x.to(dev()), f64(x)
+
+    (k, k64), (v, v64) = draw(40, Hkv, 1), draw(40, Hkv, 2)
+    s = dec.join(40, None, k, v)
+    ref.add(k64[None], v64[None])
+    u = 2.0**-8 if dtype == "bf16" else 2.0**-24
+    for step in range(4):
+        (q, q64), (k, k64), (v, v64) = (draw(1, h, 10 + 3 * step + i)
+                                        for i, h in enumerate((Hq, Hkv, Hkv)))
+        out = f64(dec.step([s], q, k, v))[0]
+        assert dec.device_errors() == 0
+        ref.add(k64[None], v64[None])
+        want, swing, top = ref.attend(q64[0], 0)
+        eps = 2 * (d + 8) * 2.0**-23 * swing + 2.0**-18
+        if dtype == "bf16":
+            eps += 2 * 2.0**-8 * top + u
+        size = np.abs(np.array(ref.v[0])).max()
+        err = np.abs(out - want).max()
+        assert err <= eps * size + u * np.abs(want).max(), (step, err)
+    torch.cuda.synchronize()
