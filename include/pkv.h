@@ -65,7 +65,8 @@ extern "C" {
 #define PKV_DEVERR_BAD_SLOT 2   /* a slot outside [0, num_blocks * 16) */
 #define PKV_DEVERR_BAD_LEN 4    /* seq_len < 0, or longer than bt_stride*16 or bias_stride */
 #define PKV_DEVERR_TIMEOUT 8    /* an internal pipeline wait gave up (never expected) */
-#define PKV_DEVERR_BAD_PLAN 16  /* PKV_ATTN_CHECK_PLAN: the plan disagrees with the metadata */
+#define PKV_DEVERR_BAD_PLAN 16  /* a plan does not fit the call, or (PKV_ATTN_CHECK_PLAN) it
+                                   disagrees with the metadata */
 
 /* flags for the attention calls */
 #define PKV_ATTN_SIMT 1         /* use the CUDA-core consumer instead of mma.sync (bf16 only;
@@ -572,9 +573,14 @@ typedef struct pkv_shared_args {
  *
  * Sizes as pkv_decode_attn_split; flags: PKV_ATTN_CHECK_PLAN,
  * PKV_ATTN_SHORT_WAITS.  out must not overlap q_rot.  A block id outside the pool sets
- * PKV_DEVERR_BAD_BLOCK and its tokens are left out; plan records that do not
- * fit the call set PKV_DEVERR_BAD_PLAN and are skipped.  plan_ints, slots and
- * num_ctas are pkv_shared_plan's.
+ * PKV_DEVERR_BAD_BLOCK and its tokens are left out.  plan_ints, slots and
+ * num_ctas are pkv_shared_plan's.  A prefix_plan made for another call (its B,
+ * num_ctas, Hkv, Hq/Hkv, or more partials than slots), or one whose records
+ * leave partials out, sets PKV_DEVERR_BAD_PLAN and the rows attend over their
+ * own tokens alone; so does a row whose prefix lies outside prefix_tables.
+ * Where a wait of the prefix kernel gives up (PKV_DEVERR_TIMEOUT), the rows
+ * with a prefix are NaN.  Records of `plan` that do not fit set
+ * PKV_DEVERR_BAD_PLAN and are skipped (their rows' outputs are then incomplete).
  */
 int pkv_decode_attn_shared(const pkv_shared_args *args, void *stream);
 

@@ -46,6 +46,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr float kLazy = 8.0f;
 constexpr int kHalf = 2;                      // 32-token pieces of P after which P V starts
 constexpr long long kDrainCycles = 1ll << 31;
+constexpr long long kPollLimit = 4096;
 
 template <int D>
 struct Lay {
@@ -197,16 +198,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// An mbarrier wait that gives up when another role has, or after the limit.
+// An mbarrier wait that gives up when another role has, or after the limit.  POLL: for
+// limits shorter than the time for which try_wait may suspend the thread (a build of its
+// own: asking at every wait cost 4 % of the kernel).
+template <bool POLL>
 struct Waiter {
   volatile int *abort;
   int32_t *err;
   long long limit;
+  __device__ __forceinline__ bool done(uint64_t *bar, uint32_t parity) const {
+    return POLL ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  }
   __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done(bar, parity)) return true;
     const long long t0 = clock64();
     for (;;) {
-      if (mbar_try_wait(bar, parity)) return true;
+      if (done(bar, parity)) return true;
       if (*abort) return false;
       if (clock64() - t0 > limit) {
         *abort = 1;
@@ -221,7 +228,7 @@ struct Waiter {
   }
 };
 
-template <int D>
+template <int D, bool POLL>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ PrefixParams p) {
@@ -237,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *turn = s_full + 9, *p_half = s_full + 11;   // [2] each
   int *rows_s = reinterpret_cast<int *>(smem + L::kRows);   // [256] batch row, [256] slot
   float *sums_s = reinterpret_cast<float *>(smem + L::kSums);
-  volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);   // abort, tmem, bad pages [2]
+  volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);
+  // misc: a wait gave up, tmem, bad pages [2], a row does not fit, partials or kPrefixSkipped
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (tid == 0) {
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&turn[0], 1);
     mbar_init(&turn[1], 1);
     misc[0] = 0;
-    misc[2] = misc[3] = 0;
+    misc[2] = misc[3] = misc[4] = misc[5] = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -278,18 +286,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   // the plan's header and this CTA's items
   const int *ctas = p.plan + plan_ctas_at(p.B);
-  int n_planned, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
-  const bool plan_ok = prefix_plan_ok(p, &n_planned);
-  i0 = uniform(plan_ok ? max(0, i0) : 0);
-  i1 = uniform(plan_ok ? min(n_planned, i1) : 0);
-  if (!plan_ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+  int i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
+  const PlanHeader head = plan_header(p.plan, p.B, p.C, p.Hkv, p.G, p.plan_ints, p.slots);
+  i0 = uniform(head.ok ? max(0, i0) : 0);
+  i1 = uniform(head.ok ? min(head.items, i1) : 0);
+  if (!head.ok && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(static_cast<uint32_t>(misc[1]));
   // (by arithmetic: arrays indexed by the slot would live in local memory)
   auto tS = [tmem](int m) { return tmem + 128u * m; };
   auto tO = [tmem](int m) { return tmem + 256u + 128u * m; };
-  const Waiter wait{misc, p.err, p.wait_limit};
+  const Waiter<POLL> wait{misc, p.err, p.wait_limit};
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -297,10 +305,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ======================= producer =======================
       int x = 0;                     // tiles of the items before
       int armed_k = 0, armed_v = 0;  // tiles whose copies were started
+      int partials = 0;              // of the items, which
+      bool fits = head.ok;           // fit
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
         PrefixItem it;
-        if (!prefix_item(p, i, kTileRowsBf16, &it)) continue;
+        const int kind = prefix_item(p, i, kTileRowsBf16, &it);
+        partials += it.rows;
+        if (kind != kItemOk) {
+          if (lane == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+          if (kind == kItemBad || __any_sync(0xffffffffu, !prefix_unread(p, it, lane, 32))) fits = false;
+          continue;
+        }
         const int32_t *table = p.tables + static_cast<size_t>(it.prefix) * p.pt_stride;
         const int tiles = (it.t1 - it.t0 + kTile - 1) / kTile;
         auto page_id = [&](int t) {   // block of page `lane` of tile t (-1: no such page)
@@ -337,6 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         x += tiles;
       }
+      // (the account of the items is kept here: in a warp of its own, or at the head of the
+      // softmax, it took 2 us of 137)
+      if (lane == 0) misc[5] = fits ? partials : kPrefixSkipped;
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, armed_k - NS); n < armed_k; ++n)
         mbar_wait_bounded(&k_full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
@@ -353,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = i0; i < i1 && ok; ++i) {
         PrefixItem it;
-        if (!uniform(prefix_item(p, i, kTileRowsBf16, &it) ? 1 : 0)) continue;
+        if (uniform(prefix_item(p, i, kTileRowsBf16, &it)) != kItemOk) continue;
         it.t0 = uniform(it.t0);
         it.t1 = uniform(it.t1);
         it.rows = uniform(it.rows);
@@ -492,10 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (int i = i0; i < i1 && ok; ++i) {
       PrefixItem it;
-      if (!prefix_item(p, i, kTileRowsBf16, &it)) {
-        if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
-        continue;
-      }
+      if (prefix_item(p, i, kTileRowsBf16, &it) != kItemOk) continue;
       const int total = it.rows * p.G;
       const int tiles = (it.t1 - it.t0 + kTile - 1) / kTile;
       const bool two = total > kTile;
@@ -509,10 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid < total) {
           int slot;
           row = prefix_row(p, it, tid / p.G, &slot);
-          if (row < 0)
+          if (row < 0) {
             set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
-          else
+            misc[4] = 1;
+          } else {
             at = slot * p.Hq + it.g * p.G + tid % p.G;
+          }
         }
         rows_s[tid] = row;
         rows_s[kSoftmax + tid] = at;
@@ -707,16 +725,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
+  if (tid == 0)
+    p.status[blockIdx.x] = misc[0] ? kPrefixGaveUp : misc[4] ? kPrefixSkipped : misc[5];
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
 }
 
-template <int D>
+template <int D, bool POLL>
 cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
                    cudaStream_t s) {
-  auto kern = prefix_tc_kernel<D>;
+  auto kern = prefix_tc_kernel<D, POLL>;
   static std::atomic<unsigned long long> attrs_set{0};
   cudaError_t e = set_attributes_once(attrs_set, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
@@ -729,7 +749,9 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixPar
 
 cudaError_t launch_prefix_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
                                int D, cudaStream_t s) {
-  return D == 64 ? launch<64>(tk, tv, p, s) : launch<128>(tk, tv, p, s);
+  if (p.wait_limit <= kPollLimit)
+    return D == 64 ? launch<64, true>(tk, tv, p, s) : launch<128, true>(tk, tv, p, s);
+  return D == 64 ? launch<64, false>(tk, tv, p, s) : launch<128, false>(tk, tv, p, s);
 }
 
 }  // namespace pkv

@@ -25,7 +25,8 @@ struct Lay {
   static constexpr int kQ = 2 * kStage;                // [64][D]
   static constexpr int kOk = kQ + kRows * D;           // [2][32] token counts (int)
   static constexpr int kRow = kOk + 2 * kTok;          // [64] batch row, [64] slot (int)
-  static constexpr int kFloats = kRow + 2 * kRows;
+  static constexpr int kState = kRow + 2 * kRows;      // something did not fit, partials (int)
+  static constexpr int kFloats = kState + 2;
 };
 
 __device__ __forceinline__ void copy16(float *dst, const float *src, bool on) {   // zeros if not
@@ -91,22 +92,32 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_f32_kernel(const PrefixPar
   float *qs = sm + L::kQ;
   int *ok_s = reinterpret_cast<int *>(sm + L::kOk);
   int *rows = reinterpret_cast<int *>(sm + L::kRow), *slots = rows + kRows;
+  volatile int *state = reinterpret_cast<volatile int *>(sm + L::kState);
   const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int *ctas = p.plan + plan_ctas_at(p.B);
-  int n_items, i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
-  if (!prefix_plan_ok(p, &n_items)) {
-    if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+  int i0 = ctas[blockIdx.x], i1 = ctas[blockIdx.x + 1];
+  const PlanHeader head = plan_header(p.plan, p.B, p.C, p.Hkv, p.G, p.plan_ints, p.slots);
+  if (!head.ok) {
+    if (tid == 0) {
+      set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+      p.status[blockIdx.x] = kPrefixSkipped;
+    }
     return;
   }
   i0 = max(0, i0);
-  i1 = min(n_items, i1);
+  i1 = min(head.items, i1);
+  if (tid == 0) state[0] = state[1] = 0;
+  __syncthreads();
   for (int i = i0; i < i1; ++i) {
     PrefixItem it;
-    if (!prefix_item(p, i, kTileRowsF32, &it)) {
+    const int fits = prefix_item(p, i, kTileRowsF32, &it);
+    if (tid == 0) state[1] = state[1] + it.rows;   // (not read where the item is kItemBad)
+    if (fits != kItemOk) {
       if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+      if (fits == kItemBad || !prefix_unread(p, it, tid, kWarps * 32)) state[0] = 1;
       continue;
     }
     const int total = it.rows * p.G;   // at most 64
@@ -148,7 +159,10 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_f32_kernel(const PrefixPar
       int row = -1, slot = -1;
       if (tid < total) {
         row = prefix_row(p, it, tid / p.G, &slot);
-        if (row < 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+        if (row < 0) {
+          set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+          state[0] = 1;
+        }
       }
       rows[tid] = row;
       slots[tid] = slot;
@@ -208,6 +222,8 @@ __global__ void __launch_bounds__(kWarps * 32) prefix_f32_kernel(const PrefixPar
       if (lane == 0) p.lse[at] = part_lse(st.mx[r], sum);
     }
   }
+  __syncthreads();
+  if (tid == 0) p.status[blockIdx.x] = state[0] ? kPrefixSkipped : state[1];
 }
 
 template <int D>

@@ -28,7 +28,7 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct SharedSpace {
-  size_t lse2, own_lse, own_o, pre_lse, pre_o, bytes;   // offsets behind the attention workspace
+  size_t lse2, own_lse, own_o, status, pre_lse, pre_o, bytes;   // offsets behind the attention workspace
 };
 
 SharedSpace shared_space(size_t attn_bytes, int B, int Hq, int d, int slots) {
@@ -36,7 +36,8 @@ SharedSpace shared_space(size_t attn_bytes, int B, int Hq, int d, int slots) {
   s.lse2 = align256(attn_bytes);
   s.own_lse = s.lse2 + align256(static_cast<size_t>(B) * Hq * sizeof(float));
   s.own_o = s.own_lse + align256(static_cast<size_t>(B) * Hq * sizeof(float));
-  s.pre_lse = s.own_o + (slots > 0 ? align256(static_cast<size_t>(B) * Hq * d * sizeof(float)) : 0);
+  s.status = s.own_o + (slots > 0 ? align256(static_cast<size_t>(B) * Hq * d * sizeof(float)) : 0);
+  s.pre_lse = s.status + (slots > 0 ? kMaxPlanCtas * sizeof(int32_t) : 0);
   s.pre_o = s.pre_lse + align256(static_cast<size_t>(slots) * Hq * sizeof(float));
   s.bytes = s.pre_o + align256(static_cast<size_t>(slots) * Hq * d * sizeof(float));
   return s;
@@ -48,32 +49,48 @@ SharedSpace shared_space(size_t attn_bytes, int B, int Hq, int d, int slots) {
 // a float4 column each; the reads of eight partials go out together.  Bound by L2
 // latency: the partials were just written (64 rows of 32 heads of 128, 17 MB: 6 us
 // behind the kernel before it).
+//
+// The partials count only if every one of the plan's was stored by this call's prefix
+// kernel, which its CTAs' status tells: otherwise what lies there may be an earlier
+// call's.  A plan that does not fit leaves the rows their own tokens; where a wait gave
+// up, the rows behind prefixes are NaN.
 struct JoinParams {
-  const int32_t *row_part;
+  const int32_t *plan, *status;
   const float *own_o, *own_lse, *pre_o, *pre_lse;
   void *out;
   float *lse2, *lse_out;
   int32_t *err;
-  int rows, Hq, slots;   // rows: B * Hq
+  int rows, B, Hq, Hkv, C, n_prefixes, pt_stride, plan_ints, slots;   // rows: B * Hq
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   pdl_launch_dependents();
   constexpr int LPR = D / 4, K = 8;
-  const int u = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, d4 = threadIdx.x % LPR;
-  if (u >= p.rows) {
-    pdl_wait();
-    return;
-  }
+  __shared__ uint32_t sums[8], flags[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int at_row = blockIdx.x * (256 / LPR) + tid / LPR, d4 = tid % LPR;
+  const bool on_row = at_row < p.rows;
+  const int u = on_row ? at_row : 0;
   const int b = u / p.Hq, h = u - b * p.Hq;
-  const int2 part = *reinterpret_cast<const int2 *>(p.row_part + 4 * b);
-  int n = part.y;
-  if (n < 0 || part.x < 0 || n > p.slots - part.x) {   // never read outside the workspace
-    if (n != 0 && d4 == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
-    n = 0;
-  }
+  const PlanHeader head = plan_header(p.plan, p.B, p.C, p.Hkv, p.Hq / p.Hkv, p.plan_ints, p.slots);
+  const int4 part = *reinterpret_cast<const int4 *>(p.plan + plan_rows_at() + 4 * b);
+  const bool fits = head.ok && plan_row_ok(part, p.n_prefixes, p.pt_stride, head.slots);
+  const int n = fits ? part.y : 0;
   pdl_wait();   // the partials come from the kernels before this one
+  uint32_t done = 0;
+  int worst = 0;
+  if (warp == 0)
+    for (int c0 = 0; c0 < p.C; c0 += 256) {
+      int s[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] = c0 + 32 * q + lane < p.C ? __ldcg(p.status + c0 + 32 * q + lane) : 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        done += static_cast<uint32_t>(max(s[q], 0));
+        worst |= s[q] == kPrefixGaveUp ? 2 : s[q] < 0 ? 1 : 0;
+      }
+    }
   MergeAcc a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   float l1[1] = {__ldcg(p.own_lse + u)};
   float4 v1[1] = {__ldcg(reinterpret_cast<const float4 *>(p.own_o + static_cast<size_t>(u) * D) + d4)};
@@ -89,7 +106,27 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     }
     merge_acc_add<K>(a, l, v);
   }
+  // (the status last: the partials' reads need not wait for it)
+  if (warp == 0) {
+    done = __reduce_add_sync(0xffffffffu, done);
+    worst = __reduce_or_sync(0xffffffffu, worst);
+    if (lane == 0) {
+      sums[0] = done;
+      flags[0] = worst;
+    }
+  }
+  __syncthreads();
+  done = sums[0];
+  worst = flags[0];
+  // (both sides modulo 2^32)
+  const bool whole = worst == 0 && done == static_cast<uint32_t>(head.slots) * p.Hkv;
+  if (!whole || !fits) {
+    a = MergeAcc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (worst < 2 && d4 == 0 && on_row) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+  }
   merge_acc_add<1>(a, l1, v1);
+  if (worst >= 2 && n > 0) a.den = __int_as_float(0x7fffffff);
+  if (!on_row) return;
   keep_nan(a);
   merge_store<T>(static_cast<T *>(p.out) + static_cast<size_t>(u) * D, d4, D, a);
   if (d4 == 0) {
@@ -300,7 +337,7 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
       rc = current_sms(&C);
       if (rc != PKV_OK) return rc;
     }
-    PKV_REQUIRE(C <= 4096, PKV_ERR_INVALID_ARG, "num_ctas must be <= 4096");
+    PKV_REQUIRE(C <= kMaxPlanCtas, PKV_ERR_INVALID_ARG, "num_ctas must be <= %d", kMaxPlanCtas);
     PKV_REQUIRE(a->prefix_plan && (reinterpret_cast<uintptr_t>(a->prefix_plan) & 15) == 0,
                 PKV_ERR_INVALID_ARG, "prefix_plan must be given, 16-byte aligned");
     PKV_REQUIRE(a->pt_stride > 0 && a->pt_stride < (1 << 26), PKV_ERR_INVALID_ARG, "pt_stride %d",
@@ -348,6 +385,8 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
       p.num_blocks = a->num_blocks;
       p.n_prefixes = a->n_prefixes;
       p.pt_stride = prefixes ? a->pt_stride : 0;
+      p.plan_ints = a->plan_ints;
+      p.slots = slots;
       p.bt_stride = a->bt_stride;
       p.bias_stride = a->attn_bias ? a->bias_stride : 0;
       p.scale_log2 = a->scale * kLog2e;
@@ -371,6 +410,7 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     p.plan = a->prefix_plan;
     p.lse = reinterpret_cast<float *>(ws + sp.pre_lse);
     p.o = reinterpret_cast<float *>(ws + sp.pre_o);
+    p.status = reinterpret_cast<int32_t *>(ws + sp.status);
     p.err = a->dev_err_flag;
     p.B = a->B;
     p.Hq = a->Hq;
@@ -406,7 +446,8 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
   float *lse2 = reinterpret_cast<float *>(ws + sp.lse2);
   if (ext.own_o) {
     JoinParams j;
-    j.row_part = a->prefix_plan + plan_rows_at();
+    j.plan = a->prefix_plan;
+    j.status = reinterpret_cast<const int32_t *>(ws + sp.status);
     j.own_o = ext.own_o;
     j.own_lse = ext.lse2;
     j.pre_o = reinterpret_cast<const float *>(ws + sp.pre_o);
@@ -416,7 +457,13 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
     j.lse_out = a->lse_out;
     j.err = a->dev_err_flag;
     j.rows = a->B * a->Hq;
+    j.B = a->B;
     j.Hq = a->Hq;
+    j.Hkv = a->Hkv;
+    j.C = C;
+    j.n_prefixes = a->n_prefixes;
+    j.pt_stride = a->pt_stride;
+    j.plan_ints = a->plan_ints;
     j.slots = slots;
     const int per_cta = 256 / (a->d / 4);
     const unsigned grid = static_cast<unsigned>((j.rows + per_cta - 1) / per_cta);

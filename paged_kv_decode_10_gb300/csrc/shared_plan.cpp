@@ -53,7 +53,8 @@ int check(int32_t B, int32_t n_prefixes, int32_t Hq, int32_t Hkv, int32_t *num_c
   const int G = Hq / Hkv;
   PKV_REQUIRE(G == 1 || G == 2 || G == 4 || G == 8, PKV_ERR_UNSUPPORTED,
               "group size %d (built: 1, 2, 4, 8)", G);
-  PKV_REQUIRE(*num_ctas <= 4096, PKV_ERR_INVALID_ARG, "num_ctas must be <= 4096");
+  PKV_REQUIRE(*num_ctas <= pkv::kMaxPlanCtas, PKV_ERR_INVALID_ARG, "num_ctas must be <= %d",
+              pkv::kMaxPlanCtas);
   if (*num_ctas <= 0) {
     int sms = 0;
     const int rc = pkv::current_sms(&sms);

@@ -10,6 +10,7 @@ namespace pkv {
 // item of every CTA, then (at a multiple of 4) items of kPlanItem words.
 constexpr int32_t kSharedMagic = 0x53506c31;
 constexpr int kPlanHead = 16;   // magic, items, B, slots, C, Hkv, G, rows per tile
+constexpr int kMaxPlanCtas = 4096;
 constexpr int kPlanItem = 8;    // prefix, KV head, first in the row list, rows, t0, t1, split
 
 inline __host__ __device__ int plan_rows_at() { return kPlanHead; }
