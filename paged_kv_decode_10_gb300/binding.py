@@ -777,7 +777,9 @@ def dense_extract(k_dense, v_dense, cap, rows, prefix_lens, padded_len, steps, k
 # --------------------------------------------------------------------------
 # These calls take argument structs made once (``make_*_args``: every pointer,
 # size and type is checked there) and launched as often as wanted; the struct
-# keeps its tensors alive.
+# keeps its tensors alive.  What a call makes itself (outputs, workspaces) is made on
+# the stream that is current: prepare a struct on the stream that it is launched on, or
+# order the two.  The calls that prepare and launch in one do that for their ``stream``.
 def _want(t, name, shape=None, dtype=None, device=None, host=False):
     """The checked address of a dense tensor: shape (None: any size there), type
     and device as stated; ``host`` allows pinned host memory read in place."""
@@ -934,12 +936,13 @@ def rotary_append(rotary, q, k, v, positions, slot_mapping=None, k_cache=None, v
     """Rotates ``q`` and ``k`` at ``positions`` and, with ``slot_mapping``, writes
     the rotated keys and the values into the cache slots; returns ``(q_out, k_out)``."""
     torch = _torch()
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    rotary_append_args(make_rotary_args(rotary, q, k, v, positions, q_out, k_out, slot_mapping,
-                                        k_cache, v_cache, err), stream)
+    with torch.cuda.stream(stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        rotary_append_args(make_rotary_args(rotary, q, k, v, positions, q_out, k_out, slot_mapping,
+                                            k_cache, v_cache, err), stream)
     return q_out, k_out
 
 
@@ -1079,9 +1082,11 @@ def decode_attention_shared(q_rot, k_cache, v_cache, block_tables, seq_lens, sca
                             stream=None, **kw):
     """Attention over shared prefixes and own tokens: returns ``out [B,Hq,d]`` (see
     ``make_shared_args`` for the rest)."""
-    out = _torch().empty_like(q_rot) if out is None else out
-    args = make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out, **kw)
-    decode_attn_shared_args(args, stream)
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        out = torch.empty_like(q_rot) if out is None else out
+        args = make_shared_args(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, out, **kw)
+        decode_attn_shared_args(args, stream)
     return out
 
 
@@ -1134,11 +1139,13 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, max_keep, s
           kept=None, err=None, stream=None):
     """Evicts rows down to ``keep_lens`` tokens by ``mass``; returns ``kept
     [B,Hkv,max_keep]``, the indices of the tokens kept."""
-    if kept is None:
-        kept = _torch().empty((block_tables.shape[0], k_cache.shape[1], max(int(max_keep), 1)),
-                              dtype=_torch().int32, device=k_cache.device)
-    evict_args(make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept, sink,
-                               recent, err=err), stream)
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        if kept is None:
+            kept = torch.empty((block_tables.shape[0], k_cache.shape[1], max(int(max_keep), 1)),
+                               dtype=torch.int32, device=k_cache.device)
+        evict_args(make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept,
+                                   sink, recent, err=err), stream)
     return kept
 
 
