@@ -513,8 +513,9 @@ def _stream(stream=None):
 def rope(q, k, positions, base=10000.0, q_out=None, k_out=None, stream=None):
     """a1: rotate-half RoPE of ``q [B,Hq,d]`` and ``k [B,Hkv,d]`` at ``positions [B]`` (int32)."""
     torch = _torch()
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None else k_out
+    with torch.cuda.stream(stream):
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        k_out = torch.empty_like(k) if k_out is None else k_out
     B, Hq, d = q.shape
     _check(load().pkv_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _meta_ptr(positions), B, Hq,
                            k.shape[1], d, float(base), dtype_code(q), _stream(stream)))
@@ -525,8 +526,9 @@ def rope_append(q, k, v, positions, slot_mapping, k_cache, v_cache, base=10000.0
                 k_out=None, err=None, stream=None):
     """a1 + a2 fused: rotate q/k and write the rotated k and raw v into the cache slots."""
     torch = _torch()
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None else k_out
+    with torch.cuda.stream(stream):
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        k_out = torch.empty_like(k) if k_out is None else k_out
     B, Hq, d = q.shape
     _check(load().pkv_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out),
                                   _meta_ptr(positions), _meta_ptr(slot_mapping), _ptr(k_cache),
@@ -670,10 +672,11 @@ def decode_attention(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, num
     Hkv = k_cache.shape[1]
     if num_parts is None:
         num_parts = default_parts(d, dtype_code(q_rot), flags, Hq, Hkv)
-    if workspace is None:
-        workspace = alloc_workspace(B, Hq, Hkv, d, num_parts, q_rot.device)
-    if out is None:
-        out = torch.empty_like(q_rot)
+    with torch.cuda.stream(stream):   # (scratch of the stream that the kernels run on)
+        if workspace is None:
+            workspace = alloc_workspace(B, Hq, Hkv, d, num_parts, q_rot.device)
+        if out is None:
+            out = torch.empty_like(q_rot)
     if plan is not None:
         decode_attn_planned(q_rot, k_cache, v_cache, block_tables, seq_lens, scale, num_parts,
                             plan, workspace, out, attn_bias, flags, err, stream)

@@ -3,6 +3,7 @@ the zero fill of a workspace is then ordered before the kernels, and the allocat
 the memory to nobody else while they run.  Checked on the host, with torch's stream
 context and allocations watched and the launches replaced."""
 import contextlib
+from unittest import mock
 
 import pytest
 import torch
@@ -78,3 +79,31 @@ def test_rotary_append_allocates_on_its_stream(bind, watched, monkeypatch, strea
     log.clear()
     bind.rotary_append(None, q, q, None, None, stream=stream)
     check(log, stream, "empty", "make_rotary_args", "rotary_append_args")
+
+
+@pytest.mark.parametrize("stream", ["side", None])
+@pytest.mark.parametrize("name", ["rope", "rope_append"])
+def test_rope_allocates_on_its_stream(bind, watched, monkeypatch, stream, name):
+    now, log = watched
+    monkeypatch.setattr(bind, "load", lambda: mock.MagicMock())
+    monkeypatch.setattr(bind, "_check", lambda rc: None)
+    for f in ("_stream", "_ptr", "_meta_ptr"):
+        monkeypatch.setattr(bind, f, lambda *a: None)
+    q, cache = torch.ones(2, 4, 64), torch.ones(4, 4, 16, 64)
+    log.clear()
+    if name == "rope":
+        bind.rope(q, q, None, stream=stream)
+    else:
+        bind.rope_append(q, q, q, None, None, cache, cache, stream=stream)
+    check(log, stream, "empty_like")
+
+
+@pytest.mark.parametrize("stream", ["side", None])
+def test_attention_allocates_on_its_stream(bind, watched, monkeypatch, stream):
+    now, log = watched
+    replace(bind, monkeypatch, log, now, "alloc_workspace")
+    monkeypatch.setattr(bind, "decode_attn_split", lambda *a: None)
+    q, cache = torch.ones(2, 4, 64), torch.ones(4, 2, 16, 64)
+    log.clear()
+    bind.decode_attention(q, cache, cache, None, None, 1.0, num_parts=4, stream=stream)
+    check(log, stream, "empty_like", "alloc_workspace")
