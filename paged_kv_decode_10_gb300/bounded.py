@@ -211,7 +211,7 @@ class BoundedDecoder(PagedDecoder):
         if key == self._plan_key:
             self._rows_now = seq_ids
             return
-        slots, self._prefix_args = 0, {}
+        slots, args = 0, {}
         if used:
             at = {p: i for i, p in enumerate(used)}
             lens = [self._prefixes[p] for p in used]
@@ -222,16 +222,18 @@ class BoundedDecoder(PagedDecoder):
             for i, b in enumerate(blocks):
                 tables[i, :len(b)] = b
             slots = int(plan[3])
-            self._prefix_args = dict(prefix_tables=torch.from_numpy(tables).to(self.device),
-                                     prefix_plan=torch.from_numpy(plan).to(self.device),
-                                     slots=slots, num_ctas=int(plan[4]))
+            args = dict(prefix_tables=torch.from_numpy(tables).to(self.device),
+                        prefix_plan=torch.from_numpy(plan).to(self.device), slots=slots,
+                        num_ctas=int(plan[4]))
         parts = max(self.num_parts, binding.shared_default_parts(
             len(rows), self.Hq, self.Hkv, self.d, self._code, self.bt_stride))
         need = binding.shared_workspace_bytes(len(rows), self.Hq, self.Hkv, self.d, parts, slots)
         # a workspace of these rows' own, zero-filled once: the counters' place in it
         # depends on the number of rows
-        self._space = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        self._plan_key, self._calls, self._rows_now = key, {}, seq_ids
+        space = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        # (all of it or, where something above raised, nothing)
+        self._prefix_args, self._space, self._calls = args, space, {}
+        self._plan_key, self._rows_now = key, seq_ids
 
     def _prepared(self, B, q, k, v):
         """The calls of every layer on the metadata buffer of this step, made once for

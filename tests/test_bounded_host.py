@@ -43,3 +43,48 @@ def test_rope_base_reaches_the_rotary_table(bind, make):
 def test_rope_base_beside_a_rotary_is_refused(bind, make):
     with pytest.raises(ValueError):
         make(rotary=bind.Rotary(64), rope_base=500000.0)
+
+
+@pytest.fixture
+def two_prefixes(bind, make, monkeypatch):
+    """A decoder with two prefixes and a sequence behind each."""
+    real = bind.shared_plan
+    monkeypatch.setattr(bind, "shared_plan", lambda *a: real(*a, num_ctas=8))
+    dec = make()
+    monkeypatch.setattr(dec, "_write", lambda *a: None)
+    prefixes = [dec.add_prefix(*[torch.zeros((n, 2, 64))] * 2) for n in (40, 100)]
+    return dec, [dec.join(prefix=p) for p in prefixes]
+
+
+@pytest.mark.parametrize("what", ["plan", "tables", "workspace bytes", "workspace"])
+def test_a_plan_that_cannot_be_made_leaves_the_last_one(bind, two_prefixes, monkeypatch, what):
+    dec, (a, b) = two_prefixes
+    dec._prefix_state([a])
+    dec._calls["buffer"] = "calls"
+    state = {k: getattr(dec, k) for k in ("_prefix_args", "_space", "_calls", "_plan_key", "_rows_now")}
+    args = dict(dec._prefix_args)
+    assert args["prefix_tables"].shape == (1, 3)
+
+    def fail(*a, **kw):
+        raise RuntimeError("out of memory")
+
+    with monkeypatch.context() as m:
+        if what == "plan":
+            m.setattr(bind, "shared_plan", fail)
+        elif what == "tables":
+            m.setattr(dec.alloc, "seq_blocks", fail)
+        elif what == "workspace bytes":
+            m.setattr(bind, "shared_workspace_bytes", fail)
+        else:
+            m.setattr(torch, "zeros", fail)
+        with pytest.raises(RuntimeError):
+            dec._prefix_state([b])
+    assert all(getattr(dec, k) is v for k, v in state.items())
+    assert dec._prefix_args.keys() == args.keys()
+    assert all(dec._prefix_args[k] is v for k, v in args.items())
+    assert dec._calls == {"buffer": "calls"}
+    dec._prefix_state([a])                    # the last batch again: nothing was lost
+    assert dec._prefix_args is state["_prefix_args"] and dec._calls == {"buffer": "calls"}
+    dec._prefix_state([b])
+    assert dec._prefix_args["prefix_tables"].shape == (1, 7) and dec._calls == {}
+    assert dec._rows_now == [b]
