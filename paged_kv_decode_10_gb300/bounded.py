@@ -25,7 +25,8 @@ class BoundedDecoder(PagedDecoder):
     ``binding.Rotary`` (default: the whole head, plain, at ``rope_base``).  ``decay``: factor on the
     weight accumulated so far at every step.  ``max_prefixes`` prefixes of up to
     ``max_prefix_len`` tokens may be live.  The rest as ``PagedDecoder``; its captured
-    forms and additive masks are not offered here."""
+    forms, additive masks, layer chains (``layer_merge_helpers``) and flags other than
+    ``ATTN_CHECK_PLAN`` and ``ATTN_SHORT_WAITS`` are not offered here."""
 
     def __init__(self, num_blocks, Hq, Hkv, d, dtype, max_seqs, budget, slack=64, sink=4,
                  recent=None, rotary=None, decay=1.0, max_prefixes=16, max_prefix_len=131072, **kw):
@@ -39,12 +40,17 @@ class BoundedDecoder(PagedDecoder):
             raise ValueError("max_prefixes and max_prefix_len must not be negative")
         if rotary is not None and kw.get("rope_base") is not None:
             raise ValueError("rotary states its own base: give rope_base or rotary")
+        if kw.get("flags", 0) & ~(binding.ATTN_CHECK_PLAN | binding.ATTN_SHORT_WAITS):
+            raise ValueError(f"flags {kw['flags']}: only ATTN_CHECK_PLAN and ATTN_SHORT_WAITS")
+        if kw.get("layer_merge_helpers") is not None:
+            raise ValueError("layer_merge_helpers: the layers are not launched as a chain")
         need = -(-(budget + slack) // binding.BLOCK_SIZE)
         bt = kw.pop("max_blocks_per_seq", need)
         if bt < need:
             raise ValueError(f"max_blocks_per_seq must be at least {need}")
         self._code = binding.F32 if dtype == "f32" else binding.BF16
-        if kw.get("num_parts") is None:
+        self._parts_given = bool(kw.get("num_parts"))
+        if not self._parts_given:
             kw["num_parts"] = binding.shared_default_parts(max_seqs, Hq, Hkv, d, self._code, bt)
         self.max_rows = max_seqs
         super().__init__(num_blocks, Hq, Hkv, d, dtype, max_seqs, bt, **kw)
@@ -241,8 +247,9 @@ class BoundedDecoder(PagedDecoder):
         key = self.positions.data_ptr()     # (one of the decoder's own buffers)
         if key not in self._calls:
             ptab = self._prefix_args.get("prefix_tables")
-            short = binding.shared_short(B, self.Hq, self.Hkv, self.d, self._code, self.bt_stride,
-                                         0 if ptab is None else ptab.shape[1])
+            short = (not self._parts_given and not self.flags
+                     and binding.shared_short(B, self.Hq, self.Hkv, self.d, self._code, self.bt_stride,
+                                              0 if ptab is None else ptab.shape[1]))
             parts = {} if short else dict(plan=self.plan, num_parts=self.num_parts)
             self._calls[key] = [(binding.make_rotary_args(
                 self.rotary, q[layer], k[layer], v[layer], self.positions,
@@ -251,8 +258,8 @@ class BoundedDecoder(PagedDecoder):
                 v_cache=self.v_caches[layer], err=self.err), binding.make_shared_args(
                 self.q_rots[layer, :B], self.k_caches[layer], self.v_caches[layer], self.tables,
                 self.seq_lens, self.scale, self.outs[layer, :B], mass=self.masses[layer],
-                scores=self.scores, decay=self.decay, workspace=self._space, err=self.err, **parts,
-                **self._prefix_args))
+                scores=self.scores, decay=self.decay, workspace=self._space, flags=self.flags,
+                err=self.err, **parts, **self._prefix_args))
                 for layer in range(self.n_layers)]
         return self._calls[key]
 

@@ -88,3 +88,36 @@ def test_a_plan_that_cannot_be_made_leaves_the_last_one(bind, two_prefixes, monk
     dec._prefix_state([b])
     assert dec._prefix_args["prefix_tables"].shape == (1, 7) and dec._calls == {}
     assert dec._rows_now == [b]
+
+
+def test_arguments_that_do_not_reach_the_step_are_refused(bind, make):
+    for flags in (bind.ATTN_SIMT, bind.ATTN_SEPARATE_MERGE, bind.STEP_FUSED,
+                  bind.ATTN_CHECK_PLAN | bind.ATTN_SIMT, 1 << 20):
+        with pytest.raises(ValueError):
+            make(flags=flags)
+    for helpers in (True, False):
+        with pytest.raises(ValueError):
+            make(layer_merge_helpers=helpers)
+    make(flags=bind.ATTN_CHECK_PLAN, layer_merge_helpers=None)
+
+
+@pytest.mark.parametrize("kw,short", [(dict(), True), (dict(num_parts=0), True),
+                                      (dict(num_parts=5), False), (dict(flags=16), False)])
+def test_flags_and_partition_reach_the_calls(bind, make, monkeypatch, kw, short):
+    """A stated partition and flags exclude the form for short contexts, as in the call."""
+    assert bind.ATTN_CHECK_PLAN == 16
+    dec = make(**kw)
+    seen = []
+    monkeypatch.setattr(bind, "make_rotary_args", lambda *a, **k: None)
+    monkeypatch.setattr(bind, "make_shared_args", lambda *a, **k: seen.append(k))
+    x = torch.zeros(1, 4, 8, 64)
+    dec.q_rots = dec.k_rots = dec.outs = x
+    dec.k_caches = dec.v_caches = dec.masses
+    dec.positions = dec.slots = dec.tables = dec.seq_lens = torch.zeros(4)
+    dec.plan, dec.err = "plan", None
+    dec._prepared(1, x[:, :1], x[:, :1], x[:, :1])
+    assert len(seen) == 1 and seen[0]["flags"] == kw.get("flags", 0)
+    if short:
+        assert "num_parts" not in seen[0] and "plan" not in seen[0]
+    else:
+        assert seen[0]["plan"] == "plan" and seen[0]["num_parts"] == kw.get("num_parts", 4)

@@ -7,7 +7,7 @@ import torch
 
 from helpers import dev, f64
 from oracle import cache_ops
-from paged_kv_decode_10_gb300 import workloads
+from paged_kv_decode_10_gb300 import binding, workloads
 from paged_kv_decode_10_gb300.bounded import BoundedDecoder
 from test_gpu_bounded import Replay
 
@@ -49,3 +49,22 @@ def test_rope_base_against_a_replay(dtype):
         err = np.abs(out - want).max()
         assert err <= eps * size + u * np.abs(want).max(), (step, err)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_checked_plan_gives_the_same_bits(dtype):
+    """ATTN_CHECK_PLAN reaches the attention call, which finds the decoder's plan right."""
+    outs = []
+    for flags in (0, binding.ATTN_CHECK_PLAN):
+        dec = BoundedDecoder(40, 8, 2, 64, dtype, 3, 24, 8, num_parts=6, flags=flags, device=dev())
+        x = workloads.normal((40, 2, 64), dtype, 1).to(dev())
+        p = dec.add_prefix(x, x.flip(0))
+        ids = [dec.join(prefix=p), dec.join(), dec.join(5, p, x[:5], x[5:10])]
+        for step in range(30):
+            q, k, v = (workloads.normal((3, h, 64), dtype, 50 + 3 * step + i).to(dev())
+                       for i, h in enumerate((8, 2, 2)))
+            out = dec.step(ids, q, k, v).clone()
+        torch.cuda.synchronize()
+        assert dec.device_errors() == 0
+        outs.append(out)
+    assert torch.equal(*outs)
