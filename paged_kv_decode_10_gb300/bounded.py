@@ -163,6 +163,7 @@ class BoundedDecoder(PagedDecoder):
     def evict(self, seq_ids, keep=None, stream=None):
         """Cuts the listed sequences back to ``keep`` (default: the budget) own tokens;
         returns the kept indices ``[L,n,Hkv,keep]`` (-1 behind a shorter sequence's)."""
+        seq_ids = [int(s) for s in seq_ids]
         for s in seq_ids:
             if s not in self._prefix_of:
                 raise binding.UnknownSequence(binding.ERR_UNKNOWN_SEQ, f"sequence {s} is not live")
@@ -172,7 +173,7 @@ class BoundedDecoder(PagedDecoder):
         if keep < 0:
             raise ValueError("keep must not be negative")
         with self._on(stream):
-            return self._evict(list(seq_ids), keep)
+            return self._evict(seq_ids, keep)
 
     def _evict(self, seq_ids, keep):
         torch = self.torch

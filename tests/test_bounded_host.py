@@ -1,6 +1,9 @@
 """``BoundedDecoder`` on the host: what it makes of its arguments and how it keeps its state,
 with the device part of ``PagedDecoder`` replaced by plain attributes."""
 import numpy as np
+import contextlib
+
+import numpy as np
 import pytest
 import torch
 
@@ -121,3 +124,16 @@ def test_flags_and_partition_reach_the_calls(bind, make, monkeypatch, kw, short)
         assert "num_parts" not in seen[0] and "plan" not in seen[0]
     else:
         assert seen[0]["plan"] == "plan" and seen[0]["num_parts"] == kw.get("num_parts", 4)
+
+
+def test_sequences_to_evict_may_come_from_an_iterator(make, monkeypatch):
+    dec = make()
+    ids = [dec.join(20), dec.join(30)]
+    seen = []
+    monkeypatch.setattr(dec, "_on", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(dec, "_evict", lambda s, keep: seen.append((s, keep)))
+    dec.evict(iter(ids), 5)
+    dec.evict(np.array(ids))
+    assert seen == [(ids, 5), (ids, 24)]
+    with pytest.raises(ValueError):
+        dec.evict(iter([ids[0], ids[0]]))
