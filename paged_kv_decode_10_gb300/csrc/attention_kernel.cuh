@@ -1207,17 +1207,20 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       if (bad && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
     }
   }
+  // (a grid that ends has waited for the one before it, whatever it had to do)
   if (start >= end) {
-    pdl_wait();   // (a grid that ends has waited for the one before it, pages or not)
+    pdl_wait();
     return;
   }
   if (use_plan && rec_h.x >= p.B) {   // a record naming no row: never read outside seq_lens
     if (tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
+    pdl_wait();
     return;
   }
   const int first_row = use_plan ? rec_h.x : misc[0];
   if (first_row < 0) {   // no owner of `start` (never expected)
     if (tid == 0) set_dev_err(p.err, PKV_DEVERR_TIMEOUT);
+    pdl_wait();
     return;
   }
 

@@ -33,7 +33,7 @@ def good_plan(c):
     return binding.shared_plan(ROWS, PLENS, HQ, HKV, D, binding.dtype_code(c["q"]), CTAS)
 
 
-def run(c, plan, general, space=None, ptab=None, **kw):
+def run(c, plan, general, space=None, ptab=None, own_plan=None, **kw):
     """The call with this plan, for the sizes of the good one."""
     good = good_plan(c)
     buf = np.zeros(max(len(plan), len(good)) + 512, np.int32)
@@ -49,7 +49,7 @@ def run(c, plan, general, space=None, ptab=None, **kw):
         c["q"], c["kc"], c["vc"], torch.from_numpy(c["tab"]).to(dev()), i32(LENS), c["scale"], out,
         prefix_tables=torch.from_numpy(c["ptab"] if ptab is None else ptab).to(dev()),
         prefix_plan=torch.from_numpy(buf).to(dev()), workspace=space, lse=lse, err=err,
-        num_parts=parts if general else None, **kw)
+        num_parts=parts if general else None, plan=own_plan, **kw)
     binding.decode_attn_shared_args(a)
     torch.cuda.synchronize()
     return out, lse, int(err), space
@@ -167,3 +167,18 @@ def test_rows_behind_a_prefix_kernel_that_gave_up_are_nan(batch):
     err.zero_()
     call(0)
     check_case(c, out, lse, err=int(err))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_records_of_the_own_plan_that_name_no_row(dtype):
+    """The own tokens' CTAs skip such records, behind a prefix kernel too, and leave the
+    workspace as the next call expects it."""
+    c = case(dtype)
+    space = after_a_good_call(c, True)
+    plan = torch.from_numpy(binding.plan_parts(c["lens"], HKV, D, c["tab"], 6))
+    bad = plan.clone()
+    bad[:, 0] = B
+    out, lse, err, _ = run(c, good_plan(c), True, space, own_plan=bad.to(dev()))
+    assert err == binding.DEVERR_BAD_PLAN
+    out, lse, err, _ = run(c, good_plan(c), True, space, own_plan=plan.to(dev()))
+    check_case(c, out, lse, err=err)
