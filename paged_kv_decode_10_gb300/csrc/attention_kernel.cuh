@@ -325,6 +325,18 @@ __device__ __forceinline__ void ext_store(MergeAcc a, const AttnParams &p, int b
   }
 }
 
+// Metadata.  EXT reads it from L2, past the SM's L1: behind the prefix kernel it is read
+// before this grid has waited for that one.  The writers' grid was waited for by the prefix
+// kernel before that released this one; it had then ended and its writes were flushed to L2,
+// where a read that goes there finds them.
+template <bool EXT, typename V>
+__device__ __forceinline__ V read_meta(const V *p) {
+  if constexpr (EXT)
+    return __ldcg(p);
+  else
+    return *p;
+}
+
 // EXT: a row without own tokens.
 template <typename T>
 __device__ __forceinline__ void ext_empty_row(const AttnParams &p, int b, int D, int tid, int nthr) {
@@ -570,13 +582,13 @@ __device__ __forceinline__ void mma_page(MmaState<D> &s, const AttnParams &p, ui
     const float *bias = p.bias + static_cast<size_t>(b) * p.bias_stride + t0;
     bool ex0 = false, ex1 = false;
     if (r < valid) {
-      const float x = bias[r] * kLog2e;
+      const float x = read_meta<EXT>(bias + r) * kLog2e;
       ex0 = x == -INFINITY;
       sc[0] += x;
       sc[1] += x;
     }
     if (r + 8 < valid) {
-      const float x = bias[r + 8] * kLog2e;
+      const float x = read_meta<EXT>(bias + r + 8) * kLog2e;
       ex1 = x == -INFINITY;
       sc[2] += x;
       sc[3] += x;
@@ -938,7 +950,7 @@ __device__ __forceinline__ void simt_page(SimtState<T, D, G> &s, const AttnParam
   for (int i = 0; i < kBlockTokens; ++i) {
     if (i < valid) {
       if (bias) {
-        const float x = bias[i] * kLog2e;
+        const float x = read_meta<EXT>(bias + i) * kLog2e;
         sc[i] += x;
         if (EXT && x == -INFINITY) {   // whatever it holds, NaN included
           sc[i] = -INFINITY;
@@ -1117,7 +1129,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     int mysum = 0;
     for (int b = r0; b < r1; ++b) {
       bool bad;
-      const int len = p.seq_lens[b];
+      const int len = read_meta<EXT>(p.seq_lens + b);
       if (b < Q::kLensCache) lens_s[b] = len;   // kept for the row search and the producer
       mysum += upos(pages_of_len(len, p.bt_stride, has_bias, p.bias_stride, &bad));
       if (bad && blockIdx.x == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
@@ -1144,7 +1156,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       long long acc = excl;
       for (int b = r0; b < r1; ++b) {
         bool bad;
-        const int len = b < Q::kLensCache ? lens_s[b] : p.seq_lens[b];   // own rows: written above
+        const int len = b < Q::kLensCache ? lens_s[b] : read_meta<EXT>(p.seq_lens + b);   // own rows: written above
         const int n = upos(pages_of_len(len, p.bt_stride, has_bias, p.bias_stride, &bad));
         if (s0 < (acc + n) * p.Hkv) {
           misc[0] = b;
@@ -1175,8 +1187,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     bool same = P_plan == P_dev;
     if (same && div_floor(P_dev * blockIdx.x, C) < div_floor(P_dev * (blockIdx.x + 1), C)) {
       const int b = misc[0];
-      same = b >= 0 && b == rec_h.x && misc[1] == rec_h.y && rec_h.z == p.seq_lens[b] &&
-             (b + 1 >= p.B || rec_h.w == p.seq_lens[b + 1]);
+      same = b >= 0 && b == rec_h.x && misc[1] == rec_h.y &&
+             rec_h.z == read_meta<EXT>(p.seq_lens + b) &&
+             (b + 1 >= p.B || rec_h.w == read_meta<EXT>(p.seq_lens + b + 1));
     }
     if (!same) {
       use_plan = false;
@@ -1196,7 +1209,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
   if ((EXT || !scanned) && warp < NW) {
     for (int b = blockIdx.x; b < p.B; b += C) {
       bool bad;
-      if (pages_of_len(p.seq_lens[b], p.bt_stride, has_bias, p.bias_stride, &bad) == 0) {
+      if (pages_of_len(read_meta<EXT>(p.seq_lens + b), p.bt_stride, has_bias, p.bias_stride, &bad) == 0) {
         if constexpr (EXT) {
           ext_empty_row<T>(p, b, D, tid, NW * 32);
         } else {
@@ -1237,8 +1250,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
     // row lengths: the prologue's copy for the first rows (or the plan's for
     // rows b0 and b0 + 1), read ahead beyond
     const int lc = scanned ? Q::kLensCache : 0;
-    const int rl0 = b0 + lane < p.B && b0 + lane >= lc ? p.seq_lens[b0 + lane] : 0;
-    const int rl1 = b0 + 32 + lane < p.B && b0 + 32 + lane >= lc ? p.seq_lens[b0 + 32 + lane] : 0;
+    const int32_t *ahead = p.seq_lens + b0 + lane;
+    const int rl0 = b0 + lane < p.B && b0 + lane >= lc ? read_meta<EXT>(ahead) : 0;
+    const int rl1 = b0 + 32 + lane < p.B && b0 + 32 + lane >= lc ? read_meta<EXT>(ahead + 32) : 0;
     auto row_len = [&](int b) {   // b is warp-uniform
       if (b < lc) return lens_s[b];
       if (use_plan && b == b0) return rec_h.z;
@@ -1246,7 +1260,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       const int r = b - b0;
       if (r < 32) return __shfl_sync(0xffffffffu, rl0, r);
       if (r < 64) return __shfl_sync(0xffffffffu, rl1, r - 32);
-      return p.seq_lens[b];
+      return read_meta<EXT>(p.seq_lens + b);
     };
     auto advance = [&](UnitCursor &c) {   // the next unit, with the read-ahead lengths
       c.off += c.n + A;
@@ -1305,7 +1319,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       ids = plan_ids;
       chunk = kPlanIds;
     } else {
-      ids = (j0 + lane < j1) ? p.block_tables[static_cast<size_t>(u.b) * p.bt_stride + j0 + lane]
+      ids = (j0 + lane < j1) ? read_meta<EXT>(p.block_tables +
+                                              static_cast<size_t>(u.b) * p.bt_stride + j0 + lane)
                              : -1;
       if (use_plan && lane < kPlanIds && j0 + lane < j1 && plan_ids != ids)
         set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
@@ -1327,7 +1342,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       if (more) {
         advance(nx);
         nj1 = static_cast<int>(min(static_cast<long long>(nx.n), end - nx.off - A));
-        nids = lane < nj1 ? p.block_tables[static_cast<size_t>(nx.b) * p.bt_stride + lane] : -1;
+        nids = lane < nj1 ? read_meta<EXT>(p.block_tables +
+                                           static_cast<size_t>(nx.b) * p.bt_stride + lane)
+                          : -1;
       }
       const int L = row_len(u.b);
       FusedAppend<T, D> app;
@@ -1404,7 +1421,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, KIND == 0 ? 2 : 1)
       };
       for (int jb = j0; jb < j1 && !aborted; jb += chunk, chunk = 32) {
         const int cur_ids = ids;
-        ids = (jb + chunk + lane < j1) ? bt[jb + chunk + lane] : -1;
+        ids = (jb + chunk + lane < j1) ? read_meta<EXT>(bt + jb + chunk + lane) : -1;
         const int cnt = min(chunk, j1 - jb);
         // pages go out kBatch at a time, lane l < kBatch taking page i + l, so
         // the barrier waits, arrivals and TMA issues of a batch share warp

@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_chunk_kernel(const Evic
   const int tid = threadIdx.x;
   const int units = p.B * p.Hkv;
   // (every row's lengths, so that they need not wait for the ticket; the choice's own
-  // wait is over)
-  if (tid < p.B) lens_s[tid] = make_int2(p.seq_lens[tid], p.keep_lens[tid]);
+  // wait was over before it released this kernel: what came before it is in L2)
+  if (tid < p.B) lens_s[tid] = make_int2(__ldcg(p.seq_lens + tid), __ldcg(p.keep_lens + tid));
   pdl_wait();
   if (tid == 0) {
     task_s = atomicAdd(p.ticket, 1);

@@ -36,8 +36,8 @@ struct PlanHeader {
 };
 __device__ __forceinline__ PlanHeader plan_header(const int32_t *plan, int B, int C, int Hkv, int G,
                                                   int plan_ints, int slots) {
-  const int4 *w = reinterpret_cast<const int4 *>(plan);
-  const int4 a = w[0], b = w[1];
+  const int4 *w = reinterpret_cast<const int4 *>(plan);   // (L2: the join reads ahead of its wait)
+  const int4 a = __ldcg(w), b = __ldcg(w + 1);
   const bool ok = (a.x == kSharedMagic) & (a.z == B) & (b.x == C) & (b.y == Hkv) & (b.z == G) &
                   (a.y >= 0) & (a.y <= (plan_ints - plan_items_at(B, C)) / kPlanItem) & (a.w >= 0) &
                   (a.w <= slots);
