@@ -68,3 +68,37 @@ def test_a_checked_plan_gives_the_same_bits(dtype):
         assert dec.device_errors() == 0
         outs.append(out)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("metadata", ["copy", "mapped"])
+def test_a_step_without_blocks_leaves_everything_as_it_was(metadata):
+    """Rows of 16, 16 and 4 tokens in 5 blocks: step 1 takes the last two, step 13 needs
+    another for the third row and changes neither allocator, weights nor caches."""
+    dec = BoundedDecoder(5, 4, 2, 64, "f32", 3, 40, 8, device=dev(), metadata=metadata)
+    kv = [workloads.normal((16, 2, 64), "f32", i).to(dev()) for i in range(6)]
+    ids = [dec.join(n, None, kv[2 * i][:n], kv[2 * i + 1][:n]) for i, n in enumerate((16, 16, 4))]
+    x = [workloads.normal((3, h, 64), "f32", 20 + h + i).to(dev()) for i, h in enumerate((4, 2, 2))]
+
+    def state():
+        torch.cuda.synchronize()
+        a = dec.alloc
+        return ([a.seq_len(s) for s in ids], [a.offset(s) for s in ids], [a.seq_blocks(s) for s in ids],
+                a.num_free(), dict(dec._held), dict(dec._known)), \
+            [t.clone() for t in (dec.masses, dec.k_caches, dec.v_caches)]
+
+    for step in range(12):
+        dec.step(ids, *x)
+    host, device = state()
+    assert host[0] == [28, 28, 16] and host[3] == 0
+    for _ in range(2):
+        with pytest.raises(binding.OutOfBlocks):
+            dec.step(ids, *x)
+        now, tensors = state()
+        assert now == host
+        # (bit for bit: slots that no token has written hold whatever was there)
+        assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(device, tensors))
+    dec.leave(ids[0])
+    out = dec.step(ids[1:], *(t[1:] for t in x))
+    torch.cuda.synchronize()
+    assert [dec.alloc.seq_len(s) for s in ids[1:]] == [29, 17] and dec.device_errors() == 0
+    assert bool(out.isfinite().all())
