@@ -446,7 +446,7 @@ typedef struct pkv_rotary_spec {
   double base;                       /* >= 1 (> 1 for RAMP) */
   double factor;                     /* >= 1 (unused by PLAIN) */
   double low, high;                  /* RAMP, BANDS: turns, 0 < low < high */
-  double amplitude;                  /* > 0; 1 for none */
+  double amplitude;                  /* > 0 and finite in float32; 1 for none */
 } pkv_rotary_spec;
 
 /* What the kernels need of a spec, filled by pkv_rotary_init (host only) and

@@ -271,8 +271,9 @@ extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *
   PKV_REQUIRE(s->scaling >= PKV_ROTARY_PLAIN && s->scaling <= PKV_ROTARY_BANDS,
               PKV_ERR_UNSUPPORTED, "scaling %d", s->scaling);
   PKV_REQUIRE(s->base >= 1.0 && std::isfinite(s->base), PKV_ERR_INVALID_ARG, "base must be >= 1");
-  PKV_REQUIRE(s->amplitude > 0.0 && std::isfinite(s->amplitude), PKV_ERR_INVALID_ARG,
-              "amplitude must be positive");
+  const float amplitude = static_cast<float>(s->amplitude);
+  PKV_REQUIRE(amplitude > 0.f && std::isfinite(amplitude), PKV_ERR_INVALID_ARG,
+              "amplitude must be positive and finite in float32");
   PKV_REQUIRE(s->scaling == PKV_ROTARY_PLAIN || (s->factor >= 1.0 && std::isfinite(s->factor)),
               PKV_ERR_INVALID_ARG, "factor must be >= 1");
   double base = s->base;
@@ -313,7 +314,7 @@ extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *
   out->d = d;
   out->rot_dim = r;
   out->layout = s->layout;
-  out->amplitude = static_cast<float>(s->amplitude);
+  out->amplitude = amplitude;
   out->check = kRotaryCheck;
   return PKV_OK;
 }
