@@ -477,7 +477,8 @@ typedef struct pkv_rotary_args {
  * Rotates the queries and keys of T tokens (a decode step's rows or a prompt's
  * tokens) and, with slot_mapping, writes the rotated keys and the values into
  * the cache as pkv_append does (negative slot: nothing; a slot beyond the pool
- * sets PKV_DEVERR_BAD_SLOT; of tokens naming one slot, any one's row may stay).
+ * sets PKV_DEVERR_BAD_SLOT).  The tokens of a call name different slots: where two
+ * name one, its rows are left holding pieces of either's.
  * Hq or Hkv may be 0.  In place (q_out == q with the same stride, k_out == k) is
  * allowed; no other overlap is.  d even, 2..256; appending needs
  * d * sizeof(dtype) and the caches' addresses to be multiples of 16 bytes.
@@ -500,6 +501,11 @@ int pkv_rotary_append(const pkv_rotary_args *args, void *stream);
  * and value hold).  A row with no token at all, or none that is not excluded, outputs
  * zeros and lse = -inf; a query, key or value of NaN or infinity in what counts gives
  * NaN where the formula does.
+ *
+ * Scores, sums and accumulators are float32.  In bf16 the softmax weights are rounded to
+ * bf16, once, ahead of the product with V (the tensor cores' operand type; the sums take
+ * them before it), except in the one-kernel form for short contexts (pkv_shared_short),
+ * which keeps them in float32.
  *
  * Positions are the caller's: a row's own token i sits at position
  * prefix length + i (pkv_seq_set_offset lets the allocator count that way).
