@@ -13,6 +13,8 @@ tokens), then per layer ``pkv_rotary_append`` and ``pkv_decode_attn_shared`` wit
 weights accumulated, and before it ``pkv_evict`` for the rows that have reached their
 bound.
 """
+import math
+
 import numpy as np
 
 from . import binding
@@ -36,6 +38,8 @@ class BoundedDecoder(PagedDecoder):
         recent = budget // 4 if recent is None else recent
         if sink < 0 or recent < 0:
             raise ValueError("sink and recent must not be negative")
+        if not math.isfinite(decay) or not math.isfinite(kw.get("scale") or 0.0):
+            raise ValueError("scale and decay must be finite")
         if max_prefixes < 0 or max_prefix_len < 0:
             raise ValueError("max_prefixes and max_prefix_len must not be negative")
         if rotary is not None and kw.get("rope_base") is not None:
@@ -302,6 +306,10 @@ class BoundedDecoder(PagedDecoder):
             raise ValueError("give q, k and v all with layers or all without")
         if B == 0:
             return self.out[:0] if L == 1 else self.outs[:, :0]
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            x = t if t.dim() == 3 else t[0]
+            if binding._heads(x, name, B, self.d, self.tdtype, self.outs.device)[1] < x.shape[1] * self.d:
+                raise ValueError(f"{name}: a row's heads overlap the next row's")
         torch = self.torch
         run = stream if stream is not None else torch.cuda.current_stream(self.device)
         with torch.cuda.stream(run):   # (copies and launches in one order)
@@ -312,12 +320,23 @@ class BoundedDecoder(PagedDecoder):
             try:
                 out = super().step(seq_ids, q, k, v, None, run)
             except Exception:
-                for s in seq_ids:
-                    self._held[s] = self.alloc.seq_len(s)
+                self._take_back(seq_ids, run)
                 raise
         for s, n in zip(seq_ids, self.last_metadata[2].tolist()):
             self._known[s] = self._held[s] = n
         return out
+
+    def _take_back(self, seq_ids, run):
+        """After a step that raised: the tokens it counted but did not (everywhere) write."""
+        if self._pending is not None:     # kernels launched before may read the buffer
+            ev = self.torch.cuda.Event()
+            ev.record(run)
+            self._pending["event"], self._pending = ev, None
+        grown = [s for s in seq_ids if self.alloc.seq_len(s) > self._held[s]]
+        offsets = [self.alloc.offset(s) for s in grown]
+        self.alloc.evict_many(grown, [self._held[s] for s in grown])
+        for s, offset in zip(grown, offsets):
+            self.alloc.set_offset(s, offset)
 
     def capture(self, *args, **kw):
         raise ValueError("BoundedDecoder changes its launches from step to step: not captured")

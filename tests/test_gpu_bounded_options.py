@@ -102,3 +102,79 @@ def test_a_step_without_blocks_leaves_everything_as_it_was(metadata):
     torch.cuda.synchronize()
     assert [dec.alloc.seq_len(s) for s in ids[1:]] == [29, 17] and dec.device_errors() == 0
     assert bool(out.isfinite().all())
+
+
+def ready(metadata="copy", n_layers=1):
+    """Two rows, one behind a prefix, and a step's inputs."""
+    dec = BoundedDecoder(40, 8, 2, 64, "f32", 2, 24, 8, device=dev(), metadata=metadata,
+                         n_layers=n_layers)
+    x = workloads.normal((n_layers, 32, 2, 64), "f32", 1).to(dev())
+    p = dec.add_prefix(x, x.flip(1))
+    ids = [dec.join(16, p, x[:, :16], x[:, 16:]), dec.join(5, None, x[:, :5], x[:, 5:10])]
+    q, k, v = (workloads.normal((n_layers, 2, h, 64), "f32", 50 + i).to(dev())
+               for i, h in enumerate((8, 2, 2)))
+    return dec, ids, (q, k, v)
+
+
+def lengths(dec, ids):
+    a = dec.alloc
+    return ([(a.seq_len(s), a.offset(s), a.seq_blocks(s), dec._held[s], dec._known[s]) for s in ids],
+            a.num_free())
+
+
+@pytest.mark.parametrize("what", ["rows expanded", "heads apart", "elements apart", "strange scale"])
+def test_inputs_that_no_launch_takes_are_refused_before_a_sequence_grows(what):
+    dec, ids, (q, k, v) = ready()
+    before = lengths(dec, ids)
+    if what == "rows expanded":
+        bad = (q, k[:, :1].expand(1, 2, 2, 64), v)
+    elif what == "heads apart":
+        bad = (q, k, torch.cat([v, v], -1)[..., :64])
+    elif what == "elements apart":
+        bad = (torch.cat([q, q], -1)[..., ::2], k, v)
+    else:
+        with pytest.raises(ValueError):
+            BoundedDecoder(40, 8, 2, 64, "f32", 2, 24, 8, device=dev(), scale=float("nan"))
+        with pytest.raises(ValueError):
+            BoundedDecoder(40, 8, 2, 64, "f32", 2, 24, 8, device=dev(), decay=float("inf"))
+        return
+    for _ in range(2):
+        with pytest.raises((ValueError, binding.PkvError)):
+            dec.step(ids, *bad)
+        assert lengths(dec, ids) == before
+    got = dec.step(ids, q, k, v).clone()
+    ref, ids2, same = ready()
+    assert torch.equal(got, ref.step(ids2, *same))
+    torch.cuda.synchronize()
+    assert dec.device_errors() == 0
+
+
+@pytest.mark.parametrize("metadata", ["copy", "mapped"])
+@pytest.mark.parametrize("layer", [0, 1])
+def test_a_step_whose_launch_fails_takes_the_token_back(metadata, layer, monkeypatch):
+    """An exception between a0 and the last launch: lengths, positions and blocks are as
+    before, and the step can be made again."""
+    dec, ids, x = ready(metadata, 2)
+    before = lengths(dec, ids)
+    calls, real = [], binding.decode_attn_shared_args
+
+    def fail(args, stream=None):
+        calls.append(args)
+        if len(calls) > layer:
+            raise RuntimeError("no memory")
+        real(args, stream)
+
+    with monkeypatch.context() as m:
+        m.setattr(binding, "decode_attn_shared_args", fail)
+        with pytest.raises(RuntimeError, match="no memory"):
+            dec.step(ids, *x)
+    now = lengths(dec, ids)
+    assert [r[:2] + r[3:] for r in now[0]] == [r[:2] + r[3:] for r in before[0]]
+    assert [r[2] for r in now[0]] == [r[2] for r in before[0]] and now[1] == before[1]
+    assert dec._pending is None
+    got = dec.step(ids, *x).clone()
+    ref, ids2, same = ready(metadata, 2)
+    want = ref.step(ids2, *same)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and dec.device_errors() == 0
+    assert dec.last_metadata[0].tolist() == ref.last_metadata[0].tolist() == [32 + 16, 5]
