@@ -200,10 +200,14 @@ class BoundedDecoder(PagedDecoder):
                 at = torch.from_numpy(slots).to(dev)
                 self.masses[:, at // binding.BLOCK_SIZE, :, at % binding.BLOCK_SIZE] = 0.0
                 self._known[s] = int(L)
-        for layer in range(self.n_layers):
-            binding.evict_args(binding.make_evict_args(
-                self.k_caches[layer], self.v_caches[layer], self.masses[layer], t, ln, kp,
-                kept[layer], self.sink, self.recent, err=self.err))
+        space = torch.empty(binding.evict_workspace_bytes(n, self.Hkv, self.d, self._code, kept.shape[-1]),
+                            dtype=torch.uint8, device=dev)
+        # (all calls are made before the first moves anything)
+        calls = [binding.make_evict_args(
+            self.k_caches[layer], self.v_caches[layer], self.masses[layer], t, ln, kp, kept[layer],
+            self.sink, self.recent, workspace=space, err=self.err) for layer in range(self.n_layers)]
+        for call in calls:
+            binding.evict_args(call)
         self.alloc.evict_many(seq_ids, np.full(n, keep, np.int32))
         for s in seq_ids:
             self._known[s], self._held[s] = min(self._known[s], keep), min(self._held[s], keep)

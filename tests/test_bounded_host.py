@@ -137,3 +137,28 @@ def test_sequences_to_evict_may_come_from_an_iterator(make, monkeypatch):
     assert seen == [(ids, 5), (ids, 24)]
     with pytest.raises(ValueError):
         dec.evict(iter([ids[0], ids[0]]))
+
+
+def test_an_eviction_that_cannot_be_prepared_moves_nothing(bind, make, monkeypatch):
+    """Every layer's call is made before the first is launched."""
+    dec = make(n_layers=3)
+    dec.k_caches = dec.v_caches = torch.zeros(3, 1)
+    dec.err, sid, launched, made = None, dec.join(20), [], []
+    monkeypatch.setattr(dec, "_on", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(bind, "evict_args", launched.append)
+
+    def prepare(*a, **kw):
+        if len(made) == fail_at:
+            raise RuntimeError("out of memory")
+        made.append(kw["workspace"])
+        return len(made)
+
+    monkeypatch.setattr(bind, "make_evict_args", prepare)
+    fail_at = 2
+    with pytest.raises(RuntimeError):
+        dec.evict([sid], 5)
+    assert launched == [] and dec.alloc.seq_len(sid) == 20 and dec._held[sid] == 20
+    fail_at, made[:] = None, []
+    dec.evict([sid], 5)
+    assert launched == [1, 2, 3] and dec.alloc.seq_len(sid) == 5 and dec._held[sid] == 5
+    assert all(w is made[0] for w in made)        # one layer after the other in one workspace
