@@ -581,9 +581,10 @@ typedef struct pkv_shared_args {
  * PKV_ATTN_SHORT_WAITS.  out must not overlap q_rot.  A block id outside the pool sets
  * PKV_DEVERR_BAD_BLOCK and its tokens are left out.  plan_ints, slots and
  * num_ctas are pkv_shared_plan's.  A prefix_plan made for another call (its B,
- * num_ctas, Hkv, Hq/Hkv, or more partials than slots), or one whose records
- * leave partials out, sets PKV_DEVERR_BAD_PLAN and the rows attend over their
- * own tokens alone; so does a row whose prefix lies outside prefix_tables.
+ * num_ctas, Hkv or Hq/Hkv) sets PKV_DEVERR_BAD_PLAN and the rows attend over
+ * their own tokens alone; so does a row whose prefix lies outside prefix_tables,
+ * and, where partials are kept (not in the one-kernel form), a plan with more of
+ * them than slots or whose records leave some out.
  * Where a wait of the prefix kernel gives up (PKV_DEVERR_TIMEOUT), the rows
  * with a prefix are NaN.  Records of `plan` that do not fit set
  * PKV_DEVERR_BAD_PLAN and are skipped (their rows' outputs are then incomplete).

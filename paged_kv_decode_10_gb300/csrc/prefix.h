@@ -102,7 +102,7 @@ struct ShortParams {
   float *mass, *lse_out;
   void *out;
   int32_t *err;
-  int B, Hq, Hkv, C, num_blocks, n_prefixes, pt_stride, plan_ints, slots, bt_stride, bias_stride;
+  int B, Hq, Hkv, C, num_blocks, n_prefixes, pt_stride, bt_stride, bias_stride;
   int cluster, pages;            // CTAs to a (row, KV head), pages one of them may get
   float scale_log2, decay;
 };

@@ -387,8 +387,6 @@ extern "C" int pkv_decode_attn_shared(const pkv_shared_args *a, void *stream) {
       p.num_blocks = a->num_blocks;
       p.n_prefixes = a->n_prefixes;
       p.pt_stride = prefixes ? a->pt_stride : 0;
-      p.plan_ints = a->plan_ints;
-      p.slots = slots;
       p.bt_stride = a->bt_stride;
       p.bias_stride = a->attn_bias ? a->bias_stride : 0;
       p.scale_log2 = a->scale * kLog2e;

@@ -88,9 +88,14 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T), D, G))
   // the row's prefix, as the plan states it
   int4 pre = make_int4(0, 0, -1, 0);
   if (p.plan) {
-    const PlanHeader head = plan_header(p.plan, p.B, p.C, p.Hkv, G, p.plan_ints, p.slots);
+    // (nothing is kept in slots here; what plan_header and plan_row_ok check beyond this
+    // took 0.2 us of 4.9)
+    const int4 *w = reinterpret_cast<const int4 *>(p.plan);
+    const int4 h0 = w[0], h1 = w[1];
     pre = *reinterpret_cast<const int4 *>(p.plan + plan_rows_at() + 4 * b);
-    const bool fits = head.ok && plan_row_ok(pre, p.n_prefixes, p.pt_stride, head.slots);
+    const bool fits = (h0.x == kSharedMagic) & (h0.z == p.B) & (h1.x == p.C) & (h1.y == p.Hkv) &
+                      (h1.z == G) & (pre.z < p.n_prefixes) & (pre.w >= 0) &
+                      (pre.w <= kBlockTokens * p.pt_stride);
     if (!fits || pre.z < 0) {
       if (!fits && tid == 0) set_dev_err(p.err, PKV_DEVERR_BAD_PLAN);
       pre.z = -1;
