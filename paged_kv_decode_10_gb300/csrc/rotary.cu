@@ -103,7 +103,7 @@ __device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w,
 // the CTA's (token, head) pairs kThreads / per_head at a time, kBatch of them with
 // their loads in flight together; the first batch's go out before the angles are
 // formed.  16384 tokens of 32 + 8 heads of 128 in bf16, whole heads turned: 64 us, 6.3
-// TB/s (float32 121 us, 6.7 TB/s); four pairs at a time, with fewer CTAs on an SM, took
+// TB/s (float32 119 us, 6.8 TB/s); four pairs at a time, with fewer CTAs on an SM, took
 // 5 % longer.
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
@@ -198,7 +198,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
 // Any even sizes, an element at a time.  A CTA serves tb tokens; an item is a pair of
 // elements of one head: a rotating pair, or two neighbours behind the pairs or in a
-// value head.
+// value head.  Bound by its instructions (an element a load, the divisions of an item):
+// 16384 tokens of 32 + 8 heads of 80, 20 rotated: 153 us in bf16 (1.6 TB/s), 151 us in
+// float32 (3.3 TB/s).
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kThreads) rotary_any_kernel(
     const __grid_constant__ RotaryParams p) {
