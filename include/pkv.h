@@ -538,8 +538,8 @@ int pkv_shared_default_parts(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int3
 int pkv_shared_short(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype,
                      int32_t bt_stride, int32_t pt_stride, int32_t *short_form);
 /* Workspace of pkv_decode_attn_shared: the bytes of pkv_attn_workspace_bytes plus
- * the row sums and the partials of `slots` (0 without prefixes; max_slots above
- * serves every plan of those sizes).  Same rules: 256-byte aligned, zero-filled once
+ * the row sums and, with prefixes, the partials of `slots` (0 without; max_slots above
+ * serves every plan of those sizes) and the prefix CTAs' account of them.  Same rules: 256-byte aligned, zero-filled once
  * for a given B and num_parts (the counters' places follow from them, so again before
  * calls with others), calls that share it, or scores, must not overlap. */
 int pkv_shared_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
