@@ -188,8 +188,54 @@ int pkv_seq_offset(const pkv_alloc *a, int32_t seq_id, int32_t *offset);
  * more; else nothing changes for it).  The blocks behind them return to the free
  * list in table order, and the offset grows by the tokens dropped, so that
  * positions go on where they were.  All or nothing: every id must be live and
- * listed once, every keep_lens[i] >= 0. */
+ * listed once, every keep_lens[i] >= 0, and a sequence that gets shorter must share no
+ * block (pkv_seq_fork): its tokens have moved within them. */
 int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_t *keep_lens, int32_t n);
+/* Forks of a sequence (several samples of one prompt, beams): n new sequences with the
+ * parent's tokens and offset, into child_ids[0..n-1] (smallest free ids, ascending).  Whole
+ * blocks are shared: a block then belongs to several sequences and is free when the last
+ * of them has given it back.  A last block that is not full is the parent's alone: every
+ * child gets a block of its own for it, and pair i of the *n_copies pairs copy_src,
+ * copy_dst (room for n each; they may be NULL where the length is a multiple of 16) says
+ * which to copy (pkv_copy_blocks, in every layer, before the next step).  All or nothing.
+ * So the block that a sequence appends to is always its own. */
+int pkv_seq_fork(pkv_alloc *a, int32_t seq_id, int32_t n, int32_t *child_ids, int32_t *copy_src,
+                 int32_t *copy_dst, int32_t *n_copies);
+/* Sequences cut back to lens[i] tokens (at most what they have): the tokens behind are
+ * forgotten, positions go on from there, and the blocks behind return to the free list in
+ * table order (after pkv_tree_accept: the drafted tokens that were not accepted).  A
+ * sequence that then ends inside a block which it shares gets a block of its own, to be
+ * copied as in pkv_seq_fork (copy_src, copy_dst: room for n, or NULL where no block is
+ * shared).  All or nothing; PKV_ERR_OUT_OF_BLOCKS unless the free list has a block for
+ * each such sequence. */
+int pkv_seqs_truncate(pkv_alloc *a, const int32_t *seq_ids, const int32_t *lens, int32_t n,
+                      int32_t *copy_src, int32_t *copy_dst, int32_t *n_copies);
+/*
+ * Host part of a step that appends counts[b] tokens (0 or more) to each of the B listed
+ * (distinct, live) sequences: T = sum(counts) new tokens (the nodes of a tree of drafted
+ * tokens, a chunk of a prompt), packed row after row.  Outputs (host arrays):
+ *   positions[T]      length before + offset + depths[i] (depths NULL: the token's number
+ *                     in its row)
+ *   slot_mapping[T]   int64 cache slots of the new tokens
+ *   node_starts[B+1]  row b's new tokens are [node_starts[b], node_starts[b+1])
+ *   seq_lens[B], block_tables[B*bt_stride] as pkv_prepare_step, after the append
+ * Atomic: on any error nothing changes.
+ */
+int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B, const int32_t *counts,
+                      const int32_t *depths, int32_t *positions, int64_t *slot_mapping,
+                      int32_t *node_starts, int32_t *seq_lens, int32_t *block_tables,
+                      int32_t bt_stride);
+/* Another size of the pool.  Larger: the new blocks come onto the free list, the last of
+ * them on top.  Smaller: blocks in use from num_blocks on move to free ones ahead of it,
+ * taken from the top of the free list; pair i of the *n pairs src, dst (room for cap) says
+ * what to copy (pkv_copy_blocks, in every layer), sequences in the order of their ids,
+ * blocks in table order; the rest of the free list keeps its order.  Then tables hold the
+ * new ids.  All or nothing: PKV_ERR_OUT_OF_BLOCKS if more blocks are in use than num_blocks,
+ * PKV_ERR_INVALID_ARG if cap is too small (*n is then what it must be). */
+int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst, int32_t cap,
+                     int32_t *n);
+/* Sequences that a block belongs to (0: it is free). */
+int pkv_block_refs(const pkv_alloc *a, int32_t block, int32_t *refs);
 int pkv_num_free(const pkv_alloc *a, int32_t *n);
 /* Pool auto-sizing ("neurogrid releases" v0.7.0: the pool is sized from the
  * VRAM budget): the number of 16-token blocks whose K and V, for every KV head
@@ -459,6 +505,33 @@ typedef struct pkv_rotary {
 } pkv_rotary;
 int pkv_rotary_init(const pkv_rotary_spec *spec, int32_t d, pkv_rotary *out);
 
+/*
+ * Positions with several axes (time, height and width of an image's or a video's patches):
+ * pair i turns by p_a * f_i, where a = axis[i] and p_a is the token's position on that axis.
+ * Axis a has sections[a] pairs (sum: rot_dim/2), in the order
+ *   PKV_AXES_BLOCKED  all of the first axis, then all of the second, ...
+ *   PKV_AXES_CYCLIC   dealt to the axes in turn, as long as they have pairs left
+ * and f_i is
+ *   PKV_AXES_SHARED   that of pair i of the whole head, as without axes
+ *   PKV_AXES_OWN      for the k-th pair of an axis, that of pair k of a head that rotates
+ *                     2 * sections[a] elements
+ * with the spec's layout, scaling and amplitude.  pkv_rotary_axes_init (host only) fills
+ * both structs; they belong together.
+ */
+#define PKV_ROTARY_MAX_AXES 8
+#define PKV_AXES_BLOCKED 0
+#define PKV_AXES_CYCLIC 1
+#define PKV_AXES_SHARED 0
+#define PKV_AXES_OWN 1
+typedef struct pkv_rotary_axes {
+  int32_t n_axes, pairs;
+  uint8_t axis[128];                 /* of every pair */
+  uint32_t check;                    /* set by pkv_rotary_axes_init */
+} pkv_rotary_axes;
+int pkv_rotary_axes_init(const pkv_rotary_spec *spec, int32_t d, const int32_t *sections,
+                         int32_t n_axes, int32_t order, int32_t ladder, pkv_rotary *out,
+                         pkv_rotary_axes *axes);
+
 typedef struct pkv_rotary_args {
   const pkv_rotary *rotary;          /* host */
   const void *q, *k, *v;             /* T tokens of [Hq,d], [Hkv,d], [Hkv,d]; a token's heads
@@ -484,6 +557,10 @@ typedef struct pkv_rotary_args {
  * d * sizeof(dtype) and the caches' addresses to be multiples of 16 bytes.
  */
 int pkv_rotary_append(const pkv_rotary_args *args, void *stream);
+/* The same with axes: args->positions holds [n_axes][T] positions, an axis' tokens dense,
+ * the axes axis_stride (>= T) entries apart. */
+int pkv_rotary_axes_append(const pkv_rotary_args *args, const pkv_rotary_axes *axes,
+                           int64_t axis_stride, void *stream);
 
 /* ======================================================================== */
 /* decode attention over shared prefixes, with per-token weights             */
@@ -630,6 +707,107 @@ typedef struct pkv_evict_args {
   int32_t B, Hkv, d, dtype;
 } pkv_evict_args;
 int pkv_evict(const pkv_evict_args *args, void *stream);
+
+/* ======================================================================== */
+/* drafted tokens: attention of a tree, its accepted path, copies of blocks  */
+/* ======================================================================== */
+/*
+ * Several new tokens a row in one step: a tree of drafted tokens to verify, or a chunk of
+ * a prompt.  They are appended like any token (pkv_prepare_nodes, then pkv_rotary_append:
+ * row b's blocks hold seq_lens[b] tokens, of which the last n_b = node_starts[b+1] -
+ * node_starts[b] are its nodes), and each attends over what is ahead of the nodes and over
+ * those nodes that its mask names:
+ *   node i, query head h:  s_t = (q_rot[node_starts[b]+i,h] . k_t) * scale
+ *   out[node_starts[b]+i,h] = sum_t softmax_t(s) v_t
+ * over tokens t < seq_lens[b] - n_b and nodes j (token seq_lens[b] - n_b + j) with bit
+ * j % 32 of mask[(node_starts[b]+i)*mask_words + j/32] set (bits from n_b on are not
+ * looked at).  Without a mask node i sees the nodes up to itself.  Node i's own bit is
+ * like any other.  A token that a node does not see may hold anything.  A node that sees
+ * nothing outputs zeros and lse = -inf; NaN and infinities in what it sees give NaN where
+ * the formula does.  Keys are in the caches as rotated; positions are the caller's
+ * (a node's: the tokens ahead of the nodes plus its depth).
+ *
+ * Scores, sums and accumulators are float32; in bf16 the softmax weights are rounded to
+ * bf16, once, ahead of the product with V (the tensor cores' operand type; the sums take
+ * them before it).
+ *
+ * q_rot, out [T,Hq,d]; query rows outside node_starts[0..B] are left as they were, and so
+ * are a row's that does not fit the call (PKV_DEVERR_BAD_LEN: starts that do not ascend
+ * within [0, T], more nodes than tokens or mask bits, seq_lens[b] > 16*bt_stride).  A block
+ * id outside the pool sets PKV_DEVERR_BAD_BLOCK and its tokens are left out (a node to
+ * which none is left is NaN).  Rows may share blocks (pkv_seq_fork, shared prefixes); a
+ * query row belongs to one batch row.  Where a wait inside the kernel gives up
+ * (PKV_DEVERR_TIMEOUT), the outputs that it was for are NaN.
+ *
+ * Types, heads and head sizes as pkv_decode_attn_split; out must not overlap q_rot.
+ * flags: 0 or PKV_ATTN_SHORT_WAITS.  Workspace: pkv_tree_workspace_bytes(...) bytes for the
+ * current device, 256-byte aligned, any contents (a call leaves nothing in it that a later
+ * one reads); calls that share it must not overlap.
+ */
+int pkv_tree_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, size_t *bytes);
+typedef struct pkv_tree_args {
+  const void *q_rot;                 /* [T,Hq,d] */
+  const void *k_cache, *v_cache;     /* [num_blocks,Hkv,16,d] */
+  const int32_t *block_tables;       /* [B*bt_stride] */
+  const int32_t *seq_lens;           /* [B] */
+  const int32_t *node_starts;        /* [B+1] */
+  const int32_t *mask;               /* nullable [T*mask_words] bits */
+  void *workspace;
+  size_t workspace_bytes;
+  void *out;                         /* [T,Hq,d] */
+  float *lse_out;                    /* nullable [T,Hq]: natural log-sum-exp */
+  int32_t *dev_err_flag;             /* nullable */
+  int32_t num_blocks, bt_stride, mask_words;
+  int32_t B, T, Hq, Hkv, d, dtype, flags;
+  float scale;
+} pkv_tree_args;
+int pkv_decode_attn_tree(const pkv_tree_args *args, void *stream);
+
+/*
+ * The accepted path of each row's tree to the front of its nodes' slots, in place, in all
+ * n_pools pools (keys and values of every layer) at once: with base = seq_lens[b] - n_b,
+ * token base + j becomes what token base + path[b*path_stride + j] held, for
+ * j < accept_lens[b].  A path ascends strictly (parents come ahead of their children) within
+ * [0, n_b).  Tokens from base + accept_lens[b] on hold nothing of use afterwards:
+ * pkv_seqs_truncate to base + accept_lens[b] frees them.  Keys stay rotated: a node's
+ * position is its depth's, which is its place on the path.
+ * A row that does not fit (lengths as in pkv_decode_attn_tree, accept_lens[b] outside
+ * [0, min(n_b, path_stride)], a path that does not ascend) sets PKV_DEVERR_BAD_LEN, one with
+ * a block id outside the pool among those that it needs PKV_DEVERR_BAD_BLOCK; it is left
+ * alone.  The blocks of a row's nodes belong to that row only.
+ */
+#define PKV_MAX_POOLS 256
+typedef struct pkv_accept_args {
+  void *const *pools;                /* host array of n_pools device pointers, each
+                                        [num_blocks,Hkv,16,d], 16-byte aligned */
+  const int32_t *block_tables;       /* [B*bt_stride] */
+  const int32_t *seq_lens;           /* [B] */
+  const int32_t *node_starts;        /* [B+1] */
+  const int32_t *path;               /* [B*path_stride] */
+  const int32_t *accept_lens;        /* [B] */
+  int32_t *dev_err_flag;             /* nullable */
+  int32_t n_pools, num_blocks, bt_stride, path_stride, B, T, Hkv, d, dtype;
+} pkv_accept_args;
+int pkv_tree_accept(const pkv_accept_args *args, void *stream);
+
+/*
+ * Copies of whole blocks, in n_pools pools at once: block dst_blocks[i] of dst[p] becomes
+ * block src_blocks[i] of src[p], for i < n and every pool p.  src[p] may be dst[p] (forks)
+ * or another pool (a pool of another size, one in mapped host memory); a destination
+ * overlaps no other pool.  A pair with a negative id copies nothing; an id beyond its pool
+ * sets PKV_DEVERR_BAD_BLOCK and its pair is skipped.  A block may be the destination of
+ * one pair only and, within one pool, not the source of another (else what it holds is
+ * undefined).
+ */
+typedef struct pkv_copy_args {
+  const void *const *src;            /* host arrays of n_pools device pointers, 16-byte aligned */
+  void *const *dst;
+  const int32_t *src_blocks, *dst_blocks;   /* [n] */
+  int32_t *dev_err_flag;             /* nullable */
+  int64_t block_bytes;               /* of one block of one pool: a multiple of 16 */
+  int32_t n_pools, n, src_num_blocks, dst_num_blocks;
+} pkv_copy_args;
+int pkv_copy_blocks(const pkv_copy_args *args, void *stream);
 
 /* ======================================================================== */
 /* the whole device step: a1 -> a2 -> a3 -> a4 on one stream                */

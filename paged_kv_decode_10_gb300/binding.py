@@ -27,6 +27,10 @@ LAYERS_MERGE_HELPERS = 32
 STEP_FUSED = 4
 ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_RAMP, ROTARY_BANDS = range(5)
+ROTARY_MAX_AXES = 8
+AXES_BLOCKED, AXES_CYCLIC = 0, 1
+AXES_SHARED, AXES_OWN = 0, 1
+MAX_POOLS = 256
 
 _c_i32 = ctypes.c_int32
 _c_i64 = ctypes.c_int64
@@ -98,6 +102,13 @@ class RotaryTable(ctypes.Structure):
     ]
 
 
+class RotaryAxes(ctypes.Structure):
+    _fields_ = [
+        ("n_axes", _c_i32), ("pairs", _c_i32), ("axis", ctypes.c_uint8 * 128),
+        ("check", ctypes.c_uint32),
+    ]
+
+
 class RotaryArgs(ctypes.Structure):
     _fields_ = [
         ("rotary", ctypes.POINTER(RotaryTable)),
@@ -134,6 +145,37 @@ class EvictArgs(ctypes.Structure):
         ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("kept_stride", _c_i32),
         ("sink", _c_i32), ("recent", _c_i32),
         ("B", _c_i32), ("Hkv", _c_i32), ("d", _c_i32), ("dtype", _c_i32),
+    ]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q_rot", _vp), ("k_cache", _vp), ("v_cache", _vp),
+        ("block_tables", _vp), ("seq_lens", _vp), ("node_starts", _vp), ("mask", _vp),
+        ("workspace", _vp), ("workspace_bytes", _size_t),
+        ("out", _vp), ("lse_out", _vp), ("dev_err_flag", _vp),
+        ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("mask_words", _c_i32),
+        ("B", _c_i32), ("T", _c_i32), ("Hq", _c_i32), ("Hkv", _c_i32), ("d", _c_i32),
+        ("dtype", _c_i32), ("flags", _c_i32), ("scale", ctypes.c_float),
+    ]
+
+
+class AcceptArgs(ctypes.Structure):
+    _fields_ = [
+        ("pools", ctypes.POINTER(_vp)),
+        ("block_tables", _vp), ("seq_lens", _vp), ("node_starts", _vp), ("path", _vp),
+        ("accept_lens", _vp), ("dev_err_flag", _vp),
+        ("n_pools", _c_i32), ("num_blocks", _c_i32), ("bt_stride", _c_i32), ("path_stride", _c_i32),
+        ("B", _c_i32), ("T", _c_i32), ("Hkv", _c_i32), ("d", _c_i32), ("dtype", _c_i32),
+    ]
+
+
+class CopyArgs(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.POINTER(_vp)), ("dst", ctypes.POINTER(_vp)),
+        ("src_blocks", _vp), ("dst_blocks", _vp), ("dev_err_flag", _vp),
+        ("block_bytes", _c_i64),
+        ("n_pools", _c_i32), ("n", _c_i32), ("src_num_blocks", _c_i32), ("dst_num_blocks", _c_i32),
     ]
 
 
@@ -229,6 +271,22 @@ SIGNATURES = {
     "pkv_evict_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
                                                  ctypes.POINTER(_size_t)]),
     "pkv_evict": (ctypes.c_int, [ctypes.POINTER(EvictArgs), _vp]),
+    "pkv_seq_fork": (ctypes.c_int, [_vp, _c_i32, _c_i32, _p_i32, _p_i32, _p_i32, _p_i32]),
+    "pkv_seqs_truncate": (ctypes.c_int, [_vp, _p_i32, _p_i32, _c_i32, _p_i32, _p_i32, _p_i32]),
+    "pkv_prepare_nodes": (ctypes.c_int, [_vp, _p_i32, _c_i32, _p_i32, _p_i32, _p_i32, _p_i64, _p_i32,
+                                         _p_i32, _p_i32, _c_i32]),
+    "pkv_alloc_resize": (ctypes.c_int, [_vp, _c_i32, _p_i32, _p_i32, _c_i32, _p_i32]),
+    "pkv_block_refs": (ctypes.c_int, [_vp, _c_i32, _p_i32]),
+    "pkv_rotary_axes_init": (ctypes.c_int, [ctypes.POINTER(RotarySpec), _c_i32, _p_i32, _c_i32, _c_i32,
+                                            _c_i32, ctypes.POINTER(RotaryTable),
+                                            ctypes.POINTER(RotaryAxes)]),
+    "pkv_rotary_axes_append": (ctypes.c_int, [ctypes.POINTER(RotaryArgs), ctypes.POINTER(RotaryAxes),
+                                              _c_i64, _vp]),
+    "pkv_tree_workspace_bytes": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32,
+                                                ctypes.POINTER(_size_t)]),
+    "pkv_decode_attn_tree": (ctypes.c_int, [ctypes.POINTER(TreeArgs), _vp]),
+    "pkv_tree_accept": (ctypes.c_int, [ctypes.POINTER(AcceptArgs), _vp]),
+    "pkv_copy_blocks": (ctypes.c_int, [ctypes.POINTER(CopyArgs), _vp]),
 }
 
 _LIB = None
@@ -443,6 +501,75 @@ class BlockAllocator:
             raise PkvError(ERR_INVALID_ARG, "one keep length per sequence")
         _check(self._lib.pkv_seqs_evict(self._h, _np_ptr(ids, ctypes.c_int32),
                                         _np_ptr(keep, ctypes.c_int32), len(ids)))
+
+    def fork(self, seq_id, n):
+        """n new sequences that share the whole blocks of ``seq_id`` (``pkv_seq_fork``):
+        ``(ids, src, dst)``, the last two the blocks to copy (``copy_blocks``, in every
+        layer) before the next step."""
+        n, copies = int(n), ctypes.c_int32()
+        ids, src, dst = (np.empty(max(n, 0), np.int32) for _ in range(3))
+        _check(self._lib.pkv_seq_fork(self._h, int(seq_id), n, _np_ptr(ids, ctypes.c_int32),
+                                      _np_ptr(src, ctypes.c_int32), _np_ptr(dst, ctypes.c_int32),
+                                      ctypes.byref(copies)))
+        return ids, src[:copies.value], dst[:copies.value]
+
+    def truncate_many(self, seq_ids, lens):
+        """Cuts the sequences back to ``lens`` tokens (``pkv_seqs_truncate``); returns the
+        blocks to copy ``(src, dst)``: none unless a sequence ends inside a shared one."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32)
+        lens = np.ascontiguousarray(lens, dtype=np.int32)
+        if len(ids) != len(lens):
+            raise PkvError(ERR_INVALID_ARG, "one length per sequence")
+        copies = ctypes.c_int32()
+        src, dst = np.empty(len(ids), np.int32), np.empty(len(ids), np.int32)
+        _check(self._lib.pkv_seqs_truncate(self._h, _np_ptr(ids, ctypes.c_int32),
+                                           _np_ptr(lens, ctypes.c_int32), len(ids),
+                                           _np_ptr(src, ctypes.c_int32), _np_ptr(dst, ctypes.c_int32),
+                                           ctypes.byref(copies)))
+        return src[:copies.value], dst[:copies.value]
+
+    def prepare_nodes(self, seq_ids, counts, bt_stride, depths=None, out=None):
+        """a0 of a step that appends ``counts[b]`` tokens to each row
+        (``pkv_prepare_nodes``): ``positions [T], slot_mapping [T], node_starts [B+1],
+        seq_lens [B], block_tables [B, bt_stride]`` (numpy; ``out`` may supply them)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32)
+        counts = np.ascontiguousarray(counts, dtype=np.int32)
+        B = len(ids)
+        if len(counts) != B:
+            raise PkvError(ERR_INVALID_ARG, "one count per sequence")
+        T = int(np.maximum(counts, 0).sum(dtype=np.int64))
+        if depths is not None:
+            depths = np.ascontiguousarray(depths, dtype=np.int32)
+            if depths.size != T:
+                raise PkvError(ERR_INVALID_ARG, f"{depths.size} depths, {T} tokens")
+        if out is None:
+            out = (np.empty(T, np.int32), np.empty(T, np.int64), np.empty(B + 1, np.int32),
+                   np.empty(B, np.int32), np.empty((B, int(bt_stride)), np.int32))
+        pos, slots, starts, lens, tables = out
+        _check(self._lib.pkv_prepare_nodes(
+            self._h, _np_ptr(ids, ctypes.c_int32), B, _np_ptr(counts, ctypes.c_int32),
+            None if depths is None else _np_ptr(depths, ctypes.c_int32), _np_ptr(pos, ctypes.c_int32, T),
+            _np_ptr(slots, ctypes.c_int64, T), _np_ptr(starts, ctypes.c_int32, B + 1),
+            _np_ptr(lens, ctypes.c_int32, B), _np_ptr(tables, ctypes.c_int32, B * int(bt_stride)),
+            int(bt_stride)))
+        return out
+
+    def resize(self, num_blocks):
+        """Makes the pool ``num_blocks`` blocks (``pkv_alloc_resize``); returns the blocks
+        that move ``(src, dst)``."""
+        used = self.num_blocks - self.num_free()
+        src, dst = np.empty(used, np.int32), np.empty(used, np.int32)
+        n = ctypes.c_int32()
+        _check(self._lib.pkv_alloc_resize(self._h, int(num_blocks), _np_ptr(src, ctypes.c_int32),
+                                          _np_ptr(dst, ctypes.c_int32), used, ctypes.byref(n)))
+        self.num_blocks = int(num_blocks)
+        return src[:n.value], dst[:n.value]
+
+    def block_refs(self, block):
+        """Sequences that the block belongs to (``pkv_block_refs``)."""
+        n = ctypes.c_int32()
+        _check(self._lib.pkv_block_refs(self._h, int(block), ctypes.byref(n)))
+        return n.value
 
     def num_free(self):
         n = ctypes.c_int32()
@@ -847,27 +974,43 @@ class Rotary:
     """Rotary frequencies of a head of ``d`` elements (``pkv_rotary_init``): the
     first ``rot_dim`` rotate, in the ``"half"`` or ``"interleaved"`` layout, scaled
     ``"plain"``, ``"linear"``, ``"ntk"``, ``"ramp"`` or ``"bands"`` (include/pkv.h
-    states the formulas)."""
+    states the formulas).  With ``sections``, pairs per axis, every token has a position
+    on each axis (``pkv_rotary_axes_init``): pairs lie axis after axis (``order``
+    ``"blocked"``) or are dealt in turn (``"cyclic"``), with the frequencies of the whole
+    head (``ladder`` ``"shared"``) or of each axis by itself (``"own"``)."""
+    ORDERS = {"blocked": AXES_BLOCKED, "cyclic": AXES_CYCLIC}
+    LADDERS = {"shared": AXES_SHARED, "own": AXES_OWN}
     LAYOUTS = {"half": ROTARY_HALF, "interleaved": ROTARY_INTERLEAVED}
     SCALINGS = {"plain": ROTARY_PLAIN, "linear": ROTARY_LINEAR, "ntk": ROTARY_NTK,
                 "ramp": ROTARY_RAMP, "bands": ROTARY_BANDS}
 
     def __init__(self, d, rot_dim=None, layout="half", scaling="plain", base=10000.0, factor=1.0,
-                 low=1.0, high=32.0, original_len=0, amplitude=1.0):
+                 low=1.0, high=32.0, original_len=0, amplitude=1.0, sections=None, order="blocked",
+                 ladder="shared"):
+        if order not in self.ORDERS or ladder not in self.LADDERS:
+            raise PkvError(ERR_UNSUPPORTED, f"order {order!r}, ladder {ladder!r}")
         if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
             raise PkvError(ERR_UNSUPPORTED, f"layout {layout!r}, scaling {scaling!r}")
         self.d, self.rot_dim = int(d), int(d if rot_dim is None else rot_dim)
         spec = RotarySpec(self.rot_dim, self.LAYOUTS[layout], self.SCALINGS[scaling],
                           int(original_len), float(base), float(factor), float(low), float(high),
                           float(amplitude))
-        self.table = RotaryTable()
-        _check(load().pkv_rotary_init(ctypes.byref(spec), self.d, ctypes.byref(self.table)))
+        self.table, self.axes, self.n_axes = RotaryTable(), None, None
+        if sections is None:
+            _check(load().pkv_rotary_init(ctypes.byref(spec), self.d, ctypes.byref(self.table)))
+            return
+        counts = np.ascontiguousarray(sections, dtype=np.int32).reshape(-1)
+        self.axes, self.n_axes = RotaryAxes(), len(counts)
+        _check(load().pkv_rotary_axes_init(ctypes.byref(spec), self.d, _np_ptr(counts, ctypes.c_int32),
+                                           len(counts), self.ORDERS[order], self.LADDERS[ladder],
+                                           ctypes.byref(self.table), ctypes.byref(self.axes)))
 
 
 def make_rotary_args(rotary, q, k, v, positions, q_out=None, k_out=None, slot_mapping=None,
                      k_cache=None, v_cache=None, err=None):
     """``pkv_rotary_args``: ``q [T,Hq,d]`` and ``k, v [T,Hkv,d]`` may be slices of
-    one projection's output (any token stride); without ``slot_mapping`` nothing is
+    one projection's output (any token stride); ``positions [T]``, or ``[axes,T]`` for a
+    ``rotary`` with sections; without ``slot_mapping`` nothing is
     appended and ``v`` may be None; ``q`` (with ``q_out``) or ``k`` may be None.
     ``q_out``/``k_out`` may be ``q``/``k`` themselves; ``k_out`` None reports no
     rotated keys (they still go to the cache)."""
@@ -894,7 +1037,12 @@ def make_rotary_args(rotary, q, k, v, positions, q_out=None, k_out=None, slot_ma
             a.k_out, a.k_out_stride = _heads(k_out, "k_out", T, d, dt, dev)
             if k_out.shape != k.shape:
                 raise PkvError(ERR_INVALID_ARG, "k_out must have k's shape")
-    a.positions = _want(positions, "positions", (T,), torch.int32, dev, host=True)
+    a.axes = None
+    if rotary.axes is None:
+        a.positions = _want(positions, "positions", (T,), torch.int32, dev, host=True)
+    else:
+        a.positions = _want(positions, "positions", (rotary.n_axes, T), torch.int32, dev, host=True)
+        a.axes, a.axis_stride = ctypes.byref(rotary.axes), T
     if slot_mapping is not None:
         if k is None or v is None or k_cache is None or v_cache is None:
             raise PkvError(ERR_INVALID_ARG, "appending needs k, v and both caches")
@@ -930,8 +1078,12 @@ def set_rotary_inputs(layers, q, k, v):
 
 
 def rotary_append_args(args, stream=None):
-    """Runs ``pkv_rotary_append`` from prepared ``RotaryArgs``."""
-    _check(load().pkv_rotary_append(ctypes.byref(args), _launch_on(args, stream)))
+    """Runs ``pkv_rotary_append`` (``pkv_rotary_axes_append``) from prepared ``RotaryArgs``."""
+    if args.axes is None:
+        _check(load().pkv_rotary_append(ctypes.byref(args), _launch_on(args, stream)))
+    else:
+        _check(load().pkv_rotary_axes_append(ctypes.byref(args), args.axes, args.axis_stride,
+                                             _launch_on(args, stream)))
 
 
 def rotary_append(rotary, q, k, v, positions, slot_mapping=None, k_cache=None, v_cache=None,
@@ -1150,6 +1302,181 @@ def evict(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, max_keep, s
         evict_args(make_evict_args(k_cache, v_cache, mass, block_tables, seq_lens, keep_lens, kept,
                                    sink, recent, err=err), stream)
     return kept
+
+
+# --------------------------------------------------------------------------
+# drafted tokens: tree attention, accepted paths, copies of blocks
+# --------------------------------------------------------------------------
+def tree_workspace_bytes(Hq, Hkv, d, dtype):
+    n = _size_t()
+    _check(load().pkv_tree_workspace_bytes(int(Hq), int(Hkv), int(d), int(dtype), ctypes.byref(n)))
+    return n.value
+
+
+def tree_mask(parents, node_starts):
+    """Mask ``int32 [T, words]`` (numpy) of the trees whose node i of row b has the parent
+    ``parents[node_starts[b] + i]``, a node of its row ahead of it, or -1: every node sees
+    its ancestors and itself."""
+    parents = np.asarray(parents, np.int64)
+    starts = np.asarray(node_starts, np.int64)
+    most = int((starts[1:] - starts[:-1]).max()) if len(starts) > 1 else 0
+    bits = np.zeros((len(parents), max(1, -(-most // 32)) * 32), np.uint8)
+    for a, b in zip(starts[:-1], starts[1:]):
+        for i in range(b - a):
+            up = parents[a + i]
+            if not -1 <= up < i:
+                raise PkvError(ERR_INVALID_ARG, f"node {i}: parent {up} is not a node ahead of it")
+            if up >= 0:
+                bits[a + i] = bits[a + up]
+            bits[a + i, i] = 1
+    return np.packbits(bits, axis=1, bitorder="little").view("<i4").astype(np.int32)
+
+
+def make_tree_args(q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts, scale, out,
+                   mask=None, lse=None, workspace=None, flags=0, err=None):
+    """``pkv_tree_args``: ``q_rot, out [T,Hq,d]``, row b's nodes at ``node_starts[b] ..``,
+    ``seq_lens`` with the nodes included, ``mask`` int32 ``[T, words]`` of bits (None: a node
+    sees the nodes up to itself).  ``workspace`` (uint8, ``tree_workspace_bytes``) is made
+    here unless given; calls that share one must not overlap."""
+    torch = _torch()
+    if q_rot.dim() != 3 or k_cache.dim() != 4 or not q_rot.is_cuda:
+        raise PkvError(ERR_INVALID_ARG, "q_rot must be [T,Hq,d] and the caches [blocks,Hkv,16,d], "
+                                        "on a CUDA device")
+    T, Hq, d = q_rot.shape
+    nb, Hkv = k_cache.shape[0], k_cache.shape[1]
+    dt, dev, i32 = q_rot.dtype, q_rot.device, torch.int32
+    a = TreeArgs()
+    a.dtype = dtype_code(q_rot)
+    a.q_rot = _want(q_rot, "q_rot", (T, Hq, d), dt, dev)
+    a.k_cache = _want(k_cache, "k_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.v_cache = _want(v_cache, "v_cache", (nb, Hkv, BLOCK_SIZE, d), dt, dev)
+    a.block_tables = _want(block_tables, "block_tables", (None, None), i32, dev, host=True)
+    B = block_tables.shape[0]
+    a.seq_lens = _want(seq_lens, "seq_lens", (B,), i32, dev, host=True)
+    a.node_starts = _want(node_starts, "node_starts", (B + 1,), i32, dev, host=True)
+    a.out = _want(out, "out", (T, Hq, d), dt, dev)
+    if _overlap(out, q_rot):
+        raise PkvError(ERR_INVALID_ARG, "out must not overlap q_rot")
+    a.num_blocks, a.bt_stride = nb, block_tables.shape[1]
+    a.B, a.T, a.Hq, a.Hkv, a.d = B, T, Hq, Hkv, d
+    a.scale, a.flags = float(scale), int(flags)
+    if mask is not None:
+        a.mask = _want(mask, "mask", (T, None), i32, dev)
+        a.mask_words = mask.shape[1]
+    if lse is not None:
+        a.lse_out = _want(lse, "lse", (T, Hq), torch.float32, dev)
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, i32, dev)
+    if workspace is None:
+        workspace = torch.empty(tree_workspace_bytes(Hq, Hkv, d, a.dtype), dtype=torch.uint8, device=dev)
+    a.workspace = _want(workspace, "workspace", (None,), torch.uint8, dev)
+    a.workspace_bytes = workspace.numel()
+    return _finish(a, dev, (q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts, out, mask, lse,
+                            workspace, err))
+
+
+def decode_attn_tree_args(args, stream=None):
+    """Runs ``pkv_decode_attn_tree`` from prepared ``TreeArgs``."""
+    _check(load().pkv_decode_attn_tree(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def decode_attention_tree(q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts, scale,
+                          out=None, stream=None, **kw):
+    """Attention of drafted tokens: returns ``out [T,Hq,d]`` (see ``make_tree_args`` for the
+    rest)."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        out = torch.empty_like(q_rot) if out is None else out
+        args = make_tree_args(q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts, scale,
+                              out, **kw)
+        decode_attn_tree_args(args, stream)
+    return out
+
+
+def _pools(pools, name, like=None):
+    """Addresses of pools of one shape, type and device (``like``: another pool's trailing
+    shape, type and device), as a host array."""
+    pools = list(pools)
+    if not 0 < len(pools) <= MAX_POOLS:
+        raise PkvError(ERR_INVALID_ARG, f"{name}: {len(pools)} pools, expected 1 to {MAX_POOLS}")
+    first = pools[0] if like is None else like
+    shape = (pools[0].shape[0],) + tuple(first.shape[1:])
+    arr = (_vp * len(pools))()
+    for i, t in enumerate(pools):
+        arr[i] = _want(t, f"{name}[{i}]", shape, first.dtype, first.device)
+    return pools, arr
+
+
+def make_accept_args(pools, block_tables, seq_lens, node_starts, path, accept_lens, err=None):
+    """``pkv_accept_args``: ``pools`` are the key and value caches of every layer
+    (``[blocks,Hkv,16,d]`` each), ``path [B, most]`` the accepted nodes of each row,
+    ``accept_lens[b]`` of them."""
+    torch = _torch()
+    pools, arr = _pools(pools, "pools")
+    if pools[0].dim() != 4 or pools[0].shape[2] != BLOCK_SIZE:
+        raise PkvError(ERR_INVALID_ARG, "pools must be [blocks,Hkv,16,d]")
+    nb, Hkv, _, d = pools[0].shape
+    dev, i32 = pools[0].device, torch.int32
+    a = AcceptArgs()
+    a.pools, a.n_pools = ctypes.cast(arr, ctypes.POINTER(_vp)), len(pools)
+    a.dtype = dtype_code(pools[0])
+    a.block_tables = _want(block_tables, "block_tables", (None, None), i32, dev, host=True)
+    B = block_tables.shape[0]
+    a.seq_lens = _want(seq_lens, "seq_lens", (B,), i32, dev, host=True)
+    a.node_starts = _want(node_starts, "node_starts", (B + 1,), i32, dev, host=True)
+    a.path = _want(path, "path", (B, None), i32, dev, host=True)
+    a.accept_lens = _want(accept_lens, "accept_lens", (B,), i32, dev, host=True)
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, i32, dev)
+    a.num_blocks, a.bt_stride, a.path_stride = nb, block_tables.shape[1], path.shape[1]
+    a.B, a.Hkv, a.d = B, Hkv, d
+    a.T = 2**31 - 1    # (the nodes' number is not known here: starts are checked by the lengths)
+    return _finish(a, dev, (pools, arr, block_tables, seq_lens, node_starts, path, accept_lens, err))
+
+
+def accept_nodes_args(args, stream=None):
+    """Runs ``pkv_tree_accept`` from prepared ``AcceptArgs``."""
+    _check(load().pkv_tree_accept(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def accept_nodes(pools, block_tables, seq_lens, node_starts, path, accept_lens, err=None,
+                 stream=None):
+    """Moves each row's accepted path to the front of its nodes' slots, in place, in all
+    ``pools``."""
+    accept_nodes_args(make_accept_args(pools, block_tables, seq_lens, node_starts, path, accept_lens,
+                                       err), stream)
+
+
+def make_copy_args(pools, src_blocks, dst_blocks, dst_pools=None, err=None):
+    """``pkv_copy_args``: block ``dst_blocks[i]`` of every pool of ``dst_pools`` (default: the
+    same pools) becomes block ``src_blocks[i]`` of ``pools``.  Pools are ``[blocks, ...]``
+    of one shape and type; ``dst_pools`` may have another number of blocks."""
+    torch = _torch()
+    pools, src = _pools(pools, "pools")
+    to, dst = (pools, src) if dst_pools is None else _pools(dst_pools, "dst_pools", pools[0])
+    if len(to) != len(pools):
+        raise PkvError(ERR_INVALID_ARG, f"{len(pools)} pools, but {len(to)} dst_pools")
+    dev, i32 = pools[0].device, torch.int32
+    a = CopyArgs()
+    a.src, a.dst = (ctypes.cast(x, ctypes.POINTER(_vp)) for x in (src, dst))
+    a.src_blocks = _want(src_blocks, "src_blocks", (None,), i32, dev, host=True)
+    a.dst_blocks = _want(dst_blocks, "dst_blocks", (src_blocks.shape[0],), i32, dev, host=True)
+    if err is not None:
+        a.dev_err_flag = _want(err, "err", None, i32, dev)
+    block = pools[0][0].numel() * pools[0].element_size() if pools[0].shape[0] else 0
+    a.block_bytes, a.n_pools, a.n = block, len(pools), src_blocks.shape[0]
+    a.src_num_blocks, a.dst_num_blocks = pools[0].shape[0], to[0].shape[0]
+    return _finish(a, dev, (pools, to, src, dst, src_blocks, dst_blocks, err))
+
+
+def copy_blocks_args(args, stream=None):
+    """Runs ``pkv_copy_blocks`` from prepared ``CopyArgs``."""
+    _check(load().pkv_copy_blocks(ctypes.byref(args), _launch_on(args, stream)))
+
+
+def copy_blocks(pools, src_blocks, dst_blocks, dst_pools=None, err=None, stream=None):
+    """Copies whole blocks within the pools or to ``dst_pools``."""
+    copy_blocks_args(make_copy_args(pools, src_blocks, dst_blocks, dst_pools, err), stream)
 
 
 def pool_blocks(budget_bytes, n_layers, Hkv, d, dtype):

@@ -28,6 +28,7 @@ struct pkv_alloc {
   std::vector<uint8_t> live;             // per sequence id
   std::vector<uint32_t> stamp;           // per sequence id, duplicate detection
   std::vector<int32_t> generation;       // per sequence id, joins and evictions so far (ids are reused)
+  std::vector<int32_t> refs;             // per block, the sequences it belongs to
   uint32_t epoch = 0;
   std::priority_queue<int32_t, std::vector<int32_t>, std::greater<int32_t>> free_ids;
 
@@ -38,6 +39,22 @@ struct pkv_alloc {
     return tables.data() + static_cast<size_t>(sid) * static_cast<size_t>(max_blocks_per_seq);
   }
   bool is_live(int32_t sid) const { return sid >= 0 && sid < max_seqs && live[sid]; }
+  int32_t take() {   // a free block
+    const int32_t b = free_stack.back();
+    free_stack.pop_back();
+    refs[b] = 1;
+    return b;
+  }
+  void give_back(int32_t b) {
+    if (--refs[b] == 0) free_stack.push_back(b);
+  }
+  // A new round of marks in `stamp`.
+  void next_epoch() {
+    if (++epoch == 0) {
+      std::fill(stamp.begin(), stamp.end(), 0u);
+      epoch = 1;
+    }
+  }
 };
 
 namespace {
@@ -86,6 +103,7 @@ extern "C" int pkv_alloc_create(int32_t num_blocks, int32_t block_size, int32_t 
     a->live.assign(max_seqs, 0);
     a->stamp.assign(max_seqs, 0);
     a->generation.assign(max_seqs, 0);
+    a->refs.assign(num_blocks, 0);
     for (int32_t i = 0; i < max_seqs; ++i) a->free_ids.push(i);
   } catch (...) {
     delete a;
@@ -113,8 +131,7 @@ extern "C" int pkv_seq_join(pkv_alloc *a, int32_t prefix_len, int32_t *seq_id) {
   a->free_ids.pop();
   int32_t *t = a->table(sid);
   for (int64_t j = 0; j < need; ++j) {
-    t[j] = a->free_stack.back();
-    a->free_stack.pop_back();
+    t[j] = a->take();
   }
   a->n_blocks[sid] = static_cast<int32_t>(need);
   a->lengths[sid] = prefix_len;
@@ -130,7 +147,7 @@ extern "C" int pkv_seq_leave(pkv_alloc *a, int32_t seq_id) {
   PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL allocator");
   PKV_REQUIRE(a->is_live(seq_id), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", seq_id);
   const int32_t *t = a->table(seq_id);
-  for (int32_t j = 0; j < a->n_blocks[seq_id]; ++j) a->free_stack.push_back(t[j]);
+  for (int32_t j = 0; j < a->n_blocks[seq_id]; ++j) a->give_back(t[j]);
   a->n_blocks[seq_id] = 0;
   a->lengths[seq_id] = 0;
   a->live[seq_id] = 0;
@@ -180,8 +197,7 @@ int prepare_step_impl(pkv_alloc *a, const int32_t *seq_ids, int32_t B, int32_t *
     const int32_t pos = a->lengths[s];
     int32_t *t = a->table(s);
     if (pos % kBlock == 0) {
-      t[a->n_blocks[s]++] = a->free_stack.back();
-      a->free_stack.pop_back();
+      t[a->n_blocks[s]++] = a->take();
     }
     positions[b] = pos + a->offsets[s];
     slot_mapping[b] = static_cast<int64_t>(t[pos / kBlock]) * kBlock + pos % kBlock;
@@ -328,6 +344,9 @@ extern "C" int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_
     const int64_t drop = static_cast<int64_t>(a->lengths[s]) - keep_lens[i];
     PKV_REQUIRE(drop <= 0 || drop + a->offsets[s] <= INT32_MAX, PKV_ERR_INVALID_ARG,
                 "sequence %d: position beyond 32 bits", s);
+    for (int32_t j = 0; drop > 0 && j < a->n_blocks[s]; ++j)
+      PKV_REQUIRE(a->refs[a->table(s)[j]] == 1, PKV_ERR_INVALID_ARG,
+                  "sequence %d shares block %d with another", s, a->table(s)[j]);
   }
   for (int32_t i = 0; i < n; ++i) {
     const int32_t s = seq_ids[i];
@@ -335,7 +354,7 @@ extern "C" int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_
     if (drop <= 0) continue;
     const int32_t left = static_cast<int32_t>(blocks_for(keep_lens[i]));
     const int32_t *t = a->table(s);
-    for (int32_t j = left; j < a->n_blocks[s]; ++j) a->free_stack.push_back(t[j]);
+    for (int32_t j = left; j < a->n_blocks[s]; ++j) a->give_back(t[j]);
     a->n_blocks[s] = left;
     a->lengths[s] = keep_lens[i];
     a->offsets[s] += drop;
@@ -343,6 +362,219 @@ extern "C" int pkv_seqs_evict(pkv_alloc *a, const int32_t *seq_ids, const int32_
     // it is rewritten like a new sequence's
     ++a->generation[s];
   }
+  return PKV_OK;
+}
+
+extern "C" int pkv_seq_fork(pkv_alloc *a, int32_t seq_id, int32_t n, int32_t *child_ids,
+                            int32_t *copy_src, int32_t *copy_dst, int32_t *n_copies) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && n >= 0 && n_copies, PKV_ERR_INVALID_ARG, "NULL argument or n < 0");
+  PKV_REQUIRE(a->is_live(seq_id), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", seq_id);
+  *n_copies = 0;
+  if (n == 0) return PKV_OK;
+  PKV_REQUIRE(child_ids, PKV_ERR_INVALID_ARG, "NULL child_ids");
+  PKV_REQUIRE(static_cast<size_t>(n) <= a->free_ids.size(), PKV_ERR_INVALID_ARG,
+              "%d forks but only %zu free sequence ids", n, a->free_ids.size());
+  const int32_t whole = a->lengths[seq_id] / kBlock, used = a->n_blocks[seq_id];
+  const bool part = whole < used;
+  PKV_REQUIRE(!part || (copy_src && copy_dst), PKV_ERR_INVALID_ARG,
+              "a last block that is not full is to be copied: NULL copy list");
+  PKV_REQUIRE(!part || static_cast<size_t>(n) <= a->free_stack.size(), PKV_ERR_OUT_OF_BLOCKS,
+              "forks need %d blocks, %zu free", n, a->free_stack.size());
+  const int32_t *from = a->table(seq_id);
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t sid = a->free_ids.top();
+    a->free_ids.pop();
+    int32_t *t = a->table(sid);
+    for (int32_t j = 0; j < whole; ++j) {
+      t[j] = from[j];
+      ++a->refs[t[j]];
+    }
+    if (part) {
+      t[whole] = a->take();
+      copy_src[i] = from[whole];
+      copy_dst[i] = t[whole];
+    }
+    a->n_blocks[sid] = used;
+    a->lengths[sid] = a->lengths[seq_id];
+    a->offsets[sid] = a->offsets[seq_id];
+    a->live[sid] = 1;
+    ++a->generation[sid];
+    child_ids[i] = sid;
+  }
+  *n_copies = part ? n : 0;
+  return PKV_OK;
+}
+
+extern "C" int pkv_seqs_truncate(pkv_alloc *a, const int32_t *seq_ids, const int32_t *lens, int32_t n,
+                                 int32_t *copy_src, int32_t *copy_dst, int32_t *n_copies) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && n >= 0 && n_copies, PKV_ERR_INVALID_ARG, "NULL argument or n < 0");
+  *n_copies = 0;
+  if (n == 0) return PKV_OK;
+  PKV_REQUIRE(seq_ids && lens, PKV_ERR_INVALID_ARG, "NULL argument");
+  a->next_epoch();
+  size_t need = 0;
+  // the block that sequence s would end inside of, -1 at a block's end
+  auto last = [&](int32_t s, int32_t len) {
+    return len % kBlock != 0 && len < a->lengths[s] ? a->table(s)[len / kBlock] : -1;
+  };
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t s = seq_ids[i];
+    PKV_REQUIRE(a->is_live(s), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", s);
+    PKV_REQUIRE(a->stamp[s] != a->epoch, PKV_ERR_INVALID_ARG, "sequence %d listed twice", s);
+    a->stamp[s] = a->epoch;
+    PKV_REQUIRE(lens[i] >= 0 && lens[i] <= a->lengths[s], PKV_ERR_INVALID_ARG,
+                "sequence %d of %d tokens cannot be cut to %d", s, a->lengths[s], lens[i]);
+    const int32_t b = last(s, lens[i]);
+    if (b >= 0 && a->refs[b] > 1) ++need;
+  }
+  PKV_REQUIRE(need == 0 || (copy_src && copy_dst), PKV_ERR_INVALID_ARG,
+              "shared blocks are to be copied: NULL copy list");
+  PKV_REQUIRE(need <= a->free_stack.size(), PKV_ERR_OUT_OF_BLOCKS,
+              "%zu shared blocks are to be copied, %zu blocks free", need, a->free_stack.size());
+  // copies' destinations first, so that no block that this call frees becomes one
+  int32_t copies = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t b = last(seq_ids[i], lens[i]);
+    if (b < 0 || a->refs[b] == 1) continue;
+    copy_src[copies] = b;
+    copy_dst[copies] = a->take();
+    --a->refs[b];   // (others have it still)
+    a->table(seq_ids[i])[lens[i] / kBlock] = copy_dst[copies++];
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t s = seq_ids[i];
+    if (lens[i] == a->lengths[s]) continue;
+    const int32_t left = static_cast<int32_t>(blocks_for(lens[i]));
+    const int32_t *t = a->table(s);
+    for (int32_t j = left; j < a->n_blocks[s]; ++j) a->give_back(t[j]);
+    a->n_blocks[s] = left;
+    a->lengths[s] = lens[i];
+    ++a->generation[s];   // a cached table row of it is rewritten
+  }
+  *n_copies = copies;
+  return PKV_OK;
+}
+
+extern "C" int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B,
+                                 const int32_t *counts, const int32_t *depths, int32_t *positions,
+                                 int64_t *slot_mapping, int32_t *node_starts, int32_t *seq_lens,
+                                 int32_t *block_tables, int32_t bt_stride) {
+  pkv::clear_error();
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "NULL allocator");
+  PKV_REQUIRE(B >= 0, PKV_ERR_INVALID_ARG, "B < 0");
+  PKV_REQUIRE(node_starts, PKV_ERR_INVALID_ARG, "NULL argument");
+  if (B == 0) {
+    node_starts[0] = 0;
+    return PKV_OK;
+  }
+  PKV_REQUIRE(seq_ids && counts && seq_lens && block_tables, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(bt_stride > 0, PKV_ERR_INVALID_ARG, "bt_stride must be positive");
+  a->next_epoch();
+  const int32_t width = bt_stride < a->max_blocks_per_seq ? bt_stride : a->max_blocks_per_seq;
+  int64_t need = 0, T = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    const int32_t s = seq_ids[b];
+    PKV_REQUIRE(a->is_live(s), PKV_ERR_UNKNOWN_SEQ, "row %d: sequence %d is not live", b, s);
+    PKV_REQUIRE(a->stamp[s] != a->epoch, PKV_ERR_INVALID_ARG, "sequence %d listed twice in one step",
+                s);
+    a->stamp[s] = a->epoch;
+    PKV_REQUIRE(counts[b] >= 0, PKV_ERR_INVALID_ARG, "row %d: %d tokens", b, counts[b]);
+    const int64_t len = static_cast<int64_t>(a->lengths[s]) + counts[b];
+    PKV_REQUIRE(blocks_for(len) <= width, PKV_ERR_INVALID_ARG,
+                "sequence %d would need %lld blocks > %d", s, (long long)blocks_for(len), width);
+    PKV_REQUIRE(T + counts[b] <= INT32_MAX, PKV_ERR_INVALID_ARG, "too many tokens in one step");
+    // (without depths the last node's position is the largest)
+    for (int32_t i = depths ? 0 : std::max(counts[b] - 1, 0); i < counts[b]; ++i) {
+      const int64_t depth = depths ? depths[T + i] : i;
+      PKV_REQUIRE(depth >= 0 && a->lengths[s] + a->offsets[s] + depth <= INT32_MAX,
+                  PKV_ERR_INVALID_ARG, "sequence %d: node %d has a bad depth or position", s, i);
+    }
+    T += counts[b];
+    need += blocks_for(len) - a->n_blocks[s];
+  }
+  PKV_REQUIRE(T == 0 || (positions && slot_mapping), PKV_ERR_INVALID_ARG, "NULL output");
+  PKV_REQUIRE(need <= static_cast<int64_t>(a->free_stack.size()), PKV_ERR_OUT_OF_BLOCKS,
+              "step needs %lld new blocks, %zu free", (long long)need, a->free_stack.size());
+  int32_t at = 0;
+  for (int32_t b = 0; b < B; ++b) {
+    const int32_t s = seq_ids[b], len = a->lengths[s], end = len + counts[b];
+    int32_t *t = a->table(s);
+    while (a->n_blocks[s] < blocks_for(end)) t[a->n_blocks[s]++] = a->take();
+    node_starts[b] = at;
+    for (int32_t p = len; p < end; ++p, ++at) {
+      positions[at] = len + a->offsets[s] + (depths ? depths[at] : p - len);
+      slot_mapping[at] = static_cast<int64_t>(t[p / kBlock]) * kBlock + p % kBlock;
+    }
+    a->lengths[s] = seq_lens[b] = end;
+    int32_t *row = block_tables + static_cast<size_t>(b) * bt_stride;
+    std::memcpy(row, t, sizeof(int32_t) * a->n_blocks[s]);
+    for (int32_t j = a->n_blocks[s]; j < bt_stride; ++j) row[j] = -1;
+  }
+  node_starts[B] = at;
+  return PKV_OK;
+}
+
+extern "C" int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst,
+                                int32_t cap, int32_t *n) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && n && cap >= 0, PKV_ERR_INVALID_ARG, "NULL argument or cap < 0");
+  PKV_REQUIRE(num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
+  *n = 0;
+  const size_t used = a->num_blocks - a->free_stack.size();
+  PKV_REQUIRE(used <= static_cast<size_t>(num_blocks), PKV_ERR_OUT_OF_BLOCKS,
+              "%zu blocks are in use, more than %d", used, num_blocks);
+  try {
+    if (num_blocks >= a->num_blocks) {
+      a->refs.resize(num_blocks, 0);
+      a->free_stack.reserve(num_blocks);   // (room for every block: giving one back cannot fail)
+      for (int32_t b = a->num_blocks; b < num_blocks; ++b) a->free_stack.push_back(b);
+      a->num_blocks = num_blocks;
+      return PKV_OK;
+    }
+    std::vector<int32_t> to(a->num_blocks, -1);   // new id of a block that moves
+    int32_t moves = 0;
+    for (int32_t b = num_blocks; b < a->num_blocks; ++b) moves += a->refs[b] > 0;
+    if (moves > cap || (moves > 0 && (!src || !dst))) {
+      *n = moves;
+      return pkv::fail(PKV_ERR_INVALID_ARG, "%d blocks move, room for %d", moves,
+                       src && dst ? cap : 0);
+    }
+    a->free_stack.erase(std::remove_if(a->free_stack.begin(), a->free_stack.end(),
+                                       [&](int32_t b) { return b >= num_blocks; }),
+                        a->free_stack.end());
+    for (int32_t s = 0; s < a->max_seqs; ++s) {
+      if (!a->live[s]) continue;
+      int32_t *t = a->table(s);
+      bool moved = false;
+      for (int32_t j = 0; j < a->n_blocks[s]; ++j) {
+        if (t[j] < num_blocks) continue;
+        if (to[t[j]] < 0) {
+          const int32_t b = a->take();
+          a->refs[b] = a->refs[t[j]];
+          src[*n] = t[j];
+          dst[(*n)++] = b;
+          to[t[j]] = b;
+        }
+        t[j] = to[t[j]];
+        moved = true;
+      }
+      if (moved) ++a->generation[s];   // a cached table row of it is rewritten
+    }
+    a->refs.resize(num_blocks);
+    a->num_blocks = num_blocks;
+  } catch (...) {
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out of host memory");
+  }
+  return PKV_OK;
+}
+
+extern "C" int pkv_block_refs(const pkv_alloc *a, int32_t block, int32_t *refs) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && refs, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(block >= 0 && block < a->num_blocks, PKV_ERR_INVALID_ARG, "block %d", block);
+  *refs = a->refs[block];
   return PKV_OK;
 }
 

@@ -1,5 +1,6 @@
 // Rotary positions in the layouts and scalings of pkv_rotary_spec, with the
-// append of the rotated key and the value (pkv_rotary_append).
+// append of the rotated key and the value (pkv_rotary_append); the same with a position
+// on each of several axes, every pair turning by its own axis' (pkv_rotary_axes_append).
 //
 // Mathematics.  Pair i of a head at position p turns by p * f_i; f_i is made
 // once on the host in double precision (pkv_rotary_init) and kept as a 64-bit
@@ -19,7 +20,7 @@
 namespace pkv {
 namespace {
 
-constexpr uint32_t kRotaryCheck = 0x526f7431u;
+constexpr uint32_t kRotaryCheck = 0x526f7431u, kAxesCheck = 0x41786573u;
 constexpr int kThreads = 256;
 
 struct RotaryParams {
@@ -35,17 +36,29 @@ struct RotaryParams {
   unsigned long long turns[128];
 };
 
+// The same with an axis for every pair (pkv_rotary_axes_append): token t's position on
+// axis a is positions[a * axis_stride + t].  (Structs of their own, so that the calls with
+// one axis carry and read nothing more than before.)
+struct AxesParams : RotaryParams {
+  long long axis_stride;
+  uint8_t axis[128];
+};
+__device__ __forceinline__ int position(const RotaryParams &p, int t, int) { return p.positions[t]; }
+__device__ __forceinline__ int position(const AxesParams &p, int t, int pair) {
+  return p.positions[p.axis[pair] * p.axis_stride + t];
+}
+
 // The angles of the CTA's tokens, amplitude * (cos, sin): cs [tokens][rot/2], or with
 // VEC > 1 [tokens][VEC/2][rot/2/VEC][2], so that threads of neighbouring items (VEC
 // pairs each) read two pairs from neighbouring 16 bytes (pair after pair, eight
 // threads met in the same banks four times over).
-template <int VEC>
-__device__ __forceinline__ void fill_angles(const RotaryParams &p, float2 *cs, int t0, int nt) {
+template <int VEC, typename P>
+__device__ __forceinline__ void fill_angles(const P &p, float2 *cs, int t0, int nt) {
   const int half = p.rot >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half, c = i - t * half;
     const unsigned long long ph =
-        static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t])) * p.turns[c];
+        static_cast<unsigned long long>(static_cast<long long>(position(p, t0 + t, c))) * p.turns[c];
     float s, co;
     // the signed fraction of a turn times 2 pi / 2^64
     sincosf(static_cast<float>(static_cast<long long>(ph)) * 3.4061215800865545e-19f, &s, &co);
@@ -105,8 +118,8 @@ __device__ __forceinline__ void rotate_item(uint4 &a, uint4 &b, const float4 *w,
 // formed.  16384 tokens of 32 + 8 heads of 128 in bf16, whole heads turned: 64 us, 6.3
 // TB/s (float32 119 us, 6.8 TB/s); four pairs at a time, with fewer CTAs on an SM, took
 // 5 % longer.
-template <typename T, bool IL>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+template <typename T, bool IL, typename P>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ P p) {
   extern __shared__ float2 cs[];
   constexpr int VEC = 16 / static_cast<int>(sizeof(T)), kBatch = 2;
   pdl_wait();
@@ -201,9 +214,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 // value head.  Bound by its instructions (an element a load, the divisions of an item):
 // 16384 tokens of 32 + 8 heads of 80, 20 rotated: 153 us in bf16 (1.6 TB/s), 151 us in
 // float32 (3.3 TB/s).
-template <typename T, bool IL>
-__global__ void __launch_bounds__(kThreads) rotary_any_kernel(
-    const __grid_constant__ RotaryParams p) {
+template <typename T, bool IL, typename P>
+__global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_constant__ P p) {
   extern __shared__ float2 cs[];
   pdl_wait();
   const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0);
@@ -248,26 +260,15 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(
   }
 }
 
-template <typename T>
-cudaError_t launch(const RotaryParams &p, bool wide, bool il, unsigned grid, size_t smem,
-                   cudaStream_t s) {
-  auto kern = wide ? (il ? rotary_kernel<T, true> : rotary_kernel<T, false>)
-                   : (il ? rotary_any_kernel<T, true> : rotary_any_kernel<T, false>);
+template <typename T, typename P>
+cudaError_t launch(const P &p, bool wide, bool il, unsigned grid, size_t smem, cudaStream_t s) {
+  auto kern = wide ? (il ? rotary_kernel<T, true, P> : rotary_kernel<T, false, P>)
+                   : (il ? rotary_any_kernel<T, true, P> : rotary_any_kernel<T, false, P>);
   return launch_waiting(kern, grid, kThreads, smem, s, p);
 }
 
-}  // namespace
-}  // namespace pkv
-
-using namespace pkv;
-
-extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *out) {
-  clear_error();
-  PKV_REQUIRE(s && out, PKV_ERR_INVALID_ARG, "NULL argument");
-  PKV_REQUIRE(d >= 2 && d <= 256 && d % 2 == 0, PKV_ERR_UNSUPPORTED, "head_dim %d", d);
-  const int r = s->rot_dim;
-  PKV_REQUIRE(r >= 2 && r <= d && r % 2 == 0, PKV_ERR_INVALID_ARG,
-              "rot_dim %d must be even, in [2, %d]", r, d);
+// What pkv_rotary_init checks of a spec besides the rotated elements' number.
+int check_spec(const pkv_rotary_spec *s) {
   PKV_REQUIRE(s->layout == PKV_ROTARY_HALF || s->layout == PKV_ROTARY_INTERLEAVED,
               PKV_ERR_UNSUPPORTED, "layout %d", s->layout);
   PKV_REQUIRE(s->scaling >= PKV_ROTARY_PLAIN && s->scaling <= PKV_ROTARY_BANDS,
@@ -278,6 +279,11 @@ extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *
               "amplitude must be positive and finite in float32");
   PKV_REQUIRE(s->scaling == PKV_ROTARY_PLAIN || (s->factor >= 1.0 && std::isfinite(s->factor)),
               PKV_ERR_INVALID_ARG, "factor must be >= 1");
+  return PKV_OK;
+}
+
+// The turns of the r/2 pairs of r rotating elements.
+int fill_turns(const pkv_rotary_spec *s, int r, uint64_t *turns) {
   double base = s->base;
   if (s->scaling == PKV_ROTARY_NTK) {
     PKV_REQUIRE(r > 2, PKV_ERR_INVALID_ARG, "this scaling needs rot_dim > 2");
@@ -310,19 +316,104 @@ extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *
       const double w = std::fmin(1.0, std::fmax(0.0, (t - s->low) / (s->high - s->low)));
       f = g * w + g / s->factor * (1.0 - w);
     }
-    out->turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));   // f <= 1
+    turns[i] = static_cast<uint64_t>(std::ldexp(f / two_pi, 64));   // f <= 1
   }
+  return PKV_OK;
+}
+
+}  // namespace
+
+int rotary_append(const pkv_rotary_args *a, const pkv_rotary_axes *axes, long long axis_stride,
+                  void *stream);
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_rotary_init(const pkv_rotary_spec *s, int32_t d, pkv_rotary *out) {
+  clear_error();
+  PKV_REQUIRE(s && out, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(d >= 2 && d <= 256 && d % 2 == 0, PKV_ERR_UNSUPPORTED, "head_dim %d", d);
+  const int r = s->rot_dim;
+  PKV_REQUIRE(r >= 2 && r <= d && r % 2 == 0, PKV_ERR_INVALID_ARG,
+              "rot_dim %d must be even, in [2, %d]", r, d);
+  int rc = check_spec(s);
+  if (rc != PKV_OK) return rc;
+  rc = fill_turns(s, r, out->turns);
+  if (rc != PKV_OK) return rc;
   for (int i = r / 2; i < 128; ++i) out->turns[i] = 0;
   out->d = d;
   out->rot_dim = r;
   out->layout = s->layout;
-  out->amplitude = amplitude;
+  out->amplitude = static_cast<float>(s->amplitude);
   out->check = kRotaryCheck;
+  return PKV_OK;
+}
+
+extern "C" int pkv_rotary_axes_init(const pkv_rotary_spec *s, int32_t d, const int32_t *sections,
+                                    int32_t n_axes, int32_t order, int32_t ladder,
+                                    pkv_rotary *out, pkv_rotary_axes *axes) {
+  clear_error();
+  PKV_REQUIRE(s && sections && out && axes, PKV_ERR_INVALID_ARG, "NULL argument");
+  PKV_REQUIRE(n_axes >= 1 && n_axes <= PKV_ROTARY_MAX_AXES, PKV_ERR_INVALID_ARG, "%d axes", n_axes);
+  PKV_REQUIRE(order == PKV_AXES_BLOCKED || order == PKV_AXES_CYCLIC, PKV_ERR_UNSUPPORTED, "order %d",
+              order);
+  PKV_REQUIRE(ladder == PKV_AXES_SHARED || ladder == PKV_AXES_OWN, PKV_ERR_UNSUPPORTED, "ladder %d",
+              ladder);
+  int pairs = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    PKV_REQUIRE(sections[a] >= 0 && sections[a] <= 128, PKV_ERR_INVALID_ARG, "axis %d: %d pairs", a,
+                sections[a]);
+    pairs += sections[a];
+  }
+  PKV_REQUIRE(2 * pairs == s->rot_dim, PKV_ERR_INVALID_ARG, "sections of %d pairs, rot_dim %d", pairs,
+              s->rot_dim);
+  // (the table without axes checks everything else, and serves PKV_AXES_SHARED)
+  pkv_rotary r;
+  int rc = pkv_rotary_init(s, d, &r);
+  if (rc != PKV_OK) return rc;
+  pkv_rotary_axes x = {};
+  x.n_axes = n_axes;
+  x.pairs = pairs;
+  int taken[PKV_ROTARY_MAX_AXES] = {};
+  for (int i = 0, a = 0; i < pairs; ++i) {
+    if (order == PKV_AXES_CYCLIC && i > 0) a = (a + 1) % n_axes;
+    while (taken[a] == sections[a]) a = (a + 1) % n_axes;
+    x.axis[i] = static_cast<uint8_t>(a);
+    ++taken[a];
+  }
+  if (ladder == PKV_AXES_OWN) {
+    for (int a = 0; a < n_axes; ++a) {
+      if (sections[a] == 0) continue;
+      uint64_t own[128];
+      rc = fill_turns(s, 2 * sections[a], own);
+      if (rc != PKV_OK) return rc;
+      for (int i = 0, k = 0; i < pairs; ++i)
+        if (x.axis[i] == a) r.turns[i] = own[k++];
+    }
+  }
+  x.check = kAxesCheck;
+  *out = r;
+  *axes = x;
   return PKV_OK;
 }
 
 extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
   clear_error();
+  return rotary_append(a, nullptr, 0, stream);
+}
+
+extern "C" int pkv_rotary_axes_append(const pkv_rotary_args *a, const pkv_rotary_axes *axes,
+                                      int64_t axis_stride, void *stream) {
+  clear_error();
+  PKV_REQUIRE(axes, PKV_ERR_INVALID_ARG, "axes is NULL");
+  PKV_REQUIRE(axes->check == kAxesCheck, PKV_ERR_INVALID_ARG,
+              "axes was not filled by pkv_rotary_axes_init");
+  return rotary_append(a, axes, axis_stride, stream);
+}
+
+int pkv::rotary_append(const pkv_rotary_args *a, const pkv_rotary_axes *axes, long long axis_stride,
+                       void *stream) {
   PKV_REQUIRE(a && a->rotary, PKV_ERR_INVALID_ARG, "NULL argument");
   const pkv_rotary &r = *a->rotary;
   PKV_REQUIRE(r.check == kRotaryCheck, PKV_ERR_INVALID_ARG,
@@ -332,6 +423,10 @@ extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
   PKV_REQUIRE(a->d == r.d, PKV_ERR_INVALID_ARG, "head_dim %d, but rotary was made for %d", a->d,
               r.d);
   PKV_REQUIRE(a->Hq <= 65536 && a->Hkv <= 65536, PKV_ERR_UNSUPPORTED, "too many heads");
+  PKV_REQUIRE(!axes || 2 * axes->pairs == r.rot_dim, PKV_ERR_INVALID_ARG,
+              "axes of %d pairs, but rotary has %d", axes->pairs, r.rot_dim / 2);
+  PKV_REQUIRE(!axes || axes->n_axes == 1 || axis_stride >= a->T, PKV_ERR_INVALID_ARG,
+              "the axes' positions overlap: axis_stride %lld < %d tokens", axis_stride, a->T);
   if (a->T == 0 || a->Hq + a->Hkv == 0) return PKV_OK;
   const bool append = a->slot_mapping != nullptr && a->Hkv > 0;
   PKV_REQUIRE(a->positions, PKV_ERR_INVALID_ARG, "positions is NULL");
@@ -439,8 +534,18 @@ extern "C" int pkv_rotary_append(const pkv_rotary_args *a, void *stream) {
   const size_t smem = static_cast<size_t>(tb) * (r.rot_dim / 2) * sizeof(float2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool il = r.layout == PKV_ROTARY_INTERLEAVED;
-  const cudaError_t e = a->dtype == PKV_BF16 ? launch<__nv_bfloat16>(p, wide, il, grid, smem, s)
-                                             : launch<float>(p, wide, il, grid, smem, s);
+  cudaError_t e;
+  if (axes) {
+    AxesParams x;
+    static_cast<RotaryParams &>(x) = p;
+    x.axis_stride = axis_stride;
+    for (int i = 0; i < 128; ++i) x.axis[i] = axes->axis[i];
+    e = a->dtype == PKV_BF16 ? launch<__nv_bfloat16>(x, wide, il, grid, smem, s)
+                             : launch<float>(x, wide, il, grid, smem, s);
+  } else {
+    e = a->dtype == PKV_BF16 ? launch<__nv_bfloat16>(p, wide, il, grid, smem, s)
+                             : launch<float>(p, wide, il, grid, smem, s);
+  }
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "rotary_kernel launch: %s", cudaGetErrorString(e));
   return PKV_OK;
 }
