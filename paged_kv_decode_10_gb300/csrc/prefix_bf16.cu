@@ -33,6 +33,7 @@
 // softmax of a step (scores in, 128 exponentials a row, weights out) between its two
 // products: a step of both slots takes 3140 clocks, its products 2048.
 #include "prefix.h"
+#include "tensor_core.cuh"
 
 namespace pkv {
 namespace {
@@ -63,169 +64,6 @@ struct Lay {
   static constexpr int kSums = kRows + 2 * kSoftmax * 4;  // m, l of the second slot
   static constexpr int kMisc = kSums + 2 * kTile * 4;
   static constexpr int kBytes = kMisc + 64 + 1024;        // + alignment slack
-};
-
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  // 128-byte swizzle (2 << 61), descriptor version 1 (1 << 46), offsets in 16 bytes
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
-         static_cast<uint64_t>(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
-// float32 accumulator, bf16 operands, M = 128; bit 16: B is MN-major
-__host__ __device__ constexpr uint32_t inst_desc(int n, bool b_mn) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 |
-         (128u / 16) << 24;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// One lane of the converged warp, picked by the hardware, and a value the compiler
-// may take as the same in every lane: the operands of the products then sit in
-// uniform registers (an ordinary lane test made each issue cost ~117 clocks).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t on;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(on));
-  return on != 0;
-}
-template <typename I>
-__device__ __forceinline__ I uniform(I x) {
-  return __shfl_sync(0xffffffffu, x, 0);
-}
-// bar gets one arrival once every product issued so far by this thread is done
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tm_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tm_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 32 columns of the warp's 32 lanes (one lane a thread)
-__device__ __forceinline__ void tm_ld32(uint32_t addr, float *r) {
-  uint32_t *u = reinterpret_cast<uint32_t *>(r);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]),
-        "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]),
-        "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(addr));
-}
-// Values that a load from tensor memory was told to bring are not used before the
-// wait ahead of this (to the compiler the load itself has written them).
-__device__ __forceinline__ void pin32(float *r) {
-  asm volatile(""
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]),
-                 "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]),
-                 "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]),
-                 "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]),
-                 "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]),
-                 "+f"(r[31]));
-}
-__device__ __forceinline__ void tm_st32(uint32_t addr, const float *r) {
-  const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
-      "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]),
-      "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
-      "r"(u[30]), "r"(u[31])
-      : "memory");
-}
-__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t *u) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16};" ::"r"(addr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
-      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-      : "memory");
-}
-__device__ __forceinline__ void store8(float *p, const float *v) {   // one 32-byte sector
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
-               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
-// Two float32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// An mbarrier wait that gives up when another role has, or after the limit.  POLL: for
-// limits shorter than the time for which try_wait may suspend the thread (a build of its
-// own: asking at every wait cost 4 % of the kernel).
-template <bool POLL>
-struct Waiter {
-  volatile int *abort;
-  int32_t *err;
-  long long limit;
-  __device__ __forceinline__ bool done(uint64_t *bar, uint32_t parity) const {
-    return POLL ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-  }
-  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-    if (done(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-      if (done(bar, parity)) return true;
-      if (*abort) return false;
-      if (clock64() - t0 > limit) {
-        *abort = 1;
-        set_dev_err(err, PKV_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-  // the same decision for the whole warp
-  __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, (*this)(bar, parity));
-  }
 };
 
 template <int D, bool POLL>

@@ -1,5 +1,5 @@
 // pkv_decode_attn_tree: attention of drafted tokens over the paged cache.  Here the call,
-// the kernel on CUDA cores and the join of items that several CTAs shared.
+// the float32 kernel (CUDA cores) and the join of items that several CTAs shared.
 //
 // Mathematics.  Node i of a row sees the row's tokens ahead of its nodes and those nodes
 // that its mask names (without one, the nodes up to itself): out = sum_t softmax_t(s) v_t
@@ -8,11 +8,12 @@
 #include "tree.h"
 
 #include "attention_host.h"
+#include "attention_kernel.cuh"
 
 namespace pkv {
 namespace {
 
-// ---- CUDA cores -----------------------------------------------------------------
+// ---- float32 -----------------------------------------------------------------
 // 64 rows (queries) against 64 tokens a step: 16 x 16 threads, thread (ty, tx) has rows
 // ty + 16 i and, for the scores, tokens tx + 16 j, for the output columns 4 tx + 64 m.
 // Items of at most 16 or 32 rows use one or two of the four row registers.
@@ -27,24 +28,14 @@ struct Lay {
   static constexpr int kFloats = kPages + kStep / kBlockTokens;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) {
-  return *reinterpret_cast<const float4 *>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-template <typename T, int D, int NR>
-__device__ __forceinline__ void simt_item(const TreeParams &p, const TreeItem &it, float *sm) {
+template <int D, int NR>
+__device__ __forceinline__ void f32_item(const TreeParams &p, const TreeItem &it, float *sm) {
   using L = Lay<D>;
   constexpr int LD = L::LD, M = D / 64, kCols = D / 4;
   float *qs = sm + L::kQ, *ks = sm + L::kK, *vs = sm + L::kV, *ps = sm + L::kP;
@@ -52,12 +43,12 @@ __device__ __forceinline__ void simt_item(const TreeParams &p, const TreeItem &i
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int rows = it.nodes * p.G;
   const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
-  const T *kc = static_cast<const T *>(p.k_cache), *vc = static_cast<const T *>(p.v_cache);
+  const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
   for (int e = tid; e < 16 * NR * kCols; e += kThreads) {
     const int r = e / kCols, c = e % kCols * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows) {
-      x = load4(static_cast<const T *>(p.q) +
+      x = load4(static_cast<const float *>(p.q) +
                 (static_cast<size_t>(it.q0 + r / p.G) * p.Hq + it.g * p.G + r % p.G) * D + c);
       x.x *= p.scale_log2;
       x.y *= p.scale_log2;
@@ -210,7 +201,7 @@ __device__ __forceinline__ void simt_item(const TreeParams &p, const TreeItem &i
                                    acc[i][m].w * inv);
       const int c = 4 * tx + 64 * m;
       if (whole)
-        store4(static_cast<T *>(p.out) + at * D + c, o);
+        store4(static_cast<float *>(p.out) + at * D + c, o);
       else
         store4(p.part_o + (static_cast<size_t>(slot) * p.tile + r) * D + c, o);
     }
@@ -223,9 +214,9 @@ __device__ __forceinline__ void simt_item(const TreeParams &p, const TreeItem &i
   }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
-    tree_simt_kernel(const __grid_constant__ TreeParams p) {
+    tree_f32_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(16) float sm[];
   pdl_wait();
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
@@ -235,23 +226,23 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   TreeItem it;
   while (walk.next(&it)) {
     if (it.t0 == 0 && it.t1 < it.steps)
-      cut = TreeCut{it.more, it.q0, it.nodes * p.G, it.g, it.base, it.n};
+      cut = TreeCut{walk.more(), it.q0, it.nodes * p.G, it.g, it.base, it.n};
     const int rows = it.nodes * p.G;
     __syncthreads();   // (the item before is done with the queries)
     if (rows <= 16)
-      simt_item<T, D, 1>(p, it, sm);
+      f32_item<D, 1>(p, it, sm);
     else if (rows <= 32)
-      simt_item<T, D, 2>(p, it, sm);
+      f32_item<D, 2>(p, it, sm);
     else
-      simt_item<T, D, 4>(p, it, sm);
+      f32_item<D, 4>(p, it, sm);
   }
   if (threadIdx.x == 0) p.cuts[cta] = cut;
 }
 
-template <typename T, int D>
-cudaError_t launch_simt(const TreeParams &p, cudaStream_t s) {
+template <int D>
+cudaError_t launch_f32(const TreeParams &p, cudaStream_t s) {
   constexpr int smem = Lay<D>::kFloats * 4;
-  auto kern = tree_simt_kernel<T, D>;
+  auto kern = tree_f32_kernel<D>;
   static std::atomic<unsigned long long> attrs_set{0};
   cudaError_t e = set_attributes_once(attrs_set, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -331,8 +322,8 @@ int tree_space(int d, int dtype, TreeSpace *s) {
   int sms = 0;
   const int rc = current_sms(&sms);
   if (rc != PKV_OK) return rc;
-  s->tile = kTile;
-  s->ctas = d == 64 ? 2 * sms : sms;
+  s->tile = dtype == PKV_BF16 ? 256 : kTile;
+  s->ctas = dtype == PKV_F32 && d == 64 ? 2 * sms : sms;
   if (s->ctas > kMaxTreeCtas) s->ctas = kMaxTreeCtas;
   const size_t rows = 2 * static_cast<size_t>(s->ctas) * s->tile;
   s->lse = align256(s->ctas * sizeof(TreeCut));
@@ -349,11 +340,6 @@ int tree_shapes(int B, int T, int Hq, int Hkv, int d, int dtype) {
 }
 
 }  // namespace
-
-cudaError_t launch_tree_simt(const TreeParams &p, int D, int dtype, cudaStream_t s) {
-  if (dtype == PKV_F32) return D == 64 ? launch_simt<float, 64>(p, s) : launch_simt<float, 128>(p, s);
-  return D == 64 ? launch_simt<__nv_bfloat16, 64>(p, s) : launch_simt<__nv_bfloat16, 128>(p, s);
-}
 
 }  // namespace pkv
 
@@ -433,7 +419,18 @@ extern "C" int pkv_decode_attn_tree(const pkv_tree_args *a, void *stream) {
   p.tile = sp.tile;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_tree_simt(p, a->d, a->dtype, s);
+  p.wait_limit = (a->flags & PKV_ATTN_SHORT_WAITS) ? 64 : kWaitLimitCycles;
+  cudaError_t e;
+  if (a->dtype == PKV_BF16) {
+    CUtensorMap tk, tv;
+    rc = get_tmap(a->k_cache, rows, a->d, a->dtype, &tk);
+    if (rc != PKV_OK) return rc;
+    rc = get_tmap(a->v_cache, rows, a->d, a->dtype, &tv);
+    if (rc != PKV_OK) return rc;
+    e = launch_tree_bf16(tk, tv, p, a->d, s);
+  } else {
+    e = a->d == 64 ? launch_f32<64>(p, s) : launch_f32<128>(p, s);
+  }
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "tree kernel launch: %s", cudaGetErrorString(e));
   const unsigned grid = static_cast<unsigned>(sp.ctas) * kJoinChunks;
   e = a->dtype == PKV_BF16

@@ -51,7 +51,6 @@ struct TreeItem {
   int b, g, n0, nodes, q0;       // batch row, KV head, first node and nodes, first query row
   int base, n, tokens;           // the row's tokens ahead of its nodes, its nodes; tokens the item sees
   int t0, t1, steps;             // this CTA's steps of the item's
-  int more;                      // with t0 == 0: CTAs behind this one that have steps of it
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == steps; }
   __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0 ? 1 : 0); }
 };
@@ -132,12 +131,13 @@ struct TreeWalk {
           loaded = false;
         }
       }
-      if (it->t0 < it->t1) {
-        it->more = static_cast<int>((at * ctas - 1) / all) - cta;   // (the CTA of the last step)
-        return true;
-      }
+      if (it->t0 < it->t1) return true;
     }
     return false;
+  }
+  // CTAs behind this one that have steps of the item that next() gave last.
+  __device__ __forceinline__ int more() const {
+    return static_cast<int>((at * ctas - 1) / all) - cta;   // (the CTA of its last step)
   }
 };
 
@@ -242,7 +242,6 @@ __device__ __forceinline__ float tree_lse(float mx, float den, bool sees_any) {
                    : den == 0.f && !sees_any ? -INFINITY : __int_as_float(0x7fffffff);
 }
 
-cudaError_t launch_tree_simt(const TreeParams &p, int D, int dtype, cudaStream_t s);
 cudaError_t launch_tree_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p, int D,
                              cudaStream_t s);
 
