@@ -9,10 +9,11 @@
 // Roles (one CTA per SM, its share of the positions of tree.h):
 //  * warps 0-3 and 4-7: a softmax warpgroup per slot, an accumulator pair (S, O) in tensor
 //    memory; thread r owns query row r, weights go back as bf16 over their scores.
-//  * warp 8: TMA producer, 16-token pages of K and V into 128-byte-swizzled slabs, K-major
-//    for the first product, the same bytes MN-major for the second.
-//  * warps 9 and 10: issue the products of one slot each; warp 11 only completes the
-//    warpgroup.
+//  * warps 8 and 11: TMA producers of K and of V, 16-token pages into 128-byte-swizzled slabs,
+//    K-major for the first product, the same bytes MN-major for the second.  (With one warp
+//    for both, a K tile waited for the V tile ahead of it, which waits for a product: a
+//    load's latency a tile, 3.7 TB/s.)
+//  * warps 9 and 10: issue the products of one slot each.
 // Above 128 query rows the slots are two row tiles that share every K and V tile; up to 128
 // they take turns in the tokens and are merged at the end.  The largest score is followed
 // only when it grows by more than 2^8 (kLazy): weights up to 2^8 are exact enough in bf16.
@@ -137,10 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) {
-      // ======================= producer =======================
-      int x = 0;                     // tiles of the items before
-      int armed_k = 0, armed_v = 0;  // tiles whose copies were started
+    if (warp == 8 || warp == 11) {
+      // ======================= producers: K (warp 8), V (warp 11) =======================
+      const bool is_v = warp == 11;
+      uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+      const void *tmap = is_v ? &tmap_v : &tmap_k;
+      const uint32_t base = smem_u32(smem + (is_v ? L::kV : L::kK)) + lane * (kBlockTokens * 128);
+      int x = 0;       // tiles of the items before
+      int armed = 0;   // tiles whose copies were started
       bool ok = true;
       TreeCut cut = {};
       while (ok && walk.next(&it)) {
@@ -153,42 +158,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           return lane < kPages && tok < it.tokens ? table[tok >> 4] : -1;
         };
         int next = page_id(0);
-        for (int t = 0; t < tiles && ok; ++t) {
+        for (int t = 0; t < tiles; ++t) {
           const int blk = next;
           next = t + 1 < tiles ? page_id(t + 1) : -1;
           const int st = (x + t) % NS;
-          const uint32_t ph = static_cast<uint32_t>((x + t) / NS) & 1u;
           const bool good = blk >= 0 && blk < p.num_blocks;
           const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, good))) *
                                  (kBlockTokens * D * 2);
           const int y = (blk * p.Hkv + it.g) * kBlockTokens;
+          ok = wait.warp(&empty[st], (static_cast<uint32_t>((x + t) / NS) & 1u) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          __syncwarp();
+          if (good) {
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            uint64_t *full = kv ? &v_full[st] : &k_full[st];
-            ok = ok && wait.warp(kv ? &v_empty[st] : &k_empty[st], ph ^ 1u);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
-            if (good) {
-              const uint32_t dst =
-                  smem_u32(smem + (kv ? L::kV : L::kK) + st * L::kMat) + lane * (kBlockTokens * 128);
-#pragma unroll
-              for (int s = 0; s < L::kSlabs; ++s)
-                tma_load_2d(dst + s * L::kSlab, kv ? &tmap_v : &tmap_k, s * 64, y, full);
-            }
-            __syncwarp();
-            (kv ? armed_v : armed_k) = x + t + 1;
+            for (int s = 0; s < L::kSlabs; ++s)
+              tma_load_2d(base + st * L::kMat + s * L::kSlab, tmap, s * 64, y, &full[st]);
           }
+          __syncwarp();
+          armed = x + t + 1;
         }
         x += tiles;
       }
-      if (lane == 0) p.cuts[cta] = cut;
+      if (lane == 0 && !is_v) p.cuts[cta] = cut;
       // every copy has landed before the CTA ends (after a normal run they have)
-      for (int n = max(0, armed_k - NS); n < armed_k; ++n)
-        mbar_wait_bounded(&k_full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
-      for (int n = max(0, armed_v - NS); n < armed_v; ++n)
-        mbar_wait_bounded(&v_full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
-    } else if (warp <= 10) {
+      for (int n = max(0, armed - NS); n < armed; ++n)
+        mbar_wait_bounded(&full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
+    } else {
       // ======================= products of slot m =======================
       const int m = warp - 9;
       constexpr uint32_t kIdescS = inst_desc(kTile, false), kIdescO = inst_desc(D, true);
@@ -253,9 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = tile_of(j), st = (x + t) % NS;
           const int tok0 = (first + t) * kTile, valid = min(kTile, tokens - tok0);
           const bool more = j + 1 < n;
-          // the tiles first (they are there well before the weights)
-          ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u) &&
-               (!more || wait_k(tile_of(j + 1)));
+          // the values first (they are there well before the weights)
+          ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u);
           if (!ok) break;
           const bool odd_values = (odd & 2) && tok0 + valid > special;
           if (valid % kBlockTokens || (odd & 1) || odd_values) {
@@ -304,10 +299,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             weighted(2 * kHalf, kPages);
             release(&v_empty[st]);
-            if (more)
-              issue_scores(tile_of(j + 1));
-            else
-              mma_commit(&o_full[m]);
+            if (!more) mma_commit(&o_full[m]);
+          }
+          __syncwarp();
+          ok = !more || wait_k(tile_of(j + 1));
+          if (!ok) break;
+          if (elect_one()) {
+            if (more) issue_scores(tile_of(j + 1));
             next_turn();
           }
           __syncwarp();
