@@ -422,12 +422,14 @@ extern "C" int pkv_decode_attn_tree(const pkv_tree_args *a, void *stream) {
   p.wait_limit = (a->flags & PKV_ATTN_SHORT_WAITS) ? 64 : kWaitLimitCycles;
   cudaError_t e;
   if (a->dtype == PKV_BF16) {
-    CUtensorMap tk, tv;
+    CUtensorMap tq, tk, tv;
+    rc = query_tmap(a->q_rot, a->T, a->Hq, p.G, a->d, &tq);
+    if (rc != PKV_OK) return rc;
     rc = get_tmap(a->k_cache, rows, a->d, a->dtype, &tk);
     if (rc != PKV_OK) return rc;
     rc = get_tmap(a->v_cache, rows, a->d, a->dtype, &tv);
     if (rc != PKV_OK) return rc;
-    e = launch_tree_bf16(tk, tv, p, a->d, s);
+    e = launch_tree_bf16(tq, tk, tv, p, a->d, s);
   } else {
     e = a->d == 64 ? launch_f32<64>(p, s) : launch_f32<128>(p, s);
   }

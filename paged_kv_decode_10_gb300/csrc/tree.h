@@ -242,7 +242,7 @@ __device__ __forceinline__ float tree_lse(float mx, float den, bool sees_any) {
                    : den == 0.f && !sees_any ? -INFINITY : __int_as_float(0x7fffffff);
 }
 
-cudaError_t launch_tree_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p, int D,
-                             cudaStream_t s);
+cudaError_t launch_tree_bf16(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                             const TreeParams &p, int D, cudaStream_t s);
 
 }  // namespace pkv

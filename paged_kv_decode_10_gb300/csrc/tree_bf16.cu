@@ -18,13 +18,16 @@
 // they take turns in the tokens and are merged at the end.  The largest score is followed
 // only when it grows by more than 2^8 (kLazy): weights up to 2^8 are exact enough in bf16.
 //
+// Nothing holds the producers and issuers back between items: the queries come by TMA once
+// the last scores of the item before are done, and the next item's first scores are
+// computed while the softmax warps still write out.
+//
 // Masks.  Only steps that reach past the tokens every row sees (the cached ones, and in a
 // chain the nodes ahead of the item's) look at mask bits, 32 at a time.  What a node does not
-// see may be anything, and 0 * NaN is NaN: so the values of such tokens are looked at ahead
-// of the item (256 threads, with the queries' loads; their bytes are wanted in L2 anyway),
-// and where one is not finite the element is zeroed in shared memory for the product and
-// added at the end to the rows that see it (any positive weight leaves NaN and infinity what
-// they are).
+// see may be anything, and 0 * NaN is NaN: so the issuing warp looks over the values of such
+// tokens while the softmax is at work, and where one is not finite the element is zeroed in
+// shared memory for the product and added at the end to the rows that see it (any positive
+// weight leaves NaN and infinity what they are).
 #include "tensor_core.cuh"
 #include "tree.h"
 
@@ -52,11 +55,14 @@ struct Lay {
   static constexpr int kQ = 0;                            // [2] tiles
   static constexpr int kK = 2 * kMat;                     // [NS]
   static constexpr int kV = kK + NS * kMat;               // [NS]
-  static constexpr int kBars = kV + NS * kMat;
-  static constexpr int kNumBars = 4 * NS + 13;
+  static constexpr int kScratch = kV + NS * kMat;         // half of the second slot's O
+  static constexpr int kBars = kScratch + kTile * D / 2 * 4;
+  static constexpr int kNumBars = 4 * NS + 14;
   static constexpr int kSums = kBars + kNumBars * 8;      // m, l of the second slot
-  static constexpr int kMisc = kSums + 2 * kTile * 4;
-  static constexpr int kBytes = kMisc + 64 + 1024;        // + alignment slack
+  static constexpr int kBad = kSums + 2 * kTile * 4;      // [kBadRing] pages outside the pool
+  static constexpr int kBadRing = 16;
+  static constexpr int kMisc = kBad + kBadRing;
+  static constexpr int kBytes = kMisc + 32 + 1024;        // + alignment slack
 };
 
 using Walk = TreeWalk<kTile, kBoundary>;
@@ -66,14 +72,18 @@ __device__ __forceinline__ int first_special(const TreeParams &p, const TreeItem
   return it.base + (p.mask ? 0 : it.n0);
 }
 __device__ __forceinline__ bool odd_bf16(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
-__device__ __forceinline__ bool odd_word(uint32_t w) { return odd_bf16(w) || odd_bf16(w >> 16); }
+// Bits 15 and 31: a half's exponent is all ones (its sum with the lowest exponent bit
+// carries into the sign's place).
+__device__ __forceinline__ uint32_t odd_word(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
 __device__ __forceinline__ uint32_t clean_word(uint32_t w) {
   return (odd_bf16(w) ? 0u : w & 0xffffu) | (odd_bf16(w >> 16) ? 0u : w & 0xffff0000u);
 }
 
 template <int D, bool POLL>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
   using L = Lay<D>;
   constexpr int NS = L::NS;
@@ -85,9 +95,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *s_full = bars + 4 * NS, *p_ready = s_full + 2, *o_full = s_full + 4;   // [2] each
   uint64_t *q_full = s_full + 6, *both = s_full + 7, *drain = s_full + 8;
   uint64_t *turn = s_full + 9, *p_half = s_full + 11;   // [2] each
+  uint64_t *q_empty = s_full + 13;
+  volatile uint8_t *bad_s = reinterpret_cast<volatile uint8_t *>(smem + L::kBad);
   float *sums_s = reinterpret_cast<float *>(smem + L::kSums);
   volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);
-  // misc: a wait gave up, tmem, what is odd about an item (bit 0: pages, bit 1: values) [2]
+  // misc: a wait gave up, tmem, the last item of odd and of even number with values that are
+  // not finite [2] (its number + 1)
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (tid == 0) {
@@ -103,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_half[m], kTile / 32);
       mbar_init(&o_full[m], 1);
     }
-    mbar_init(q_full, kSoftmax / 32);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);   // one arrival per slot
     mbar_init(both, kSoftmax / 32);
     mbar_init(drain, 2);
     mbar_init(&turn[0], 1);
@@ -121,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   if (warp == 8 && lane == 0) {
+    prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
@@ -146,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = smem_u32(smem + (is_v ? L::kV : L::kK)) + lane * (kBlockTokens * 128);
       int x = 0;       // tiles of the items before
       int armed = 0;   // tiles whose copies were started
+      int n_items = 0, armed_q = 0;
       bool ok = true;
       TreeCut cut = {};
       while (ok && walk.next(&it)) {
@@ -168,6 +184,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int y = (blk * p.Hkv + it.g) * kBlockTokens;
           ok = wait.warp(&empty[st], (static_cast<uint32_t>((x + t) / NS) & 1u) ^ 1u);
           if (!ok) break;
+          if (!is_v) {
+            const uint32_t bad =
+                __ballot_sync(0xffffffffu, !good && lane < kPages &&
+                                               (it.t0 + t) * kTile + lane * kBlockTokens < it.tokens);
+            if (lane == 0) {
+              bad_s[(x + t) % L::kBadRing] = static_cast<uint8_t>(bad);
+              if (bad) set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
+            }
+          }
           if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
           __syncwarp();
           if (good) {
@@ -177,6 +202,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           armed = x + t + 1;
+          if (is_v && t == 0) {   // the queries, once the products of the item before are done with them
+            ok = wait.warp(q_empty, (static_cast<uint32_t>(n_items) & 1u) ^ 1u);
+            if (!ok) break;
+            const int q_tiles = it.nodes * p.G > kTile ? 2 : 1;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(q_full, q_tiles * L::kMat);
+              for (int e = 0; e < q_tiles; ++e)
+#pragma unroll
+                for (int s = 0; s < L::kSlabs; ++s)
+                  tma_load_3d(smem_u32(smem + L::kQ) + e * L::kMat + s * L::kSlab, &tmap_q, s * 64,
+                              it.g * p.G, it.q0 + e * (kTile / p.G), q_full);
+            }
+            __syncwarp();
+            armed_q = ++n_items;
+          }
         }
         x += tiles;
       }
@@ -184,10 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, armed - NS); n < armed; ++n)
         mbar_wait_bounded(&full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
+      if (armed_q) mbar_wait_bounded(q_full, static_cast<uint32_t>(armed_q - 1) & 1u, kDrainCycles);
     } else {
       // ======================= products of slot m =======================
       const int m = warp - 9;
-      constexpr uint32_t kIdescS = inst_desc(kTile, false), kIdescO = inst_desc(D, true);
+      constexpr uint32_t kIdescO = inst_desc(D, true);
+      // a negative scale is taken into Q (bit 13: A negated), so that the largest score
+      // stays the largest
+      const uint32_t idesc_s = inst_desc(kTile, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
       const uint32_t q_addr = smem_u32(smem + L::kQ), k_addr = smem_u32(smem + L::kK),
                      v_addr = smem_u32(smem + L::kV);
       int x = 0, n_items = 0;
@@ -200,7 +244,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait.warp(q_full, static_cast<uint32_t>(n_items) & 1u);
         if (!ok) break;
         tc_fence_after();
-        const int odd = uniform(misc[2 + (n_items & 1)] + 0);
         const int special = first_special(p, it);
         ++n_items;
         const int turns = two ? tiles : (tiles + 1) / 2;   // slot 0's tiles, at least this slot's
@@ -221,21 +264,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(empty);
           if (!two) mma_commit(empty);
         };
-        // S = Q K^T for tile t (issued by one lane)
-        auto issue_scores = [&](int t) {
+        // S = Q K^T for the slot's tile j (issued by one lane)
+        auto issue_scores = [&](int j) {
+          const int t = tile_of(j);
           const int st = (x + t) % NS;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = (ks / 4) * L::kSlab + (ks % 4) * 32;
             mma_ss(tS(m), smem_desc(q_addr + (two ? m * L::kMat : 0) + off, 16, 1024),
-                   smem_desc(k_addr + st * L::kMat + off, 16, 1024), kIdescS, ks > 0);
+                   smem_desc(k_addr + st * L::kMat + off, 16, 1024), idesc_s, ks > 0);
           }
           mma_commit(&s_full[m]);
           release(&k_empty[st]);
+          if (j + 1 == n) mma_commit(q_empty);
         };
         ok = (n == 0 || wait_k(tile_of(0))) && my_turn();
         if (ok && elect_one()) {
-          if (n > 0) issue_scores(tile_of(0));
+          if (n > 0)
+            issue_scores(0);
+          else
+            mbar_arrive(q_empty);
           next_turn();
         }
         __syncwarp();
@@ -252,30 +300,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the values first (they are there well before the weights)
           ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u);
           if (!ok) break;
-          const bool odd_values = (odd & 2) && tok0 + valid > special;
-          if (valid % kBlockTokens || (odd & 1) || odd_values) {
+          unsigned char *vt = smem + L::kV + st * L::kMat;
+          // 16-byte pieces of the tile's tokens from `first` to `last`: piece e, or where it lies
+          auto piece = [&](int e, int first, int last) {
+            const int s = e / ((last - first) * 8), c = e - s * ((last - first) * 8);
+            return reinterpret_cast<uint4 *>(vt + s * L::kSlab + first * 128 + c * 16);
+          };
+          bool changed = false;
+          const uint32_t bad = bad_s[(x + t) % L::kBadRing];
+          if (valid % kBlockTokens || bad) {
             // values of tokens that do not count may be anything: their weights are
             // zero, and so must they be (both slots of a shared tile write the zeros)
-            const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
-            unsigned char *vt = smem + L::kV + st * L::kMat;
             for (int pg = 0; pg * kBlockTokens < valid; ++pg) {
-              const int blk = table[tok0 / kBlockTokens + pg];
-              const int none =
-                  blk < 0 || blk >= p.num_blocks ? 0 : min(kBlockTokens, valid - pg * kBlockTokens);
-              const int look = odd_values ? 0 : none;   // tokens from here on are looked at
-              for (int e = lane; e < (kBlockTokens - look) * 8 * L::kSlabs; e += 32) {
-                const int s = e / ((kBlockTokens - look) * 8), c = e % ((kBlockTokens - look) * 8);
-                const int r = look + c / 8;   // (a 16-byte piece of it)
-                uint4 *at = reinterpret_cast<uint4 *>(vt + s * L::kSlab + (pg * kBlockTokens + look) * 128 +
-                                                      c * 16);
-                if (r >= none) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else if (tok0 + pg * kBlockTokens + r >= special) {
-                  const uint4 v = *at;
-                  *at = make_uint4(clean_word(v.x), clean_word(v.y), clean_word(v.z), clean_word(v.w));
-                }
-              }
+              const int end = (pg + 1) * kBlockTokens;
+              const int from = bad >> pg & 1 ? end - kBlockTokens : min(end, valid);
+              for (int e = lane; e < (end - from) * 8 * L::kSlabs; e += 32)
+                *piece(e, from, end) = make_uint4(0u, 0u, 0u, 0u);
             }
+            changed = true;
+          }
+          const int look = max(0, special - tok0);
+          if (look < valid) {
+            uint32_t odd = 0;
+            for (int e = lane; e < (valid - look) * 8 * L::kSlabs; e += 32) {
+              const uint4 v = *piece(e, look, valid);
+              odd |= odd_word(v.x) | odd_word(v.y) | odd_word(v.z) | odd_word(v.w);
+            }
+            if (__any_sync(0xffffffffu, odd != 0)) {
+              // (the note first: the other slot may find the tile clean already)
+              if (lane == 0) misc[2 + (n_items & 1)] = n_items;
+              __threadfence_block();
+              __syncwarp();
+              for (int e = lane; e < (valid - look) * 8 * L::kSlabs; e += 32) {
+                uint4 *at = piece(e, look, valid);
+                const uint4 v = *at;
+                *at = make_uint4(clean_word(v.x), clean_word(v.y), clean_word(v.z), clean_word(v.w));
+              }
+              changed = true;
+            }
+          }
+          if (changed) {
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -305,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = !more || wait_k(tile_of(j + 1));
           if (!ok) break;
           if (elect_one()) {
-            if (more) issue_scores(tile_of(j + 1));
+            if (more) issue_scores(j + 1);
             next_turn();
           }
           __syncwarp();
@@ -324,11 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes
     const uint32_t sS = tS(m) + lanes, sO = tO(m) + lanes;
-    // a negative scale is taken into Q, so that the largest score stays the largest
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     const int lg = __ffs(p.G) - 1;
-    int n_items = 0;
+    int x = 0, n_items = 0;
     uint32_t s_ph = 0, o_ph = 0, b_ph = 0;
     bool ok = true;
     auto arrive = [&](uint64_t *bar) {   // for the warp, after all of its lanes
@@ -348,61 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
       const int special = first_special(p, it);
       const int end = min(it.tokens, it.t1 * kTile);   // of this CTA's tokens
-      volatile int *odd_s = misc + 2 + (n_items & 1);
-      if (tid == 0) misc[2 + ((n_items + 1) & 1)] = 0;   // (read last in the item before)
       ++n_items;
-      constexpr int kStep = kSoftmax / (D / 8);   // rows between a thread's pieces
-      const int ch = tid % (D / 8);
-      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
-      for (int r0 = tid / (D / 8); r0 < (two ? 2 : 1) * kTile; r0 += 16 * kStep) {
-        uint4 v[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          // (rows that do not count read the last: a branch here would make the loads
-          // wait for one another)
-          const int row = min(r0 + u * kStep, total - 1);
-          v[u] = *reinterpret_cast<const uint4 *>(
-              q + (static_cast<size_t>(it.q0 + (row >> lg)) * p.Hq + it.g * p.G + (row & (p.G - 1))) * D +
-              ch * 8);
-        }
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int row = r0 + u * kStep;
-          uint4 x = make_uint4(v[u].x ^ flip, v[u].y ^ flip, v[u].z ^ flip, v[u].w ^ flip);
-          if (row >= total) x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < (two ? 2 : 1) * kTile)
-            *reinterpret_cast<uint4 *>(smem + L::kQ + (row / kTile) * L::kMat +
-                                       (ch / 8) * L::kSlab + (row % kTile) * 128 +
-                                       (((ch & 7) ^ (row & 7)) << 4)) = x;
-        }
-      }
-      // pages outside the pool, and values that are not finite where rows differ in what
-      // they see
-      int odd = 0;
-      for (int j = it.t0 * kPages + tid; j * kBlockTokens < end; j += kSoftmax) {
-        const int blk = table[j];
-        if (blk < 0 || blk >= p.num_blocks) {
-          odd |= 1;
-          set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
-        }
-      }
-      const int from = max(special, it.t0 * kTile);
-      for (int tok = from + tid / (D / 8); tok < end; tok += kStep) {
-        const int blk = table[tok / kBlockTokens];
-        if (blk < 0 || blk >= p.num_blocks) continue;
-        const uint4 v = *reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(p.v_cache) +
-            ((static_cast<size_t>(blk) * p.Hkv + it.g) * kBlockTokens + tok % kBlockTokens) * D + ch * 8);
-        if (odd_word(v.x) || odd_word(v.y) || odd_word(v.z) || odd_word(v.w)) odd |= 2;
-      }
-      odd = __reduce_or_sync(0xffffffffu, odd);
-      if (odd && lane == 0) atomicOr(const_cast<int *>(odd_s), odd);
-      meet();   // both have read the item before's odd_s, and written this one's
-      if (!ok) break;
-      fence_proxy_async_smem();
-      tc_fence_before();   // the reads of the item before's O
-      arrive(q_full);
-      odd = *odd_s;
+      const int from = max(special, it.t0 * kTile);    // of them, first that rows may differ in
       const int mine = (two ? m * kTile : 0) + r;   // this thread's row of the item
       const bool active = (two ? m * kTile : 0) + (warp & 3) * 32 < total;
       const int node = min(mine >> lg, it.nodes - 1);
@@ -415,24 +424,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int t = two ? j : 2 * j + m;
         const int tok0 = (it.t0 + t) * kTile;
-        const bool masked = tok0 + kTile > special || (odd & 1);
+        bool masked = tok0 + kTile > special;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (masked && active) {   // (ahead of the scores)
 #pragma unroll
           for (int q = 0; q < 4; ++q) vis[q] = sees(tok0 + 32 * q);
-          if (odd & 1) {
-#pragma unroll
-            for (int pg = 0; pg < kPages; ++pg) {
-              if (tok0 + pg * kBlockTokens >= it.tokens) continue;
-              const int blk = table[tok0 / kBlockTokens + pg];
-              if (blk < 0 || blk >= p.num_blocks) vis[pg / 2] &= pg & 1 ? 0xffffu : 0xffff0000u;
-            }
-          }
         }
         ok = wait.warp(&s_full[m], s_ph);
         if (!ok) break;
         s_ph ^= 1u;
         tc_fence_after();
+        const uint32_t bad = bad_s[(x + t) % L::kBadRing];
+        if (bad) {
+          masked = true;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            vis[q] &= (bad >> 2 * q & 1 ? 0u : 0xffffu) | (bad >> (2 * q + 1) & 1 ? 0u : 0xffff0000u);
+        }
         if (active) {
           float s[kTile];
 #pragma unroll
@@ -497,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&p_ready[m]);
       }
+      x += tiles;
       if (ok && n > 0) {
         ok = wait.warp(&o_full[m], o_ph);
         o_ph ^= 1u;
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sums_s[r] = mx;
         sums_s[kTile + r] = l;
       }
-      float *scratch = reinterpret_cast<float *>(smem + L::kQ + L::kMat);   // [D/2][128]
+      float *scratch = reinterpret_cast<float *>(smem + L::kScratch);   // [D/2][128]
       const bool whole = it.whole();
       const bool on = mine < total;
       const size_t out_at = static_cast<size_t>(it.q0 + node) * p.Hq + it.g * p.G + (mine & (p.G - 1));
@@ -531,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           meet();
         }
         if ((two || m == 0) && active && ok) {
+          // (behind the merge's meeting: the other slot's products are done, too)
+          const bool odd = misc[2 + (n_items & 1)] == n_items;
           if (h == 0) {
             float den = l;
             if (merge) {
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[e] *= w0;
               if (merge) o[e] = fmaf(w1, scratch[(32 * q + e) * kTile + r], o[e]);
             }
-            if (on && (odd & 2)) {   // what was left out of the products
+            if (on && odd) {   // what was left out of the products
 #pragma unroll 1
               for (int tok = from; tok < end; ++tok) {
                 if (!(sees(tok) & 1u)) continue;
@@ -604,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (merge) meet();
       }
-      meet();   // both are done with the item
     }
     tc_fence_before();
   }
@@ -632,23 +642,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool POLL>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                   cudaStream_t s) {
   auto kern = tree_tc_kernel<D, POLL>;
   static std::atomic<unsigned long long> attrs_set{0};
   cudaError_t e = set_attributes_once(attrs_set, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch_waiting(kern, p.C, kThreads, Lay<D>::kBytes, s, tk, tv, p);
+  return launch_waiting(kern, p.C, kThreads, Lay<D>::kBytes, s, tq, tk, tv, p);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_bf16(const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p, int D,
-                             cudaStream_t s) {
+cudaError_t launch_tree_bf16(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                             const TreeParams &p, int D, cudaStream_t s) {
   if (p.wait_limit <= kPollLimit)
-    return D == 64 ? launch<64, true>(tk, tv, p, s) : launch<128, true>(tk, tv, p, s);
-  return D == 64 ? launch<64, false>(tk, tv, p, s) : launch<128, false>(tk, tv, p, s);
+    return D == 64 ? launch<64, true>(tq, tk, tv, p, s) : launch<128, true>(tq, tk, tv, p, s);
+  return D == 64 ? launch<64, false>(tq, tk, tv, p, s) : launch<128, false>(tq, tk, tv, p, s);
 }
 
 }  // namespace pkv

@@ -146,3 +146,200 @@ def test_tree_attention(cached, nodes, Hq, Hkv, d, kind, dtype):
     c.check(out, lse)
     again, lse2 = c.run()       # the partition and the joins' order are fixed
     assert torch.equal(out, again) and torch.equal(lse.nan_to_num(9.0), lse2.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11, 3.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales(scale, dtype):
+    c = Case([200, 3], [40, 7], 8, 2, 64, dtype, "any", seed=5)
+    c.scale = scale
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,kind", [(1, "tree"), (8, "tree"), (8, "chain"), (2, "chain"), (4, "any")])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_what_a_node_does_not_see_may_be_anything(value, G, kind, dtype):
+    """Nodes whose key and value (and query) are not finite: those that see them get what the
+    formula gives, the others nothing of it."""
+    nodes = [40, 150, 3]
+    c = Case([130, 0, 17], nodes, 2 * G, 2, 128, dtype, kind, seed=8, extra=1)
+    if kind == "chain":
+        spoiled = {0: [38, 39], 1: [140], 2: [2]}
+    else:
+        spoiled = {0: [5, 39], 1: [60, 130, 149], 2: [1]}
+    for b, some in spoiled.items():
+        base = int(c.lens[b]) - nodes[b]
+        for i in some:
+            blk, r = c.tables[b, (base + i) // 16], (base + i) % 16
+            if i % 2:
+                c.k[blk, :, r] = value
+            c.v[blk, :, r, ::3] = value
+    c.q[int(c.starts[1]) + 7] = value
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_that_are_all_minus_infinity_give_nan(dtype):
+    c = Case([0, 20], [2, 3], 2, 2, 64, dtype, "chain", seed=2)
+    c.k.fill_(float("-inf"))
+    c.q.copy_(c.q.abs() + 1)
+    out, lse = c.run()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_do_not_fit_are_left_alone(dtype):
+    c = Case([30] * 6, [4] * 6, 4, 2, 64, dtype, "tree", seed=3, extra=2)
+    good = c.run()[0]
+    c.lens[1] = 3                                   # fewer tokens than nodes
+    c.lens[2] = 16 * c.tables.shape[1] + 1          # more than its table
+    c.lens[4] = -1
+    out = torch.full_like(good, 7.0)
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    binding.decode_attn_tree_args(c.args(out, err=err))
+    torch.cuda.synchronize()
+    assert int(err) == binding.DEVERR_BAD_LEN
+    for b in range(6):
+        a, e = int(c.starts[b]), int(c.starts[b + 1])
+        assert torch.equal(out[a:e], torch.full_like(out[a:e], 7.0) if b in (1, 2, 4) else good[a:e])
+    # starts that do not ascend, or leave the queries
+    for starts in ([0, 4, 2, 12, 16, 20, 24], [-4, 4, 8, 12, 16, 20, 24], [0, 4, 8, 12, 16, 20, 99]):
+        c.starts = np.array(starts, np.int32)
+        err.zero_()
+        binding.decode_attn_tree_args(c.args(out, err=err))
+        torch.cuda.synchronize()
+        assert int(err) & binding.DEVERR_BAD_LEN
+    # a row with more nodes than mask bits
+    c = Case([0, 30], [33, 4], 4, 2, 64, dtype, "tree", seed=3)
+    good = c.run()[0]
+    c.mask = np.ascontiguousarray(c.mask[:, :1])
+    out, err = torch.full_like(good, 7.0), torch.zeros(1, dtype=torch.int32, device=dev())
+    binding.decode_attn_tree_args(c.args(out, err=err))
+    torch.cuda.synchronize()
+    assert int(err) == binding.DEVERR_BAD_LEN
+    assert (out[:33] == 7.0).all() and torch.equal(out[33:], good[33:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+def test_blocks_outside_the_pool_are_left_out(kind, dtype):
+    c = Case([400, 90], [20, 70], 8, 2, 128, dtype, kind, seed=4)
+    whole = c.run()[0]
+    for b, j, bad in ((0, 3, -1), (0, 25, 10**6), (1, 5, -7)):
+        c.tables[b, j] = bad
+    out, err = torch.full_like(whole, 7.0), torch.zeros(1, dtype=torch.int32, device=dev())
+    lse = torch.empty(whole.shape[:2], device=dev())
+    binding.decode_attn_tree_args(c.args(out, lse=lse, err=err))
+    torch.cuda.synchronize()
+    assert int(err) == binding.DEVERR_BAD_BLOCK
+    # the same as not seeing those tokens: every row alone, its tokens as nodes of a wide mask
+    for b in range(2):
+        L, n = int(c.lens[b]), int(c.starts[b + 1] - c.starts[b])
+        a = int(c.starts[b])
+        there = np.array([0 <= c.tables[b, t // 16] < len(c.k) for t in range(L)])
+        sees = drafted.tree_visible(c.mask, a, n, L - n) & there
+        tab = np.where((c.tables[b] >= 0) & (c.tables[b] < len(c.k)), c.tables[b], 0)[None]
+        words = np.packbits(np.pad(sees, ((L - n, 0), (0, -L % 32))), axis=1, bitorder="little").view("<i4")
+        q = np.zeros((L,) + tuple(c.q.shape[1:]))
+        q[L - n:] = f64(c.q)[a:a + n]
+        kv = [np.nan_to_num(f64(x)) for x in (c.k, c.v)]
+        want = drafted.tree_attention(q, *kv, tab, [L], [0, L], c.scale, words)
+        check(f64(out)[a:a + n], f64(lse)[a:a + n], [x[L - n:] for x in want], dtype, 128)
+
+
+def test_rows_that_share_blocks_and_rows_without_nodes():
+    """Forks: three rows over the same whole blocks, each with nodes of its own; one has none."""
+    c = Case([64, 64, 64], [5, 0, 9], 8, 2, 64, "bf16", "tree", seed=6)
+    for b in (1, 2):
+        c.tables[b, :4] = c.tables[0, :4]
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_replayed_graphs_that_share_a_workspace(dtype):
+    cases = [Case([300, 20], [30, 9], 8, 2, 128, dtype, "tree", seed=1),
+             Case([10] * 9, [3] * 9, 8, 2, 128, dtype, "chain", seed=2)]
+    space = torch.full((binding.tree_workspace_bytes(8, 2, 128, binding.dtype_code(cases[0].q)),), 255,
+                       dtype=torch.uint8, device=dev())
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for c in cases:
+        out = torch.zeros_like(c.q)
+        args = c.args(out, workspace=space)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            binding.decode_attn_tree_args(args)
+        graphs.append((g, args))
+        outs.append(out)
+    for _ in range(3):
+        for (g, _), out in zip(graphs, outs):
+            out.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for c, out in zip(cases, outs):
+        assert torch.equal(out, c.run()[0])
+
+
+def test_side_stream_and_plain_call():
+    c = Case([100, 7], [12, 5], 8, 2, 64, "bf16", "tree", seed=9)
+    want = c.run()[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = binding.decode_attention_tree(c.q, c.k, c.v, i32(c.tables), i32(c.lens), i32(c.starts), c.scale,
+                                        mask=i32(c.mask), stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_metadata_in_mapped_host_memory():
+    c = Case([100, 7], [12, 5], 8, 2, 64, "bf16", "tree", seed=9)
+    want = c.run()[0]
+    host = [torch.from_numpy(np.ascontiguousarray(x, np.int32)).pin_memory()
+            for x in (c.tables, c.lens, c.starts)]
+    out = binding.decode_attention_tree(c.q, c.k, c.v, *host, c.scale, mask=i32(c.mask))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_waits_that_give_up_leave_nan_and_the_next_call_is_whole():
+    c = Case([4000, 50], [40, 9], 8, 2, 128, "bf16", "tree", seed=9)
+    want = c.run()[0]
+    space = torch.zeros(binding.tree_workspace_bytes(8, 2, 128, binding.BF16), dtype=torch.uint8,
+                        device=dev())
+    out, err = torch.full_like(want, 7.0), torch.zeros(1, dtype=torch.int32, device=dev())
+    binding.decode_attn_tree_args(c.args(out, workspace=space, err=err, flags=binding.ATTN_SHORT_WAITS))
+    torch.cuda.synchronize()
+    assert int(err) == binding.DEVERR_TIMEOUT
+    assert torch.isnan(out).any() and (torch.isnan(out) | (out == want)).all()
+    err.zero_()
+    binding.decode_attn_tree_args(c.args(out, workspace=space, err=err))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_caches_beyond_32_bit_offsets(dtype):
+    """Blocks whose first byte lies beyond 2^32 elements."""
+    Hkv, d = 8, 128
+    nb = 2**32 // (Hkv * 16 * d) + 40
+    small = Case([200, 33], [20, 5], 16, Hkv, d, dtype, "tree", seed=11)
+    want = small.run()[0]
+    far = nb - 1 - np.arange(len(small.k))
+    k, v = (torch.empty((nb, Hkv, 16, d), dtype=TD[dtype], device=dev()) for _ in range(2))
+    idx = torch.from_numpy(far).to(dev())
+    k[idx], v[idx] = small.k, small.v
+    small.k, small.v = k, v
+    small.tables = np.where(small.tables >= 0, far[np.maximum(small.tables, 0)], -1).astype(np.int32)
+    assert torch.equal(small.run()[0], want)
+
+
+def test_a_batch_of_many_rows():
+    """More rows than threads that look for a CTA's share, lengths and nodes of every kind."""
+    rng = np.random.default_rng(5)
+    B = 1000
+    nodes = rng.integers(0, 5, B)
+    cached = np.where(rng.random(B) < 0.1, 0, rng.integers(0, 40, B))
+    for dtype in ("bf16", "f32"):
+        c = Case(cached, nodes, 2, 1, 64, dtype, "tree", seed=12)
+        c.check(*c.run())
