@@ -7,20 +7,20 @@
 // the group.
 //
 // Roles (one CTA per SM, its share of the positions of tree.h):
-//  * warps 0-3 and 4-7: a softmax warpgroup per slot, an accumulator pair (S, O) in tensor
-//    memory; thread r owns query row r, weights go back as bf16 over their scores.
-//  * warps 8 and 11: TMA producers of K and of V, 16-token pages into 128-byte-swizzled slabs,
-//    K-major for the first product, the same bytes MN-major for the second.  (With one warp
-//    for both, a K tile waited for the V tile ahead of it, which waits for a product: a
-//    load's latency a tile, 3.7 TB/s.)
-//  * warps 9 and 10: issue the products of one slot each.
-// Above 128 query rows the slots are two row tiles that share every K and V tile; up to 128
-// they take turns in the tokens and are merged at the end.  The largest score is followed
-// only when it grows by more than 2^8 (kLazy): weights up to 2^8 are exact enough in bf16.
-//
-// Nothing holds the producers and issuers back between items: the queries come by TMA once
-// the last scores of the item before are done, and the next item's first scores are
-// computed while the softmax warps still write out.
+//  * warp 8 finds the CTA's items, hands them out through a short queue in shared memory
+//    and loads Q and K by TMA; warp 11 loads V.  16-token pages go into 128-byte-swizzled
+//    slabs, K-major for the first product, the same bytes MN-major for the second.  (With
+//    one warp for both, a K tile waited for the V tile ahead of it, which waits for a
+//    product: a load's latency a tile, 3.7 TB/s.)
+//  * warps 0-3 and 4-7: a softmax warpgroup per slot.  A slot is a Q tile and an
+//    accumulator pair (S, O) in tensor memory; thread r owns query row r, weights go back
+//    as bf16 over their scores.
+//  * warps 9 and 10 issue the products of one slot each.
+// An item of more than 128 rows takes both slots, which share its K and V tiles and take
+// turns in the products.  Smaller ones take one slot each, alternately: while one slot
+// finishes an item and writes it out, the other is at work on the next, so the loads never
+// pause between items.  The largest score is followed only when it grows by more than 2^8
+// (kLazy): weights up to 2^8 are exact enough in bf16.
 //
 // Masks.  Only steps that reach past the tokens every row sees (the cached ones, and in a
 // chain the nodes ahead of the item's) look at mask bits, 32 at a time.  What a node does not
@@ -28,6 +28,11 @@
 // tokens while the softmax is at work, and where one is not finite the element is zeroed in
 // shared memory for the product and added at the end to the rows that see it (any positive
 // weight leaves NaN and infinity what they are).
+//
+// The code is kept short: rare paths are functions of their own, the rows' output is written
+// in a loop.  A first form of 150 KB (two slots merged at the end of every item, everything
+// unrolled) spent 8 us an item on instructions that were not in the cache and on stores of
+// one row a lane.
 #include "tensor_core.cuh"
 #include "tree.h"
 
@@ -45,6 +50,8 @@ constexpr int kHalf = 2;                      // 32-token pieces of P after whic
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr long long kPollLimit = 4096;
 constexpr int kBoundary = 2, kMin = 1;
+constexpr int kQueue = 4;                     // items handed out ahead
+constexpr int kBadRing = 16, kOddRing = 4;
 
 template <int D>
 struct Lay {
@@ -52,33 +59,146 @@ struct Lay {
   static constexpr int kSlab = kTile * 128;               // bytes of a slab of a tile
   static constexpr int kMat = kSlabs * kSlab;             // bytes of a tile of Q, K or V
   static constexpr int NS = D == 128 ? 2 : 4;             // K and V stages
-  static constexpr int kQ = 0;                            // [2] tiles
+  static constexpr int kQ = 0;                            // [2] tiles, one per slot
   static constexpr int kK = 2 * kMat;                     // [NS]
   static constexpr int kV = kK + NS * kMat;               // [NS]
-  static constexpr int kScratch = kV + NS * kMat;         // half of the second slot's O
-  static constexpr int kBars = kScratch + kTile * D / 2 * 4;
-  static constexpr int kNumBars = 4 * NS + 14;
-  static constexpr int kSums = kBars + kNumBars * 8;      // m, l of the second slot
-  static constexpr int kBad = kSums + 2 * kTile * 4;      // [kBadRing] pages outside the pool
-  static constexpr int kBadRing = 16;
+  static constexpr int kOut = kV + NS * kMat;             // [8 warps] 32 rows of 128 bytes
+  static constexpr int kItems = kOut + 8 * 32 * 128;      // [kQueue] 64 bytes
+  static constexpr int kBars = kItems + kQueue * 64;
+  static constexpr int kNumBars = 4 * NS + 2 * kQueue + 16;
+  static constexpr int kBad = kBars + kNumBars * 8;       // [kBadRing] pages outside the pool
   static constexpr int kMisc = kBad + kBadRing;
-  static constexpr int kBytes = kMisc + 32 + 1024;        // + alignment slack
+  static constexpr int kBytes = kMisc + 4 * (kOddRing + 4) + 1024;   // + alignment slack
 };
 
 using Walk = TreeWalk<kTile, kBoundary>;
 
-// First token from which on rows of an item may differ in what they see.
-__device__ __forceinline__ int first_special(const TreeParams &p, const TreeItem &it) {
-  return it.base + (p.mask ? 0 : it.n0);
-}
-__device__ __forceinline__ bool odd_bf16(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+// An item as it is handed out: 64 bytes.
+struct Handed {
+  int q0, nodes, g, b;
+  int base, n, tokens, n0;
+  int t0, t1, slots, part;       // slots: 1, 2 or both; part: partial slot or -1 (whole)
+  int special, pad[3];           // first token that rows may differ in
+};
+
 // Bits 15 and 31: a half's exponent is all ones (its sum with the lowest exponent bit
 // carries into the sign's place).
 __device__ __forceinline__ uint32_t odd_word(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 __device__ __forceinline__ uint32_t clean_word(uint32_t w) {
-  return (odd_bf16(w) ? 0u : w & 0xffffu) | (odd_bf16(w >> 16) ? 0u : w & 0xffff0000u);
+  const uint32_t odd = odd_word(w);
+  return w & ~((odd & 0x8000u ? 0xffffu : 0u) | (odd >> 31 ? 0xffff0000u : 0u));
+}
+
+__device__ __forceinline__ bool in_pool(const TreeParams &p, int blk) {
+  return blk >= 0 && blk < p.num_blocks;
+}
+
+// A wait of the whole warp: what is not there at once is waited for in a function (of 30
+// waits, each with its own loop, the kernel would be a third longer).
+template <bool POLL>
+__device__ __noinline__ bool wait_longer(const Waiter<POLL> w, uint64_t *bar, uint32_t parity) {
+  return w(bar, parity);
+}
+template <bool POLL>
+struct WarpWaiter {
+  Waiter<POLL> w;
+  __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
+    if (__all_sync(0xffffffffu, w.done(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_longer<POLL>(w, bar, parity));
+  }
+};
+
+// Until the copies of more than `tile` tiles were started.  A barrier says only whether its
+// phase is even or odd, and a slot that comes back to the stages after the other slot's items
+// does not know how many phases went by: once its tile's copies are under way, the phase is
+// the tile's until this slot hands the stage back.
+template <bool POLL>
+__device__ __noinline__ bool wait_started(const Waiter<POLL> w, volatile int *started, int tile) {
+  const long long t0 = clock64();
+  while (*started <= tile) {
+    if (*w.abort) return false;
+    if (clock64() - t0 > w.limit) {
+      *w.abort = 1;
+      set_dev_err(w.err, PKV_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Values of rows [first, last) of a V tile that are not finite become zero (one warp);
+// whether there were any.
+template <int D>
+__device__ __noinline__ void clean_values(unsigned char *vt, int first, int last, int lane) {
+  for (int s = 0; s < Lay<D>::kSlabs; ++s)
+    for (int c = first * 8 + lane; c < last * 8; c += 32) {
+      uint4 *at = reinterpret_cast<uint4 *>(vt + s * Lay<D>::kSlab + c * 16);
+      const uint4 v = *at;
+      *at = make_uint4(clean_word(v.x), clean_word(v.y), clean_word(v.z), clean_word(v.w));
+    }
+}
+// Rows of a V tile that do not count become zero (one warp): pages of `bad`, and those behind
+// the last token within its page.
+template <int D>
+__device__ __noinline__ void zero_values(unsigned char *vt, int valid, uint32_t bad, int lane) {
+  for (int pg = 0; pg * kBlockTokens < valid; ++pg) {
+    const int end = (pg + 1) * kBlockTokens;
+    const int from = bad >> pg & 1 ? end - kBlockTokens : min(end, valid);
+    for (int s = 0; s < Lay<D>::kSlabs; ++s)
+      for (int c = from * 8 + lane; c < end * 8; c += 32)
+        *reinterpret_cast<uint4 *>(vt + s * Lay<D>::kSlab + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// What clean_values left out, added to the outputs of one query row (`out`: bf16 or, of a
+// part, float32): any positive weight leaves infinity and NaN what they are.
+template <int D>
+__device__ __noinline__ void add_odd_values(const TreeParams &p, const Handed it, int node, void *out,
+                                            bool part) {
+  const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
+  const uint32_t *words =
+      p.mask ? p.mask + static_cast<size_t>(it.q0 + node) * p.mask_words : nullptr;
+  for (int tok = max(it.special, it.t0 * kTile); tok < min(it.tokens, it.t1 * kTile); ++tok) {
+    const int blk = table[tok / kBlockTokens];
+    if (!in_pool(p, blk) ||
+        !(tree_sees(words, p.mask_words, it.n0 + node, it.base, it.tokens, tok) & 1u))
+      continue;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                             ((static_cast<size_t>(blk) * p.Hkv + it.g) * kBlockTokens +
+                              tok % kBlockTokens) * D;
+    for (int c = 0; c < D; ++c) {
+      const float x = __bfloat162float(v[c]);
+      if (isfinite(x)) continue;
+      if (part) {
+        static_cast<float *>(out)[c] += x;
+      } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out) + c;
+        *o = __float2bfloat16_rn(__bfloat162float(*o) + x);
+      }
+    }
+  }
+}
+
+// After a wait that gave up: no output of this CTA's counts.
+template <int D>
+__device__ __noinline__ void all_nan(const TreeParams &p) {
+  const int cta = blockIdx.x;
+  Walk walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);
+  TreeItem it;
+  const float nan = __int_as_float(0x7fffffff);
+  while (walk.next(&it))
+    for (int e = threadIdx.x; e < it.nodes * p.G; e += kThreads) {
+      if (!it.whole()) {   // (the join makes NaN of it)
+        p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;
+        continue;
+      }
+      const size_t at = static_cast<size_t>(it.q0 + e / p.G) * p.Hq + it.g * p.G + e % p.G;
+      if (p.lse_out) p.lse_out[at] = nan;
+      for (int c = 0; c < D; ++c)
+        static_cast<__nv_bfloat16 *>(p.out)[at * D + c] = __float2bfloat16_rn(nan);
+    }
 }
 
 template <int D, bool POLL>
@@ -92,15 +212,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
   uint64_t *k_full = bars, *k_empty = bars + NS, *v_full = bars + 2 * NS, *v_empty = bars + 3 * NS;
-  uint64_t *s_full = bars + 4 * NS, *p_ready = s_full + 2, *o_full = s_full + 4;   // [2] each
-  uint64_t *q_full = s_full + 6, *both = s_full + 7, *drain = s_full + 8;
-  uint64_t *turn = s_full + 9, *p_half = s_full + 11;   // [2] each
-  uint64_t *q_empty = s_full + 13;
+  uint64_t *i_full = bars + 4 * NS, *i_empty = i_full + kQueue;
+  uint64_t *s_full = i_empty + kQueue, *p_ready = s_full + 2, *o_full = s_full + 4;   // [2] each
+  uint64_t *q_full = s_full + 6, *q_empty = s_full + 8, *turn = s_full + 10, *p_half = s_full + 12;
+  uint64_t *drain = s_full + 14;
   volatile uint8_t *bad_s = reinterpret_cast<volatile uint8_t *>(smem + L::kBad);
-  float *sums_s = reinterpret_cast<float *>(smem + L::kSums);
   volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);
-  // misc: a wait gave up, tmem, the last item of odd and of even number with values that are
-  // not finite [2] (its number + 1)
+  // misc: a wait gave up, tmem, items with values that are not finite [kOddRing] (number + 1),
+  // tiles whose copies of K and of V were started
+  constexpr int kStartedK = 2 + kOddRing, kStartedV = kStartedK + 1;
 
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (tid == 0) {
@@ -110,20 +230,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 2);
     }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], 3 + kSoftmax / 32);   // V, issuers, softmax warps
+    }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
       mbar_init(&p_ready[m], kTile / 32);   // one arrival per warp
       mbar_init(&p_half[m], kTile / 32);
       mbar_init(&o_full[m], 1);
+      mbar_init(&q_full[m], 1);
+      mbar_init(&q_empty[m], 1);
+      mbar_init(&turn[m], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);   // one arrival per slot
-    mbar_init(both, kSoftmax / 32);
     mbar_init(drain, 2);
-    mbar_init(&turn[0], 1);
-    mbar_init(&turn[1], 1);
     misc[0] = 0;
-    misc[2] = misc[3] = 0;
+    for (int i = 0; i < kOddRing + 2; ++i) misc[2 + i] = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -143,30 +265,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int cta = blockIdx.x;
   Walk walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
-  TreeItem it;
   tc_fence_after();
   const uint32_t tmem = uniform(static_cast<uint32_t>(misc[1]));
   // (by arithmetic: arrays indexed by the slot would live in local memory)
   auto tS = [tmem](int m) { return tmem + 128u * m; };
   auto tO = [tmem](int m) { return tmem + 256u + 128u * m; };
-  const Waiter<POLL> wait{misc, p.err, p.wait_limit};
+  const Waiter<POLL> wait_here{misc, p.err, p.wait_limit};
+  const WarpWaiter<POLL> wait_there{wait_here};
+  Handed *items = reinterpret_cast<Handed *>(smem + L::kItems);
+  // The i-th item of the queue (for the whole warp; t1 == 0: there are no more).
+  auto take = [&](const auto &wait, int i, Handed *it) {
+    if (!wait.warp(&i_full[i % kQueue], static_cast<uint32_t>(i / kQueue) & 1u)) return false;
+    *it = items[i % kQueue];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[i % kQueue]);
+    return it->t1 > 0;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    const auto &wait = wait_there;
     if (warp == 8 || warp == 11) {
-      // ======================= producers: K (warp 8), V (warp 11) =======================
+      // ======================= loads: items, Q and K (warp 8), V (warp 11) =======================
       const bool is_v = warp == 11;
       uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
       const void *tmap = is_v ? &tmap_v : &tmap_k;
       const uint32_t base = smem_u32(smem + (is_v ? L::kV : L::kK)) + lane * (kBlockTokens * 128);
-      int x = 0;       // tiles of the items before
-      int armed = 0;   // tiles whose copies were started
-      int n_items = 0, armed_q = 0;
-      bool ok = true;
+      int x = 0;                      // tiles so far
+      int used[2] = {0, 0};           // items of each slot so far
+      int single = 0;                 // the slot of the next item that takes one
       TreeCut cut = {};
-      while (ok && walk.next(&it)) {
-        if (it.t0 == 0 && it.t1 < it.steps)
-          cut = TreeCut{walk.more(), it.q0, it.nodes * p.G, it.g, it.base, it.n};
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        Handed it;
+        if (is_v) {
+          if (!take(wait, i, &it)) break;
+        } else {
+          TreeItem w;
+          const bool some = walk.next(&w);
+          if (some) {
+            if (w.t0 == 0 && w.t1 < w.steps)
+              cut = TreeCut{walk.more(), w.q0, w.nodes * p.G, w.g, w.base, w.n};
+            const bool two = w.nodes * p.G > kTile;
+            it = Handed{w.q0, w.nodes, w.g, w.b, w.base, w.n, w.tokens, w.n0, w.t0, w.t1,
+                        two ? 3 : 1 << single, w.whole() ? -1 : w.slot(cta),
+                        w.base + (p.mask ? 0 : w.n0), {}};
+            if (!two) single ^= 1;
+          } else {
+            it = Handed{};
+          }
+          ok = wait.warp(&i_empty[i % kQueue], (static_cast<uint32_t>(i / kQueue) & 1u) ^ 1u);
+          if (!ok) break;
+          if (lane == 0) {
+            items[i % kQueue] = it;
+            mbar_arrive(&i_full[i % kQueue]);
+          }
+          __syncwarp();
+          if (!some) break;
+        }
         const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
         const int tiles = it.t1 - it.t0;
         auto page_id = [&](int t) {   // block of page `lane` of tile t (-1: no such page)
@@ -174,26 +330,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           return lane < kPages && tok < it.tokens ? table[tok >> 4] : -1;
         };
         int next = page_id(0);
-        for (int t = 0; t < tiles; ++t) {
+        for (int t = 0; t < tiles; ++t, ++x) {
           const int blk = next;
           next = t + 1 < tiles ? page_id(t + 1) : -1;
-          const int st = (x + t) % NS;
-          const bool good = blk >= 0 && blk < p.num_blocks;
+          const int st = x % NS;
+          const bool good = in_pool(p, blk);
           const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, good))) *
                                  (kBlockTokens * D * 2);
           const int y = (blk * p.Hkv + it.g) * kBlockTokens;
-          ok = wait.warp(&empty[st], (static_cast<uint32_t>((x + t) / NS) & 1u) ^ 1u);
+          ok = wait.warp(&empty[st], (static_cast<uint32_t>(x / NS) & 1u) ^ 1u);
           if (!ok) break;
           if (!is_v) {
             const uint32_t bad =
                 __ballot_sync(0xffffffffu, !good && lane < kPages &&
                                                (it.t0 + t) * kTile + lane * kBlockTokens < it.tokens);
             if (lane == 0) {
-              bad_s[(x + t) % L::kBadRing] = static_cast<uint8_t>(bad);
+              bad_s[x % kBadRing] = static_cast<uint8_t>(bad);
               if (bad) set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
             }
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[st], bytes);
+            __threadfence_block();
+            misc[is_v ? kStartedV : kStartedK] = x + 1;
+          }
           __syncwarp();
           if (good) {
 #pragma unroll
@@ -201,30 +361,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(base + st * L::kMat + s * L::kSlab, tmap, s * 64, y, &full[st]);
           }
           __syncwarp();
-          armed = x + t + 1;
-          if (is_v && t == 0) {   // the queries, once the products of the item before are done with them
-            ok = wait.warp(q_empty, (static_cast<uint32_t>(n_items) & 1u) ^ 1u);
+          if (is_v || t > 0) continue;
+          // the queries of the item's slots, once the slots' last item is done with them
+          for (int m = 0; m < 2; ++m) {
+            if (!(it.slots >> m & 1)) continue;
+            ok = ok && wait.warp(&q_empty[m], (static_cast<uint32_t>(used[m]) & 1u) ^ 1u);
             if (!ok) break;
-            const int q_tiles = it.nodes * p.G > kTile ? 2 : 1;
-            if (elect_one()) {
-              mbar_arrive_expect_tx(q_full, q_tiles * L::kMat);
-              for (int e = 0; e < q_tiles; ++e)
+            ++used[m];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[m], L::kMat);
 #pragma unroll
-                for (int s = 0; s < L::kSlabs; ++s)
-                  tma_load_3d(smem_u32(smem + L::kQ) + e * L::kMat + s * L::kSlab, &tmap_q, s * 64,
-                              it.g * p.G, it.q0 + e * (kTile / p.G), q_full);
+              for (int s = 0; s < L::kSlabs; ++s)
+                tma_load_3d(smem_u32(smem + L::kQ) + m * L::kMat + s * L::kSlab, &tmap_q, s * 64,
+                            it.g * p.G, it.q0 + (it.slots == 3 ? m * (kTile / p.G) : 0), &q_full[m]);
             }
             __syncwarp();
-            armed_q = ++n_items;
+          }
+          if (!ok) {
+            ++x;
+            break;
           }
         }
-        x += tiles;
       }
       if (lane == 0 && !is_v) p.cuts[cta] = cut;
       // every copy has landed before the CTA ends (after a normal run they have)
-      for (int n = max(0, armed - NS); n < armed; ++n)
+      for (int n = max(0, x - NS); n < x; ++n)
         mbar_wait_bounded(&full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
-      if (armed_q) mbar_wait_bounded(q_full, static_cast<uint32_t>(armed_q - 1) & 1u, kDrainCycles);
+      for (int m = 0; m < 2; ++m)
+        if (used[m]) mbar_wait_bounded(&q_full[m], static_cast<uint32_t>(used[m] - 1) & 1u, kDrainCycles);
     } else {
       // ======================= products of slot m =======================
       const int m = warp - 9;
@@ -232,148 +396,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a negative scale is taken into Q (bit 13: A negated), so that the largest score
       // stays the largest
       const uint32_t idesc_s = inst_desc(kTile, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
-      const uint32_t q_addr = smem_u32(smem + L::kQ), k_addr = smem_u32(smem + L::kK),
+      const uint32_t q_addr = smem_u32(smem + L::kQ) + m * L::kMat, k_addr = smem_u32(smem + L::kK),
                      v_addr = smem_u32(smem + L::kV);
-      int x = 0, n_items = 0;
+      int x = 0, used = 0;
       uint32_t p_ph = 0, turn_ph = 0;
       bool ok = true;
-      while (ok && walk.next(&it)) {
+      for (int i = 0;; ++i) {
+        Handed it;
+        if (!take(wait, i, &it)) break;
         const int first = uniform(it.t0), tiles = uniform(it.t1) - first, tokens = uniform(it.tokens);
-        const bool two = uniform(it.nodes) * p.G > kTile;   // the slots are two row tiles
-        const int n = two ? tiles : (tiles + 1 - m) / 2;
-        ok = wait.warp(q_full, static_cast<uint32_t>(n_items) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        const int special = first_special(p, it);
-        ++n_items;
-        const int turns = two ? tiles : (tiles + 1) / 2;   // slot 0's tiles, at least this slot's
-        auto tile_of = [&](int j) { return two ? j : 2 * j + m; };
-        // the slots' products alternate in whole batches: interleaved one by one, both
-        // slots would finish late and then share the exponential unit as well
+        const int slots = uniform(it.slots), special = uniform(it.special);
+        if (!(slots >> m & 1)) {   // the other slot's
+          x += tiles;
+          continue;
+        }
+        const bool two = slots == 3;
+        // With two slots at work on the same tiles their products alternate in whole batches:
+        // interleaved one by one, both would finish late and then share the exponential
+        // unit as well.
         auto my_turn = [&]() {
+          if (!two) return true;
           const bool r = wait.warp(&turn[m], turn_ph ^ (m == 0 ? 1u : 0u));
           turn_ph ^= 1u;
           return r;
         };
-        auto next_turn = [&]() { mbar_arrive(&turn[m ^ 1]); };   // (one lane)
-        auto wait_k = [&](int t) {
-          return wait.warp(&k_full[(x + t) % NS], static_cast<uint32_t>((x + t) / NS) & 1u);
+        // (one lane; a tile that one slot alone uses is handed back by it for both)
+        auto next_turn = [&]() {
+          if (two) mbar_arrive(&turn[m ^ 1]);
         };
-        // a tile that one slot alone uses is handed back by it for both
+        auto wait_tile = [&](uint64_t *full, int started, int t) {
+          const bool r = t >= NS || __all_sync(0xffffffffu, misc[started] > x + t) ||
+                         __all_sync(0xffffffffu, wait_started<POLL>(wait_here, misc + started, x + t));
+          return r && wait.warp(&full[(x + t) % NS], static_cast<uint32_t>((x + t) / NS) & 1u);
+        };
         auto release = [&](uint64_t *empty) {
           mma_commit(empty);
           if (!two) mma_commit(empty);
         };
-        // S = Q K^T for the slot's tile j (issued by one lane)
-        auto issue_scores = [&](int j) {
-          const int t = tile_of(j);
-          const int st = (x + t) % NS;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks / 4) * L::kSlab + (ks % 4) * 32;
-            mma_ss(tS(m), smem_desc(q_addr + (two ? m * L::kMat : 0) + off, 16, 1024),
-                   smem_desc(k_addr + st * L::kMat + off, 16, 1024), idesc_s, ks > 0);
-          }
-          mma_commit(&s_full[m]);
-          release(&k_empty[st]);
-          if (j + 1 == n) mma_commit(q_empty);
-        };
-        ok = (n == 0 || wait_k(tile_of(0))) && my_turn();
-        if (ok && elect_one()) {
-          if (n > 0)
-            issue_scores(0);
-          else
-            mbar_arrive(q_empty);
-          next_turn();
-        }
-        __syncwarp();
-        for (int j = 0; j < turns && ok; ++j) {
-          if (j >= n) {   // slot 1 has a tile less: its turn goes by
-            ok = my_turn();
-            if (ok && elect_one()) next_turn();
-            __syncwarp();
-            continue;
-          }
-          const int t = tile_of(j), st = (x + t) % NS;
-          const int tok0 = (first + t) * kTile, valid = min(kTile, tokens - tok0);
-          const bool more = j + 1 < n;
-          // the values first (they are there well before the weights)
-          ok = wait.warp(&v_full[st], static_cast<uint32_t>((x + t) / NS) & 1u);
-          if (!ok) break;
-          unsigned char *vt = smem + L::kV + st * L::kMat;
-          // 16-byte pieces of the tile's tokens from `first` to `last`: piece e, or where it lies
-          auto piece = [&](int e, int first, int last) {
-            const int s = e / ((last - first) * 8), c = e - s * ((last - first) * 8);
-            return reinterpret_cast<uint4 *>(vt + s * L::kSlab + first * 128 + c * 16);
-          };
-          bool changed = false;
-          const uint32_t bad = bad_s[(x + t) % L::kBadRing];
-          if (valid % kBlockTokens || bad) {
-            // values of tokens that do not count may be anything: their weights are
-            // zero, and so must they be (both slots of a shared tile write the zeros)
-            for (int pg = 0; pg * kBlockTokens < valid; ++pg) {
-              const int end = (pg + 1) * kBlockTokens;
-              const int from = bad >> pg & 1 ? end - kBlockTokens : min(end, valid);
-              for (int e = lane; e < (end - from) * 8 * L::kSlabs; e += 32)
-                *piece(e, from, end) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            changed = true;
-          }
-          const int look = max(0, special - tok0);
-          if (look < valid) {
-            uint32_t odd = 0;
-            for (int e = lane; e < (valid - look) * 8 * L::kSlabs; e += 32) {
-              const uint4 v = *piece(e, look, valid);
-              odd |= odd_word(v.x) | odd_word(v.y) | odd_word(v.z) | odd_word(v.w);
-            }
-            if (__any_sync(0xffffffffu, odd != 0)) {
-              // (the note first: the other slot may find the tile clean already)
-              if (lane == 0) misc[2 + (n_items & 1)] = n_items;
-              __threadfence_block();
-              __syncwarp();
-              for (int e = lane; e < (valid - look) * 8 * L::kSlabs; e += 32) {
-                uint4 *at = piece(e, look, valid);
-                const uint4 v = *at;
-                *at = make_uint4(clean_word(v.x), clean_word(v.y), clean_word(v.z), clean_word(v.w));
-              }
+        ok = wait.warp(&q_full[m], static_cast<uint32_t>(used) & 1u);
+        if (!ok) break;
+        ++used;
+        for (int t = -1; t < tiles; ++t) {   // P V of tile t, then the scores of tile t + 1
+          if (t >= 0) {
+            const int st = (x + t) % NS, tok0 = (first + t) * kTile, valid = min(kTile, tokens - tok0);
+            ok = wait_tile(v_full, kStartedV, t);
+            if (!ok) break;
+            // values of tokens that do not count may be anything: their weights are zero,
+            // and so must they be (both slots of a shared tile write the zeros)
+            unsigned char *vt = smem + L::kV + st * L::kMat;
+            bool changed = false;
+            const uint32_t bad = uniform(static_cast<uint32_t>(bad_s[(x + t) % kBadRing]));
+            if (valid % kBlockTokens || bad) {
+              zero_values<D>(vt, valid, bad, lane);
               changed = true;
             }
-          }
-          if (changed) {
-            fence_proxy_async_smem();
+            const int look = max(0, special - tok0);
+            if (look < valid) {
+              uint32_t odd = 0;
+#pragma unroll 1
+              for (int s = 0; s < L::kSlabs; ++s)
+#pragma unroll 4
+                for (int c = look * 8 + lane; c < valid * 8; c += 32) {
+                  const uint4 v = *reinterpret_cast<const uint4 *>(vt + s * L::kSlab + c * 16);
+                  odd |= odd_word(v.x) | odd_word(v.y) | odd_word(v.z) | odd_word(v.w);
+                }
+              if (__any_sync(0xffffffffu, odd != 0)) {
+                // (the note first: the other slot may find the tile clean already)
+                if (lane == 0) misc[2 + i % kOddRing] = i + 1;
+                __threadfence_block();
+                __syncwarp();
+                clean_values<D>(vt, look, valid, lane);
+                changed = true;
+              }
+            }
+            if (changed) {
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            auto weighted = [&](int from, int to) {   // O += P V, a page at a time
+#pragma unroll
+              for (int ks = from; ks < to; ++ks)
+                if (ks * kBlockTokens < valid)
+                  mma_ts(tO(m), tS(m) + ks * 8,
+                         smem_desc(v_addr + st * L::kMat + ks * (kBlockTokens * 128), L::kSlab, 1024),
+                         kIdescO, t > 0 || ks > 0);
+            };
+            ok = wait.warp(&p_half[m], p_ph) && my_turn();
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) weighted(0, 2 * kHalf);
+            __syncwarp();
+            ok = wait.warp(&p_ready[m], p_ph);
+            if (!ok) break;
+            p_ph ^= 1u;
+            tc_fence_after();
+            if (elect_one()) {
+              weighted(2 * kHalf, kPages);
+              release(&v_empty[st]);
+              if (t + 1 == tiles) mma_commit(&o_full[m]);
+            }
             __syncwarp();
           }
-          auto weighted = [&](int from, int to) {   // O += P V, a page at a time
+          const int st = (x + t + 1) % NS;
+          ok = t + 1 == tiles || wait_tile(k_full, kStartedK, t + 1);
+          ok = ok && (t >= 0 || my_turn());
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (t + 1 < tiles) {   // S = Q K^T
 #pragma unroll
-            for (int ks = from; ks < to; ++ks)
-              if (ks * kBlockTokens < valid)
-                mma_ts(tO(m), tS(m) + ks * 8,
-                       smem_desc(v_addr + st * L::kMat + ks * (kBlockTokens * 128), L::kSlab, 1024),
-                       kIdescO, j > 0 || ks > 0);
-          };
-          ok = wait.warp(&p_half[m], p_ph) && my_turn();
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) weighted(0, 2 * kHalf);
-          __syncwarp();
-          ok = wait.warp(&p_ready[m], p_ph);
-          if (!ok) break;
-          p_ph ^= 1u;
-          tc_fence_after();
-          if (elect_one()) {
-            weighted(2 * kHalf, kPages);
-            release(&v_empty[st]);
-            if (!more) mma_commit(&o_full[m]);
-          }
-          __syncwarp();
-          ok = !more || wait_k(tile_of(j + 1));
-          if (!ok) break;
-          if (elect_one()) {
-            if (more) issue_scores(j + 1);
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks / 4) * L::kSlab + (ks % 4) * 32;
+                mma_ss(tS(m), smem_desc(q_addr + off, 16, 1024),
+                       smem_desc(k_addr + st * L::kMat + off, 16, 1024), idesc_s, ks > 0);
+              }
+              mma_commit(&s_full[m]);
+              release(&k_empty[st]);
+              if (t + 2 == tiles) mma_commit(&q_empty[m]);
+            }
             next_turn();
           }
           __syncwarp();
         }
+        if (!ok) break;
         x += tiles;
       }
       // every product is done before tensor memory is given back (the lane that issued
@@ -384,57 +529,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const auto &wait = wait_here;
     // ======================= softmax =======================
-    const int m = warp >> 2, r = tid & (kTile - 1);
+    const int m = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes
     const uint32_t sS = tS(m) + lanes, sO = tO(m) + lanes;
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);
     const int lg = __ffs(p.G) - 1;
-    int x = 0, n_items = 0;
-    uint32_t s_ph = 0, o_ph = 0, b_ph = 0;
-    bool ok = true;
+    unsigned char *stage = smem + L::kOut + warp * (32 * 128);
+    int x = 0;
+    uint32_t s_ph = 0, o_ph = 0;
     auto arrive = [&](uint64_t *bar) {   // for the warp, after all of its lanes
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto meet = [&]() {   // both warpgroups
-      arrive(both);
-      ok = ok && wait.warp(both, b_ph);
-      b_ph ^= 1u;
-    };
-    while (ok && walk.next(&it)) {
-      const int total = it.nodes * p.G;
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      Handed it;
+      if (!take(wait, i, &it)) break;
       const int tiles = it.t1 - it.t0;
-      const bool two = total > kTile;
-      const int n = two ? tiles : (tiles + 1 - m) / 2;
-      const int32_t *table = p.tables + static_cast<size_t>(it.b) * p.bt_stride;
-      const int special = first_special(p, it);
-      const int end = min(it.tokens, it.t1 * kTile);   // of this CTA's tokens
-      ++n_items;
-      const int from = max(special, it.t0 * kTile);    // of them, first that rows may differ in
-      const int mine = (two ? m * kTile : 0) + r;   // this thread's row of the item
-      const bool active = (two ? m * kTile : 0) + (warp & 3) * 32 < total;
-      const int node = min(mine >> lg, it.nodes - 1);
+      if (!(it.slots >> m & 1)) {   // the other slot's
+        x += tiles;
+        continue;
+      }
+      const int total = it.nodes << lg;
+      const int row0 = (it.slots == 3 ? m * kTile : 0) + (warp & 3) * 32;   // this warp's first row
+      const bool active = row0 < total;
+      const int node = min((row0 + lane) >> lg, it.nodes - 1);
       const uint32_t *words =
           p.mask ? p.mask + static_cast<size_t>(it.q0 + node) * p.mask_words : nullptr;
-      auto sees = [&](int tok) {
-        return tree_sees(words, p.mask_words, it.n0 + node, it.base, it.tokens, tok);
-      };
       float mx = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
-        const int t = two ? j : 2 * j + m;
+      for (int t = 0; t < tiles; ++t, ++x) {
         const int tok0 = (it.t0 + t) * kTile;
-        bool masked = tok0 + kTile > special;
+        bool masked = tok0 + kTile > it.special;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (masked && active) {   // (ahead of the scores)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) vis[q] = sees(tok0 + 32 * q);
+          for (int q = 0; q < 4; ++q)
+            vis[q] = tree_sees(words, p.mask_words, it.n0 + node, it.base, it.tokens, tok0 + 32 * q);
         }
         ok = wait.warp(&s_full[m], s_ph);
         if (!ok) break;
         s_ph ^= 1u;
         tc_fence_after();
-        const uint32_t bad = bad_s[(x + t) % L::kBadRing];
+        const uint32_t bad = bad_s[x % kBadRing];
         if (bad) {
           masked = true;
 #pragma unroll
@@ -462,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float al = top == -INFINITY ? 1.f : ex2(mx - top);   // 0 before the first score
             mx = top;
             l *= al;
-            if (j > 0) {   // the slot's last P V is done: its scores came after it
-#pragma unroll
+            if (t > 0) {   // the slot's last P V is done: its scores came after it
+#pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 float o[32];
                 tm_ld32(sO + 32 * q, o);
@@ -483,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 x =
+              const float2 y =
                   unpair(fma2(pair(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mu2));
-              const float a = ex2(x.x), b = ex2(x.y);
+              const float a = ex2(y.x), b = ex2(y.y);
               l2[e & 1] = add2(l2[e & 1], pair(a, b));
               w[e] = pack_bf16(a, b);
             }
@@ -505,136 +643,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&p_ready[m]);
       }
-      x += tiles;
-      if (ok && n > 0) {
-        ok = wait.warp(&o_full[m], o_ph);
-        o_ph ^= 1u;
-        tc_fence_after();
-      }
-      // ---- results: the second slot of a single row tile is merged into the first ----
-      float w0 = 1.f, w1 = 0.f;
-      const bool merge = !two && tiles > 1;
-      if (merge && m == 1 && ok) {
-        sums_s[r] = mx;
-        sums_s[kTile + r] = l;
-      }
-      float *scratch = reinterpret_cast<float *>(smem + L::kScratch);   // [D/2][128]
-      const bool whole = it.whole();
-      const bool on = mine < total;
-      const size_t out_at = static_cast<size_t>(it.q0 + node) * p.Hq + it.g * p.G + (mine & (p.G - 1));
-      const size_t part_at = static_cast<size_t>(it.slot(cta)) * p.tile + mine;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (merge) {
-          if (m == 1 && active && ok) {
-#pragma unroll
-            for (int q = 0; q < D / 64; ++q) {
-              float o[32];
-              tm_ld32(sO + h * (D / 2) + 32 * q, o);
-              tm_wait_ld();
-              pin32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) scratch[(32 * q + e) * kTile + r] = o[e];
-            }
-          }
-          meet();
+      if (!ok) break;
+      ok = wait.warp(&o_full[m], o_ph);
+      if (!ok) break;
+      o_ph ^= 1u;
+      tc_fence_after();
+      if (!active) continue;
+      // ---- results: rows go through shared memory, so that neighbouring lanes write
+      // neighbouring bytes ----
+      const bool whole = it.part < 0, on = row0 + lane < total;
+      auto out_at = [&](int row) {   // of the outputs [T, Hq]
+        return static_cast<size_t>(it.q0 + (row >> lg)) * p.Hq + it.g * p.G + (row & (p.G - 1));
+      };
+      const size_t part0 = static_cast<size_t>(max(it.part, 0)) * p.tile;
+      float inv = l > 0.f ? 1.f / l : 0.f;
+      if (on) {
+        if (whole) {
+          const bool any = l > 0.f || tree_sees_any(p, it.q0 + node, it.base, it.n);
+          inv = tree_inverse(l, any);
+          if (p.lse_out) p.lse_out[out_at(row0 + lane)] = tree_lse(mx, l, any);
+        } else {
+          p.part_lse[part0 + row0 + lane] = part_lse(mx, l);
         }
-        if ((two || m == 0) && active && ok) {
-          // (behind the merge's meeting: the other slot's products are done, too)
-          const bool odd = misc[2 + (n_items & 1)] == n_items;
-          if (h == 0) {
-            float den = l;
-            if (merge) {
-              const float m1 = sums_s[r], l1 = sums_s[kTile + r];
-              const float M = fmaxf(mx, m1);
-              w0 = M == -INFINITY ? 0.f : ex2(mx - M);
-              w1 = M == -INFINITY ? 0.f : ex2(m1 - M);
-              den = l * w0 + l1 * w1;
-              mx = M;
-            }
-            float inv = den > 0.f ? 1.f / den : 0.f;
-            if (on && whole) {
-              const bool any = den > 0.f || tree_sees_any(p, it.q0 + node, it.base, it.n);
-              inv = tree_inverse(den, any);
-              if (p.lse_out) p.lse_out[out_at] = tree_lse(mx, den, any);
-            } else if (on) {
-              p.part_lse[part_at] = part_lse(mx, den);
-            }
-            w0 *= inv;
-            w1 *= inv;
-          }
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            float o[32];
-            const int col = h * (D / 2) + 32 * q;
-            __syncwarp();
-            tm_ld32(sO + col, o);
-            tm_wait_ld();
-            pin32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              o[e] *= w0;
-              if (merge) o[e] = fmaf(w1, scratch[(32 * q + e) * kTile + r], o[e]);
-            }
-            if (on && odd) {   // what was left out of the products
+      }
+      // 16-byte pieces of a row's 32 columns: 4 in bf16, 8 in float32
+      const int lp = whole ? 2 : 3, rows = 32 >> lp;   // rows that the warp writes at once
+      __syncwarp();
 #pragma unroll 1
-              for (int tok = from; tok < end; ++tok) {
-                if (!(sees(tok) & 1u)) continue;
-                const int blk = table[tok / kBlockTokens];
-                if (blk < 0 || blk >= p.num_blocks) continue;
-                const uint4 *v = reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                    ((static_cast<size_t>(blk) * p.Hkv + it.g) * kBlockTokens + tok % kBlockTokens) * D +
-                    col);
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tm_ld32(sO + 32 * q, o);
+        tm_wait_ld();
+        pin32(o);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint4 w = v[e];
-                  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        auto piece = [&](int row, int e) {
+          return reinterpret_cast<uint4 *>(stage + row * 128 + ((e ^ (row & 7)) << 4));
+        };
+        if (whole) {
 #pragma unroll
-                  for (int f = 0; f < 4; ++f) {
-                    if (odd_bf16(u[f])) o[8 * e + 2 * f] += bf16_lo(u[f]);
-                    if (odd_bf16(u[f] >> 16)) o[8 * e + 2 * f + 1] += bf16_hi(u[f]);
-                  }
-                }
-              }
-            }
-            if (on && whole) {
-              uint4 *dst =
-                  reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_at * D + col);
+          for (int e = 0; e < 4; ++e)
+            *piece(lane, e) =
+                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+        } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                    pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                                    pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-            } else if (on) {
-              float *dst = p.part_o + part_at * D + col;
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) store8(dst + e, o + e);
-            }
-          }
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4 *>(piece(lane, e)) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
-        if (merge) meet();
+        __syncwarp();
+        for (int k = lane >> lp; k < 32 && row0 + k < total; k += rows) {
+          const int e = lane & ((1 << lp) - 1);
+          const uint4 v = *piece(k, e);
+          if (whole)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_at(row0 + k) * D +
+                                       32 * q + 8 * e) = v;
+          else
+            *reinterpret_cast<uint4 *>(p.part_o + (part0 + row0 + k) * D + 32 * q + 4 * e) = v;
+        }
+        __syncwarp();
       }
+      if (misc[2 + i % kOddRing] == i + 1 && on)
+        add_odd_values<D>(p, it, node,
+                          whole ? static_cast<void *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                      out_at(row0 + lane) * D)
+                                : static_cast<void *>(p.part_o + (part0 + row0 + lane) * D),
+                          !whole);
+      __syncwarp();
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (misc[0]) {   // a wait gave up: no output of this CTA's counts
-    Walk again = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);
-    const float nan = __int_as_float(0x7fffffff);
-    while (again.next(&it)) {
-      for (int e = tid; e < it.nodes * p.G; e += kThreads) {
-        if (!it.whole()) {
-          p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;   // (the join makes NaN of it)
-          continue;
-        }
-        const size_t at = static_cast<size_t>(it.q0 + e / p.G) * p.Hq + it.g * p.G + e % p.G;
-        if (p.lse_out) p.lse_out[at] = nan;
-        for (int col = 0; col < D; ++col)
-          static_cast<__nv_bfloat16 *>(p.out)[at * D + col] = __float2bfloat16_rn(nan);
-      }
-    }
-  }
+  if (misc[0]) all_nan<D>(p);
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

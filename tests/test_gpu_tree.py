@@ -343,3 +343,19 @@ def test_a_batch_of_many_rows():
     for dtype in ("bf16", "f32"):
         c = Case(cached, nodes, 2, 1, 64, dtype, "tree", seed=12)
         c.check(*c.run())
+
+
+@pytest.mark.parametrize("d,Hkv", [(128, 8), (64, 4)])
+@pytest.mark.parametrize("kind", ["tree", "chain"])
+def test_many_items_of_many_steps_to_a_cta(d, Hkv, kind):
+    """Several items to a CTA, of one or both row tiles and of 1 to 20 steps, in every order."""
+    rng = np.random.default_rng(d)
+    B = 48
+    nodes = rng.choice([1, 3, 8, 16, 40, 70], B)
+    cached = rng.choice([0, 5, 100, 600, 1100, 2400], B)
+    c = Case(cached, nodes, 4 * Hkv, Hkv, d, "bf16", kind, seed=13)
+    first, lse = c.run()
+    for _ in range(3):
+        again, _ = c.run()
+        assert torch.equal(first, again)
+    c.check(first, lse)
