@@ -733,7 +733,8 @@ int pkv_evict(const pkv_evict_args *args, void *stream);
  *
  * q_rot, out [T,Hq,d]; query rows outside node_starts[0..B] are left as they were, and so
  * are a row's that does not fit the call (PKV_DEVERR_BAD_LEN: starts that do not ascend
- * within [0, T], more nodes than tokens or mask bits, seq_lens[b] > 16*bt_stride).  A block
+ * within [0, T], more nodes than tokens or mask bits, seq_lens[b] > 16*bt_stride); rows that
+ * add up to 2^31 steps of 64 tokens and more set it too, and nothing is computed.  A block
  * id outside the pool sets PKV_DEVERR_BAD_BLOCK and its tokens are left out (a node to
  * which none is left is NaN).  Rows may share blocks (pkv_seq_fork, shared prefixes); a
  * query row belongs to one batch row.  Where a wait inside the kernel gives up

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   TreeItem it;
   while (walk.next(&it)) {
     if (it.t0 == 0 && it.t1 < it.steps)
-      cut = TreeCut{walk.more(), it.q0, it.nodes * p.G, it.g, it.base, it.n};
+      cut = TreeCut{walk.more(walk.at), it.q0, it.nodes * p.G, it.g, it.base, it.n};
     const int rows = it.nodes * p.G;
     __syncthreads();   // (the item before is done with the queries)
     if (rows <= 16)
@@ -417,6 +417,7 @@ extern "C" int pkv_decode_attn_tree(const pkv_tree_args *a, void *stream) {
   p.mask_words = a->mask ? a->mask_words : 0;
   p.C = sp.ctas;
   p.tile = sp.tile;
+  while (p.G << p.lg_nodes < sp.tile) ++p.lg_nodes;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.wait_limit = (a->flags & PKV_ATTN_SHORT_WAITS) ? 64 : kWaitLimitCycles;

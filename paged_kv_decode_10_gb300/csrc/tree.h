@@ -42,7 +42,7 @@ struct TreeParams {
   TreeCut *cuts;                 // [C]
   int32_t *err;
   int B, T, Hq, Hkv, G, num_blocks, bt_stride, mask_words;
-  int C, tile;                   // CTAs, rows of an item
+  int C, tile, lg_nodes;         // CTAs, rows of an item, log2 of the nodes that these are
   float scale_log2;
   long long wait_limit;
 };
@@ -70,28 +70,31 @@ __device__ __forceinline__ int tree_tokens(const TreeParams &p, int n, int len, 
   return p.mask ? len : len - n + min(last, n);
 }
 
-// The items of a CTA, in order.  STEP: tokens of a step, BOUND: kBoundary.
+// Positions of one KV head of a row (0 for a row without nodes).  STEP: tokens of a step,
+// BOUND: what an item costs by itself.
+template <int STEP, int BOUND>
+__device__ __forceinline__ uint32_t tree_head_cost(const TreeParams &p, int n, int len) {
+  const uint32_t tiles = static_cast<uint32_t>(n + (1 << p.lg_nodes) - 1) >> p.lg_nodes;
+  if (p.mask) return tiles * (BOUND + (len + STEP - 1) / STEP);
+  uint32_t sum = tiles * BOUND;
+  for (uint32_t c = 1; c <= tiles; ++c)
+    sum += (tree_tokens(p, n, len, static_cast<int>(c << p.lg_nodes)) + STEP - 1) / STEP;
+  return sum;
+}
+
+// The items of a CTA, in order.  (32 bits: a call of 2^31 positions and more is refused.)
 template <int STEP, int BOUND>
 struct TreeWalk {
   const TreeParams &p;
-  long long at, lo, hi, all;     // position of the next item; this CTA's; of the whole call
-  int ctas, cta;                 // CTAs with a share
+  uint32_t at, lo, hi;           // position of the next item; this CTA's
+  uint32_t all, ctas;            // of the whole call, CTAs with a share
+  int cta;
   int b, g, c;                   // the next item
-  int s0 = 0, n = 0, len = 0;    // its row
-  bool loaded = false;
-
-  static __device__ __forceinline__ int steps_of(int tokens) { return (tokens + STEP - 1) / STEP; }
-  // positions of one KV head of a row
-  static __device__ __forceinline__ long long head_cost(const TreeParams &p, int n, int len) {
-    const int per = p.tile / p.G, tiles = (n + per - 1) / per;
-    if (p.mask) return static_cast<long long>(tiles) * (BOUND + steps_of(len));
-    long long sum = 0;
-    for (int c = 0; c < tiles; ++c) sum += BOUND + steps_of(tree_tokens(p, n, len, (c + 1) * per));
-    return sum;
-  }
+  int s0, n, len;                // its row
+  bool loaded;
 
   __device__ __forceinline__ bool next(TreeItem *it) {
-    const int per = p.tile / p.G;
+    const int per = 1 << p.lg_nodes;
     while (at < hi) {
       if (!loaded) {
         if (b >= p.B) return false;
@@ -102,14 +105,16 @@ struct TreeWalk {
         loaded = true;
         g = c = 0;
         if (at < lo) {   // (the first row: whole heads ahead of the CTA's share)
-          const long long head = head_cost(p, n, len);
-          g = static_cast<int>(min((lo - at) / head, static_cast<long long>(p.Hkv - 1)));
-          at += g * head;
+          const uint32_t head = tree_head_cost<STEP, BOUND>(p, n, len);
+          while (g + 1 < p.Hkv && at + head <= lo) {
+            at += head;
+            ++g;
+          }
         }
       }
       const int tokens = tree_tokens(p, n, len, (c + 1) * per);
-      const int steps = steps_of(tokens);
-      const long long first = at + BOUND;
+      const int steps = (tokens + STEP - 1) / STEP;
+      const uint32_t first = at + BOUND;
       it->b = b;
       it->g = g;
       it->n0 = c * per;
@@ -121,7 +126,7 @@ struct TreeWalk {
       it->steps = steps;
       at = first + steps;
       it->t0 = static_cast<int>(max(lo, first) - first);
-      it->t1 = static_cast<int>(min(hi, at) - first);
+      it->t1 = static_cast<int>(min(hi, at)) - static_cast<int>(first);
       if ((c + 1) * per < n) {
         ++c;
       } else {
@@ -135,9 +140,9 @@ struct TreeWalk {
     }
     return false;
   }
-  // CTAs behind this one that have steps of the item that next() gave last.
-  __device__ __forceinline__ int more() const {
-    return static_cast<int>((at * ctas - 1) / all) - cta;   // (the CTA of its last step)
+  // CTAs behind this one that have steps of an item that ends ahead of position `end`.
+  __device__ __forceinline__ int more(uint32_t end) const {
+    return static_cast<int>((static_cast<unsigned long long>(end) * ctas - 1) / all) - cta;
   }
 };
 
@@ -146,59 +151,62 @@ struct TreeWalk {
 // MIN: positions a CTA gets at least, while there are CTAs to spare.
 template <int STEP, int BOUND, int MIN, int NT>
 __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p, int cta) {
-  using Walk = TreeWalk<STEP, BOUND>;
-  __shared__ long long sums[NT / 32], start_at[1];
-  __shared__ int start_row[1];
+  __shared__ unsigned long long sums[NT / 32];
+  __shared__ int start[2];   // first row, its position
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (p.B + NT - 1) / NT, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
-  long long mine = 0;
+  const int each = p.B <= NT ? 1 : (p.B + NT - 1) / NT;
+  const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
+  unsigned long long mine = 0;
   bool bad = false;
+  uint32_t cost = 0;   // of the thread's last row
   for (int b = b0; b < b1; ++b) {
     int s0, n, len;
-    if (!tree_row(p, b, &s0, &n, &len))
-      bad = true;
-    else
-      mine += p.Hkv * Walk::head_cost(p, n, len);
+    const bool fits = tree_row(p, b, &s0, &n, &len);
+    bad |= !fits;
+    cost = fits ? tree_head_cost<STEP, BOUND>(p, n, len) : 0;
+    mine += static_cast<unsigned long long>(cost) * p.Hkv;
   }
-  if (bad && cta == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
-  long long incl = mine;   // positions up to this thread's rows, them included
+  unsigned long long incl = mine;   // positions up to this thread's rows, them included
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += x;
   }
   if (lane == 31) sums[warp] = incl;
-  if (tid == 0) start_row[0] = p.B;
+  if (tid == 0) start[0] = p.B;
   __syncthreads();
-  long long before = 0, all = 0;
+  unsigned long long before = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += sums[w];
-    all += sums[w];
+    sum += sums[w];
   }
-  incl += before;
-  long long shares = all / MIN;
-  shares = shares < 1 ? 1 : shares;
-  const int ctas = static_cast<int>(min(shares, static_cast<long long>(p.C)));
-  const long long lo = cta < ctas ? cta * all / ctas : all;
-  const long long hi = cta < ctas ? (cta + 1) * all / ctas : all;
-  if (lo < hi && incl - mine <= lo && lo < incl) {   // one thread has the row
-    long long at = incl - mine;
-    for (int b = b0; b < b1; ++b) {
+  const bool fits = sum < 1ull << 31;
+  const uint32_t all = fits ? static_cast<uint32_t>(sum) : 0;
+  if (cta == 0 && (bad || !fits)) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
+  const uint32_t ctas = max(1u, min(all / MIN, static_cast<uint32_t>(p.C)));
+  // floor(c all / ctas) by 32-bit divisions.  (The rest dealt to the first CTAs, one each,
+  // instead of evenly, took 3 % longer.)
+  const uint32_t share = all / ctas, rest = all - share * ctas;
+  const uint32_t c = min(static_cast<uint32_t>(cta), ctas), c1 = min(c + 1, ctas);
+  const uint32_t lo = c * share + c * rest / ctas, hi = c1 * share + c1 * rest / ctas;
+  uint32_t at = static_cast<uint32_t>(before + incl - mine);
+  if (lo < hi && at <= lo && lo < at + mine) {   // one thread has the row
+    int b = b0;
+    for (; b + 1 < b1; ++b) {   // (more rows than threads)
       int s0, n, len;
-      const long long cost =
-          tree_row(p, b, &s0, &n, &len) ? p.Hkv * Walk::head_cost(p, n, len) : 0;
-      if (lo < at + cost) {
-        start_row[0] = b;
-        start_at[0] = at;
-        break;
-      }
-      at += cost;
+      const uint32_t rows =
+          tree_row(p, b, &s0, &n, &len) ? tree_head_cost<STEP, BOUND>(p, n, len) * p.Hkv : 0;
+      if (lo < at + rows) break;
+      at += rows;
     }
+    start[0] = b;
+    start[1] = static_cast<int>(at);
   }
   __syncthreads();
-  const int row = start_row[0];
-  return Walk{p, row < p.B ? start_at[0] : hi, lo, hi, all, ctas, cta, row, 0, 0};
+  const int row = start[0];
+  return TreeWalk<STEP, BOUND>{p,   row < p.B ? static_cast<uint32_t>(start[1]) : hi, lo, hi, all, ctas,
+                               cta, row, 0, 0, 0, 0, 0, false};
 }
 
 // 32 visibility bits of a query row: tokens tok .. tok + 31 of its row, bit j for token

@@ -50,7 +50,7 @@ constexpr int kHalf = 2;                      // 32-token pieces of P after whic
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr long long kPollLimit = 4096;
 constexpr int kBoundary = 2, kMin = 1;
-constexpr int kQueue = 4;                     // items handed out ahead
+constexpr int kQueue = 8;                     // items handed out and not yet written out
 constexpr int kBadRing = 16, kOddRing = 4;
 
 template <int D>
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WarpWaiter<POLL> wait_there{wait_here};
   Handed *items = reinterpret_cast<Handed *>(smem + L::kItems);
   // The i-th item of the queue (for the whole warp; t1 == 0: there are no more).
-  auto take = [&](const auto &wait, int i, Handed *it) {
-    if (!wait.warp(&i_full[i % kQueue], static_cast<uint32_t>(i / kQueue) & 1u)) return false;
+  auto take = [&](int i, Handed *it) {
+    if (!wait_there.warp(&i_full[i % kQueue], static_cast<uint32_t>(i / kQueue) & 1u)) return false;
     *it = items[i % kQueue];
     __syncwarp();
     if (lane == 0) mbar_arrive(&i_empty[i % kQueue]);
@@ -295,17 +295,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       int used[2] = {0, 0};           // items of each slot so far
       int single = 0;                 // the slot of the next item that takes one
       TreeCut cut = {};
+      uint32_t cut_end = 0;           // where the cut item ends
       bool ok = true;
       for (int i = 0; ok; ++i) {
         Handed it;
         if (is_v) {
-          if (!take(wait, i, &it)) break;
+          if (!take(i, &it)) break;
         } else {
           TreeItem w;
           const bool some = walk.next(&w);
           if (some) {
-            if (w.t0 == 0 && w.t1 < w.steps)
-              cut = TreeCut{walk.more(), w.q0, w.nodes * p.G, w.g, w.base, w.n};
+            if (w.t0 == 0 && w.t1 < w.steps) {
+              cut = TreeCut{0, w.q0, w.nodes * p.G, w.g, w.base, w.n};
+              cut_end = walk.at;
+            }
             const bool two = w.nodes * p.G > kTile;
             it = Handed{w.q0, w.nodes, w.g, w.b, w.base, w.n, w.tokens, w.n0, w.t0, w.t1,
                         two ? 3 : 1 << single, w.whole() ? -1 : w.slot(cta),
@@ -383,7 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (lane == 0 && !is_v) p.cuts[cta] = cut;
+      if (lane == 0 && !is_v) {
+        if (cut_end) cut.more = walk.more(cut_end);
+        p.cuts[cta] = cut;
+      }
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, x - NS); n < x; ++n)
         mbar_wait_bounded(&full[n % NS], static_cast<uint32_t>(n / NS) & 1u, kDrainCycles);
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = 0;; ++i) {
         Handed it;
-        if (!take(wait, i, &it)) break;
+        if (!take(i, &it)) break;
         const int first = uniform(it.t0), tiles = uniform(it.t1) - first, tokens = uniform(it.tokens);
         const int slots = uniform(it.slots), special = uniform(it.special);
         if (!(slots >> m & 1)) {   // the other slot's
@@ -545,11 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     for (int i = 0;; ++i) {
-      Handed it;
-      if (!take(wait, i, &it)) break;
+      // (an item stays in the queue until its results are out, and is read there again: what
+      // it says would take 16 of the registers that hold the scores)
+      const Handed &it = items[i % kQueue];
+      if (!wait.warp(&i_full[i % kQueue], static_cast<uint32_t>(i / kQueue) & 1u)) break;
       const int tiles = it.t1 - it.t0;
+      if (tiles <= 0) break;
       if (!(it.slots >> m & 1)) {   // the other slot's
         x += tiles;
+        arrive(&i_empty[i % kQueue]);
         continue;
       }
       const int total = it.nodes << lg;
@@ -648,7 +658,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_ph ^= 1u;
       tc_fence_after();
-      if (!active) continue;
+      if (!active) {
+        arrive(&i_empty[i % kQueue]);
+        continue;
+      }
       // ---- results: rows go through shared memory, so that neighbouring lanes write
       // neighbouring bytes ----
       const bool whole = it.part < 0, on = row0 + lane < total;
@@ -666,51 +679,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_lse[part0 + row0 + lane] = part_lse(mx, l);
         }
       }
-      // 16-byte pieces of a row's 32 columns: 4 in bf16, 8 in float32
-      const int lp = whole ? 2 : 3, rows = 32 >> lp;   // rows that the warp writes at once
-      __syncwarp();
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        float o[32];
+      // 32 columns at a time; a row's 16-byte pieces lie permuted within 128 bytes
+      auto piece = [&](int row, int e) {
+        return reinterpret_cast<uint4 *>(stage + row * 128 + ((e ^ (row & 7)) << 4));
+      };
+      auto columns = [&](int q, float *o) {
+        __syncwarp();
         tm_ld32(sO + 32 * q, o);
         tm_wait_ld();
         pin32(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] *= inv;
-        auto piece = [&](int row, int e) {
-          return reinterpret_cast<uint4 *>(stage + row * 128 + ((e ^ (row & 7)) << 4));
-        };
-        if (whole) {
+      };
+      if (whole) {   // 4 pieces a row: the warp writes 8 rows at once
+        __nv_bfloat16 *to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          to[k] = static_cast<__nv_bfloat16 *>(p.out) +
+                  out_at(min(row0 + 8 * k + (lane >> 2), total - 1)) * D + 8 * (lane & 3);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          columns(q, o);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *piece(lane, e) =
                 make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
                            pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-        } else {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (row0 + 8 * k + (lane >> 2) < total)
+              *reinterpret_cast<uint4 *>(to[k] + 32 * q) = *piece(8 * k + (lane >> 2), lane & 3);
+        }
+      } else {   // 8 pieces a row: 4 rows at once
+        float *to = p.part_o + (part0 + row0 + (lane >> 3)) * D + 4 * (lane & 7);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          columns(q, o);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4 *>(piece(lane, e)) =
                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (row0 + 4 * k + (lane >> 3) < total)
+              *reinterpret_cast<uint4 *>(to + 4 * k * D + 32 * q) = *piece(4 * k + (lane >> 3), lane & 7);
         }
-        __syncwarp();
-        for (int k = lane >> lp; k < 32 && row0 + k < total; k += rows) {
-          const int e = lane & ((1 << lp) - 1);
-          const uint4 v = *piece(k, e);
-          if (whole)
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_at(row0 + k) * D +
-                                       32 * q + 8 * e) = v;
-          else
-            *reinterpret_cast<uint4 *>(p.part_o + (part0 + row0 + k) * D + 32 * q + 4 * e) = v;
-        }
-        __syncwarp();
       }
+      __syncwarp();
       if (misc[2 + i % kOddRing] == i + 1 && on)
         add_odd_values<D>(p, it, node,
                           whole ? static_cast<void *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                       out_at(row0 + lane) * D)
                                 : static_cast<void *>(p.part_o + (part0 + row0 + lane) * D),
                           !whole);
-      __syncwarp();
+      arrive(&i_empty[i % kQueue]);
     }
     tc_fence_before();
   }
