@@ -222,11 +222,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int cta = blockIdx.x;
   auto walk = tree_begin<kStep, kBoundary, kMin, kThreads>(p, cta);
-  TreeCut cut = {};
+  TreeCut cuts[2] = {};
   TreeItem it;
   while (walk.next(&it)) {
-    if (it.t0 == 0 && it.t1 < it.steps)
-      cut = TreeCut{walk.more(walk.at), it.q0, it.nodes * p.G, it.g, it.base, it.n};
+    if (!it.whole()) (it.t0 == 0 ? cuts[1] : cuts[0]) = walk.cut(it, walk.at);
     const int rows = it.nodes * p.G;
     __syncthreads();   // (the item before is done with the queries)
     if (rows <= 16)
@@ -236,7 +235,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
     else
       f32_item<D, 4>(p, it, sm);
   }
-  if (threadIdx.x == 0) p.cuts[cta] = cut;
+  if (threadIdx.x == 0) {
+    p.cuts[2 * cta] = cuts[0];
+    p.cuts[2 * cta + 1] = cuts[1];
+  }
 }
 
 template <int D>
@@ -253,62 +255,103 @@ cudaError_t launch_f32(const TreeParams &p, cudaStream_t s) {
 
 // ---- the join ---------------------------------------------------------------------
 // out = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M), M the largest lse_s, over the parts
-// of an item, in the order of its tokens: chunk by chunk of an item's rows, D / 4 lanes to
-// a row.  Bound by L2 latency: the partials were just written.
-constexpr int kJoinChunks = 8;
+// of an item, in the order of its tokens.  Every slot stands for one share of its item's
+// rows, kJoinChunks CTAs to a slot, D / 4 lanes to a row.  Bound by the launch and by L2
+// latency (the partials were just written, by other SMs: about 1 us a round trip), so 8
+// reads of a lane are under way together: K parts of F rows.  (Joined by the CTAs of an
+// item's first part alone, one item of 131072 tokens and 19 parts took 20 us; two parts at
+// once whatever their number, 8 parts took 7 us, now 3.)
+constexpr int kJoinChunks = 2;
+
+template <typename T, int D, int F, int K>
+__device__ __forceinline__ void join_rows(const TreeParams &p, const TreeCut &cut, int first, int end,
+                                          int step) {
+  const int d4 = threadIdx.x % (D / 4);
+  for (int r = first; r < end; r += F * step) {
+    float M[F], den[F];
+    float4 acc[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      M[f] = -INFINITY;
+      den[f] = 0.f;
+      acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i = 0; i < cut.parts; i += K) {
+      float l[F][K];
+      float4 v[F][K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        // (what does not count is read from the last part or row: a branch would make the
+        // reads wait for one another)
+        const int part = min(i + k, cut.parts - 1);
+        const size_t slot =
+            static_cast<size_t>(part == 0 ? 2 * cut.first + 1 : 2 * (cut.first + part)) * p.tile;
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const size_t at = slot + min(r + f * step, end - 1);
+          l[f][k] = __ldcg(p.part_lse + at);
+          v[f][k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * D) + d4);
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        float top = M[f];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (i + k >= cut.parts) l[f][k] = -INFINITY;
+          top = fmaxf(top, l[f][k]);
+        }
+        const float mu = top == -INFINITY ? 0.f : top, al = ex2(M[f] - mu);
+        den[f] *= al;
+        acc[f] = make_float4(acc[f].x * al, acc[f].y * al, acc[f].z * al, acc[f].w * al);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          // (a part of which the row sees nothing counts for nothing, whatever it holds)
+          if (l[f][k] == -INFINITY) continue;
+          const float w = ex2(l[f][k] - mu);
+          den[f] += w;
+          acc[f].x = fmaf(w, v[f][k].x, acc[f].x);
+          acc[f].y = fmaf(w, v[f][k].y, acc[f].y);
+          acc[f].z = fmaf(w, v[f][k].z, acc[f].z);
+          acc[f].w = fmaf(w, v[f][k].w, acc[f].w);
+        }
+        M[f] = top;
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int row = r + f * step;
+      if (row >= end) continue;
+      const int q_row = cut.q0 + (row >> p.lg_g);
+      const size_t at = static_cast<size_t>(q_row) * p.Hq + cut.g * p.G + (row & (p.G - 1));
+      const bool any = den[f] > 0.f || tree_sees_any(p, q_row, cut.base, cut.n);
+      const float inv = tree_inverse(den[f], any);
+      store4(static_cast<T *>(p.out) + at * D + 4 * d4,
+             make_float4(acc[f].x * inv, acc[f].y * inv, acc[f].z * inv, acc[f].w * inv));
+      if (d4 == 0 && p.lse_out) p.lse_out[at] = tree_lse(M[f], den[f], any);
+    }
+  }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int LPR = D / 4, kRows = 256 / LPR, K = 4;
+  constexpr int kRows = 256 / (D / 4);
+  pdl_launch_dependents();   // (every CTA waits before it ends)
   pdl_wait();
-  const int cta = blockIdx.x / kJoinChunks, chunk = blockIdx.x % kJoinChunks;
-  const TreeCut cut = p.cuts[cta];
-  if (cut.more <= 0) return;
-  const int d4 = threadIdx.x % LPR;
-  for (int r = chunk * kRows + threadIdx.x / LPR; r < cut.rows; r += kJoinChunks * kRows) {
-    float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 <= cut.more; i0 += K) {
-      float l[K];
-      float4 v[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int i = min(i0 + k, cut.more);
-        const size_t at =
-            static_cast<size_t>(i == 0 ? 2 * cta + 1 : 2 * (cta + i)) * p.tile + r;
-        l[k] = i0 + k <= cut.more ? __ldcg(p.part_lse + at) : -INFINITY;
-        v[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + at * D) + d4);
-      }
-      float top = M;
-#pragma unroll
-      for (int k = 0; k < K; ++k) top = fmaxf(top, l[k]);
-      const float mu = top == -INFINITY ? 0.f : top;
-      const float al = ex2(M - mu);
-      den *= al;
-      acc.x *= al;
-      acc.y *= al;
-      acc.z *= al;
-      acc.w *= al;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float w = ex2(l[k] - mu);
-        if (l[k] == -INFINITY) continue;   // (a part of which the row sees nothing)
-        den += w;
-        acc.x = fmaf(w, v[k].x, acc.x);
-        acc.y = fmaf(w, v[k].y, acc.y);
-        acc.z = fmaf(w, v[k].z, acc.z);
-        acc.w = fmaf(w, v[k].w, acc.w);
-      }
-      M = top;
-    }
-    const int q_row = cut.q0 + r / p.G;
-    const size_t at = static_cast<size_t>(q_row) * p.Hq + cut.g * p.G + r % p.G;
-    const bool any = den > 0.f || tree_sees_any(p, q_row, cut.base, cut.n);
-    const float inv = tree_inverse(den, any);
-    store4(static_cast<T *>(p.out) + at * D + 4 * d4,
-           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (d4 == 0 && p.lse_out) p.lse_out[at] = tree_lse(M, den, any);
-  }
+  const int mine = blockIdx.x / kJoinChunks, chunk = blockIdx.x % kJoinChunks;
+  const int4 *said = reinterpret_cast<const int4 *>(p.cuts + mine);
+  const int4 c0 = __ldcg(said), c1 = __ldcg(said + 1);
+  const TreeCut cut{c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  if (cut.parts <= 0) return;
+  const int part = mine / 2 - cut.first;   // this slot's place among the item's
+  const int r0 = cut.rows * part / cut.parts + chunk * kRows + threadIdx.x / (D / 4),
+            r1 = cut.rows * (part + 1) / cut.parts;
+  if (cut.parts <= 2)
+    join_rows<T, D, 4, 2>(p, cut, r0, r1, kJoinChunks * kRows);
+  else if (cut.parts <= 4)
+    join_rows<T, D, 2, 4>(p, cut, r0, r1, kJoinChunks * kRows);
+  else
+    join_rows<T, D, 1, 8>(p, cut, r0, r1, kJoinChunks * kRows);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -326,7 +369,7 @@ int tree_space(int d, int dtype, TreeSpace *s) {
   s->ctas = dtype == PKV_F32 && d == 64 ? 2 * sms : sms;
   if (s->ctas > kMaxTreeCtas) s->ctas = kMaxTreeCtas;
   const size_t rows = 2 * static_cast<size_t>(s->ctas) * s->tile;
-  s->lse = align256(s->ctas * sizeof(TreeCut));
+  s->lse = align256(2 * s->ctas * sizeof(TreeCut));
   s->o = s->lse + align256(rows * sizeof(float));
   s->bytes = s->o + align256(rows * d * sizeof(float));
   return PKV_OK;
@@ -418,6 +461,7 @@ extern "C" int pkv_decode_attn_tree(const pkv_tree_args *a, void *stream) {
   p.C = sp.ctas;
   p.tile = sp.tile;
   while (p.G << p.lg_nodes < sp.tile) ++p.lg_nodes;
+  while (1 << p.lg_g < p.G) ++p.lg_g;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.wait_limit = (a->flags & PKV_ATTN_SHORT_WAITS) ? 64 : kWaitLimitCycles;
@@ -435,7 +479,7 @@ extern "C" int pkv_decode_attn_tree(const pkv_tree_args *a, void *stream) {
     e = a->d == 64 ? launch_f32<64>(p, s) : launch_f32<128>(p, s);
   }
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "tree kernel launch: %s", cudaGetErrorString(e));
-  const unsigned grid = static_cast<unsigned>(sp.ctas) * kJoinChunks;
+  const unsigned grid = 2 * static_cast<unsigned>(sp.ctas) * kJoinChunks;
   e = a->dtype == PKV_BF16
           ? (a->d == 64 ? launch_waiting(tree_join_kernel<__nv_bfloat16, 64>, grid, 256, 0, s, p)
                         : launch_waiting(tree_join_kernel<__nv_bfloat16, 128>, grid, 256, 0, s, p))

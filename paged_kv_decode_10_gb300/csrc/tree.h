@@ -13,8 +13,9 @@
 // An item whose steps lie in one CTA is finished there.  Of the others every CTA leaves a
 // partial (float32 output, base-2 log-sum-exp) in a slot of its own: a CTA has at most
 // two cut items, the one it begins with (slot 2 c) and the one it ends with (slot
-// 2 c + 1).  The CTA that has an item's first step writes which slots hold the rest
-// (TreeCut), and the join kernel combines them, in the order of the tokens.
+// 2 c + 1), and writes for each slot which item and which CTAs it belongs to (TreeCut).  The
+// join kernel combines an item's parts in the order of the tokens, every slot's share of
+// its rows on its own, so that an item of many parts is joined by many.
 #pragma once
 #include <cuda.h>
 
@@ -24,11 +25,11 @@ namespace pkv {
 
 constexpr int kMaxTreeCtas = 1024;
 
-// Of the item whose first part lies in CTA c's slot 2 c + 1 (more == 0: there is none):
-// `more` further parts in slots 2 (c + 1), 2 (c + 2), ...
-struct TreeCut {
-  int32_t more, q0, rows, g;     // first query row, rows, KV head
-  int32_t base, n, pad[2];       // the row's tokens ahead of its nodes, its nodes
+// A slot's item: its parts lie in slot 2 first + 1 and slots 2 (first + 1), ...,
+// 2 (first + parts - 1); parts == 0: the slot is not used.
+struct alignas(16) TreeCut {
+  int32_t parts, first, q0, rows;   // first query row, rows
+  int32_t g, base, n, pad;          // KV head; the row's tokens ahead of its nodes, its nodes
 };
 
 struct TreeParams {
@@ -39,10 +40,10 @@ struct TreeParams {
   void *out;                     // [T, Hq, D]
   float *lse_out;                // nullable [T, Hq]
   float *part_o, *part_lse;      // [2 C, tile, D], [2 C, tile]
-  TreeCut *cuts;                 // [C]
+  TreeCut *cuts;                 // [2 C]
   int32_t *err;
   int B, T, Hq, Hkv, G, num_blocks, bt_stride, mask_words;
-  int C, tile, lg_nodes;         // CTAs, rows of an item, log2 of the nodes that these are
+  int C, tile, lg_nodes, lg_g;   // CTAs, rows of an item, log2 of the nodes that these are, of G
   float scale_log2;
   long long wait_limit;
 };
@@ -140,9 +141,14 @@ struct TreeWalk {
     }
     return false;
   }
-  // CTAs behind this one that have steps of an item that ends ahead of position `end`.
-  __device__ __forceinline__ int more(uint32_t end) const {
-    return static_cast<int>((static_cast<unsigned long long>(end) * ctas - 1) / all) - cta;
+  // The CTA that has the step at position x.
+  __device__ __forceinline__ int owner(uint32_t x) const {
+    return static_cast<int>((static_cast<unsigned long long>(x + 1) * ctas - 1) / all);
+  }
+  // What is to be written down of a cut item whose last step is ahead of position `end`.
+  __device__ __forceinline__ TreeCut cut(const TreeItem &it, uint32_t end) const {
+    const int from = owner(end - it.steps);
+    return TreeCut{owner(end - 1) - from + 1, from, it.q0, it.nodes * p.G, it.g, it.base, it.n};
   }
 };
 

@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int x = 0;                      // tiles so far
       int used[2] = {0, 0};           // items of each slot so far
       int single = 0;                 // the slot of the next item that takes one
-      TreeCut cut = {};
-      uint32_t cut_end = 0;           // where the cut item ends
+      TreeItem first = {}, last = {};             // the cut items, and where they end
+      uint32_t first_end = 0, last_end = 0;
       bool ok = true;
       for (int i = 0; ok; ++i) {
         Handed it;
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           TreeItem w;
           const bool some = walk.next(&w);
           if (some) {
-            if (w.t0 == 0 && w.t1 < w.steps) {
-              cut = TreeCut{0, w.q0, w.nodes * p.G, w.g, w.base, w.n};
-              cut_end = walk.at;
+            if (!w.whole()) {   // (at most two of them)
+              (w.t0 == 0 ? last : first) = w;
+              (w.t0 == 0 ? last_end : first_end) = walk.at;
             }
             const bool two = w.nodes * p.G > kTile;
             it = Handed{w.q0, w.nodes, w.g, w.b, w.base, w.n, w.tokens, w.n0, w.t0, w.t1,
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && !is_v) {
-        if (cut_end) cut.more = walk.more(cut_end);
-        p.cuts[cta] = cut;
+        p.cuts[2 * cta] = first_end ? walk.cut(first, first_end) : TreeCut{};
+        p.cuts[2 * cta + 1] = last_end ? walk.cut(last, last_end) : TreeCut{};
       }
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, x - NS); n < x; ++n)
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's 32 lanes
     const uint32_t sS = tS(m) + lanes, sO = tO(m) + lanes;
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);
-    const int lg = __ffs(p.G) - 1;
+    const int lg = p.lg_g;
     unsigned char *stage = smem + L::kOut + warp * (32 * 128);
     int x = 0;
     uint32_t s_ph = 0, o_ph = 0;
