@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const __grid_cons
 // Token base + j of row b takes the key and value of token base + path[j].  path ascends
 // strictly, so path[j] >= j: going up in j, whatever is overwritten has been read, and a
 // thread that owns one 16-byte column of one head of one pool needs nobody else for
-// that.  A CTA serves up to kThreads columns of one row; it checks the row first (every
+// that.  A CTA serves kThreads columns of one row at a time; it checks the row first (every
 // CTA of a row comes to the same answer) and lists its moves in shared memory.
 struct AcceptParams {
   const int32_t *block_tables, *seq_lens, *node_starts, *path, *accept_lens;
@@ -98,16 +98,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const __grid_cons
     return;
   }
   const int per_pool = p.Hkv * p.cols;
-  const long long item = static_cast<long long>(chunk) * kThreads + tid;
-  const bool on = item < static_cast<long long>(per_pool) * p.n_pools;
-  const int pool = on ? static_cast<int>(item / per_pool) : 0;
-  const int r = on ? static_cast<int>(item - static_cast<long long>(pool) * per_pool) : 0;
-  const int h = r / p.cols, c = r - h * p.cols;
-  uint4 *mine = p.pool[pool] + c;
-  auto at = [&](int slot) {   // [num_blocks, Hkv, 16, cols]
-    return (static_cast<size_t>(slot / kBlockTokens) * p.Hkv + h) * (kBlockTokens * p.cols) +
-           (slot % kBlockTokens) * p.cols;
-  };
+  const long long items = static_cast<long long>(per_pool) * p.n_pools;
   for (int j0 = 0; j0 < a; j0 += kMoves) {
     const int m = min(kMoves, a - j0);
     if (j0) __syncthreads();
@@ -117,15 +108,25 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const __grid_cons
       to_s[tid] = i == j0 + tid ? -1 : slot(base + j0 + tid);
     }
     __syncthreads();
-    if (!on) continue;
-    for (int j = 0; j < m; j += kFlight) {
-      uint4 v[kFlight];
+    for (long long item = static_cast<long long>(chunk) * kThreads + tid; item < items;
+         item += static_cast<long long>(p.chunks) * kThreads) {
+      const int pool = static_cast<int>(item / per_pool);
+      const int r = static_cast<int>(item - static_cast<long long>(pool) * per_pool);
+      const int h = r / p.cols, c = r - h * p.cols;
+      uint4 *mine = p.pool[pool] + c;
+      auto at = [&](int slot) {   // [num_blocks, Hkv, 16, cols]
+        return (static_cast<size_t>(slot / kBlockTokens) * p.Hkv + h) * (kBlockTokens * p.cols) +
+               (slot % kBlockTokens) * p.cols;
+      };
+      for (int j = 0; j < m; j += kFlight) {
+        uint4 v[kFlight];
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k)
-        if (j + k < m && from_s[j + k] >= 0) v[k] = mine[at(from_s[j + k])];
+        for (int k = 0; k < kFlight; ++k)
+          if (j + k < m && from_s[j + k] >= 0) v[k] = mine[at(from_s[j + k])];
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k)
-        if (j + k < m && from_s[j + k] >= 0) mine[at(to_s[j + k])] = v[k];
+        for (int k = 0; k < kFlight; ++k)
+          if (j + k < m && from_s[j + k] >= 0) mine[at(to_s[j + k])] = v[k];
+      }
     }
   }
 }
@@ -256,9 +257,10 @@ extern "C" int pkv_tree_accept(const pkv_accept_args *a, void *stream) {
   p.path_stride = a->path_stride;
   p.n_pools = a->n_pools;
   const long long items = static_cast<long long>(a->Hkv) * p.cols * a->n_pools;
-  p.chunks = static_cast<int>((items + kThreads - 1) / kThreads);
-  PKV_REQUIRE(static_cast<long long>(p.chunks) * a->B < (1ll << 31), PKV_ERR_UNSUPPORTED,
-              "too many rows and pools for one call");
+  // As many CTAs as there are pieces of kThreads columns, but no more than fit on the GPU
+  // at once: looking the row over takes a CTA longer than a piece's moves.
+  const long long pieces = (items + kThreads - 1) / kThreads, most = a->B < 1216 ? 1216 / a->B : 1;
+  p.chunks = static_cast<int>(pieces < most ? pieces : most);
   const unsigned grid = static_cast<unsigned>(p.chunks) * a->B;
   const cudaError_t e =
       launch_waiting(tree_accept_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), p);
