@@ -256,6 +256,26 @@ __device__ __forceinline__ float tree_lse(float mx, float den, bool sees_any) {
                    : den == 0.f && !sees_any ? -INFINITY : __int_as_float(0x7fffffff);
 }
 
+// After a wait that gave up (by all NT threads of the CTA): no output of it counts.
+template <typename T, int D, int STEP, int BOUND, int MIN, int NT>
+__device__ __noinline__ void tree_all_nan(const TreeParams &p) {
+  const int cta = blockIdx.x;
+  auto walk = tree_begin<STEP, BOUND, MIN, NT>(p, cta);
+  TreeItem it;
+  const float nan = __int_as_float(0x7fffffff);
+  while (walk.next(&it))
+    for (int e = threadIdx.x; e < it.nodes * p.G; e += NT) {
+      if (!it.whole()) {   // (the join makes NaN of it)
+        p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;
+        continue;
+      }
+      const size_t at = static_cast<size_t>(it.q0 + e / p.G) * p.Hq + it.g * p.G + e % p.G;
+      if (p.lse_out) p.lse_out[at] = nan;
+      for (int c = 0; c < D; ++c) static_cast<T *>(p.out)[at * D + c] = from_f32<T>(nan);
+    }
+}
+
+cudaError_t launch_tree_f32(const TreeParams &p, int D, cudaStream_t s);
 cudaError_t launch_tree_bf16(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                              const TreeParams &p, int D, cudaStream_t s);
 

@@ -181,26 +181,6 @@ __device__ __noinline__ void add_odd_values(const TreeParams &p, const Handed it
   }
 }
 
-// After a wait that gave up: no output of this CTA's counts.
-template <int D>
-__device__ __noinline__ void all_nan(const TreeParams &p) {
-  const int cta = blockIdx.x;
-  Walk walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);
-  TreeItem it;
-  const float nan = __int_as_float(0x7fffffff);
-  while (walk.next(&it))
-    for (int e = threadIdx.x; e < it.nodes * p.G; e += kThreads) {
-      if (!it.whole()) {   // (the join makes NaN of it)
-        p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;
-        continue;
-      }
-      const size_t at = static_cast<size_t>(it.q0 + e / p.G) * p.Hq + it.g * p.G + e % p.G;
-      if (p.lse_out) p.lse_out[at] = nan;
-      for (int c = 0; c < D; ++c)
-        static_cast<__nv_bfloat16 *>(p.out)[at * D + c] = __float2bfloat16_rn(nan);
-    }
-}
-
 template <int D, bool POLL>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -741,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (misc[0]) all_nan<D>(p);
+  if (misc[0]) tree_all_nan<__nv_bfloat16, D, kTile, kBoundary, kMin, kThreads>(p);
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
