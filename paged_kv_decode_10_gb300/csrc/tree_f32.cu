@@ -8,7 +8,10 @@
 // Items of at most 16 or 32 rows use one or two of the four row registers.  Keys lie in
 // shared memory with rows 4 floats longer than a head, so that a warp's reads spread over
 // the banks.  A ninth warp finds the CTA's items (tree.h), hands them out through a short
-// queue and loads K and V a step ahead, a bulk copy for every token.
+// queue and loads K and V a step ahead, a bulk copy for every token.  (By tensor copies
+// into swizzled slabs the loads of a call of two steps a CTA were 2 us sooner, but the
+// permuted addresses took the products 10 to 20 % longer.)  Multiplications and additions
+// go two to an instruction (16 rows of 1000 tokens, 16 nodes, 32/8 heads of 128: 139 -> 128 us).
 //
 // Masks.  Steps that reach past the tokens every row sees mark what a row does not see with
 // a weight of -1 and skip it in the product with V: it may hold anything, the tail of a
@@ -22,7 +25,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kStep = 64, kTile = 64, kCompute = 256, kThreads = kCompute + 32, kBoundary = 1, kMin = 2;
+constexpr int kStep = 64, kTile = 64, kCompute = 256, kThreads = kCompute + 32, kBoundary = 1, kMin = 1;
 constexpr int kStages = 2, kQueue = 4;
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr long long kPollLimit = 4096;
@@ -44,7 +47,7 @@ struct Lay {
   static constexpr int kBars = kItems + kQueue * 16;
   static constexpr int kThere = kBars + 2 * (2 * kStages + 2 * kQueue);   // pages of a stage in the pool
   static constexpr int kMisc = kThere + kStages;    // a wait gave up
-  static constexpr int kFloats = kMisc + 2;
+  static constexpr int kBytes = 4 * (kMisc + 2);
 };
 
 template <int D, int NR, typename Wait>
@@ -75,37 +78,46 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
   }
   __syncwarp();
   float mx[NR], l[NR];
-  float4 acc[NR][M];
+  uint64_t acc[NR][M][2];   // columns 4 tx + 64 m ..., two in one
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     mx[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int m = 0; m < M; ++m) acc[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int m = 0; m < M; ++m) acc[i][m][0] = acc[i][m][1] = 0;
   }
   for (int t = it.t0; t < it.t1; ++t, ++*step) {
     const int tok0 = t * kStep, st = *step % kStages;
     if (!wait.warp(&full[st], static_cast<uint32_t>(*step / kStages) & 1u)) return false;
     const float *ks = sm + L::kKV + 2 * st * L::kMat, *vs = ks + L::kMat;
     const uint32_t there = there_s[st];
+    // scores: sums over the even and the odd elements of a head, two in one instruction
+    uint64_t s2[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2[i][j] = 0;   // (two zeros)
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      ulonglong2 k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k[j] = *reinterpret_cast<const ulonglong2 *>(ks + (tx + 16 * j) * LD + c);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(qs + (ty + 16 * i) * LD + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2[i][j] = fma2(q.y, k[j].y, fma2(q.x, k[j].x, s2[i][j]));
+      }
+    }
     float s[NR][4];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      float4 k[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * j) * LD + c);
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float4 q = *reinterpret_cast<const float4 *>(qs + (ty + 16 * i) * LD + c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(q.x, k[j].x, fmaf(q.y, k[j].y, fmaf(q.z, k[j].z, fmaf(q.w, k[j].w, s[i][j]))));
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = unpair(s2[i][j]);
+        s[i][j] = x.x + x.y;
       }
-    }
     // a step that every row sees whole needs no masks
     const bool masked = tok0 + kStep > it.base || there != (1u << (kStep / kBlockTokens)) - 1u;
 #pragma unroll
@@ -138,9 +150,11 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
         // (a weight of -1: what lies there is not looked at)
         ps[r * L::kLP + tx + 16 * j] = sees[j >> 1] >> (tx + 16 * (j & 1)) & 1 ? w : -1.f;
       }
+      const uint64_t al2 = pair(al, al);
 #pragma unroll
       for (int m = 0; m < M; ++m)
-        acc[i][m] = make_float4(acc[i][m].x * al, acc[i][m].y * al, acc[i][m].z * al, acc[i][m].w * al);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[i][m][h] = mul2(acc[i][m][h], al2);
     }
     __syncwarp();   // (a row's weights come from its own half warp)
     auto weighted = [&](auto check) {
@@ -151,20 +165,26 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
         for (int i = 0; i < NR; ++i)
           w[i] = *reinterpret_cast<const float4 *>(ps + (ty + 16 * i) * L::kLP + u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
+          uint64_t x2[NR];
+          bool on[NR];
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const float x = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+            x2[i] = pair(x, x);
+            on[i] = !decltype(check)::value || !(x < 0.f);
+          }
 #pragma unroll
           for (int m = 0; m < M; ++m) {
-            const float4 v = *reinterpret_cast<const float4 *>(vs + (u + e) * LD + 4 * tx + 64 * m);
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(vs + (u + e) * LD + 4 * tx + 64 * m);
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-              const float x = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
-              if (decltype(check)::value && x < 0.f) continue;
-              acc[i][m].x = fmaf(x, v.x, acc[i][m].x);
-              acc[i][m].y = fmaf(x, v.y, acc[i][m].y);
-              acc[i][m].z = fmaf(x, v.z, acc[i][m].z);
-              acc[i][m].w = fmaf(x, v.w, acc[i][m].w);
+              if (!on[i]) continue;
+              acc[i][m][0] = fma2(x2[i], v.x, acc[i][m][0]);
+              acc[i][m][1] = fma2(x2[i], v.y, acc[i][m][1]);
             }
           }
+        }
       }
     };
     if (masked)
@@ -189,9 +209,11 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
     const float inv = whole ? tree_inverse(den, any) : den > 0.f ? 1.f / den : 0.f;
     float *to = whole ? static_cast<float *>(p.out) + at * D : p.part_o + part * D;
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-      *reinterpret_cast<float4 *>(to + 4 * tx + 64 * m) = make_float4(
-          acc[i][m].x * inv, acc[i][m].y * inv, acc[i][m].z * inv, acc[i][m].w * inv);
+    for (int m = 0; m < M; ++m) {
+      const float2 x = unpair(acc[i][m][0]), y = unpair(acc[i][m][1]);
+      *reinterpret_cast<float4 *>(to + 4 * tx + 64 * m) =
+          make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+    }
     if (tx == 0) {
       if (!whole)
         p.part_lse[part] = part_lse(mx[i], den);
@@ -234,16 +256,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   if (warp == kCompute / 32) {
     // ======================= items, K and V =======================
     int x = 0;   // steps so far
-    TreeItem first = {}, last = {};             // the cut items, and where they end
-    uint32_t first_end = 0, last_end = 0;
+    uint32_t cut = 0;   // slots that were written down
     bool ok = true;
     for (int i = 0; ok; ++i) {
       TreeItem w;
       const bool some = walk.next(&w);
-      if (some && !w.whole()) {   // (at most two of them)
-        (w.t0 == 0 ? last : first) = w;
-        (w.t0 == 0 ? last_end : first_end) = walk.at;
-      }
       ok = wait.warp(&i_empty[i % kQueue], (static_cast<uint32_t>(i / kQueue) & 1u) ^ 1u);
       if (!ok) break;
       if (lane == 0) {
@@ -268,20 +285,19 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
         const int st = x % kStages;
         ok = wait.warp(&empty[st], (static_cast<uint32_t>(x / kStages) & 1u) ^ 1u);
         if (!ok) break;
-        uint32_t there = 0, tokens = 0;
+        uint32_t bad = 0, tokens = 0;   // pages outside the pool
         bool on[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           on[h] = blk[h] >= 0 && blk[h] < p.num_blocks;
-          const uint32_t b = __ballot_sync(0xffffffffu, on[h]);
-          tokens += __popc(b);
-          there |= ((b & 0xffffu ? 1u : 0u) | (b >> 16 ? 2u : 0u)) << (2 * h);
-          if (!on[h] && t * kStep + lane + 32 * h < w.tokens) set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
+          tokens += __popc(__ballot_sync(0xffffffffu, on[h]));
+          const uint32_t b = __ballot_sync(0xffffffffu, !on[h] && t * kStep + lane + 32 * h < w.tokens);
+          bad |= ((b & 0xffffu ? 1u : 0u) | (b >> 16 ? 2u : 0u)) << (2 * h);
         }
         if (lane == 0) {
-          // pages behind the last token count as there (their tokens are masked by number)
-          const int pages = (w.tokens - t * kStep + kBlockTokens - 1) / kBlockTokens;
-          there_s[st] = static_cast<int>(there | (pages < 4 ? 0xfu & ~((1u << pages) - 1u) : 0u));
+          // (pages behind the last token count as there: their tokens are masked by number)
+          there_s[st] = static_cast<int>(~bad & 0xfu);
+          if (bad) set_dev_err(p.err, PKV_DEVERR_BAD_BLOCK);
           mbar_arrive_expect_tx(&full[st], tokens * 2 * D * 4);
         }
         __syncwarp();
@@ -296,11 +312,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
         }
         __syncwarp();
       }
+      if (!w.whole()) {   // (at most two of them)
+        cut |= w.t0 == 0 ? 2u : 1u;
+        if (lane == 0) p.cuts[w.slot(cta)] = walk.cut(w, walk.at);
+      }
     }
-    if (lane == 0) {
-      p.cuts[2 * cta] = first_end ? walk.cut(first, first_end) : TreeCut{};
-      p.cuts[2 * cta + 1] = last_end ? walk.cut(last, last_end) : TreeCut{};
-    }
+    if (lane < 2 && !(cut >> lane & 1u)) p.cuts[2 * cta + lane] = TreeCut{};
     // every copy has landed before the CTA ends (after a normal run they have)
     for (int n = max(0, x - kStages); n < x; ++n)
       mbar_wait_bounded(&full[n % kStages], static_cast<uint32_t>(n / kStages) & 1u, kDrainCycles);
@@ -308,15 +325,15 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
     int step = 0;
     for (int i = 0;; ++i) {
       if (!wait.warp(&i_full[i % kQueue], static_cast<uint32_t>(i / kQueue) & 1u)) break;
-      const Handed it = items[i % kQueue];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&i_empty[i % kQueue]);
+      const Handed &it = items[i % kQueue];   // (read again where it is used)
       if (it.t1 <= it.t0) break;
       const int rows = it.nodes * p.G;
       const bool ok = rows <= 16   ? compute_item<D, 1>(p, it, sm, full, empty, wait, &step)
                       : rows <= 32 ? compute_item<D, 2>(p, it, sm, full, empty, wait, &step)
                                    : compute_item<D, 4>(p, it, sm, full, empty, wait, &step);
       if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[i % kQueue]);
     }
   }
   __syncthreads();
@@ -325,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 
 template <int D, bool POLL>
 cudaError_t launch(const TreeParams &p, cudaStream_t s) {
-  constexpr int smem = Lay<D>::kFloats * 4;
+  constexpr int smem = Lay<D>::kBytes;
   auto kern = tree_f32_kernel<D, POLL>;
   static std::atomic<unsigned long long> attrs_set{0};
   cudaError_t e = set_attributes_once(attrs_set, [&] {
