@@ -13,9 +13,11 @@
 // permuted addresses took the products 10 to 20 % longer.)  Multiplications and additions
 // go two to an instruction (16 rows of 1000 tokens, 16 nodes, 32/8 heads of 128: 139 -> 128 us).
 //
-// Masks.  Steps that reach past the tokens every row sees mark what a row does not see with
-// a weight of -1 and skip it in the product with V: it may hold anything, the tail of a
-// last page and pages outside the pool included (they are not even loaded).
+// Masks.  Only steps that reach past the tokens every row sees look at mask bits.  What a row
+// does not see may hold anything, the tail of a last page and pages outside the pool
+// included (they are not even loaded): where one of those values is not finite (sums of
+// four that overflow count as such), what a row does not see gets a weight of -1 and is
+// skipped in the product with V instead of being multiplied by zero.
 //
 // Bound by the FMA and shared-memory pipes where rows are many, by the loads' latency where
 // they are few.
@@ -119,7 +121,17 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
         s[i][j] = x.x + x.y;
       }
     // a step that every row sees whole needs no masks
-    const bool masked = tok0 + kStep > it.base || there != (1u << (kStep / kBlockTokens)) - 1u;
+    const int special = it.base + (p.mask ? 0 : it.n0);
+    bool odd = there != (1u << (kStep / kBlockTokens)) - 1u;
+    const bool masked = tok0 + kStep > special || odd;
+    if (masked) {   // (every warp looks for itself: 16 tokens of 64 are 8 reads a lane)
+#pragma unroll 4
+      for (int e = max(special - tok0, 0) * (D / 4) + lane; e < kStep * (D / 4); e += 32) {
+        const float4 v = *reinterpret_cast<const float4 *>(vs + e / (D / 4) * LD + e % (D / 4) * 4);
+        odd |= !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY);
+      }
+      odd = __any_sync(0xffffffffu, odd);
+    }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int r = ty + 16 * i;
@@ -148,7 +160,8 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
         const float w = ex2(s[i][j] - mu);
         l[i] += w;
         // (a weight of -1: what lies there is not looked at)
-        ps[r * L::kLP + tx + 16 * j] = sees[j >> 1] >> (tx + 16 * (j & 1)) & 1 ? w : -1.f;
+        ps[r * L::kLP + tx + 16 * j] =
+            odd && !(sees[j >> 1] >> (tx + 16 * (j & 1)) & 1) ? -1.f : w;
       }
       const uint64_t al2 = pair(al, al);
 #pragma unroll
@@ -187,7 +200,7 @@ __device__ __forceinline__ bool compute_item(const TreeParams &p, const Handed &
         }
       }
     };
-    if (masked)
+    if (odd)
       weighted(std::true_type());
     else
       weighted(std::false_type());
