@@ -279,3 +279,18 @@ def test_steps_on_a_side_stream():
         got.append(outs)
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_readme_example_of_drafted_tokens_runs():
+    import os
+    import re
+    readme = os.path.join(os.path.dirname(os.path.dirname(__file__)), "README.md")
+    blocks = re.findall(r"```python\n(.*?)```", open(readme).read(), flags=re.S)
+    example, = [b for b in blocks if "DraftDecoder" in b]
+    scope = dict(torch=torch, np=np, binding=binding, dev=dev())
+    exec(compile(example, "readme example", "exec"), scope)
+    torch.cuda.synchronize()
+    dec, a, b = scope["dec"], scope["a"], scope["b"]
+    assert tuple(scope["out"].shape) == (9, 32, 128) and bool(scope["out"].float().isfinite().all())
+    assert dec.alloc.seq_len(a) == 703 and dec.alloc.seq_len(b) == 701 and dec.k_cache.shape[0] == 2048
+    assert dec.device_errors() == 0
