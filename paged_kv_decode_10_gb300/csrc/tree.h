@@ -74,10 +74,10 @@ __device__ __forceinline__ int tree_tokens(const TreeParams &p, int n, int len, 
 // Positions of one KV head of a row (0 for a row without nodes).  STEP: tokens of a step,
 // BOUND: what an item costs by itself.
 template <int STEP, int BOUND>
-__device__ __forceinline__ uint32_t tree_head_cost(const TreeParams &p, int n, int len) {
-  const uint32_t tiles = static_cast<uint32_t>(n + (1 << p.lg_nodes) - 1) >> p.lg_nodes;
-  if (p.mask) return tiles * (BOUND + (len + STEP - 1) / STEP);
-  uint32_t sum = tiles * BOUND;
+__device__ __forceinline__ unsigned long long tree_head_cost(const TreeParams &p, int n, int len) {
+  const uint32_t tiles = (static_cast<uint32_t>(n) + (1u << p.lg_nodes) - 1) >> p.lg_nodes;
+  if (p.mask) return static_cast<unsigned long long>(tiles) * (BOUND + (len + STEP - 1) / STEP);
+  unsigned long long sum = static_cast<unsigned long long>(tiles) * BOUND;
   for (uint32_t c = 1; c <= tiles; ++c)
     sum += (tree_tokens(p, n, len, static_cast<int>(c << p.lg_nodes)) + STEP - 1) / STEP;
   return sum;
@@ -86,7 +86,6 @@ __device__ __forceinline__ uint32_t tree_head_cost(const TreeParams &p, int n, i
 // The items of a CTA, in order.  (32 bits: a call of 2^31 positions and more is refused.)
 template <int STEP, int BOUND>
 struct TreeWalk {
-  const TreeParams &p;
   uint32_t at, lo, hi;           // position of the next item; this CTA's
   uint32_t all, ctas;            // of the whole call, CTAs with a share
   int cta;
@@ -94,7 +93,7 @@ struct TreeWalk {
   int s0, n, len;                // its row
   bool loaded;
 
-  __device__ __forceinline__ bool next(TreeItem *it) {
+  __device__ __forceinline__ bool next(const TreeParams &p, TreeItem *it) {
     const int per = 1 << p.lg_nodes;
     while (at < hi) {
       if (!loaded) {
@@ -106,7 +105,7 @@ struct TreeWalk {
         loaded = true;
         g = c = 0;
         if (at < lo) {   // (the first row: whole heads ahead of the CTA's share)
-          const uint32_t head = tree_head_cost<STEP, BOUND>(p, n, len);
+          const uint32_t head = static_cast<uint32_t>(tree_head_cost<STEP, BOUND>(p, n, len));
           while (g + 1 < p.Hkv && at + head <= lo) {
             at += head;
             ++g;
@@ -146,15 +145,65 @@ struct TreeWalk {
     return static_cast<int>((static_cast<unsigned long long>(x + 1) * ctas - 1) / all);
   }
   // What is to be written down of a cut item whose last step is ahead of position `end`.
-  __device__ __forceinline__ TreeCut cut(const TreeItem &it, uint32_t end) const {
+  __device__ __forceinline__ TreeCut cut(const TreeParams &p, const TreeItem &it, uint32_t end) const {
     const int from = owner(end - it.steps);
     return TreeCut{owner(end - 1) - from + 1, from, it.q0, it.nodes * p.G, it.g, it.base, it.n};
   }
 };
 
-// Where CTA `cta` of p.C begins, found by all NT threads of the CTA together from the
-// rows' lengths (rows that do not fit have no positions; CTA 0 reports them).
-// MIN: positions a CTA gets at least, while there are CTAs to spare.
+// A CTA's share of `sum` positions: floor(c all / ctas) by 32-bit divisions.  (The rest
+// dealt to the first CTAs, one each, instead of evenly, took 3 % longer.)  MIN: positions a CTA
+// gets at least, while there are CTAs to spare.
+template <int STEP, int BOUND, int MIN>
+__device__ __forceinline__ TreeWalk<STEP, BOUND> tree_share(const TreeParams &p, int cta,
+                                                            unsigned long long sum, bool bad) {
+  const bool fits = sum < 1ull << 31;
+  const uint32_t all = fits ? static_cast<uint32_t>(sum) : 0;
+  if (cta == 0 && (bad || !fits)) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
+  const uint32_t ctas = max(1u, min(all / MIN, static_cast<uint32_t>(p.C)));
+  const uint32_t share = all / ctas, rest = all - share * ctas;
+  const uint32_t c = min(static_cast<uint32_t>(cta), ctas), c1 = min(c + 1, ctas);
+  const uint32_t lo = c * share + c * rest / ctas, hi = c1 * share + c1 * rest / ctas;
+  return TreeWalk<STEP, BOUND>{hi, lo, hi, all, ctas, cta, p.B, 0, 0, 0, 0, 0, false};
+}
+template <int STEP, int BOUND>
+__device__ __forceinline__ unsigned long long tree_row_cost(const TreeParams &p, int b, bool *bad) {
+  int s0, n, len;
+  if (!tree_row(p, b, &s0, &n, &len)) {
+    *bad = true;
+    return 0;
+  }
+  return tree_head_cost<STEP, BOUND>(p, n, len) * p.Hkv;
+}
+__device__ __forceinline__ unsigned long long warp_sum_up(unsigned long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Where CTA `cta` of p.C begins, from the rows' lengths (rows that do not fit have no
+// positions; CTA 0 reports them): found by one warp, for batches of at most 32 rows ...
+constexpr int kWarpRows = 32;
+template <int STEP, int BOUND, int MIN>
+__device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin_warp(const TreeParams &p, int cta) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  const unsigned long long mine = lane < p.B ? tree_row_cost<STEP, BOUND>(p, lane, &bad) : 0;
+  const unsigned long long incl = warp_sum_up(mine, lane);
+  auto walk = tree_share<STEP, BOUND, MIN>(p, cta, __shfl_sync(0xffffffffu, incl, 31),
+                                           __any_sync(0xffffffffu, bad));
+  const uint32_t row =   // the lane that has the first position
+      __ballot_sync(0xffffffffu, walk.lo < walk.hi && incl - mine <= walk.lo && walk.lo < incl);
+  if (row) {
+    walk.b = __ffs(row) - 1;
+    walk.at = static_cast<uint32_t>(__shfl_sync(0xffffffffu, incl - mine, walk.b));
+  }
+  return walk;
+}
+// ... or by all NT threads of the CTA together.
 template <int STEP, int BOUND, int MIN, int NT>
 __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p, int cta) {
   __shared__ unsigned long long sums[NT / 32];
@@ -164,20 +213,10 @@ __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p,
   const int b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
   unsigned long long mine = 0;
   bool bad = false;
-  uint32_t cost = 0;   // of the thread's last row
-  for (int b = b0; b < b1; ++b) {
-    int s0, n, len;
-    const bool fits = tree_row(p, b, &s0, &n, &len);
-    bad |= !fits;
-    cost = fits ? tree_head_cost<STEP, BOUND>(p, n, len) : 0;
-    mine += static_cast<unsigned long long>(cost) * p.Hkv;
-  }
-  unsigned long long incl = mine;   // positions up to this thread's rows, them included
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
+  for (int b = b0; b < b1; ++b) mine += tree_row_cost<STEP, BOUND>(p, b, &bad);
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && cta == 0 && lane == 0) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
+  const unsigned long long incl = warp_sum_up(mine, lane);
   if (lane == 31) sums[warp] = incl;
   if (tid == 0) start[0] = p.B;
   __syncthreads();
@@ -187,32 +226,22 @@ __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p,
     if (w < warp) before += sums[w];
     sum += sums[w];
   }
-  const bool fits = sum < 1ull << 31;
-  const uint32_t all = fits ? static_cast<uint32_t>(sum) : 0;
-  if (cta == 0 && (bad || !fits)) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
-  const uint32_t ctas = max(1u, min(all / MIN, static_cast<uint32_t>(p.C)));
-  // floor(c all / ctas) by 32-bit divisions.  (The rest dealt to the first CTAs, one each,
-  // instead of evenly, took 3 % longer.)
-  const uint32_t share = all / ctas, rest = all - share * ctas;
-  const uint32_t c = min(static_cast<uint32_t>(cta), ctas), c1 = min(c + 1, ctas);
-  const uint32_t lo = c * share + c * rest / ctas, hi = c1 * share + c1 * rest / ctas;
-  uint32_t at = static_cast<uint32_t>(before + incl - mine);
-  if (lo < hi && at <= lo && lo < at + mine) {   // one thread has the row
+  auto walk = tree_share<STEP, BOUND, MIN>(p, cta, sum, false);
+  unsigned long long at = before + incl - mine;
+  if (walk.lo < walk.hi && at <= walk.lo && walk.lo < at + mine) {   // one thread has the row
     int b = b0;
     for (; b + 1 < b1; ++b) {   // (more rows than threads)
-      int s0, n, len;
-      const uint32_t rows =
-          tree_row(p, b, &s0, &n, &len) ? tree_head_cost<STEP, BOUND>(p, n, len) * p.Hkv : 0;
-      if (lo < at + rows) break;
+      const unsigned long long rows = tree_row_cost<STEP, BOUND>(p, b, &bad);
+      if (walk.lo < at + rows) break;
       at += rows;
     }
     start[0] = b;
     start[1] = static_cast<int>(at);
   }
   __syncthreads();
-  const int row = start[0];
-  return TreeWalk<STEP, BOUND>{p,   row < p.B ? static_cast<uint32_t>(start[1]) : hi, lo, hi, all, ctas,
-                               cta, row, 0, 0, 0, 0, 0, false};
+  walk.b = start[0];
+  if (walk.b < p.B) walk.at = static_cast<uint32_t>(start[1]);
+  return walk;
 }
 
 // 32 visibility bits of a query row: tokens tok .. tok + 31 of its row, bit j for token
@@ -263,7 +292,7 @@ __device__ __noinline__ void tree_all_nan(const TreeParams &p) {
   auto walk = tree_begin<STEP, BOUND, MIN, NT>(p, cta);
   TreeItem it;
   const float nan = __int_as_float(0x7fffffff);
-  while (walk.next(&it))
+  while (walk.next(p, &it))
     for (int e = threadIdx.x; e < it.nodes * p.G; e += NT) {
       if (!it.whole()) {   // (the join makes NaN of it)
         p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;

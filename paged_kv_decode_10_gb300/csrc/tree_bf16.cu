@@ -244,7 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int cta = blockIdx.x;
-  Walk walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+  // (few rows: warp 8 finds its share by itself, while nobody waits for it)
+  Walk walk = {};
+  if (p.B > kWarpRows)
+    walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(static_cast<uint32_t>(misc[1]));
   // (by arithmetic: arrays indexed by the slot would live in local memory)
@@ -277,13 +282,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       TreeItem first = {}, last = {};             // the cut items, and where they end
       uint32_t first_end = 0, last_end = 0;
       bool ok = true;
+      if (!is_v && p.B <= kWarpRows) walk = tree_begin_warp<kTile, kBoundary, kMin>(p, cta);
       for (int i = 0; ok; ++i) {
         Handed it;
         if (is_v) {
           if (!take(i, &it)) break;
         } else {
           TreeItem w;
-          const bool some = walk.next(&w);
+          const bool some = walk.next(p, &w);
           if (some) {
             if (!w.whole()) {   // (at most two of them)
               (w.t0 == 0 ? last : first) = w;
@@ -367,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && !is_v) {
-        p.cuts[2 * cta] = first_end ? walk.cut(first, first_end) : TreeCut{};
-        p.cuts[2 * cta + 1] = last_end ? walk.cut(last, last_end) : TreeCut{};
+        p.cuts[2 * cta] = first_end ? walk.cut(p, first, first_end) : TreeCut{};
+        p.cuts[2 * cta + 1] = last_end ? walk.cut(p, last, last_end) : TreeCut{};
       }
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, x - NS); n < x; ++n)

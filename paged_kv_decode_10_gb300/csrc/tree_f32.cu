@@ -264,16 +264,22 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   pdl_wait();
   pdl_launch_dependents();   // (after the wait: what starts then may read what was there before)
   const int cta = blockIdx.x;
-  auto walk = tree_begin<kStep, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+  // (few rows: the loading warp finds its share by itself)
+  TreeWalk<kStep, kBoundary> walk = {};
+  if (p.B > kWarpRows)
+    walk = tree_begin<kStep, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+  else
+    __syncthreads();
   const Waiter<POLL> wait{gave_up, p.err, p.wait_limit};
   if (warp == kCompute / 32) {
     // ======================= items, K and V =======================
+    if (p.B <= kWarpRows) walk = tree_begin_warp<kStep, kBoundary, kMin>(p, cta);
     int x = 0;   // steps so far
     uint32_t cut = 0;   // slots that were written down
     bool ok = true;
     for (int i = 0; ok; ++i) {
       TreeItem w;
-      const bool some = walk.next(&w);
+      const bool some = walk.next(p, &w);
       ok = wait.warp(&i_empty[i % kQueue], (static_cast<uint32_t>(i / kQueue) & 1u) ^ 1u);
       if (!ok) break;
       if (lane == 0) {
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       }
       if (!w.whole()) {   // (at most two of them)
         cut |= w.t0 == 0 ? 2u : 1u;
-        if (lane == 0) p.cuts[w.slot(cta)] = walk.cut(w, walk.at);
+        if (lane == 0) p.cuts[w.slot(cta)] = walk.cut(p, w, walk.at);
       }
     }
     if (lane < 2 && !(cut >> lane & 1u)) p.cuts[2 * cta + lane] = TreeCut{};
