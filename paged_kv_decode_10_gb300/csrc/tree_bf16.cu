@@ -31,8 +31,7 @@
 //
 // The code is kept short: rare paths are functions of their own, the rows' output is written
 // in a loop.  A first form of 150 KB (two slots merged at the end of every item, everything
-// unrolled) spent 8 us an item on instructions that were not in the cache and on stores of
-// one row a lane.
+// unrolled) spent 8 us an item, mostly on instructions that were not in the cache.
 #include "tensor_core.cuh"
 #include "tree.h"
 
@@ -62,8 +61,7 @@ struct Lay {
   static constexpr int kQ = 0;                            // [2] tiles, one per slot
   static constexpr int kK = 2 * kMat;                     // [NS]
   static constexpr int kV = kK + NS * kMat;               // [NS]
-  static constexpr int kOut = kV + NS * kMat;             // [8 warps] 32 rows of 128 bytes
-  static constexpr int kItems = kOut + 8 * 32 * 128;      // [kQueue] 64 bytes
+  static constexpr int kItems = kV + NS * kMat;           // [kQueue] 64 bytes
   static constexpr int kBars = kItems + kQueue * 64;
   static constexpr int kNumBars = 4 * NS + 2 * kQueue + 16;
   static constexpr int kBad = kBars + kNumBars * 8;       // [kBadRing] pages outside the pool
@@ -528,7 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sS = tS(m) + lanes, sO = tO(m) + lanes;
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);
     const int lg = p.lg_g;
-    unsigned char *stage = smem + L::kOut + warp * (32 * 128);
     int x = 0;
     uint32_t s_ph = 0, o_ph = 0;
     auto arrive = [&](uint64_t *bar) {   // for the warp, after all of its lanes
@@ -648,8 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(&i_empty[i % kQueue]);
         continue;
       }
-      // ---- results: rows go through shared memory, so that neighbouring lanes write
-      // neighbouring bytes ----
+      // ---- results: a lane writes its row, whole 32-byte sectors at a time ----
       const bool whole = it.part < 0, on = row0 + lane < total;
       auto out_at = [&](int row) {   // of the outputs [T, Hq]
         return static_cast<size_t>(it.q0 + (row >> lg)) * p.Hq + it.g * p.G + (row & (p.G - 1));
@@ -665,63 +661,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.part_lse[part0 + row0 + lane] = part_lse(mx, l);
         }
       }
-      // 32 columns at a time; a row's 16-byte pieces lie permuted within 128 bytes
-      auto piece = [&](int row, int e) {
-        return reinterpret_cast<uint4 *>(stage + row * 128 + ((e ^ (row & 7)) << 4));
-      };
-      auto columns = [&](int q, float *o) {
+      unsigned char *to =
+          whole ? static_cast<unsigned char *>(p.out) + out_at(min(row0 + lane, total - 1)) * (D * 2)
+                : reinterpret_cast<unsigned char *>(p.part_o + (part0 + row0 + lane) * D);
+      const bool sectors = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
         __syncwarp();
         tm_ld32(sO + 32 * q, o);
         tm_wait_ld();
         pin32(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] *= inv;
-      };
-      if (whole) {   // 4 pieces a row: the warp writes 8 rows at once
-        __nv_bfloat16 *to[4];
+        if (!on) continue;   // (the warp meets again ahead of the next load)
+        if (!whole) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          to[k] = static_cast<__nv_bfloat16 *>(p.out) +
-                  out_at(min(row0 + 8 * k + (lane >> 2), total - 1)) * D + 8 * (lane & 3);
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          columns(q, o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *piece(lane, e) =
-                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (row0 + 8 * k + (lane >> 2) < total)
-              *reinterpret_cast<uint4 *>(to[k] + 32 * q) = *piece(8 * k + (lane >> 2), lane & 3);
+          for (int e = 0; e < 32; e += 8) store8(reinterpret_cast<float *>(to) + 32 * q + e, o + e);
+          continue;
         }
-      } else {   // 8 pieces a row: 4 rows at once
-        float *to = p.part_o + (part0 + row0 + (lane >> 3)) * D + 4 * (lane & 7);
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          columns(q, o);
+        uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4 *>(piece(lane, e)) =
-                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          __syncwarp();
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
+        if (sectors) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (row0 + 4 * k + (lane >> 3) < total)
-              *reinterpret_cast<uint4 *>(to + 4 * k * D + 32 * q) = *piece(4 * k + (lane >> 3), lane & 7);
+          for (int e = 0; e < 16; e += 8)
+            store8(reinterpret_cast<float *>(to + 64 * q) + e, reinterpret_cast<const float *>(w) + e);
+        } else {   // (outputs need not be aligned to more than 16 bytes)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4 *>(to + 64 * q + 4 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         }
       }
       __syncwarp();
       if (misc[2 + i % kOddRing] == i + 1 && on)
-        add_odd_values<D>(p, it, node,
-                          whole ? static_cast<void *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                      out_at(row0 + lane) * D)
-                                : static_cast<void *>(p.part_o + (part0 + row0 + lane) * D),
-                          !whole);
+        add_odd_values<D>(p, it, node, to, !whole);
       arrive(&i_empty[i % kQueue]);
     }
     tc_fence_before();

@@ -359,3 +359,21 @@ def test_many_items_of_many_steps_to_a_cta(d, Hkv, kind):
         again, _ = c.run()
         assert torch.equal(first, again)
     c.check(first, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tensors_aligned_to_16_bytes(dtype):
+    """Queries and outputs that begin 16 bytes into a buffer."""
+    c = Case([100, 7, 900], [12, 5, 70], 8, 2, 128, dtype, "tree", seed=9)
+    want = c.run()[0]
+    skip = 16 // c.q.element_size()
+    buf = torch.empty(2, c.q.numel() + 2 * skip, dtype=c.q.dtype, device=dev())
+    q, out = (b[skip:skip + c.q.numel()].view(c.q.shape) for b in buf)
+    q.copy_(c.q)
+    buf[1] = 7.0
+    assert out.data_ptr() % 32 == 16 or q.data_ptr() % 32 == 16
+    c.q = q
+    binding.decode_attn_tree_args(c.args(out))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert (buf[1, :skip] == 7.0).all() and (buf[1, -skip:] == 7.0).all()
