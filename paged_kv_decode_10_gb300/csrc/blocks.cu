@@ -11,21 +11,26 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+// Pools that a small call has room for: the parameters of a call of 256 pools, 2 to 4 KB, are
+// handed over at every launch.
+constexpr int kFewPools = 8;
 
 // ---- whole blocks ---------------------------------------------------------------
 // A CTA copies one chunk of one block of one pool: kWide 16-byte pieces a thread, all
 // read before the first is written.  Bound by memory.
+template <int POOLS>
 struct CopyParams {
   const int32_t *src_blocks, *dst_blocks;
   int32_t *err;
   int n, src_num, dst_num, chunks;
   long long pieces;                    // of 16 bytes, a block
-  const uint4 *src[PKV_MAX_POOLS];
-  uint4 *dst[PKV_MAX_POOLS];
+  const uint4 *src[POOLS];
+  uint4 *dst[POOLS];
 };
 
-template <int WIDE>
-__global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const __grid_constant__ CopyParams p) {
+template <int WIDE, int POOLS>
+__global__ void __launch_bounds__(kThreads)
+    copy_blocks_kernel(const __grid_constant__ CopyParams<POOLS> p) {
   pdl_wait();
   const unsigned u = blockIdx.x / static_cast<unsigned>(p.chunks);
   const int chunk = static_cast<int>(blockIdx.x - u * p.chunks);
@@ -55,16 +60,19 @@ __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const __grid_cons
 // thread that owns one 16-byte column of one head of one pool needs nobody else for
 // that.  A CTA serves kThreads columns of one row at a time; it checks the row first (every
 // CTA of a row comes to the same answer) and lists its moves in shared memory.
+template <int POOLS>
 struct AcceptParams {
   const int32_t *block_tables, *seq_lens, *node_starts, *path, *accept_lens;
   int32_t *err;
   int B, T, Hkv, cols, num_blocks, bt_stride, path_stride, n_pools, chunks;   // cols: 16-byte columns of a head
-  uint4 *pool[PKV_MAX_POOLS];
+  uint4 *pool[POOLS];
 };
 constexpr int kMoves = 256;   // listed at a time
 constexpr int kFlight = 8;    // tokens a thread reads before it writes them
 
-__global__ void __launch_bounds__(kThreads) tree_accept_kernel(const __grid_constant__ AcceptParams p) {
+template <int POOLS>
+__global__ void __launch_bounds__(kThreads)
+    tree_accept_kernel(const __grid_constant__ AcceptParams<POOLS> p) {
   __shared__ int from_s[kMoves], to_s[kMoves];   // block * 16 + token in it
   pdl_wait();
   const int tid = threadIdx.x;
@@ -151,24 +159,9 @@ bool written_overlap(Span *spans, int n) {
   return false;
 }
 
-}  // namespace
-}  // namespace pkv
-
-using namespace pkv;
-
-extern "C" int pkv_copy_blocks(const pkv_copy_args *a, void *stream) {
-  clear_error();
-  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "args is NULL");
-  PKV_REQUIRE(a->n >= 0 && a->n_pools >= 0, PKV_ERR_INVALID_ARG, "negative size");
-  PKV_REQUIRE(a->n_pools <= PKV_MAX_POOLS, PKV_ERR_UNSUPPORTED, "%d pools > %d", a->n_pools,
-              PKV_MAX_POOLS);
-  if (a->n == 0 || a->n_pools == 0) return PKV_OK;
-  PKV_REQUIRE(a->src && a->dst && a->src_blocks && a->dst_blocks, PKV_ERR_INVALID_ARG, "NULL pointer");
-  PKV_REQUIRE(a->src_num_blocks > 0 && a->dst_num_blocks > 0, PKV_ERR_INVALID_ARG,
-              "pools must have blocks");
-  PKV_REQUIRE(a->block_bytes > 0 && a->block_bytes % 16 == 0, PKV_ERR_INVALID_ARG,
-              "block_bytes %lld must be a positive multiple of 16", (long long)a->block_bytes);
-  CopyParams p;
+template <int POOLS>
+int copy_blocks(const pkv_copy_args *a, void *stream) {
+  CopyParams<POOLS> p;
   for (int i = 0; i < a->n_pools; ++i) {
     PKV_REQUIRE(a->src[i] && a->dst[i], PKV_ERR_INVALID_ARG, "pool %d is NULL", i);
     PKV_REQUIRE(((reinterpret_cast<uintptr_t>(a->src[i]) | reinterpret_cast<uintptr_t>(a->dst[i])) &
@@ -179,7 +172,7 @@ extern "C" int pkv_copy_blocks(const pkv_copy_args *a, void *stream) {
   }
   const long long src_bytes = a->src_num_blocks * a->block_bytes,
                   dst_bytes = a->dst_num_blocks * a->block_bytes;
-  Span spans[2 * PKV_MAX_POOLS];
+  Span spans[2 * POOLS];
   int n_spans = 0;
   for (int i = 0; i < a->n_pools; ++i) {
     spans[n_spans++] = Span{reinterpret_cast<uintptr_t>(a->dst[i]), dst_bytes, true};
@@ -204,36 +197,16 @@ extern "C" int pkv_copy_blocks(const pkv_copy_args *a, void *stream) {
   p.chunks = static_cast<int>(chunks);
   const unsigned grid = static_cast<unsigned>(blocks * chunks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = wide == 8 ? launch_waiting(copy_blocks_kernel<8>, grid, kThreads, 0, s, p)
-                                  : launch_waiting(copy_blocks_kernel<2>, grid, kThreads, 0, s, p);
+  const cudaError_t e = wide == 8 ? launch_waiting(copy_blocks_kernel<8, POOLS>, grid, kThreads, 0, s, p)
+                                  : launch_waiting(copy_blocks_kernel<2, POOLS>, grid, kThreads, 0, s, p);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "copy_blocks launch: %s", cudaGetErrorString(e));
   return PKV_OK;
 }
 
-extern "C" int pkv_tree_accept(const pkv_accept_args *a, void *stream) {
-  clear_error();
-  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "args is NULL");
-  PKV_REQUIRE(a->B >= 0 && a->T >= 0 && a->n_pools >= 0, PKV_ERR_INVALID_ARG, "negative size");
-  PKV_REQUIRE(a->B <= 65536, PKV_ERR_UNSUPPORTED, "B %d > 65536", a->B);
-  PKV_REQUIRE(a->n_pools <= PKV_MAX_POOLS, PKV_ERR_UNSUPPORTED, "%d pools > %d", a->n_pools,
-              PKV_MAX_POOLS);
-  PKV_REQUIRE(dtype_ok(a->dtype), PKV_ERR_UNSUPPORTED, "dtype %d", a->dtype);
-  if (a->B == 0 || a->n_pools == 0) return PKV_OK;
-  PKV_REQUIRE(a->pools && a->block_tables && a->seq_lens && a->node_starts && a->path &&
-                  a->accept_lens,
-              PKV_ERR_INVALID_ARG, "NULL pointer");
-  PKV_REQUIRE(a->Hkv > 0 && a->d > 0, PKV_ERR_INVALID_ARG, "non-positive size");
-  PKV_REQUIRE(a->num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
-  PKV_REQUIRE(static_cast<long long>(a->num_blocks) * kBlockTokens < (1ll << 31), PKV_ERR_UNSUPPORTED,
-              "pool too large for 32-bit slots");
-  PKV_REQUIRE(a->bt_stride > 0 && a->bt_stride < (1 << 26), PKV_ERR_INVALID_ARG, "bt_stride %d",
-              a->bt_stride);
-  PKV_REQUIRE(a->path_stride > 0, PKV_ERR_INVALID_ARG, "path_stride %d", a->path_stride);
-  const long long head = static_cast<long long>(a->d) * static_cast<long long>(dtype_size(a->dtype));
-  PKV_REQUIRE(head % 16 == 0, PKV_ERR_UNSUPPORTED, "a head of %lld bytes is no multiple of 16", head);
-  PKV_REQUIRE(a->Hkv * (head / 16) <= (1 << 20), PKV_ERR_UNSUPPORTED, "too many heads");
-  AcceptParams p;
-  Span spans[PKV_MAX_POOLS];
+template <int POOLS>
+int tree_accept(const pkv_accept_args *a, long long head, void *stream) {
+  AcceptParams<POOLS> p;
+  Span spans[POOLS];
   const long long bytes = a->num_blocks * kBlockTokens * head * a->Hkv;
   for (int i = 0; i < a->n_pools; ++i) {
     PKV_REQUIRE(a->pools[i] && (reinterpret_cast<uintptr_t>(a->pools[i]) & 15) == 0,
@@ -263,7 +236,56 @@ extern "C" int pkv_tree_accept(const pkv_accept_args *a, void *stream) {
   p.chunks = static_cast<int>(pieces < most ? pieces : most);
   const unsigned grid = static_cast<unsigned>(p.chunks) * a->B;
   const cudaError_t e =
-      launch_waiting(tree_accept_kernel, grid, kThreads, 0, static_cast<cudaStream_t>(stream), p);
+      launch_waiting(tree_accept_kernel<POOLS>, grid, kThreads, 0, static_cast<cudaStream_t>(stream), p);
   PKV_REQUIRE(e == cudaSuccess, PKV_ERR_CUDA, "tree_accept launch: %s", cudaGetErrorString(e));
   return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int pkv_copy_blocks(const pkv_copy_args *a, void *stream) {
+  clear_error();
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "args is NULL");
+  PKV_REQUIRE(a->n >= 0 && a->n_pools >= 0, PKV_ERR_INVALID_ARG, "negative size");
+  PKV_REQUIRE(a->n_pools <= PKV_MAX_POOLS, PKV_ERR_UNSUPPORTED, "%d pools > %d", a->n_pools,
+              PKV_MAX_POOLS);
+  if (a->n == 0 || a->n_pools == 0) return PKV_OK;
+  PKV_REQUIRE(a->src && a->dst && a->src_blocks && a->dst_blocks, PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(a->src_num_blocks > 0 && a->dst_num_blocks > 0, PKV_ERR_INVALID_ARG,
+              "pools must have blocks");
+  PKV_REQUIRE(a->block_bytes > 0 && a->block_bytes % 16 == 0 && a->block_bytes < (1ll << 31),
+              PKV_ERR_INVALID_ARG, "block_bytes %lld must be a positive multiple of 16 below 2^31",
+              (long long)a->block_bytes);
+  PKV_REQUIRE(static_cast<long long>(a->n) * a->n_pools < (1ll << 31), PKV_ERR_UNSUPPORTED,
+              "too many blocks for one call");
+  return a->n_pools <= kFewPools ? copy_blocks<kFewPools>(a, stream) : copy_blocks<PKV_MAX_POOLS>(a, stream);
+}
+
+extern "C" int pkv_tree_accept(const pkv_accept_args *a, void *stream) {
+  clear_error();
+  PKV_REQUIRE(a, PKV_ERR_INVALID_ARG, "args is NULL");
+  PKV_REQUIRE(a->B >= 0 && a->T >= 0 && a->n_pools >= 0, PKV_ERR_INVALID_ARG, "negative size");
+  PKV_REQUIRE(a->B <= 65536, PKV_ERR_UNSUPPORTED, "B %d > 65536", a->B);
+  PKV_REQUIRE(a->n_pools <= PKV_MAX_POOLS, PKV_ERR_UNSUPPORTED, "%d pools > %d", a->n_pools,
+              PKV_MAX_POOLS);
+  PKV_REQUIRE(dtype_ok(a->dtype), PKV_ERR_UNSUPPORTED, "dtype %d", a->dtype);
+  if (a->B == 0 || a->n_pools == 0) return PKV_OK;
+  PKV_REQUIRE(a->pools && a->block_tables && a->seq_lens && a->node_starts && a->path &&
+                  a->accept_lens,
+              PKV_ERR_INVALID_ARG, "NULL pointer");
+  PKV_REQUIRE(a->Hkv > 0 && a->d > 0, PKV_ERR_INVALID_ARG, "non-positive size");
+  PKV_REQUIRE(a->num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
+  PKV_REQUIRE(static_cast<long long>(a->num_blocks) * kBlockTokens < (1ll << 31), PKV_ERR_UNSUPPORTED,
+              "pool too large for 32-bit slots");
+  PKV_REQUIRE(a->bt_stride > 0 && a->bt_stride < (1 << 26), PKV_ERR_INVALID_ARG, "bt_stride %d",
+              a->bt_stride);
+  PKV_REQUIRE(a->path_stride > 0, PKV_ERR_INVALID_ARG, "path_stride %d", a->path_stride);
+  const long long head = static_cast<long long>(a->d) * static_cast<long long>(dtype_size(a->dtype));
+  PKV_REQUIRE(head % 16 == 0, PKV_ERR_UNSUPPORTED, "a head of %lld bytes is no multiple of 16", head);
+  PKV_REQUIRE(a->Hkv * (head / 16) <= (1 << 20), PKV_ERR_UNSUPPORTED, "too many heads");
+  return a->n_pools <= kFewPools ? tree_accept<kFewPools>(a, head, stream)
+                                 : tree_accept<PKV_MAX_POOLS>(a, head, stream);
 }

@@ -349,7 +349,7 @@ def pointers(bind, *values):
 
 @pytest.mark.parametrize("bad", [
     dict(n=-1), dict(n_pools=-1), dict(n_pools=257), dict(src_blocks=None), dict(dst_blocks=None),
-    dict(block_bytes=0), dict(block_bytes=24), dict(src_num_blocks=0), dict(dst_num_blocks=0),
+    dict(block_bytes=0), dict(block_bytes=24), dict(block_bytes=1 << 31), dict(n=2**31 - 1), dict(src_num_blocks=0), dict(dst_num_blocks=0),
     dict(dst=(1 << 20, 0)), dict(dst=(1 << 20, (1 << 21) + 8)), dict(dst=(1 << 20, 1 << 20)),
     dict(dst=(1 << 20, (1 << 20) + 64)), dict(dst=((1 << 21) + 64, 1 << 23)), dict(src=None), dict(dst=None)])
 def test_copy_call_refuses(bind, bad):
