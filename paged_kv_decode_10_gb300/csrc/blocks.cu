@@ -64,7 +64,8 @@ template <int POOLS>
 struct AcceptParams {
   const int32_t *block_tables, *seq_lens, *node_starts, *path, *accept_lens;
   int32_t *err;
-  int B, T, Hkv, cols, num_blocks, bt_stride, path_stride, n_pools, chunks;   // cols: 16-byte columns of a head
+  int B, T, Hkv, num_blocks, bt_stride, path_stride, n_pools, chunks;
+  unsigned cols;                       // of 16 bytes, a head
   uint4 *pool[POOLS];
 };
 constexpr int kMoves = 256;   // listed at a time
@@ -73,7 +74,7 @@ constexpr int kFlight = 8;    // tokens a thread reads before it writes them
 template <int POOLS>
 __global__ void __launch_bounds__(kThreads)
     tree_accept_kernel(const __grid_constant__ AcceptParams<POOLS> p) {
-  __shared__ int from_s[kMoves], to_s[kMoves];   // block * 16 + token in it
+  __shared__ long long from_s[kMoves], to_s[kMoves];   // offsets in a pool, of head 0's column 0
   pdl_wait();
   const int tid = threadIdx.x;
   const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.chunks));
@@ -105,35 +106,32 @@ __global__ void __launch_bounds__(kThreads)
     if (tid == 0) set_dev_err(p.err, bad ? PKV_DEVERR_BAD_LEN : PKV_DEVERR_BAD_BLOCK);
     return;
   }
-  const int per_pool = p.Hkv * p.cols;
-  const long long items = static_cast<long long>(per_pool) * p.n_pools;
+  auto offset = [&](int slot) {   // [num_blocks, Hkv, 16, cols]
+    return (static_cast<long long>(slot / kBlockTokens) * p.Hkv * kBlockTokens + slot % kBlockTokens) *
+           p.cols;
+  };
+  const unsigned per_pool = static_cast<unsigned>(p.Hkv * p.cols), items = per_pool * p.n_pools;
   for (int j0 = 0; j0 < a; j0 += kMoves) {
     const int m = min(kMoves, a - j0);
     if (j0) __syncthreads();
     if (tid < m) {
-      const int i = path[j0 + tid];
-      from_s[tid] = i == j0 + tid ? -1 : slot(base + i);   // (-1: stays where it is)
-      to_s[tid] = i == j0 + tid ? -1 : slot(base + j0 + tid);
+      const int j = j0 + tid, i = path[j];
+      from_s[tid] = i == j ? -1 : offset(slot(base + i));   // (-1: stays where it is)
+      to_s[tid] = i == j ? -1 : offset(slot(base + j));
     }
     __syncthreads();
-    for (long long item = static_cast<long long>(chunk) * kThreads + tid; item < items;
-         item += static_cast<long long>(p.chunks) * kThreads) {
-      const int pool = static_cast<int>(item / per_pool);
-      const int r = static_cast<int>(item - static_cast<long long>(pool) * per_pool);
-      const int h = r / p.cols, c = r - h * p.cols;
-      uint4 *mine = p.pool[pool] + c;
-      auto at = [&](int slot) {   // [num_blocks, Hkv, 16, cols]
-        return (static_cast<size_t>(slot / kBlockTokens) * p.Hkv + h) * (kBlockTokens * p.cols) +
-               (slot % kBlockTokens) * p.cols;
-      };
+    for (unsigned item = chunk * kThreads + tid; item < items; item += p.chunks * kThreads) {
+      const unsigned pool = item / per_pool, r = item - pool * per_pool;
+      const unsigned h = r / p.cols, c = r - h * p.cols;
+      uint4 *mine = p.pool[pool] + static_cast<size_t>(h) * (kBlockTokens * p.cols) + c;
       for (int j = 0; j < m; j += kFlight) {
         uint4 v[kFlight];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k)
-          if (j + k < m && from_s[j + k] >= 0) v[k] = mine[at(from_s[j + k])];
+          if (j + k < m && from_s[j + k] >= 0) v[k] = mine[from_s[j + k]];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k)
-          if (j + k < m && from_s[j + k] >= 0) mine[at(to_s[j + k])] = v[k];
+          if (j + k < m && from_s[j + k] >= 0) mine[to_s[j + k]] = v[k];
       }
     }
   }
@@ -224,12 +222,12 @@ int tree_accept(const pkv_accept_args *a, long long head, void *stream) {
   p.B = a->B;
   p.T = a->T;
   p.Hkv = a->Hkv;
-  p.cols = static_cast<int>(head / 16);
+  p.cols = static_cast<unsigned>(head / 16);
   p.num_blocks = a->num_blocks;
   p.bt_stride = a->bt_stride;
   p.path_stride = a->path_stride;
   p.n_pools = a->n_pools;
-  const long long items = static_cast<long long>(a->Hkv) * p.cols * a->n_pools;
+  const long long items = static_cast<long long>(a->Hkv) * p.cols * a->n_pools;   // below 2^28
   // As many CTAs as there are pieces of kThreads columns, but no more than fit on the GPU
   // at once: looking the row over takes a CTA longer than a piece's moves.
   const long long pieces = (items + kThreads - 1) / kThreads, most = a->B < 1216 ? 1216 / a->B : 1;
