@@ -231,7 +231,8 @@ int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B, const int
  * what to copy (pkv_copy_blocks, in every layer), sequences in the order of their ids,
  * blocks in table order; the rest of the free list keeps its order.  Then tables hold the
  * new ids.  All or nothing: PKV_ERR_OUT_OF_BLOCKS if more blocks are in use than num_blocks,
- * PKV_ERR_INVALID_ARG if cap is too small (*n is then what it must be). */
+ * PKV_ERR_INVALID_ARG if cap is too small (*n is then what it must be).  Not for an allocator
+ * that a pkv_server manages (its captured steps name the caches). */
 int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst, int32_t cap,
                      int32_t *n);
 /* Sequences that a block belongs to (0: it is free). */

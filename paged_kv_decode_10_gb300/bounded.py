@@ -67,6 +67,8 @@ class BoundedDecoder(PagedDecoder):
         self.rotary = binding.Rotary(d, base=self.rope_base) if rotary is None else rotary
         if self.rotary.d != d:
             raise ValueError(f"rotary was made for heads of {self.rotary.d}, not {d}")
+        if self.rotary.axes is not None:
+            raise ValueError("rotary has sections: positions have one axis here")
         self.decay = float(decay)
         self.masses = torch.zeros((self.n_layers, num_blocks, Hkv, binding.BLOCK_SIZE),
                                   device=self.device)

@@ -56,10 +56,11 @@ struct TreeItem {
   __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (t0 == 0 ? 1 : 0); }
 };
 
-// Nodes and length of a row; false where they do not fit the call.
+// Nodes and length of a row; false where they do not fit the call.  (Plain loads: constant
+// ones, which depend on nothing, might be moved ahead of the wait for the grid before.)
 __device__ __forceinline__ bool tree_row(const TreeParams &p, int b, int *s0, int *n, int *len) {
-  const int a = __ldg(p.starts + b), e = __ldg(p.starts + b + 1);
-  *len = __ldg(p.lens + b);
+  const int a = p.starts[b], e = p.starts[b + 1];
+  *len = p.lens[b];
   *s0 = a;
   *n = e - a;
   return a >= 0 && e >= a && e <= p.T && *len >= *n && *len <= 16ll * p.bt_stride &&
@@ -81,6 +82,19 @@ __device__ __forceinline__ unsigned long long tree_head_cost(const TreeParams &p
   for (uint32_t c = 1; c <= tiles; ++c)
     sum += (tree_tokens(p, n, len, static_cast<int>(c << p.lg_nodes)) + STEP - 1) / STEP;
   return sum;
+}
+
+// Writes down a cut item's CTAs: it ends ahead of position `end` of `all`, shared by `ctas`
+// CTAs.  (A function, for its 64-bit divisions: inline, they took the kernels 1 to 2 % longer.)
+static __device__ __noinline__ void tree_cut(const TreeParams &p, const TreeItem it, int cta, uint32_t end,
+                                      uint32_t all, uint32_t ctas) {
+  // the CTA that has the step at position x
+  auto owner = [&](uint32_t x) {
+    return static_cast<int>((static_cast<unsigned long long>(x + 1) * ctas - 1) / all);
+  };
+  const int from = owner(end - it.steps);
+  p.cuts[it.slot(cta)] =
+      TreeCut{owner(end - 1) - from + 1, from, it.q0, it.nodes * p.G, it.g, it.base, it.n, 0};
 }
 
 // The items of a CTA, in order.  (32 bits: a call of 2^31 positions and more is refused.)
@@ -139,15 +153,6 @@ struct TreeWalk {
       if (it->t0 < it->t1) return true;
     }
     return false;
-  }
-  // The CTA that has the step at position x.
-  __device__ __forceinline__ int owner(uint32_t x) const {
-    return static_cast<int>((static_cast<unsigned long long>(x + 1) * ctas - 1) / all);
-  }
-  // What is to be written down of a cut item whose last step is ahead of position `end`.
-  __device__ __forceinline__ TreeCut cut(const TreeParams &p, const TreeItem &it, uint32_t end) const {
-    const int from = owner(end - it.steps);
-    return TreeCut{owner(end - 1) - from + 1, from, it.q0, it.nodes * p.G, it.g, it.base, it.n};
   }
 };
 
@@ -292,7 +297,9 @@ __device__ __noinline__ void tree_all_nan(const TreeParams &p) {
   auto walk = tree_begin<STEP, BOUND, MIN, NT>(p, cta);
   TreeItem it;
   const float nan = __int_as_float(0x7fffffff);
-  while (walk.next(p, &it))
+  while (walk.next(p, &it)) {
+    // (what was not come to was not written down either)
+    if (!it.whole() && threadIdx.x == 0) tree_cut(p, it, cta, walk.at, walk.all, walk.ctas);
     for (int e = threadIdx.x; e < it.nodes * p.G; e += NT) {
       if (!it.whole()) {   // (the join makes NaN of it)
         p.part_lse[static_cast<size_t>(it.slot(cta)) * p.tile + e] = INFINITY;
@@ -302,6 +309,7 @@ __device__ __noinline__ void tree_all_nan(const TreeParams &p) {
       if (p.lse_out) p.lse_out[at] = nan;
       for (int c = 0; c < D; ++c) static_cast<T *>(p.out)[at * D + c] = from_f32<T>(nan);
     }
+  }
 }
 
 cudaError_t launch_tree_f32(const TreeParams &p, int D, cudaStream_t s);

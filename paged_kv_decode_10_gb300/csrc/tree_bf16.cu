@@ -371,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (lane == 0 && !is_v) {
-        p.cuts[2 * cta] = first_end ? walk.cut(p, first, first_end) : TreeCut{};
-        p.cuts[2 * cta + 1] = last_end ? walk.cut(p, last, last_end) : TreeCut{};
+        p.cuts[2 * cta] = p.cuts[2 * cta + 1] = TreeCut{};
+        if (first_end) tree_cut(p, first, cta, first_end, walk.all, walk.ctas);
+        if (last_end) tree_cut(p, last, cta, last_end, walk.all, walk.ctas);
       }
       // every copy has landed before the CTA ends (after a normal run they have)
       for (int n = max(0, x - NS); n < x; ++n)

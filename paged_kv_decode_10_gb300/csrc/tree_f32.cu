@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       }
       if (!w.whole()) {   // (at most two of them)
         cut |= w.t0 == 0 ? 2u : 1u;
-        if (lane == 0) p.cuts[w.slot(cta)] = walk.cut(p, w, walk.at);
+        if (lane == 0) tree_cut(p, w, cta, walk.at, walk.all, walk.ctas);
       }
     }
     if (lane < 2 && !(cut >> lane & 1u)) p.cuts[2 * cta + lane] = TreeCut{};

@@ -294,3 +294,10 @@ def test_readme_example_of_drafted_tokens_runs():
     assert tuple(scope["out"].shape) == (9, 32, 128) and bool(scope["out"].float().isfinite().all())
     assert dec.alloc.seq_len(a) == 703 and dec.alloc.seq_len(b) == 701 and dec.k_cache.shape[0] == 2048
     assert dec.device_errors() == 0
+
+
+def test_a_bounded_decoder_takes_no_rotary_with_sections():
+    from paged_kv_decode_10_gb300.bounded import BoundedDecoder
+    with pytest.raises(ValueError):
+        BoundedDecoder(20, 4, 2, 64, "f32", 4, 24, 8, rotary=binding.Rotary(64, sections=(16, 16)),
+                       device=dev())

@@ -377,3 +377,41 @@ def test_tensors_aligned_to_16_bytes(dtype):
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert (buf[1, :skip] == 7.0).all() and (buf[1, -skip:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("f32", 128), ("bf16", 64)])
+def test_whatever_a_wait_gave_up_on_is_nan(dtype, d):
+    """Items of many parts and whole ones: every output is its value or NaN, none is left as it was."""
+    c = Case([4000, 50, 3, 900], [40, 9, 1, 70], 8, 2, d, dtype, "tree", seed=9)
+    want = c.run()[0]
+    for _ in range(5):
+        out, err = torch.full_like(want, 7.0), torch.zeros(1, dtype=torch.int32, device=dev())
+        binding.decode_attn_tree_args(c.args(out, err=err, flags=binding.ATTN_SHORT_WAITS))
+        torch.cuda.synchronize()
+        assert int(err) == binding.DEVERR_TIMEOUT
+        assert torch.isnan(out).any() and (torch.isnan(out) | (out == want)).all()
+    assert torch.equal(c.run()[0], want)
+
+
+def test_lengths_written_by_the_kernel_before():
+    """Metadata that a kernel ahead on the stream writes (its call may start while that one runs)."""
+    c = Case([300, 7], [12, 5], 8, 2, 128, "bf16", "tree", seed=9)
+    want = c.run()[0]
+    out = torch.zeros_like(want)
+    args = c.args(out)
+    block_tables, lens, starts, mask = (args.keep[i] for i in (3, 4, 5, 7))
+    wrong, right = [], []
+    for t in (block_tables, lens, starts, mask):
+        right.append(t.clone())
+        wrong.append(torch.zeros_like(t))
+    busy = torch.randn(4096, 4096, device=dev())
+    for _ in range(3):
+        for t, w in zip((block_tables, lens, starts, mask), wrong):
+            t.copy_(w)
+        busy = busy @ busy * 1e-3
+        for t, r in zip((block_tables, lens, starts, mask), right):
+            t.copy_(r)
+        binding.decode_attn_tree_args(args)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        out.zero_()
