@@ -1320,16 +1320,16 @@ def tree_mask(parents, node_starts):
     parents = np.asarray(parents, np.int64)
     starts = np.asarray(node_starts, np.int64)
     most = int((starts[1:] - starts[:-1]).max()) if len(starts) > 1 else 0
-    bits = np.zeros((len(parents), max(1, -(-most // 32)) * 32), np.uint8)
-    for a, b in zip(starts[:-1], starts[1:]):
+    words = max(1, -(-most // 32))
+    parents, bits = parents.tolist(), [0] * len(parents)     # (of a node: one long integer)
+    for a, b in zip(starts[:-1].tolist(), starts[1:].tolist()):
         for i in range(b - a):
             up = parents[a + i]
             if not -1 <= up < i:
                 raise PkvError(ERR_INVALID_ARG, f"node {i}: parent {up} is not a node ahead of it")
-            if up >= 0:
-                bits[a + i] = bits[a + up]
-            bits[a + i, i] = 1
-    return np.packbits(bits, axis=1, bitorder="little").view("<i4").astype(np.int32)
+            bits[a + i] = 1 << i | (bits[a + up] if up >= 0 else 0)
+    words_of = b"".join(x.to_bytes(4 * words, "little") for x in bits)
+    return np.frombuffer(words_of, "<i4").reshape(len(bits), words).astype(np.int32)
 
 
 def make_tree_args(q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts, scale, out,

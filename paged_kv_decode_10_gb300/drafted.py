@@ -8,7 +8,8 @@ positions on several axes (a ``binding.Rotary`` with sections).
 
 A step is a0 on the host (``pkv_prepare_nodes``), one copy of its metadata to the GPU, then per
 layer ``pkv_rotary_append`` and ``pkv_decode_attn_tree``; ``accept`` is ``pkv_tree_accept`` over
-all layers, then ``pkv_seqs_truncate`` on the host.
+all layers, then ``pkv_seqs_truncate`` on the host.  A call on another stream than the call
+before waits for that one's; what the caller hands in is ready on the stream that it names.
 """
 import math
 
@@ -45,16 +46,20 @@ class DraftDecoder(PagedDecoder):
         # of the last verify: sequences (None: left since), lengths before, nodes, device
         # metadata, stream
         self._drafted = None
+        self._last = torch.cuda.current_stream(self.device)   # stream of the last call
         self._waiting = set()       # sequences that hold drafted tokens
         self._pinned = [[None, None], [None, None]]   # host buffer, event of its last copy
 
     # -- helpers ------------------------------------------------------------------
     def _on(self, stream):
         """The stream of a call as torch's current one, so that copies, small tensors and
-        launches are ordered."""
+        launches are ordered, behind what the call before launched on another."""
         torch = self.torch
-        return torch.cuda.stream(stream if stream is not None
-                                 else torch.cuda.current_stream(self.device))
+        now = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if now != self._last:
+            now.wait_stream(self._last)
+            self._last = now
+        return torch.cuda.stream(now)
 
     def _upload(self, arrays):
         """Device copies of numpy arrays (int64 ones first), by one copy on the current
@@ -250,9 +255,11 @@ class DraftDecoder(PagedDecoder):
                 raise ValueError(f"parents {parents.shape}, expected [{T}]")
             mask = binding.tree_mask(parents, starts)
             depths = np.zeros(T, np.int32)
-            for a, b in zip(starts[:-1], starts[1:]):
-                for i in range(a, b):
-                    depths[i] = depths[a + parents[i]] + 1 if parents[i] >= 0 else 0
+            above = np.where(parents >= 0, parents + np.repeat(starts[:-1], counts), -1)
+            up = above
+            while (up >= 0).any():      # (a parent a turn)
+                depths += up >= 0
+                up = np.where(up >= 0, above[up], -1)
         elif mask is not None:
             mask = np.ascontiguousarray(mask, np.int32)
             if mask.ndim != 2 or len(mask) != T or 32 * mask.shape[1] < counts.max(initial=0):
@@ -260,10 +267,9 @@ class DraftDecoder(PagedDecoder):
             if depths is None and positions is None:
                 raise ValueError("a mask needs depths or positions")
         out, before, meta = self._run(seq_ids, counts, q, k, v, mask, depths, positions, stream)
-        if before is not None:
-            run = stream if stream is not None else self.torch.cuda.current_stream(self.device)
-            self._drafted = (seq_ids, before, counts, meta, run)
-            self._waiting.update(s for s, n in zip(seq_ids, counts) if n)
+        run = stream if stream is not None else self.torch.cuda.current_stream(self.device)
+        self._drafted = (seq_ids, before, counts, meta, run)
+        self._waiting.update(s for s, n in zip(seq_ids, counts) if n)
         return out
 
     def accept(self, paths, stream=None):
@@ -291,7 +297,6 @@ class DraftDecoder(PagedDecoder):
             with self._on(stream):
                 now = torch.cuda.current_stream(self.device)
                 if now != run:
-                    now.wait_stream(run)
                     for t in meta:
                         t.record_stream(now)
                 path, kept = self._upload([path, kept])

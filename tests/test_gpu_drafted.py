@@ -301,3 +301,52 @@ def test_a_bounded_decoder_takes_no_rotary_with_sections():
     with pytest.raises(ValueError):
         BoundedDecoder(20, 4, 2, 64, "f32", 4, 24, 8, rotary=binding.Rotary(64, sections=(16, 16)),
                        device=dev())
+
+
+def test_a_verify_without_nodes_is_accepted_like_any():
+    dec = DraftDecoder(20, 4, 2, 64, "f32", 4, 8, device=dev())
+    s, t = dec.join(5, *inputs(5, dec)[1:]), dec.join()
+    out = dec.verify([s, t], [0, 0], *inputs(0, dec), parents=[])
+    assert tuple(out.shape) == (0, 4, 64)
+    with pytest.raises(ValueError):
+        dec.accept([[0], []])
+    dec.accept([[], []])
+    with pytest.raises(ValueError):
+        dec.accept([[], []])
+    assert dec.alloc.seq_len(s) == 5 and dec.alloc.seq_len(t) == 0
+    dec.step([s, t], *inputs(2, dec))
+    assert dec.alloc.seq_len(s) == 6 and dec.alloc.seq_len(t) == 1 and dec.device_errors() == 0
+
+
+def test_every_call_on_another_stream():
+    """A life whose calls change the stream each time, nobody waiting in between: the bits of
+    the same life on one stream."""
+    got = []
+    for sides in (1, 4):
+        dec = DraftDecoder(4000, 8, 2, 128, "bf16", 8, 600, device=dev(), n_layers=2)
+        x = [workloads.normal((2, 5200, h, 128), "bf16", h).to(dev()) for h in (8, 2, 3)]
+        x[2] = x[2][:, :, :2].contiguous()
+        streams = [torch.cuda.Stream() for _ in range(sides)]
+        torch.cuda.synchronize()
+        turn = [0]
+
+        def on():
+            turn[0] += 1
+            return streams[turn[0] % sides]
+        at = lambda a, n: [t[:, a:a + n].contiguous() for t in x]
+        many, nine, two = at(0, 5000), at(5000, 9), at(5100, 2)
+        torch.cuda.synchronize()
+        s = dec.join(5000, many[1], many[2], stream=on())
+        (c,) = dec.fork(s, stream=on())
+        outs = []
+        for turns in range(4):
+            outs.append(dec.verify([s, c], [5, 4], *nine, parents=[-1, 0, 0, 1, 2, -1, 0, 0, 2], stream=on()))
+            dec.accept([[0, 2, 4], [0, 2]], stream=on())
+            if turns == 1:
+                dec.resize(1000, stream=on())
+            outs.append(dec.step([c, s], *two, stream=on()))
+        torch.cuda.synchronize()
+        assert dec.device_errors() == 0
+        got.append(outs)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
