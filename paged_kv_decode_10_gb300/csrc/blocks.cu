@@ -17,7 +17,8 @@ constexpr int kFewPools = 8;
 
 // ---- whole blocks ---------------------------------------------------------------
 // A CTA copies one chunk of one block of one pool: kWide 16-byte pieces a thread, all
-// read before the first is written.  Bound by memory.
+// read before the first is written.  Bound by memory: 1023 blocks of 32 KB in 16 pools, 156
+// us, 6.9 TB/s.  (A few blocks: by the call, 1.6 us in a graph.)
 template <int POOLS>
 struct CopyParams {
   const int32_t *src_blocks, *dst_blocks;
@@ -59,7 +60,10 @@ __global__ void __launch_bounds__(kThreads)
 // strictly, so path[j] >= j: going up in j, whatever is overwritten has been read, and a
 // thread that owns one 16-byte column of one head of one pool needs nobody else for
 // that.  A CTA serves kThreads columns of one row at a time; it checks the row first (every
-// CTA of a row comes to the same answer) and lists its moves in shared memory.
+// CTA of a row comes to the same answer) and lists its moves in shared memory.  Bound by the
+// scattered pieces, a head of a token each (256 bytes, the next head's 4 KB further: 64 rows
+// that accept 1 to 12 nodes, 64 pools of 8 heads of 128, 21 us, 4.6 TB/s), or by the chain of
+// reads before them (3 rows, 2 pools: 3 us).
 template <int POOLS>
 struct AcceptParams {
   const int32_t *block_tables, *seq_lens, *node_starts, *path, *accept_lens;

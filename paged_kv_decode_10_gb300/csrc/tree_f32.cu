@@ -11,7 +11,10 @@
 // queue and loads K and V a step ahead, a bulk copy for every token.  (By tensor copies
 // into swizzled slabs the loads of a call of two steps a CTA were 2 us sooner, but the
 // permuted addresses took the products 10 to 20 % longer.)  Multiplications and additions
-// go two to an instruction (16 rows of 1000 tokens, 16 nodes, 32/8 heads of 128: 139 -> 128 us).
+// go two to an instruction (16 rows of 1000 tokens, 16 nodes, 32/8 heads of 128: 139 -> 119
+// us).  Twice the rows to a thread, with half the threads to a step, took 10 % less for 16
+// to 32 rows of 64-wide heads, but 18 % more for full tiles, and 1.7 times as long for
+// 128-wide heads, whose accumulators did not fit the registers.
 //
 // Masks.  Only steps that reach past the tokens every row sees look at mask bits.  What a row
 // does not see may hold anything, the tail of a last page and pages outside the pool
@@ -19,8 +22,9 @@
 // four that overflow count as such), what a row does not see gets a weight of -1 and is
 // skipped in the product with V instead of being multiplied by zero.
 //
-// Bound by the FMA and shared-memory pipes where rows are many, by the loads' latency where
-// they are few.
+// Bound by the FMA and shared-memory pipes where rows are many (4 rows of 4000 tokens, 32
+// nodes, 32/8 heads of 128: 199 us, 42 TFLOP/s), by the loads' latency where they are few
+// (one row of 500 tokens, 8 nodes, 8/2 heads of 64: 13 us).
 #include "tensor_core.cuh"
 #include "tree.h"
 
