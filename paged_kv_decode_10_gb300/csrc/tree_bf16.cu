@@ -580,21 +580,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             vis[q] &= (bad >> 2 * q & 1 ? 0u : 0xffffu) | (bad >> (2 * q + 1) & 1 ? 0u : 0xffff0000u);
         }
         if (active) {
-          float s[kTile];
+          float s[kTile], t4[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tm_ld32(sS + 32 * q, s + 32 * q);
+          for (int q = 0; q < 4; ++q) tm_ld32_max(sS + 32 * q, s + 32 * q, &t4[q]);
           tm_wait_ld();
 #pragma unroll
           for (int q = 0; q < 4; ++q) pin32(s + 32 * q);
+          asm volatile("" : "+f"(t4[0]), "+f"(t4[1]), "+f"(t4[2]), "+f"(t4[3]));
           if (masked) {
+            t4[0] = t4[1] = t4[2] = t4[3] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < kTile; ++e)
+            for (int e = 0; e < kTile; e += 2) {
               if (!(vis[e / 32] >> (e % 32) & 1u)) s[e] = -INFINITY;
+              if (!(vis[e / 32] >> (e % 32 + 1) & 1u)) s[e + 1] = -INFINITY;
+              t4[(e >> 1) & 3] = max3(t4[(e >> 1) & 3], s[e], s[e + 1]);
+            }
           }
-          float t4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int e = 4; e + 1 < kTile; e += 2)
-            t4[(e >> 1) & 3] = max3(t4[(e >> 1) & 3], s[e], s[e + 1]);
           const float top = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * c);
           if (__any_sync(0xffffffffu, top > mx + kLazy)) {
             const float al = top == -INFINITY ? 1.f : ex2(mx - top);   // 0 before the first score
