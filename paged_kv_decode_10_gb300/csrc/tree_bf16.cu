@@ -426,6 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                          __all_sync(0xffffffffu, wait_started<POLL>(wait_here, misc + started, x + t));
           return r && wait.warp(&full[(x + t) % NS], static_cast<uint32_t>((x + t) / NS) & 1u);
         };
+        auto tile_there = [&](uint64_t *full, int started, int t) {
+          return __all_sync(0xffffffffu, (t >= NS || misc[started] > x + t) &&
+                                             mbar_test_wait(&full[(x + t) % NS],
+                                                            static_cast<uint32_t>((x + t) / NS) & 1u));
+        };
         auto release = [&](uint64_t *empty) {
           mma_commit(empty);
           if (!two) mma_commit(empty);
@@ -470,36 +475,48 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
-            auto weighted = [&](int from, int to) {   // O += P V, a page at a time
+          }
+          // (looked for here, where there is time, the next tile of K does not hold up the
+          // products: S follows P V at once)
+          const bool k_there = t + 1 == tiles || tile_there(k_full, kStartedK, t + 1);
+          ok = (t < 0 || wait.warp(&p_half[m], p_ph)) && my_turn();
+          if (!ok) break;
+          const int vst = (x + t + NS) % NS, valid = min(kTile, tokens - (first + t) * kTile);
+          auto weighted = [&](int from, int to) {   // O += P V, a page at a time
 #pragma unroll
-              for (int ks = from; ks < to; ++ks)
-                if (ks * kBlockTokens < valid)
-                  mma_ts(tO(m), tS(m) + ks * 8,
-                         smem_desc(v_addr + st * L::kMat + ks * (kBlockTokens * 128), L::kSlab, 1024),
-                         kIdescO, t > 0 || ks > 0);
-            };
-            ok = wait.warp(&p_half[m], p_ph) && my_turn();
-            if (!ok) break;
+            for (int ks = from; ks < to; ++ks)
+              if (ks * kBlockTokens < valid)
+                mma_ts(tO(m), tS(m) + ks * 8,
+                       smem_desc(v_addr + vst * L::kMat + ks * (kBlockTokens * 128), L::kSlab, 1024),
+                       kIdescO, t > 0 || ks > 0);
+          };
+          if (t >= 0) {
             tc_fence_after();
             if (elect_one()) weighted(0, 2 * kHalf);
             __syncwarp();
+          }
+          if (t >= 0) {
             ok = wait.warp(&p_ready[m], p_ph);
             if (!ok) break;
             p_ph ^= 1u;
-            tc_fence_after();
-            if (elect_one()) {
-              weighted(2 * kHalf, kPages);
-              release(&v_empty[st]);
-              if (t + 1 == tiles) mma_commit(&o_full[m]);
-            }
+          }
+          tc_fence_after();
+          auto rest = [&]() {
+            if (t < 0) return;
+            weighted(2 * kHalf, kPages);
+            release(&v_empty[vst]);
+            if (t + 1 == tiles) mma_commit(&o_full[m]);
+          };
+          if (!k_there) {
+            if (elect_one()) rest();
             __syncwarp();
+            ok = wait_tile(k_full, kStartedK, t + 1);
+            if (!ok) break;
+            tc_fence_after();
           }
           const int st = (x + t + 1) % NS;
-          ok = t + 1 == tiles || wait_tile(k_full, kStartedK, t + 1);
-          ok = ok && (t >= 0 || my_turn());
-          if (!ok) break;
-          tc_fence_after();
           if (elect_one()) {
+            if (k_there) rest();
             if (t + 1 < tiles) {   // S = Q K^T
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
