@@ -34,10 +34,12 @@
 // unrolled) spent 8 us an item, mostly on instructions that were not in the cache.
 //
 // Bound by the loads while rows are few (64 rows of 4000 tokens, 4 nodes, 32/8 heads of 128:
-// 176 us with the join, 5.9 TB/s), by the chain product, maxima, exponentials, product of
-// the two slots where they are many: a step of 256 rows takes 3300 clocks, 2048 of them
-// products (one row of 131072 tokens, 64 nodes, 32/4 heads of 128: 104 us with the join, 1.3
-// PFLOP/s).  A third stage for K or V, and Q loaded ahead of K, gained nothing or lost 2 %.
+// 169 us with the join, 6.2 TB/s), by the chain product, exponentials, product of the two
+// slots where they are many: a step of 256 rows takes 2850 clocks, 2048 of them products (one
+// row of 131072 tokens, 61 nodes, 32/4 heads of 128: 98 us with the join, 1.3 PFLOP/s).  The
+// largest scores come with their load (a search of its own: 103 us against 101), the next tile
+// of K is looked for while there is time (101 to 98).  A third stage for K or V, and Q loaded
+// ahead of K, gained nothing or lost 2 %.
 #include "tensor_core.cuh"
 #include "tree.h"
 
