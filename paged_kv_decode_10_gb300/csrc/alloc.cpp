@@ -488,7 +488,7 @@ extern "C" int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B
     // (without depths the last node's position is the largest)
     for (int32_t i = depths ? 0 : std::max(counts[b] - 1, 0); i < counts[b]; ++i) {
       const int64_t depth = depths ? depths[T + i] : i;
-      PKV_REQUIRE(depth >= 0 && a->lengths[s] + a->offsets[s] + depth <= INT32_MAX,
+      PKV_REQUIRE(depth >= 0 && depth + a->lengths[s] + a->offsets[s] <= INT32_MAX,
                   PKV_ERR_INVALID_ARG, "sequence %d: node %d has a bad depth or position", s, i);
     }
     T += counts[b];

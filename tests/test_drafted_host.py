@@ -395,3 +395,22 @@ def test_axes_call_refuses(bind):
         rc = lib.pkv_rotary_axes_append(ctypes.byref(a), None if axes is None else ctypes.byref(axes), stride,
                                         None)
         assert rc == bind.ERR_INVALID_ARG
+
+
+def test_positions_near_the_limit_are_refused_not_wrapped(bind):
+    """length + offset may pass 32 bits before the depth is added."""
+    a = bind.BlockAllocator(16, 4, 8)
+    s = a.join(20)
+    for offset, count, good in ((2**31 - 1, 1, False), (2**31 - 21, 1, True), (2**31 - 22, 2, True),
+                                (2**31 - 10, 2, False), (2**31 - 22, 5, False)):
+        a.set_offset(s, offset)
+        state = a.free_stack()
+        if not good:
+            for depths in (None, np.arange(count)):
+                with pytest.raises(bind.PkvError):
+                    a.prepare_nodes([s], [count], 8, depths)
+                assert a.seq_len(s) == 20 and a.free_stack() == state
+            continue
+        pos = a.prepare_nodes([s], [count], 8)[0]
+        assert pos.tolist() == [20 + offset + i for i in range(count)]
+        a.truncate_many([s], [20])
