@@ -235,6 +235,11 @@ int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B, const int
  * that a pkv_server manages (its captured steps name the caches). */
 int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst, int32_t cap,
                      int32_t *n);
+/* The pairs that pkv_alloc_resize with these arguments would give (and its refusals); nothing
+ * changes.  For a caller who copies into the new pools first and takes the new size once
+ * that has succeeded. */
+int pkv_alloc_resize_pairs(const pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst,
+                           int32_t cap, int32_t *n);
 /* Sequences that a block belongs to (0: it is free). */
 int pkv_block_refs(const pkv_alloc *a, int32_t block, int32_t *refs);
 int pkv_num_free(const pkv_alloc *a, int32_t *n);

@@ -276,6 +276,7 @@ SIGNATURES = {
     "pkv_prepare_nodes": (ctypes.c_int, [_vp, _p_i32, _c_i32, _p_i32, _p_i32, _p_i32, _p_i64, _p_i32,
                                          _p_i32, _p_i32, _c_i32]),
     "pkv_alloc_resize": (ctypes.c_int, [_vp, _c_i32, _p_i32, _p_i32, _c_i32, _p_i32]),
+    "pkv_alloc_resize_pairs": (ctypes.c_int, [_vp, _c_i32, _p_i32, _p_i32, _c_i32, _p_i32]),
     "pkv_block_refs": (ctypes.c_int, [_vp, _c_i32, _p_i32]),
     "pkv_rotary_axes_init": (ctypes.c_int, [ctypes.POINTER(RotarySpec), _c_i32, _p_i32, _c_i32, _c_i32,
                                             _c_i32, ctypes.POINTER(RotaryTable),
@@ -554,16 +555,24 @@ class BlockAllocator:
             int(bt_stride)))
         return out
 
-    def resize(self, num_blocks):
-        """Makes the pool ``num_blocks`` blocks (``pkv_alloc_resize``); returns the blocks
-        that move ``(src, dst)``."""
+    def _resize(self, call, num_blocks):
         used = self.num_blocks - self.num_free()
         src, dst = np.empty(used, np.int32), np.empty(used, np.int32)
         n = ctypes.c_int32()
-        _check(self._lib.pkv_alloc_resize(self._h, int(num_blocks), _np_ptr(src, ctypes.c_int32),
-                                          _np_ptr(dst, ctypes.c_int32), used, ctypes.byref(n)))
-        self.num_blocks = int(num_blocks)
+        _check(call(self._h, int(num_blocks), _np_ptr(src, ctypes.c_int32),
+                    _np_ptr(dst, ctypes.c_int32), used, ctypes.byref(n)))
         return src[:n.value], dst[:n.value]
+
+    def resize(self, num_blocks):
+        """Makes the pool ``num_blocks`` blocks (``pkv_alloc_resize``); returns the blocks
+        that move ``(src, dst)``."""
+        pairs = self._resize(self._lib.pkv_alloc_resize, num_blocks)
+        self.num_blocks = int(num_blocks)
+        return pairs
+
+    def resize_pairs(self, num_blocks):
+        """What ``resize`` would return; nothing changes (``pkv_alloc_resize_pairs``)."""
+        return self._resize(self._lib.pkv_alloc_resize_pairs, num_blocks)
 
     def block_refs(self, block):
         """Sequences that the block belongs to (``pkv_block_refs``)."""

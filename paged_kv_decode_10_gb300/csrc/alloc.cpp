@@ -516,15 +516,64 @@ extern "C" int pkv_prepare_nodes(pkv_alloc *a, const int32_t *seq_ids, int32_t B
   return PKV_OK;
 }
 
-extern "C" int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst,
-                                int32_t cap, int32_t *n) {
-  pkv::clear_error();
+namespace {
+
+// The moves of a pool that shrinks to num_blocks (pkv_alloc_resize), into `to` (room for every
+// block: the new id of each that moves, else -1) and the pairs src, dst (room for cap).
+int shrink_pairs(const pkv_alloc *a, int32_t num_blocks, std::vector<int32_t> *to, int32_t *src,
+                 int32_t *dst, int32_t cap, int32_t *n) {
+  int32_t moves = 0;
+  for (int32_t b = num_blocks; b < a->num_blocks; ++b) moves += a->refs[b] > 0;
+  *n = moves;
+  PKV_REQUIRE(moves <= cap && (moves == 0 || (src && dst)), PKV_ERR_INVALID_ARG,
+              "%d blocks move, room for %d", moves, src && dst ? cap : 0);
+  size_t top = a->free_stack.size();
+  int32_t at = 0;
+  for (int32_t s = 0; s < a->max_seqs; ++s) {
+    if (!a->live[s]) continue;
+    const int32_t *t = a->table(s);
+    for (int32_t j = 0; j < a->n_blocks[s]; ++j) {
+      if (t[j] < num_blocks || (*to)[t[j]] >= 0) continue;
+      do --top;   // (the blocks in use fit: there is one)
+      while (a->free_stack[top] >= num_blocks);
+      (*to)[t[j]] = a->free_stack[top];
+      src[at] = t[j];
+      dst[at++] = a->free_stack[top];
+    }
+  }
+  return PKV_OK;
+}
+
+int check_resize(const pkv_alloc *a, int32_t num_blocks, int32_t cap, int32_t *n) {
   PKV_REQUIRE(a && n && cap >= 0, PKV_ERR_INVALID_ARG, "NULL argument or cap < 0");
   PKV_REQUIRE(num_blocks > 0, PKV_ERR_INVALID_ARG, "num_blocks must be positive");
   *n = 0;
   const size_t used = a->num_blocks - a->free_stack.size();
   PKV_REQUIRE(used <= static_cast<size_t>(num_blocks), PKV_ERR_OUT_OF_BLOCKS,
               "%zu blocks are in use, more than %d", used, num_blocks);
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" int pkv_alloc_resize_pairs(const pkv_alloc *a, int32_t num_blocks, int32_t *src,
+                                      int32_t *dst, int32_t cap, int32_t *n) {
+  pkv::clear_error();
+  const int rc = check_resize(a, num_blocks, cap, n);
+  if (rc != PKV_OK || num_blocks >= a->num_blocks) return rc;
+  try {
+    std::vector<int32_t> to(a->num_blocks, -1);
+    return shrink_pairs(a, num_blocks, &to, src, dst, cap, n);
+  } catch (...) {
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+extern "C" int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst,
+                                int32_t cap, int32_t *n) {
+  pkv::clear_error();
+  int rc = check_resize(a, num_blocks, cap, n);
+  if (rc != PKV_OK) return rc;
   try {
     if (num_blocks >= a->num_blocks) {
       a->refs.resize(num_blocks, 0);
@@ -534,34 +583,25 @@ extern "C" int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, 
       return PKV_OK;
     }
     std::vector<int32_t> to(a->num_blocks, -1);   // new id of a block that moves
-    int32_t moves = 0;
-    for (int32_t b = num_blocks; b < a->num_blocks; ++b) moves += a->refs[b] > 0;
-    if (moves > cap || (moves > 0 && (!src || !dst))) {
-      *n = moves;
-      return pkv::fail(PKV_ERR_INVALID_ARG, "%d blocks move, room for %d", moves,
-                       src && dst ? cap : 0);
-    }
-    a->free_stack.erase(std::remove_if(a->free_stack.begin(), a->free_stack.end(),
-                                       [&](int32_t b) { return b >= num_blocks; }),
-                        a->free_stack.end());
+    rc = shrink_pairs(a, num_blocks, &to, src, dst, cap, n);
+    if (rc != PKV_OK) return rc;
+    // (nothing fails from here on)
+    for (int32_t b = num_blocks; b < a->num_blocks; ++b)
+      if (to[b] >= 0) a->refs[to[b]] = a->refs[b];
     for (int32_t s = 0; s < a->max_seqs; ++s) {
       if (!a->live[s]) continue;
       int32_t *t = a->table(s);
       bool moved = false;
       for (int32_t j = 0; j < a->n_blocks[s]; ++j) {
         if (t[j] < num_blocks) continue;
-        if (to[t[j]] < 0) {
-          const int32_t b = a->take();
-          a->refs[b] = a->refs[t[j]];
-          src[*n] = t[j];
-          dst[(*n)++] = b;
-          to[t[j]] = b;
-        }
         t[j] = to[t[j]];
         moved = true;
       }
       if (moved) ++a->generation[s];   // a cached table row of it is rewritten
     }
+    a->free_stack.erase(std::remove_if(a->free_stack.begin(), a->free_stack.end(),
+                                       [&](int32_t b) { return b >= num_blocks || a->refs[b] > 0; }),
+                        a->free_stack.end());
     a->refs.resize(num_blocks);
     a->num_blocks = num_blocks;
   } catch (...) {

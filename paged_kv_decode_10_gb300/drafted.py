@@ -163,21 +163,22 @@ class DraftDecoder(PagedDecoder):
 
     def resize(self, num_blocks, stream=None):
         """Another size of the pool: new caches, into which the blocks in use are copied
-        (those beyond a smaller pool onto free places).  The old caches are let go."""
+        (those beyond a smaller pool onto free places).  The old caches are let go.  A call that
+        raises changes nothing."""
         torch = self.torch
         if self._waiting:
             raise ValueError("drafted tokens are to be accepted first")
         num_blocks = int(num_blocks)
-        old = self.num_blocks
         with self._on(stream):
             shape = (self.n_layers, num_blocks) + tuple(self.k_caches.shape[2:])
+            moved, onto = self.alloc.resize_pairs(num_blocks)
+            used = set(range(self.num_blocks)) - set(self.alloc.free_stack())
+            stay = np.array(sorted(used - set(moved.tolist())), np.int32)
             k, v = (torch.empty(shape, dtype=self.tdtype, device=self.device) for _ in range(2))
-            used = set(range(old)) - set(self.alloc.free_stack())
-            moved, onto = self.alloc.resize(num_blocks)
-            stay = sorted(used - set(moved.tolist()))
-            self._copy(np.concatenate([np.array(stay, np.int32), moved]),
-                       np.concatenate([np.array(stay, np.int32), onto]),
+            self._copy(np.concatenate([stay, moved]), np.concatenate([stay, onto]),
                        [c[layer] for layer in range(self.n_layers) for c in (k, v)])
+            # (the allocator follows once nothing can raise any more)
+            self.alloc.resize(num_blocks)
             for c in (self.k_caches, self.v_caches):   # (not another's before the copy has read it)
                 c.record_stream(torch.cuda.current_stream(self.device))
         self.k_caches, self.v_caches, self.num_blocks = k, v, num_blocks
