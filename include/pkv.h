@@ -240,6 +240,9 @@ int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *ds
  * that has succeeded. */
 int pkv_alloc_resize_pairs(const pkv_alloc *a, int32_t num_blocks, int32_t *src, int32_t *dst,
                            int32_t cap, int32_t *n);
+/* shared[i]: the blocks of sequence seq_ids[i] that belong to another one too.  (To be asked
+ * before anything moves tokens within a sequence's blocks: pkv_evict.) */
+int pkv_seqs_shared(const pkv_alloc *a, const int32_t *seq_ids, int32_t n, int32_t *shared);
 /* Sequences that a block belongs to (0: it is free). */
 int pkv_block_refs(const pkv_alloc *a, int32_t block, int32_t *refs);
 int pkv_num_free(const pkv_alloc *a, int32_t *n);

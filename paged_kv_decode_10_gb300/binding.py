@@ -277,6 +277,7 @@ SIGNATURES = {
                                          _p_i32, _p_i32, _c_i32]),
     "pkv_alloc_resize": (ctypes.c_int, [_vp, _c_i32, _p_i32, _p_i32, _c_i32, _p_i32]),
     "pkv_alloc_resize_pairs": (ctypes.c_int, [_vp, _c_i32, _p_i32, _p_i32, _c_i32, _p_i32]),
+    "pkv_seqs_shared": (ctypes.c_int, [_vp, _p_i32, _c_i32, _p_i32]),
     "pkv_block_refs": (ctypes.c_int, [_vp, _c_i32, _p_i32]),
     "pkv_rotary_axes_init": (ctypes.c_int, [ctypes.POINTER(RotarySpec), _c_i32, _p_i32, _c_i32, _c_i32,
                                             _c_i32, ctypes.POINTER(RotaryTable),
@@ -573,6 +574,14 @@ class BlockAllocator:
     def resize_pairs(self, num_blocks):
         """What ``resize`` would return; nothing changes (``pkv_alloc_resize_pairs``)."""
         return self._resize(self._lib.pkv_alloc_resize_pairs, num_blocks)
+
+    def shared_blocks(self, seq_ids):
+        """Of every sequence, the blocks that belong to another one too (``pkv_seqs_shared``)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int32)
+        shared = np.empty(len(ids), np.int32)
+        _check(self._lib.pkv_seqs_shared(self._h, _np_ptr(ids, ctypes.c_int32), len(ids),
+                                         _np_ptr(shared, ctypes.c_int32)))
+        return shared
 
     def block_refs(self, block):
         """Sequences that the block belongs to (``pkv_block_refs``)."""

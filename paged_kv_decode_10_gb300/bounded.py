@@ -168,7 +168,9 @@ class BoundedDecoder(PagedDecoder):
     # -- eviction -------------------------------------------------------------------
     def evict(self, seq_ids, keep=None, stream=None):
         """Cuts the listed sequences back to ``keep`` (default: the budget) own tokens;
-        returns the kept indices ``[L,n,Hkv,keep]`` (-1 behind a shorter sequence's)."""
+        returns the kept indices ``[L,n,Hkv,keep]`` (-1 behind a shorter sequence's).  A sequence
+        that would get shorter and shares blocks (``alloc.fork``) is refused before anything
+        moves."""
         seq_ids = [int(s) for s in seq_ids]
         for s in seq_ids:
             if s not in self._prefix_of:
@@ -189,6 +191,12 @@ class BoundedDecoder(PagedDecoder):
         if n == 0:
             return kept
         lens = np.array([self._held[s] for s in seq_ids], np.int32)
+        # (the allocator refuses these too, but only after their tokens have moved)
+        for s, L, shared in zip(seq_ids, lens, self.alloc.shared_blocks(seq_ids)):
+            if L > keep and shared:
+                raise binding.PkvError(binding.ERR_INVALID_ARG,
+                                       f"sequence {s} shares {shared} blocks with another: they are not "
+                                       "compacted")
         blocks = [self.alloc.seq_blocks(s) for s in seq_ids]
         tables = np.full((n, max(1, max(len(b) for b in blocks))), -1, np.int32)
         for i, b in enumerate(blocks):

@@ -610,6 +610,20 @@ extern "C" int pkv_alloc_resize(pkv_alloc *a, int32_t num_blocks, int32_t *src, 
   return PKV_OK;
 }
 
+extern "C" int pkv_seqs_shared(const pkv_alloc *a, const int32_t *seq_ids, int32_t n, int32_t *shared) {
+  pkv::clear_error();
+  PKV_REQUIRE(a && n >= 0 && (n == 0 || (seq_ids && shared)), PKV_ERR_INVALID_ARG,
+              "NULL argument or n < 0");
+  for (int32_t i = 0; i < n; ++i)
+    PKV_REQUIRE(a->is_live(seq_ids[i]), PKV_ERR_UNKNOWN_SEQ, "sequence %d is not live", seq_ids[i]);
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t *t = a->table(seq_ids[i]);
+    shared[i] = 0;
+    for (int32_t j = 0; j < a->n_blocks[seq_ids[i]]; ++j) shared[i] += a->refs[t[j]] > 1;
+  }
+  return PKV_OK;
+}
+
 extern "C" int pkv_block_refs(const pkv_alloc *a, int32_t block, int32_t *refs) {
   pkv::clear_error();
   PKV_REQUIRE(a && refs, PKV_ERR_INVALID_ARG, "NULL argument");
