@@ -346,11 +346,9 @@ class BoundedDecoder(PagedDecoder):
             ev = self.torch.cuda.Event()
             ev.record(run)
             self._pending["event"], self._pending = ev, None
+        # (a block that a token went into is its sequence's alone: nothing is to be copied)
         grown = [s for s in seq_ids if self.alloc.seq_len(s) > self._held[s]]
-        offsets = [self.alloc.offset(s) for s in grown]
-        self.alloc.evict_many(grown, [self._held[s] for s in grown])
-        for s, offset in zip(grown, offsets):
-            self.alloc.set_offset(s, offset)
+        self.alloc.truncate_many(grown, [self._held[s] for s in grown])
 
     def capture(self, *args, **kw):
         raise ValueError("BoundedDecoder changes its launches from step to step: not captured")

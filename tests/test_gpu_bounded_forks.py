@@ -1,5 +1,5 @@
 """``BoundedDecoder`` over sequences that share blocks with a fork: eviction, which moves tokens within
-their blocks, is refused before anything has moved."""
+their blocks, is refused before anything has moved, and a step that raises is taken back."""
 import numpy as np
 import pytest
 import torch
@@ -80,3 +80,23 @@ def test_a_step_at_the_bound_of_a_shared_sequence_changes_nothing():
     dec.alloc.leave(child)
     step(dec, [t, s], 80)
     assert dec.alloc.seq_len(s) == 33 and dec.alloc.seq_len(t) == 22 and dec.device_errors() == 0
+
+
+def test_a_step_that_raises_is_taken_back_where_blocks_are_shared(monkeypatch):
+    dec, (s, t) = make([32, 20])
+    (child,), src, _ = dec.alloc.fork(s, 1)
+    assert len(src) == 0
+    positions = [dec.alloc.offset(x) for x in (s, t)]
+    free = sorted(dec.alloc.free_stack())
+
+    def raises(*args, **kw):
+        raise RuntimeError("planted")
+    with monkeypatch.context() as m:
+        m.setattr(binding, "decode_attn_shared_args", raises)
+        with pytest.raises(RuntimeError):
+            step(dec, [s, t], 60)
+    assert [dec.alloc.seq_len(x) for x in (s, t, child)] == [32, 20, 32]
+    assert [dec.alloc.offset(x) for x in (s, t)] == positions and sorted(dec.alloc.free_stack()) == free
+    alone, ids = make([32, 20])
+    assert torch.equal(step(dec, [s, t], 60), step(alone, ids, 60))
+    assert dec.device_errors() == 0
