@@ -510,7 +510,7 @@ typedef struct pkv_rotary {
   int32_t d, rot_dim, layout;
   float amplitude;
   uint64_t turns[128];               /* 2^64 * f_i / (2 pi) */
-  uint32_t check;                    /* set by pkv_rotary_init */
+  uint32_t check;                    /* set by pkv_rotary_init, pkv_rotary_axes_init */
 } pkv_rotary;
 int pkv_rotary_init(const pkv_rotary_spec *spec, int32_t d, pkv_rotary *out);
 
@@ -525,7 +525,8 @@ int pkv_rotary_init(const pkv_rotary_spec *spec, int32_t d, pkv_rotary *out);
  *   PKV_AXES_OWN      for the k-th pair of an axis, that of pair k of a head that rotates
  *                     2 * sections[a] elements
  * with the spec's layout, scaling and amplitude.  pkv_rotary_axes_init (host only) fills
- * both structs; they belong together.
+ * both structs; they belong together: pkv_rotary_axes_append refuses a pair of other origin,
+ * pkv_rotary_append a table with axes.
  */
 #define PKV_ROTARY_MAX_AXES 8
 #define PKV_AXES_BLOCKED 0

@@ -20,7 +20,10 @@
 namespace pkv {
 namespace {
 
-constexpr uint32_t kRotaryCheck = 0x526f7431u, kAxesCheck = 0x41786573u;
+// What the structs' `check` holds: one number in every plain table; in a table with axes and in
+// its axes a kind each and, alike in both, 24 bits of a hash of what they say together.
+constexpr uint32_t kRotaryCheck = 0x526f7431u, kAxesTable = 0x54000000u, kAxesCheck = 0x41000000u;
+constexpr uint32_t kAxesKind = 0xff000000u;
 constexpr int kThreads = 256;
 
 struct RotaryParams {
@@ -392,7 +395,13 @@ extern "C" int pkv_rotary_axes_init(const pkv_rotary_spec *s, int32_t d, const i
         if (x.axis[i] == a) r.turns[i] = own[k++];
     }
   }
-  x.check = kAxesCheck;
+  uint64_t hash = 14695981039346656037ull;   // (FNV-1a, by words)
+  for (uint64_t word : {uint64_t(d), uint64_t(r.rot_dim), uint64_t(r.layout), uint64_t(n_axes)})
+    hash = (hash ^ word) * 1099511628211ull;
+  for (int i = 0; i < pairs; ++i) hash = ((hash ^ r.turns[i]) * 1099511628211ull ^ x.axis[i]) * 1099511628211ull;
+  const uint32_t both = static_cast<uint32_t>((hash ^ hash >> 32) & ~uint64_t(kAxesKind));
+  r.check = kAxesTable | both;
+  x.check = kAxesCheck | both;
   *out = r;
   *axes = x;
   return PKV_OK;
@@ -407,7 +416,7 @@ extern "C" int pkv_rotary_axes_append(const pkv_rotary_args *a, const pkv_rotary
                                       int64_t axis_stride, void *stream) {
   clear_error();
   PKV_REQUIRE(axes, PKV_ERR_INVALID_ARG, "axes is NULL");
-  PKV_REQUIRE(axes->check == kAxesCheck, PKV_ERR_INVALID_ARG,
+  PKV_REQUIRE((axes->check & kAxesKind) == kAxesCheck, PKV_ERR_INVALID_ARG,
               "axes was not filled by pkv_rotary_axes_init");
   return rotary_append(a, axes, axis_stride, stream);
 }
@@ -416,8 +425,11 @@ int pkv::rotary_append(const pkv_rotary_args *a, const pkv_rotary_axes *axes, lo
                        void *stream) {
   PKV_REQUIRE(a && a->rotary, PKV_ERR_INVALID_ARG, "NULL argument");
   const pkv_rotary &r = *a->rotary;
-  PKV_REQUIRE(r.check == kRotaryCheck, PKV_ERR_INVALID_ARG,
-              "rotary was not filled by pkv_rotary_init");
+  PKV_REQUIRE(axes || (r.check & kAxesKind) != kAxesTable, PKV_ERR_INVALID_ARG,
+              "rotary has axes: it needs them, and positions on each (pkv_rotary_axes_append)");
+  PKV_REQUIRE(r.check == (axes ? kAxesTable | (axes->check & ~kAxesKind) : kRotaryCheck), PKV_ERR_INVALID_ARG,
+              axes ? "rotary and axes were not filled by one pkv_rotary_axes_init"
+                   : "rotary was not filled by pkv_rotary_init");
   PKV_REQUIRE(a->T >= 0 && a->Hq >= 0 && a->Hkv >= 0, PKV_ERR_INVALID_ARG, "negative size");
   PKV_REQUIRE(dtype_ok(a->dtype), PKV_ERR_UNSUPPORTED, "dtype %d", a->dtype);
   PKV_REQUIRE(a->d == r.d, PKV_ERR_INVALID_ARG, "head_dim %d, but rotary was made for %d", a->d,
