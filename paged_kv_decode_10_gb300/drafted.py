@@ -61,6 +61,11 @@ class DraftDecoder(PagedDecoder):
             self._last = now
         return torch.cuda.stream(now)
 
+    def device_errors(self):
+        """As ``PagedDecoder``'s, behind the last call on whichever stream it ran."""
+        with self._on(None):
+            return super().device_errors()
+
     def _upload(self, arrays):
         """Device copies of numpy arrays (int64 ones first), by one copy on the current
         stream out of page-locked memory."""
