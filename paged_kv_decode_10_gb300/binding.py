@@ -1379,6 +1379,8 @@ def make_tree_args(q_rot, k_cache, v_cache, block_tables, seq_lens, node_starts,
     a.B, a.T, a.Hq, a.Hkv, a.d = B, T, Hq, Hkv, d
     a.scale, a.flags = float(scale), int(flags)
     if mask is not None:
+        if mask.dim() == 2 and mask.shape[1] == 0:    # (its address would be that of no mask: a chain)
+            raise PkvError(ERR_INVALID_ARG, "mask: a row needs a word at least")
         a.mask = _want(mask, "mask", (T, None), i32, dev)
         a.mask_words = mask.shape[1]
     if lse is not None:

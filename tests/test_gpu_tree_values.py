@@ -75,8 +75,8 @@ def test_keys_and_queries_that_are_not_finite(value, dtype):
 def test_shared_tiles_with_values_that_are_not_finite(nodes, d):
     """Items of both row tiles whose last tiles hold such values, many at once, again and
     again: one of the two issuers of a tile cleans it for both."""
-    B = 96
-    c = tree.Case([100 + 7 * b for b in range(B)], [nodes] * B, 16, 4, d, "bf16", "tree", seed=4)
+    B = 64
+    c = tree.Case([100 + 7 * b for b in range(B)], [nodes] * B, 8, 2, d, "bf16", "tree", seed=4)
     for b in range(B):
         base = int(c.lens[b]) - nodes
         spoil(c, b, [base + 1 + b % (nodes - 1), base + nodes - 1], float("nan") if b % 2 else float("inf"))
