@@ -24,10 +24,10 @@
 //
 // Masks.  Only steps that reach past the tokens every row sees (the cached ones, and in a
 // chain the nodes ahead of the item's) look at mask bits, 32 at a time.  What a node does not
-// see may be anything, and 0 * NaN is NaN: so the issuing warp looks over the values of such
-// tokens while the softmax is at work, and where one is not finite the element is zeroed in
-// shared memory for the product and added at the end to the rows that see it (any positive
-// weight leaves NaN and infinity what they are).
+// see may be anything, and 0 * NaN is NaN: so the issuing warp (of a tile that both slots use,
+// slot 0's) looks over the values of such tokens while the softmax is at work, and where one
+// is not finite the element is zeroed in shared memory for the product and added at the end
+// to the rows that see it (any positive weight leaves NaN and infinity what they are).
 //
 // The code is kept short: rare paths are functions of their own, the rows' output is written
 // in a loop.  A first form of 150 KB (two slots merged at the end of every item, everything
@@ -134,8 +134,7 @@ __device__ __noinline__ bool wait_started(const Waiter<POLL> w, volatile int *st
   return true;
 }
 
-// Values of rows [first, last) of a V tile that are not finite become zero (one warp);
-// whether there were any.
+// Values of rows [first, last) of a V tile that are not finite become zero (one warp).
 template <int D>
 __device__ __noinline__ void clean_values(unsigned char *vt, int first, int last, int lane) {
   for (int s = 0; s < Lay<D>::kSlabs; ++s)
@@ -446,16 +445,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_tile(v_full, kStartedV, t);
             if (!ok) break;
             // values of tokens that do not count may be anything: their weights are zero,
-            // and so must they be (both slots of a shared tile write the zeros)
+            // and so must they be.  (Of a tile that both slots use slot 0's issuer sees to
+            // it: its product comes first, and its turn, handed over behind the fence,
+            // orders what it wrote ahead of slot 1's.)
             unsigned char *vt = smem + L::kV + st * L::kMat;
             bool changed = false;
             const uint32_t bad = uniform(static_cast<uint32_t>(bad_s[(x + t) % kBadRing]));
-            if (valid % kBlockTokens || bad) {
+            const bool mine = !two || m == 0;
+            if (mine && (valid % kBlockTokens || bad)) {
               zero_values<D>(vt, valid, bad, lane);
               changed = true;
             }
             const int look = max(0, special - tok0);
-            if (look < valid) {
+            if (mine && look < valid) {
               uint32_t odd = 0;
 #pragma unroll 1
               for (int s = 0; s < L::kSlabs; ++s)
@@ -465,10 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   odd |= odd_word(v.x) | odd_word(v.y) | odd_word(v.z) | odd_word(v.w);
                 }
               if (__any_sync(0xffffffffu, odd != 0)) {
-                // (the note first: the other slot may find the tile clean already)
                 if (lane == 0) misc[2 + i % kOddRing] = i + 1;
-                __threadfence_block();
-                __syncwarp();
                 clean_values<D>(vt, look, valid, lane);
                 changed = true;
               }
