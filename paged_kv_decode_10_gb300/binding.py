@@ -1571,9 +1571,13 @@ class Server:
     """The native serving loop (``pkv_server``) over a single-layer
     ``engine.PagedDecoder``'s device buffers for the sequences ``rows`` (one
     per row); joins and leaves then go through ``step``.  Holds the pinned host
-    buffers the server needs."""
+    buffers the server needs.  ``BoundedDecoder`` and ``DraftDecoder`` are refused."""
 
     def __init__(self, dec, rows, max_prefix_tokens):
+        self._h = None
+        if not getattr(dec, "served", True):
+            raise PkvError(ERR_UNSUPPORTED, f"{type(dec).__name__} has a step of its own: the server would "
+                                            "run pkv_decode_step on its caches, with another rotary")
         torch = _torch()
         lib = load()
         B = len(rows)

@@ -30,6 +30,8 @@ class BoundedDecoder(PagedDecoder):
     forms, additive masks, layer chains (``layer_merge_helpers``) and flags other than
     ``ATTN_CHECK_PLAN`` and ``ATTN_SHORT_WAITS`` are not offered here."""
 
+    served = False
+
     def __init__(self, num_blocks, Hq, Hkv, d, dtype, max_seqs, budget, slack=64, sink=4,
                  recent=None, rotary=None, decay=1.0, max_prefixes=16, max_prefix_len=131072, **kw):
         import torch

@@ -25,6 +25,8 @@ class DraftDecoder(PagedDecoder):
     ``plan``, ``layer_merge_helpers``) and flags other than ``ATTN_SHORT_WAITS`` are not
     offered here."""
 
+    served = False
+
     def __init__(self, num_blocks, Hq, Hkv, d, dtype, max_seqs, max_blocks_per_seq, rotary=None, **kw):
         import torch
         for name in ("num_parts", "plan", "layer_merge_helpers", "metadata"):

@@ -69,6 +69,9 @@ def long_units(seq_lens, Hkv, d, num_parts, min_parts=8):
 
 
 class PagedDecoder:
+    # whether the step is pkv_decode_step over buffers that stay (what binding.Server captures)
+    served = True
+
     def __init__(self, num_blocks, Hq, Hkv, d, dtype, max_seqs, max_blocks_per_seq,
                  initial_free=None, device="cuda", num_parts=None, rope_base=10000.0,
                  scale=None, flags=0, k_cache=None, v_cache=None, metadata="copy", n_layers=1,
