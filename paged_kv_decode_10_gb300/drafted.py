@@ -19,6 +19,15 @@ from . import binding
 from .engine import PagedDecoder
 
 
+def _int32(x, name, end=2**31):
+    """Whole numbers from -2^31 below ``end`` as a dense int32 array (those behind 2^31: as bits)."""
+    x = np.asarray(x)
+    if x.dtype != np.int32 and x.size:
+        if x.dtype.kind not in "iu" or int(x.min()) < -2**31 or int(x.max()) >= end:
+            raise ValueError(f"{name}: {x.dtype}, expected whole numbers of 32 bits")
+    return np.ascontiguousarray(x, np.int32)
+
+
 class DraftDecoder(PagedDecoder):
     """``rotary``: a ``binding.Rotary`` (default: the whole head, plain, at ``rope_base``).  The
     rest as ``PagedDecoder``; its captured forms, additive masks, partitions (``num_parts``,
@@ -114,7 +123,7 @@ class DraftDecoder(PagedDecoder):
     def _axes(self, positions, T):
         """Positions ``[T]`` or ``[axes,T]`` (numpy int32) as the rotary takes them."""
         n = self.rotary.n_axes
-        positions = np.ascontiguousarray(positions, np.int32)
+        positions = _int32(positions, "positions")
         if n is None:
             if positions.shape != (T,):
                 raise ValueError(f"positions {positions.shape}, expected [{T}]")
@@ -269,11 +278,13 @@ class DraftDecoder(PagedDecoder):
                 depths += up >= 0
                 up = np.where(up >= 0, above[up], -1)
         elif mask is not None:
-            mask = np.ascontiguousarray(mask, np.int32)
+            mask = _int32(mask, "mask", 2**32)
             if mask.ndim != 2 or len(mask) != T or 32 * mask.shape[1] < counts.max(initial=0):
                 raise ValueError(f"mask {mask.shape}, expected [{T}, words] with a bit for every node")
             if depths is None and positions is None:
                 raise ValueError("a mask needs depths or positions")
+        if depths is not None:
+            depths = _int32(depths, "depths")
         out, before, meta = self._run(seq_ids, counts, q, k, v, mask, depths, positions, stream)
         run = stream if stream is not None else self.torch.cuda.current_stream(self.device)
         self._drafted = (seq_ids, before, counts, meta, run)
