@@ -141,6 +141,8 @@ class DraftDecoder(PagedDecoder):
         n = int(prefix_len)
         if (k is None) != (v is None) or k is not None and (v.shape != k.shape or k.shape[-3] != n):
             raise ValueError("k and v must hold prefix_len tokens")
+        if k is not None and (k.shape[0] if k.dim() == 4 else 1) != self.n_layers:
+            raise ValueError(f"k and v must hold {self.n_layers} layers")
         if k is not None:
             pos = self._axes(np.arange(n) if positions is None else positions, n)
         sid = self.alloc.join(n)

@@ -43,3 +43,14 @@ def test_masks_and_depths(dec):
         with pytest.raises(ValueError):
             call(**kw)
         assert len(dec.reached) == n
+
+
+@pytest.mark.parametrize("L,given", [(1, (2,)), (2, (3,)), (2, (1,)), (2, ()), (3, (2,))])
+def test_join_takes_keys_and_values_of_every_layer(dec, L, given):
+    import torch
+    from paged_kv_decode_10_gb300 import binding
+    dec.n_layers, dec.alloc = L, binding.BlockAllocator(4, 2, 4)
+    k = torch.zeros(given + (5, 2, 64))
+    with pytest.raises(ValueError):
+        dec.join(5, k, k)
+    assert dec.alloc.num_free() == 4
