@@ -157,15 +157,15 @@ struct TreeWalk {
 };
 
 // A CTA's share of `sum` positions: floor(c all / ctas) by 32-bit divisions.  (The rest
-// dealt to the first CTAs, one each, instead of evenly, took 3 % longer.)  MIN: positions a CTA
-// gets at least, while there are CTAs to spare.
-template <int STEP, int BOUND, int MIN>
+// dealt to the first CTAs, one each, instead of evenly, took 3 % longer.)  A call of fewer
+// positions than CTAs leaves the rest of them without any.
+template <int STEP, int BOUND>
 __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_share(const TreeParams &p, int cta,
                                                             unsigned long long sum, bool bad) {
   const bool fits = sum < 1ull << 31;
   const uint32_t all = fits ? static_cast<uint32_t>(sum) : 0;
   if (cta == 0 && (bad || !fits)) set_dev_err(p.err, PKV_DEVERR_BAD_LEN);
-  const uint32_t ctas = max(1u, min(all / MIN, static_cast<uint32_t>(p.C)));
+  const uint32_t ctas = max(1u, min(all, static_cast<uint32_t>(p.C)));
   const uint32_t share = all / ctas, rest = all - share * ctas;
   const uint32_t c = min(static_cast<uint32_t>(cta), ctas), c1 = min(c + 1, ctas);
   const uint32_t lo = c * share + c * rest / ctas, hi = c1 * share + c1 * rest / ctas;
@@ -192,13 +192,13 @@ __device__ __forceinline__ unsigned long long warp_sum_up(unsigned long long x, 
 // Where CTA `cta` of p.C begins, from the rows' lengths (rows that do not fit have no
 // positions; CTA 0 reports them): found by one warp, for batches of at most 32 rows ...
 constexpr int kWarpRows = 32;
-template <int STEP, int BOUND, int MIN>
+template <int STEP, int BOUND>
 __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin_warp(const TreeParams &p, int cta) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   const unsigned long long mine = lane < p.B ? tree_row_cost<STEP, BOUND>(p, lane, &bad) : 0;
   const unsigned long long incl = warp_sum_up(mine, lane);
-  auto walk = tree_share<STEP, BOUND, MIN>(p, cta, __shfl_sync(0xffffffffu, incl, 31),
+  auto walk = tree_share<STEP, BOUND>(p, cta, __shfl_sync(0xffffffffu, incl, 31),
                                            __any_sync(0xffffffffu, bad));
   const uint32_t row =   // the lane that has the first position
       __ballot_sync(0xffffffffu, walk.lo < walk.hi && incl - mine <= walk.lo && walk.lo < incl);
@@ -209,7 +209,7 @@ __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin_warp(const TreeParam
   return walk;
 }
 // ... or by all NT threads of the CTA together.
-template <int STEP, int BOUND, int MIN, int NT>
+template <int STEP, int BOUND, int NT>
 __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p, int cta) {
   __shared__ unsigned long long sums[NT / 32];
   __shared__ int start[2];   // first row, its position
@@ -231,7 +231,7 @@ __device__ __forceinline__ TreeWalk<STEP, BOUND> tree_begin(const TreeParams &p,
     if (w < warp) before += sums[w];
     sum += sums[w];
   }
-  auto walk = tree_share<STEP, BOUND, MIN>(p, cta, sum, false);
+  auto walk = tree_share<STEP, BOUND>(p, cta, sum, false);
   unsigned long long at = before + incl - mine;
   if (walk.lo < walk.hi && at <= walk.lo && walk.lo < at + mine) {   // one thread has the row
     int b = b0;
@@ -291,10 +291,10 @@ __device__ __forceinline__ float tree_lse(float mx, float den, bool sees_any) {
 }
 
 // After a wait that gave up (by all NT threads of the CTA): no output of it counts.
-template <typename T, int D, int STEP, int BOUND, int MIN, int NT>
+template <typename T, int D, int STEP, int BOUND, int NT>
 __device__ __noinline__ void tree_all_nan(const TreeParams &p) {
   const int cta = blockIdx.x;
-  auto walk = tree_begin<STEP, BOUND, MIN, NT>(p, cta);
+  auto walk = tree_begin<STEP, BOUND, NT>(p, cta);
   TreeItem it;
   const float nan = __int_as_float(0x7fffffff);
   while (walk.next(p, &it)) {

@@ -56,7 +56,7 @@ constexpr float kLazy = 8.0f;
 constexpr int kHalf = 2;                      // 32-token pieces of P after which P V starts
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr long long kPollLimit = 4096;
-constexpr int kBoundary = 2, kMin = 1;
+constexpr int kBoundary = 2;
 constexpr int kQueue = 8;                     // items handed out and not yet written out
 constexpr int kBadRing = 16, kOddRing = 4;
 
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (few rows: warp 8 finds its share by itself, while nobody waits for it)
   Walk walk = {};
   if (p.B > kWarpRows)
-    walk = tree_begin<kTile, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+    walk = tree_begin<kTile, kBoundary, kThreads>(p, cta);   // (synchronises the CTA)
   else
     __syncthreads();
   tc_fence_after();
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       TreeItem first = {}, last = {};             // the cut items, and where they end
       uint32_t first_end = 0, last_end = 0;
       bool ok = true;
-      if (!is_v && p.B <= kWarpRows) walk = tree_begin_warp<kTile, kBoundary, kMin>(p, cta);
+      if (!is_v && p.B <= kWarpRows) walk = tree_begin_warp<kTile, kBoundary>(p, cta);
       for (int i = 0; ok; ++i) {
         Handed it;
         if (is_v) {
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (misc[0]) tree_all_nan<__nv_bfloat16, D, kTile, kBoundary, kMin, kThreads>(p);
+  if (misc[0]) tree_all_nan<__nv_bfloat16, D, kTile, kBoundary, kThreads>(p);
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

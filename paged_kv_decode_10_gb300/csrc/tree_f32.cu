@@ -31,7 +31,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kStep = 64, kTile = 64, kCompute = 256, kThreads = kCompute + 32, kBoundary = 1, kMin = 1;
+constexpr int kStep = 64, kTile = 64, kCompute = 256, kThreads = kCompute + 32, kBoundary = 1;
 constexpr int kStages = 2, kQueue = 4;
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr long long kPollLimit = 4096;
@@ -271,13 +271,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
   // (few rows: the loading warp finds its share by itself)
   TreeWalk<kStep, kBoundary> walk = {};
   if (p.B > kWarpRows)
-    walk = tree_begin<kStep, kBoundary, kMin, kThreads>(p, cta);   // (synchronises the CTA)
+    walk = tree_begin<kStep, kBoundary, kThreads>(p, cta);   // (synchronises the CTA)
   else
     __syncthreads();
   const Waiter<POLL> wait{gave_up, p.err, p.wait_limit};
   if (warp == kCompute / 32) {
     // ======================= items, K and V =======================
-    if (p.B <= kWarpRows) walk = tree_begin_warp<kStep, kBoundary, kMin>(p, cta);
+    if (p.B <= kWarpRows) walk = tree_begin_warp<kStep, kBoundary>(p, cta);
     int x = 0;   // steps so far
     uint32_t cut = 0;   // slots that were written down
     bool ok = true;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
     }
   }
   __syncthreads();
-  if (*gave_up) tree_all_nan<float, D, kStep, kBoundary, kMin, kThreads>(p);
+  if (*gave_up) tree_all_nan<float, D, kStep, kBoundary, kThreads>(p);
 }
 
 template <int D, bool POLL>

@@ -59,3 +59,20 @@ def test_pairs_are_refused_like_the_resize(bind):
         assert call(a._h, 0, None, None, 0, ctypes.byref(n)) == bind.ERR_INVALID_ARG
         assert call(a._h, 14, None, None, 0, None) == bind.ERR_INVALID_ARG
         assert call(None, 14, None, None, 0, ctypes.byref(n)) == bind.ERR_INVALID_ARG
+
+
+def test_prepare_nodes_into_given_arrays(bind):
+    a, b = (bind.BlockAllocator(20, 4, 8) for _ in range(2))
+    for x in (a, b):
+        assert [x.join(17), x.join(0)] == [0, 1]
+    out = (np.empty(7, np.int32), np.empty(7, np.int64), np.empty(3, np.int32), np.empty(2, np.int32),
+           np.empty((2, 8), np.int32))
+    got = a.prepare_nodes([1, 0], [5, 2], 8, out=out)
+    assert all(x is y for x, y in zip(got, out))
+    for x, y in zip(out, b.prepare_nodes([1, 0], [5, 2], 8)):
+        assert np.array_equal(x, y)
+    short = (out[0][:6],) + out[1:]
+    state = a.free_stack()
+    with pytest.raises(bind.PkvError):
+        a.prepare_nodes([1, 0], [5, 2], 8, out=short)
+    assert a.free_stack() == state and a.seq_len(1) == 5
