@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kThreads)
 // strictly, so path[j] >= j: going up in j, whatever is overwritten has been read, and a
 // thread that owns one 16-byte column of one head of one pool needs nobody else for
 // that.  A CTA serves kThreads columns of one row at a time; it checks the row first (every
-// CTA of a row comes to the same answer) and lists its moves in shared memory.  Bound by the
-// scattered pieces, a head of a token each (256 bytes, the next head's 4 KB further: 64 rows
-// that accept 1 to 12 nodes, 64 pools of 8 heads of 128, 21 us, 4.6 TB/s), or by the chain of
-// reads before them (3 rows, 2 pools: 3 us).
+// CTA of a row comes to the same answer) and lists its moves in shared memory.  A piece is a
+// head of a token (256 bytes, the next head's 4 KB further).  64 rows that accept 1 to 12
+// nodes, 64 pools of 8 heads of 128: 21 us, 4.6 TB/s, in two waves of CTAs whose shares are
+// uneven (DRAM 34 % busy); 3 rows, 2 pools: 3 us, the chain of reads before the moves.
 template <int POOLS>
 struct AcceptParams {
   const int32_t *block_tables, *seq_lens, *node_starts, *path, *accept_lens;
@@ -191,7 +191,7 @@ int copy_blocks(const pkv_copy_args *a, void *stream) {
   p.dst_num = a->dst_num_blocks;
   p.pieces = a->block_bytes / 16;
   // Chunks of 8 KB (2 pieces a thread) while larger ones would leave SMs without work, 32 KB
-  // once they fill the GPU several times over.
+  // once they give each of the 152 SMs 8 and more.
   const long long blocks = static_cast<long long>(a->n) * a->n_pools;
   const int wide = blocks * p.pieces >= 8ll * 8 * kThreads * 152 ? 8 : 2;
   const long long chunks = (p.pieces + wide * kThreads - 1) / (wide * kThreads);
@@ -232,8 +232,9 @@ int tree_accept(const pkv_accept_args *a, long long head, void *stream) {
   p.path_stride = a->path_stride;
   p.n_pools = a->n_pools;
   const long long items = static_cast<long long>(a->Hkv) * p.cols * a->n_pools;   // below 2^28
-  // As many CTAs as there are pieces of kThreads columns, but no more than fit on the GPU
-  // at once: looking the row over takes a CTA longer than a piece's moves.
+  // As many CTAs as there are pieces of kThreads columns, but no more than about 8 to each of
+  // the 152 SMs (two waves: at 58 registers 4 fit at once): looking the row over takes a CTA
+  // longer than a piece's moves.
   const long long pieces = (items + kThreads - 1) / kThreads, most = a->B < 1216 ? 1216 / a->B : 1;
   p.chunks = static_cast<int>(pieces < most ? pieces : most);
   const unsigned grid = static_cast<unsigned>(p.chunks) * a->B;

@@ -6,6 +6,11 @@ single token: ``step``).  Sequences fork (``fork``: several samples of one promp
 blocks), and the pool takes another size while sequences live (``resize``).  Tokens may have
 positions on several axes (a ``binding.Rotary`` with sections).
 
+Positions that a call does not name count tokens: those held, the sequence's offset and the
+depth, the same on every axis.  Where earlier tokens were placed otherwise (the patches of an
+image or a video share positions, so that text behind them goes on from the largest one, below
+the number of tokens), every later ``verify``, ``extend`` and ``step`` has to name its own.
+
 A step is a0 on the host (``pkv_prepare_nodes``), one copy of its metadata to the GPU, then per
 layer ``pkv_rotary_append`` and ``pkv_decode_attn_tree``; ``accept`` is ``pkv_tree_accept`` over
 all layers, then ``pkv_seqs_truncate`` on the host.  A call on another stream than the call
@@ -260,7 +265,8 @@ class DraftDecoder(PagedDecoder):
         ``q``'s shape.  ``parents [T]``: the node of its own row that a token goes on from, or -1
         (None: the one before).  Instead of parents ``mask`` (int32 ``[T,words]`` of bits) and
         ``depths [T]`` may be given.  ``positions``: ``[T]`` or ``[axes,T]`` (default: the tokens
-        ahead plus the depth, on every axis).  ``accept`` must follow."""
+        ahead plus the depth, on every axis: not the place of text behind an image's patches).
+        ``accept`` must follow."""
         if self._waiting:
             raise ValueError("the last verify's tokens are to be accepted first")
         seq_ids = self._settled(seq_ids)
