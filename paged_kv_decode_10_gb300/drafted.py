@@ -327,9 +327,12 @@ class DraftDecoder(PagedDecoder):
                     for t in meta:
                         t.record_stream(now)
                 path, kept = self._upload([path, kept])
-                for i in range(0, len(pools), binding.MAX_POOLS):
-                    binding.accept_nodes_args(binding.make_accept_args(
-                        pools[i:i + binding.MAX_POOLS], *meta, path, kept, self.err))
+                # (all calls are made before the first moves anything: moved tokens must not
+                # move again when the caller tries once more)
+                for call in [binding.make_accept_args(pools[i:i + binding.MAX_POOLS], *meta, path, kept,
+                                                      self.err)
+                             for i in range(0, len(pools), binding.MAX_POOLS)]:
+                    binding.accept_nodes_args(call)
         rows = [b for b, (s, n) in enumerate(zip(seq_ids, counts)) if s is not None and n]
         self.alloc.truncate_many([seq_ids[b] for b in rows], [before[b] + len(paths[b]) for b in rows])
         self._waiting.clear()
