@@ -24,12 +24,23 @@ from . import binding
 from .engine import PagedDecoder
 
 
-def _int32(x, name, end=2**31):
-    """Whole numbers from -2^31 below ``end`` as a dense int32 array (those behind 2^31: as bits)."""
+def _int32(x, name):
+    """Whole numbers of 32 bits (of any type that holds them) as a dense int32 array."""
     x = np.asarray(x)
     if x.dtype != np.int32 and x.size:
-        if x.dtype.kind not in "iu" or int(x.min()) < -2**31 or int(x.max()) >= end:
-            raise ValueError(f"{name}: {x.dtype}, expected whole numbers of 32 bits")
+        whole = x.dtype.kind in "iu" or x.dtype.kind == "f" and bool((np.isfinite(x) & (x == np.rint(x))).all())
+        if not whole or int(x.min()) < -2**31 or int(x.max()) >= 2**31:
+            raise ValueError(f"{name}: expected whole numbers of 32 bits")
+    return np.ascontiguousarray(x, np.int32)
+
+
+def _words(x):
+    """Mask words (signed or not) as a dense int32 array of the same bits."""
+    x = np.asarray(x)
+    if x.dtype != np.int32 and x.size:
+        if x.dtype.kind not in "iu" or int(x.min()) < -2**31 or int(x.max()) >= 2**32:
+            raise ValueError(f"mask: {x.dtype}, expected words of 32 bits")
+        x = (x.astype(np.int64) & 0xffffffff).astype(np.uint32).view(np.int32)
     return np.ascontiguousarray(x, np.int32)
 
 
@@ -253,7 +264,7 @@ class DraftDecoder(PagedDecoder):
         return out[0] if L == 1 else out, before, (tables, lens, starts)
 
     def _counts(self, seq_ids, counts):
-        counts = np.ascontiguousarray(counts, np.int32)
+        counts = _int32(counts, "counts")
         if counts.shape != (len(seq_ids),) or (counts < 0).any():
             raise ValueError("one number of tokens per sequence, 0 or more")
         return counts
@@ -275,7 +286,7 @@ class DraftDecoder(PagedDecoder):
         if parents is not None:
             if mask is not None or depths is not None:
                 raise ValueError("give parents, or mask and depths")
-            parents = np.ascontiguousarray(parents, np.int64)
+            parents = _int32(parents, "parents").astype(np.int64)
             if parents.shape != (T,):
                 raise ValueError(f"parents {parents.shape}, expected [{T}]")
             mask = binding.tree_mask(parents, starts)
@@ -286,7 +297,7 @@ class DraftDecoder(PagedDecoder):
                 depths += up >= 0
                 up = np.where(up >= 0, above[up], -1)
         elif mask is not None:
-            mask = _int32(mask, "mask", 2**32)
+            mask = _words(mask)
             if mask.ndim != 2 or len(mask) != T or 32 * mask.shape[1] < counts.max(initial=0):
                 raise ValueError(f"mask {mask.shape}, expected [{T}, words] with a bit for every node")
             if depths is None and positions is None:

@@ -19,12 +19,13 @@ def dec(host_lib):
 
 
 def test_positions(dec):
-    for good in ([3, 2**31 - 1], np.array([-2**31, 5]), np.array([1, 2], np.uint8), np.array([[1, 2], [3, 4]], np.int64)):
+    for good in ([3, 2**31 - 1], np.array([-2**31, 5]), np.array([1, 2], np.uint8), np.array([[1, 2], [3, 4]], np.int64),
+                 [3.0, 2**31 - 1]):
         got = dec._axes(good, 2)
         assert got.dtype == np.int32 and got.shape == (2, 2)
         assert got.tolist() == np.broadcast_to(np.asarray(good, np.int64), (2, 2)).tolist()
     assert dec._axes([], 0).shape == (2, 0)
-    for bad in ([1.0, 2.0], [0.5, 1], [True, False], [2**31, 0], [-2**31 - 1, 0], np.array([2**63, 0], np.uint64)):
+    for bad in ([0.5, 1], [np.nan, 1], [np.inf, 1], [2.0**31, 1], [True, False], [2**31, 0], [-2**31 - 1, 0], np.array([2**63, 0], np.uint64)):
         with pytest.raises(ValueError):
             dec._axes(bad, 2)
 
@@ -34,10 +35,14 @@ def test_masks_and_depths(dec):
     call(mask=np.array([[1], [2**31 + 3]]), depths=[0, 1])
     _, _, _, _, _, mask, depths, _, _ = dec.reached[-1]
     assert mask.dtype == np.int32 and mask.tolist() == [[1], [3 - 2**31]] and depths.tolist() == [0, 1]
+    for mask in (np.array([[-1], [3]]), np.array([[2**32 - 1], [3]], np.uint32), np.array([[-1], [3]], np.int8)):
+        dec._waiting.clear()
+        call(mask=mask, depths=[0, 1])
+        assert dec.reached[-1][5].dtype == np.int32 and dec.reached[-1][5].tolist() == [[-1], [3]]
     n = len(dec.reached)
     seen = np.tril(np.ones((2, 2)))
     for kw in (dict(mask=seen.astype(bool), depths=[0, 1]), dict(mask=seen, depths=[0, 1]),
-               dict(mask=[[1], [2**32]], depths=[0, 1]), dict(mask=[[1], [3]], depths=[0.0, 1.0]),
+               dict(mask=[[1], [2**32]], depths=[0, 1]), dict(mask=[[1], [3]], depths=[0.0, 1.5]),
                dict(depths=[0, 2**32])):
         dec._waiting.clear()
         with pytest.raises(ValueError):
@@ -54,3 +59,18 @@ def test_join_takes_keys_and_values_of_every_layer(dec, L, given):
     with pytest.raises(ValueError):
         dec.join(5, k, k)
     assert dec.alloc.num_free() == 4
+
+
+def test_counts_and_parents(dec):
+    call = lambda counts=(2,), **kw: dec.verify([0], counts, None, None, None, **kw)
+    call(np.array([2], np.uint16), parents=np.array([-1, 0], np.int8))
+    dec._waiting.clear()
+    call([2.0], parents=[-1.0, 0.0])
+    assert dec.reached[-1][5].tolist() == [[1], [3]] and dec.reached[-1][6].tolist() == [0, 1]
+    n = len(dec.reached)
+    for kw in (dict(counts=[2.5]), dict(counts=[2**32 + 2]), dict(counts=[True]),
+               dict(parents=[-0.5, 0.5]), dict(parents=[-1, 2**32])):
+        dec._waiting.clear()
+        with pytest.raises(ValueError):
+            call(**kw)
+        assert len(dec.reached) == n
