@@ -131,25 +131,6 @@ int get_tmap(const void *base, long long rows, int D, int dtype, CUtensorMap *ou
   return PKV_OK;
 }
 
-// Queries [T, Hq, D] (bf16) as a 3-D tensor; the box is one 128-byte column slab of 128 rows,
-// 128 / G tokens of the G heads of one KV head, swizzled 128B.
-int query_tmap(const void *base, int T, int Hq, int G, int D, CUtensorMap *out) {
-  EncodeFn enc = encode_fn();
-  PKV_REQUIRE(enc, PKV_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
-                              static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  std::memset(out, 0, sizeof(*out));
-  const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  PKV_REQUIRE(r == CUDA_SUCCESS, PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)",
-              static_cast<int>(r));
-  return PKV_OK;
-}
-
 int current_sms(int *sms) {
   int dev = 0;
   PKV_CUDA_CHECK(cudaGetDevice(&dev));

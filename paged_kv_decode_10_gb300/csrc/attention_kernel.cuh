@@ -1900,6 +1900,5 @@ bool attn_variant_ext_f32(int D, int G, AttnVariant *v);
 
 // The cached TMA descriptor of a cache [rows, D] (attention.cu).
 int get_tmap(const void *base, long long rows, int D, int dtype, CUtensorMap *out);
-int query_tmap(const void *base, int T, int Hq, int G, int D, CUtensorMap *out);
 
 }  // namespace pkv

@@ -146,15 +146,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const void *tmap,
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap, int32_t x, int32_t y,
-                                            int32_t z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-// The 2-D load with an L2 cache policy (createpolicy): pages streamed once
+// The same load with an L2 cache policy (createpolicy): pages streamed once
 // per step go in as evict-first, so they do not push the kernel's code, the
 // step metadata and the merge partials out of L2.
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t smem_dst, const void *tmap, int32_t x,

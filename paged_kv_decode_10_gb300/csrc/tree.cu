@@ -7,6 +7,8 @@
 // tokens are joined by their log-sum-exp.
 #include "tree.h"
 
+#include <cstring>
+
 #include "attention_host.h"
 #include "attention_kernel.cuh"
 
@@ -137,6 +139,33 @@ int tree_space(int d, int dtype, TreeSpace *s) {
   s->lse = align256(2 * s->ctas * sizeof(TreeCut));
   s->o = s->lse + align256(rows * sizeof(float));
   s->bytes = s->o + align256(rows * d * sizeof(float));
+  return PKV_OK;
+}
+
+// Queries [T, Hq, D] (bf16) as a 3-D tensor; the box is one 128-byte column slab of 128 rows,
+// 128 / G tokens of the G heads of one KV head, swizzled 128B.
+int query_tmap(const void *base, int T, int Hq, int G, int D, CUtensorMap *out) {
+  static const auto encode = [] {   // the driver's function, through the runtime
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)
+               : nullptr;
+  }();
+  PKV_REQUIRE(encode, PKV_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  std::memset(out, 0, sizeof(*out));
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  PKV_REQUIRE(r == CUDA_SUCCESS, PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)",
+              static_cast<int>(r));
   return PKV_OK;
 }
 
